@@ -576,6 +576,188 @@ int ssm_scan_bwd_trap(int64_t batch, int64_t L, int64_t D, int64_t N, int dtype,
                       void *dx_prev, float *dB_prev, float *dstate_in, void *workspace, size_t workspace_bytes,
                       void *stream);
 
+/*
+ * Scratch bytes ssm_ssd_fwd_cache needs for these sizes (0 for invalid or
+ * empty sizes). It needs no clearing; calls that share a workspace must not
+ * run at the same time.
+ */
+size_t ssm_ssd_fwd_cache_workspace_bytes(int64_t seqs, int64_t rows, int64_t H, int64_t P, int64_t G, int64_t N,
+                                         int dtype);
+
+/*
+ * The Mamba-2 SSD layer (ssm_ssd_fwd) behind its short causal convolution
+ * and the softplus of its step size, over packed prompts of different
+ * lengths, on a cache of windows and states ("Mamba-2 e State Space Duality
+ * (SSD)": the layer and its width-4 convolution over x, B and C; "Notas sobre
+ * Mamba", section "O bloco Mamba"). A row of xBC holds one token's x (H, P),
+ * B (G, N) and C (G, N), C_all = H P + 2 G N channels in all. Sequence s takes
+ * rows cu_seqlens[s] .. cu_seqlens[s+1] - 1, token 0 first. Per sequence, with
+ * raw[t] its rows and g = h / (H / G):
+ *
+ *   u[t,c]     = conv_b[c] + sum_{j=0..3} conv_w[c,j] * raw[t-3+j, c]
+ *   x | B | C  = u / (1 + exp(-u))                                  (SiLU)
+ *   delta[t,h] = softplus(dt_raw[t,h] + dt_bias[h])
+ *   a[t,h]     = exp(delta[t,h] * A[h])
+ *   S[p][n]    = a[t] * S[p][n] + delta[t] * x[t,h,p] * B[t,g,n]
+ *   y[t,h,p]   = sum_n C[t,g,n] * S[p][n]  (+ Dskip[h] * x[t,h,p])
+ *
+ * The cache keeps, per slot, the raw rows of a sequence's last three tokens
+ * (conv_cache, oldest first) and its state. A sequence with resume[s] != 0
+ * starts from its slot's window and state, any other from zeros (whatever the
+ * slot holds); after the call the slot holds the window and state behind the
+ * sequence's last token. A sequence of no tokens leaves its slot as it is, or
+ * clears it if it does not resume.
+ *
+ *   cu_seqlens    (seqs + 1)     int32      row offsets, not decreasing, from
+ *                                           0 to at most `rows`
+ *   slots         (seqs)         int32      cache slot per sequence
+ *   resume        (seqs)         int32      NULL = every sequence starts from zero
+ *   num_slots                               slots of the two caches
+ *   xBC           (rows, C_all)  dtype      rows xBC_stride elements apart
+ *   conv_w        (C_all, 4)     float      taps; conv_w[c,3] on the token itself
+ *   conv_b        (C_all)        float      NULL = zero
+ *   dt_raw        (rows, H)      dtype      rows dt_stride elements apart
+ *   dt_bias       (H)            float      NULL = zero
+ *   A             (H)            float      negative scalar per head
+ *   Dskip         (H)            float      NULL = no skip term
+ *   conv_cache    (num_slots, C_all, 3)   dtype   read and written
+ *   state_cache   (num_slots, H, P, N)    float   read and written
+ *   y             (rows, H, P)   dtype      written
+ *   workspace     ssm_ssd_fwd_cache_workspace_bytes() bytes
+ *
+ * The offsets, slots and flags are read on the device, so a call may be
+ * captured and replayed with other values in them. A slot outside
+ * [0, num_slots), or one that an earlier sequence of the call names, marks a
+ * sequence to leave out: its rows of y are zeros and no cache entry is
+ * touched. Rows of y outside every sequence are not written. Offsets outside
+ * [0, rows] or decreasing ones are cut to the range, so no access leaves the
+ * tensors; what such a call computes is otherwise unspecified.
+ *
+ * Supported: dtype SSM_BF16, P = 64, 128, 192 or 256, N = 64 or 128, at most
+ * 65535 sequences, rows within 2^31 - 1, strides below 2^23 elements; anything
+ * else returns SSM_ERR_UNSUPPORTED. H must be a multiple of G, strides at
+ * least the row's width (else SSM_ERR_SHAPE), rows of xBC whole 16-byte pieces
+ * apart (else SSM_ERR_ALIGN). Conventions otherwise as above.
+ */
+int ssm_ssd_fwd_cache(int64_t seqs, int64_t rows, int64_t H, int64_t P, int64_t G, int64_t N, int dtype,
+                      const int32_t *cu_seqlens, const int32_t *slots, const int32_t *resume, int64_t num_slots,
+                      const void *xBC, int64_t xBC_stride, const float *conv_w, const float *conv_b,
+                      const void *dt_raw, int64_t dt_stride, const float *dt_bias, const float *A,
+                      const float *Dskip, void *conv_cache, float *state_cache, void *y, void *workspace,
+                      size_t workspace_bytes, void *stream);
+
+/* Scratch bytes ssm_ssd_step_cache needs (0 for invalid or empty sizes); as
+ * for ssm_ssd_fwd_cache. */
+size_t ssm_ssd_step_cache_workspace_bytes(int64_t batch, int64_t H, int64_t P, int64_t G, int64_t N);
+
+/*
+ * One decode token per request on the cache of ssm_ssd_fwd_cache: row b is one
+ * more token of the sequence whose window and state slot slots[b] holds, both
+ * updated in place. Equal to ssm_ssd_fwd_cache over sequences of one token
+ * that resume (up to rounding).
+ *
+ *   slots         (batch)        int32
+ *   xBC           (batch, C_all) dtype      rows xBC_stride elements apart
+ *   dt_raw        (batch, H)     dtype      rows dt_stride elements apart
+ *   y             (batch, H, P)  dtype      written
+ *
+ * Every other argument as there; dtype SSM_F32 or SSM_BF16. A slot outside
+ * [0, num_slots), or one that an earlier row names, marks a padding row: its y
+ * is zeros and no cache entry is touched.
+ */
+int ssm_ssd_step_cache(int64_t batch, int64_t H, int64_t P, int64_t G, int64_t N, int dtype, const int32_t *slots,
+                       int64_t num_slots, const void *xBC, int64_t xBC_stride, const float *conv_w,
+                       const float *conv_b, const void *dt_raw, int64_t dt_stride, const float *dt_bias,
+                       const float *A, const float *Dskip, void *conv_cache, float *state_cache, void *y,
+                       void *workspace, size_t workspace_bytes, void *stream);
+
+/* Scratch bytes ssm_add_norm_bwd and ssm_gate_norm_bwd need (0 for empty or
+ * invalid sizes); no clearing, not shared by calls that run at the same time. */
+size_t ssm_norm_bwd_workspace_bytes(int64_t rows, int64_t D);
+
+/*
+ * The residual sum and the root-mean-square norm ahead of a block, per row:
+ *
+ *   r = residual + scale * x          (r = scale * x where residual is NULL)
+ *   y = r / sqrt(mean(r^2) + eps) * weight
+ *
+ *   x, y          (rows, D)      dtype
+ *   residual      (rows, D)      res_dtype  NULL = zeros
+ *   scale         (D)            float      per-channel scale of x; NULL = 1
+ *   weight        (D)            float
+ *   residual_out  (rows, D)      res_dtype  r (written); may equal residual
+ *
+ * res_dtype is SSM_F32 or dtype. y comes from r before its rounding to
+ * res_dtype; y may equal x. D at most 16384 (else SSM_ERR_UNSUPPORTED).
+ */
+int ssm_add_norm_fwd(int64_t rows, int64_t D, int dtype, int res_dtype, const void *x, const void *residual,
+                     const float *scale, const float *weight, float eps, void *y, void *residual_out, void *stream);
+
+/*
+ * Gradient of ssm_add_norm_fwd, for the loss sum(dy * y) + sum(dres * r). With
+ * rstd = 1 / sqrt(mean(r^2) + eps), hat = r rstd and g = dy weight:
+ *
+ *   dresidual = rstd * (g - hat * mean(g * hat)) + dres      dx = scale * dresidual
+ *   dweight   = sum over rows of dy * hat                    dscale = sum over rows of dresidual * x
+ *
+ *   dy            (rows, D)      dtype
+ *   r             (rows, D)      res_dtype  residual_out of the forward
+ *   x             (rows, D)      dtype      required when scale is given
+ *   dres          (rows, D)      res_dtype  gradient of residual_out from the
+ *                                           layers above; NULL = zeros
+ *   dx            (rows, D)      dtype      written; may equal dy or x
+ *   dresidual     (rows, D)      res_dtype  written; may equal dres or r
+ *   dweight       (D)            float      written
+ *   dscale        (D)            float      written when scale and dscale are given
+ *   workspace     ssm_norm_bwd_workspace_bytes() bytes
+ *
+ * Every sum runs in a fixed order, so equal inputs give equal bits. rows = 0
+ * writes zeros to dweight and dscale.
+ */
+int ssm_add_norm_bwd(int64_t rows, int64_t D, int dtype, int res_dtype, const void *dy, const void *r,
+                     const float *weight, const void *x, const float *scale, const void *dres, float eps, void *dx,
+                     void *dresidual, float *dweight, float *dscale, void *workspace, size_t workspace_bytes,
+                     void *stream);
+
+/*
+ * The gate and the root-mean-square norm behind a scan ("Mamba-2 e State Space
+ * Duality (SSD)": the norm ahead of the Mamba-2 block's output projection), per
+ * row and per group of D / groups channels:
+ *
+ *   u = x * z / (1 + exp(-z))
+ *   y = u / sqrt(mean over the group(u^2) + eps) * weight
+ *
+ *   x             (rows, D)      dtype      rows x_stride elements apart
+ *   z             (rows, D)      dtype      rows z_stride elements apart (a
+ *                                           part of the projection's rows)
+ *   weight        (D)            float
+ *   y             (rows, D)      dtype      written, dense; may equal a dense x
+ *
+ * D must be a multiple of groups and the strides at least D (else
+ * SSM_ERR_SHAPE); D / groups at most 16384 and groups at most 65535 (else
+ * SSM_ERR_UNSUPPORTED).
+ */
+int ssm_gate_norm_fwd(int64_t rows, int64_t D, int64_t groups, int dtype, const void *x, int64_t x_stride,
+                      const void *z, int64_t z_stride, const float *weight, float eps, void *y, void *stream);
+
+/*
+ * Gradient of ssm_gate_norm_fwd, for the loss sum(dy * y). With s = 1 / (1 +
+ * exp(-z)), hat = u rstd, g = dy weight and du = rstd (g - hat mean(g hat)):
+ *
+ *   dx = du * z * s        dz = du * x * s * (1 + z * (1 - s))        dweight = sum over rows of dy * hat
+ *
+ *   dy, dx        (rows, D)      dtype      dense; dx written, may equal dy
+ *   dz            (rows, D)      dtype      rows dz_stride elements apart; written
+ *   dweight       (D)            float      written
+ *   workspace     ssm_norm_bwd_workspace_bytes() bytes
+ *
+ * Sums, rows = 0 and status codes as in ssm_add_norm_bwd.
+ */
+int ssm_gate_norm_bwd(int64_t rows, int64_t D, int64_t groups, int dtype, const void *dy, const void *x,
+                      int64_t x_stride, const void *z, int64_t z_stride, const float *weight, float eps, void *dx,
+                      void *dz, int64_t dz_stride, float *dweight, void *workspace, size_t workspace_bytes,
+                      void *stream);
+
 #ifdef __cplusplus
 }
 #endif

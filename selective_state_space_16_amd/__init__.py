@@ -33,6 +33,16 @@ Functions (same names as the C ABI):
       ssm_scan_fwd_trap, with dlam, and dx_prev, dB_prev for the earlier token
   ssm_ssd_step(x, delta, A, Bt, Ct, state, Dskip=None, y=None) -> y: one SSD
       decode token (x (batch, H, P), Bt/Ct (batch, G, N), state in place)
+  ssm_ssd_fwd_cache(xBC, dt_raw, A, conv_w, cu_seqlens, slots, conv_cache,
+      state_cache, ...) -> y: the SSD layer behind its convolution over packed
+      prompts, with windows and states in a cache of slots
+  ssm_ssd_step_cache(xBC, dt_raw, A, conv_w, slots, conv_cache, state_cache, ...)
+      -> y: one token per request on the same cache
+  ssm_add_norm_fwd(x, weight, residual=None, scale=None, ...) -> (y, residual_out)
+      and ssm_add_norm_bwd(dy, r, weight, ...) -> dict: the residual sum with the
+      root-mean-square norm ahead of a block, and its gradient
+  ssm_gate_norm_fwd(x, z, weight, groups=1, ...) -> y and ssm_gate_norm_bwd(dy, x,
+      z, weight, ...) -> dict: the gate with the (grouped) norm behind a scan
   ssm_scan_workspace_bytes(batch, L, D, N, dtype) -> int
   ssm_scan_workspace_status(workspace, stream=None) -> int: SSM_OK, or
       SSM_ERR_TIMEOUT when a wait of the last scan on that workspace gave up
@@ -52,6 +62,9 @@ __all__ = [
     "ssm_scan_fwd_trap", "ssm_step_trap", "ssm_ssd_fwd", "ssm_ssd_step", "ssm_scan_bwd", "ssm_scan_bwd_dt", "ssm_scan_bwd_trap", "ssm_scan_workspace_bytes",
     "ssm_scan_bwd_workspace_bytes", "ssm_status_string", "ssm_version", "EXPORTS", "new_workspace",
     "workspace_error", "ssm_scan_workspace_status", "SSM_ERR_TIMEOUT", "ssm_scan_fwd_noalloc",
+    "ssm_ssd_fwd_cache", "ssm_ssd_fwd_cache_workspace_bytes", "ssm_ssd_step_cache",
+    "ssm_ssd_step_cache_workspace_bytes", "ssm_add_norm_fwd", "ssm_add_norm_bwd", "ssm_gate_norm_fwd",
+    "ssm_gate_norm_bwd", "ssm_norm_bwd_workspace_bytes",
 ]
 
 SSM_F32 = 0
@@ -71,7 +84,10 @@ EXPORTS = ("ssm_status_string", "ssm_version", "ssm_scan_workspace_bytes", "ssm_
            "ssm_scan_fwd_dt", "ssm_step_dt", "ssm_scan_fwd_trap", "ssm_step_trap", "ssm_ssd_fwd",
            "ssm_scan_bwd_workspace_bytes", "ssm_scan_bwd", "ssm_scan_bwd_dt", "ssm_scan_bwd_trap", "ssm_ssd_step",
            "ssm_scan_workspace_status", "ssm_scan_fwd_noalloc", "ssm_scan_fwd_conv", "ssm_step_conv",
-           "ssm_scan_bwd_conv_workspace_bytes", "ssm_scan_bwd_conv")
+           "ssm_scan_bwd_conv_workspace_bytes", "ssm_scan_bwd_conv",
+           "ssm_ssd_fwd_cache_workspace_bytes", "ssm_ssd_fwd_cache", "ssm_ssd_step_cache_workspace_bytes",
+           "ssm_ssd_step_cache", "ssm_norm_bwd_workspace_bytes", "ssm_add_norm_fwd", "ssm_add_norm_bwd",
+           "ssm_gate_norm_fwd", "ssm_gate_norm_bwd")
 
 _lib: Optional[ctypes.CDLL] = None
 
@@ -134,6 +150,27 @@ def lib() -> ctypes.CDLL:
     L.ssm_scan_bwd_conv.restype = ci
     L.ssm_scan_bwd_trap.argtypes = [i64, i64, i64, i64, ci] + [vp] * 24 + [vp, sz, vp]
     L.ssm_scan_bwd_trap.restype = ci
+    cf = ctypes.c_float
+    L.ssm_ssd_fwd_cache_workspace_bytes.argtypes = [i64] * 6 + [ci]
+    L.ssm_ssd_fwd_cache_workspace_bytes.restype = sz
+    L.ssm_ssd_fwd_cache.argtypes = ([i64] * 6 + [ci, vp, vp, vp, i64, vp, i64, vp, vp, vp, i64] + [vp] * 3 + [vp] * 3 +
+                                    [vp, sz, vp])
+    L.ssm_ssd_fwd_cache.restype = ci
+    L.ssm_ssd_step_cache_workspace_bytes.argtypes = [i64] * 5
+    L.ssm_ssd_step_cache_workspace_bytes.restype = sz
+    L.ssm_ssd_step_cache.argtypes = ([i64] * 5 + [ci, vp, i64, vp, i64, vp, vp, vp, i64] + [vp] * 3 + [vp] * 3 +
+                                     [vp, sz, vp])
+    L.ssm_ssd_step_cache.restype = ci
+    L.ssm_norm_bwd_workspace_bytes.argtypes = [i64, i64]
+    L.ssm_norm_bwd_workspace_bytes.restype = sz
+    L.ssm_add_norm_fwd.argtypes = [i64, i64, ci, ci, vp, vp, vp, vp, cf, vp, vp, vp]
+    L.ssm_add_norm_fwd.restype = ci
+    L.ssm_add_norm_bwd.argtypes = [i64, i64, ci, ci] + [vp] * 6 + [cf] + [vp] * 4 + [vp, sz, vp]
+    L.ssm_add_norm_bwd.restype = ci
+    L.ssm_gate_norm_fwd.argtypes = [i64, i64, i64, ci, vp, i64, vp, i64, vp, cf, vp, vp]
+    L.ssm_gate_norm_fwd.restype = ci
+    L.ssm_gate_norm_bwd.argtypes = [i64, i64, i64, ci, vp, vp, i64, vp, i64, vp, cf, vp, vp, i64, vp, vp, sz, vp]
+    L.ssm_gate_norm_bwd.restype = ci
     _lib = L
     return L
 
@@ -643,3 +680,223 @@ def ssm_ssd_step(x, delta, A, Bt, Ct, state, Dskip=None, y=None, stream=None):
     if st != 0:
         raise SSMError(st, "ssm_ssd_step")
     return y
+
+
+def ssm_ssd_fwd_cache_workspace_bytes(seqs: int, rows: int, H: int, P: int, G: int, N: int, dtype: int) -> int:
+    return int(lib().ssm_ssd_fwd_cache_workspace_bytes(seqs, rows, H, P, G, N, dtype))
+
+
+def ssm_ssd_step_cache_workspace_bytes(batch: int, H: int, P: int, G: int, N: int) -> int:
+    return int(lib().ssm_ssd_step_cache_workspace_bytes(batch, H, P, G, N))
+
+
+def ssm_norm_bwd_workspace_bytes(rows: int, D: int) -> int:
+    return int(lib().ssm_norm_bwd_workspace_bytes(rows, D))
+
+
+def _rows(t, name, dtype, shape):
+    """Device pointer and row stride (elements) of a 2-D GPU tensor whose rows
+    are dense but may lie apart (a slice of a wider one)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    # with one row the stride is never used: any allowed one
+    return t.data_ptr(), (t.stride(0) if shape[0] > 1 else -(-shape[1] // 8) * 8)
+
+
+def _call(name, on, tensors, stream, allocated, *args):
+    """Launch on the device of `on` (which need not be the current one), on its
+    current stream unless one is given."""
+    import torch
+    for t in tensors:
+        if t is not None and t.device != on.device:
+            raise ValueError(f"every tensor must be on {on.device}, got one on {t.device}")
+    with torch.cuda.device(on.device):
+        _order_after_alloc(stream, allocated)
+        st = getattr(lib(), name)(*args, _stream(stream))
+    if st != 0:
+        raise SSMError(st, name)
+
+
+def _ssd_cache(name, xBC, dt_raw, A, conv_w, cu_seqlens, slots, conv_cache, state_cache, conv_b, dt_bias, Dskip,
+               resume, y, workspace, stream):
+    import torch
+    if xBC.dim() != 2 or state_cache.dim() != 4 or slots.dim() != 1:
+        raise ValueError("xBC must be (rows, H P + 2 G N), state_cache (slots, H, P, N) and slots (sequences,)")
+    rows, C = xBC.shape
+    num_slots, H, P, N = state_cache.shape
+    if N == 0 or (C - H * P) % (2 * N) or C < H * P:
+        raise ValueError(f"a row of {C} channels does not hold x ({H}, {P}) and B, C of {N} states per group")
+    G = (C - H * P) // (2 * N)
+    seqs = slots.shape[0]
+    act, f32, i32 = xBC.dtype, torch.float32, torch.int32
+    code = _dtype_code(xBC)
+    prompt = name == "ssm_ssd_fwd_cache"
+    if not prompt and rows != seqs:
+        raise ValueError(f"one row per request: {rows} rows, {seqs} slots")
+    x_ptr, x_stride = _rows(xBC, "xBC", act, (rows, C))
+    dt_ptr, dt_stride = _rows(dt_raw, "dt_raw", act, (rows, H))
+    allocated = []
+    if y is None:
+        # rows outside every sequence are not written
+        y = torch.zeros((rows, H, P), dtype=act, device=xBC.device) if prompt else torch.empty(
+            (rows, H, P), dtype=act, device=xBC.device)
+        allocated.append(y)
+    need = ssm_ssd_fwd_cache_workspace_bytes(seqs, rows, H, P, G, N, code) if prompt else \
+        ssm_ssd_step_cache_workspace_bytes(seqs, H, P, G, N)
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=xBC.device)
+        allocated.append(workspace)
+    sizes = [seqs, rows, H, P, G, N, code] if prompt else [seqs, H, P, G, N, code]
+    args = [_ptr(cu_seqlens, "cu_seqlens", i32, (seqs + 1,))] if prompt else []
+    args.append(_ptr(slots, "slots", i32, (seqs,)))
+    if prompt:
+        args.append(_ptr(resume, "resume", i32, (seqs,)))
+    args += [num_slots, x_ptr, x_stride, _ptr(conv_w, "conv_w", f32, (C, 4)), _ptr(conv_b, "conv_b", f32, (C,)),
+             dt_ptr, dt_stride, _ptr(dt_bias, "dt_bias", f32, (H,)), _ptr(A, "A", f32, (H,)),
+             _ptr(Dskip, "Dskip", f32, (H,)), _ptr(conv_cache, "conv_cache", act, (num_slots, C, 3)),
+             _ptr(state_cache, "state_cache", f32, (num_slots, H, P, N)), _ptr(y, "y", act, (rows, H, P)),
+             _ptr(workspace, "workspace"), workspace.numel() * workspace.element_size()]
+    _call(name, xBC, (dt_raw, A, conv_w, cu_seqlens, slots, conv_cache, state_cache, conv_b, dt_bias, Dskip, resume, y,
+                      workspace), stream, allocated, *sizes, *args)
+    return y
+
+
+def ssm_ssd_fwd_cache(xBC, dt_raw, A, conv_w, cu_seqlens, slots, conv_cache, state_cache, conv_b=None, dt_bias=None,
+                      Dskip=None, resume=None, y=None, workspace=None, stream=None):
+    """Mamba-2 SSD layer behind its convolution over packed prompts, on a cache.
+    Shapes: xBC (rows, H P + 2 G N) and dt_raw (rows, H) bfloat16, rows dense but
+    possibly apart (slices of the projection); A, dt_bias, Dskip (H,), conv_w
+    (C, 4), conv_b (C,) float32; cu_seqlens (seqs + 1,), slots, resume (seqs,)
+    int32 on the device; conv_cache (slots, C, 3) bfloat16 and state_cache
+    (slots, H, P, N) float32, updated in place; y (rows, H, P). A y that the call
+    allocates is zero in rows outside every sequence; a given one keeps them."""
+    return _ssd_cache("ssm_ssd_fwd_cache", xBC, dt_raw, A, conv_w, cu_seqlens, slots, conv_cache, state_cache, conv_b,
+                      dt_bias, Dskip, resume, y, workspace, stream)
+
+
+def ssm_ssd_step_cache(xBC, dt_raw, A, conv_w, slots, conv_cache, state_cache, conv_b=None, dt_bias=None, Dskip=None,
+                       y=None, workspace=None, stream=None):
+    """One decode token per request on the cache of ssm_ssd_fwd_cache: xBC
+    (batch, C) and dt_raw (batch, H), float32 or bfloat16; slots (batch,) int32,
+    a slot outside the cache (or named by an earlier row) marking a padding row
+    whose y is zeros."""
+    return _ssd_cache("ssm_ssd_step_cache", xBC, dt_raw, A, conv_w, None, slots, conv_cache, state_cache, conv_b,
+                      dt_bias, Dskip, None, y, workspace, stream)
+
+
+def _res_code(residual, act):
+    import torch
+    if residual.dtype not in (torch.float32, act):
+        raise TypeError(f"the residual must be float32 or {act}, got {residual.dtype}")
+    return _dtype_code(residual)
+
+
+def ssm_add_norm_fwd(x, weight, residual=None, scale=None, eps=1e-5, y=None, residual_out=None, stream=None):
+    """r = residual + scale * x, y = rms_norm(r) * weight; returns (y, r). Shapes:
+    x, y (rows, D); residual, r (rows, D) float32 or x's dtype (r is float32
+    without a residual); scale, weight (D,) float32."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError("x must be (rows, D)")
+    rows, D = x.shape
+    act, f32 = x.dtype, torch.float32
+    code = _dtype_code(x)
+    allocated = []
+    if y is None:
+        y = torch.empty_like(x)
+        allocated.append(y)
+    if residual_out is None:
+        residual_out = torch.empty((rows, D), dtype=f32 if residual is None else residual.dtype, device=x.device)
+        allocated.append(residual_out)
+    rcode = _res_code(residual_out, act)
+    _call("ssm_add_norm_fwd", x, (weight, residual, scale, y, residual_out), stream, allocated, rows, D, code, rcode,
+          _ptr(x, "x", act), _ptr(residual, "residual", residual_out.dtype, (rows, D)),
+          _ptr(scale, "scale", f32, (D,)), _ptr(weight, "weight", f32, (D,)), float(eps), _ptr(y, "y", act, (rows, D)),
+          _ptr(residual_out, "residual_out", residual_out.dtype, (rows, D)))
+    return y, residual_out
+
+
+def ssm_add_norm_bwd(dy, r, weight, x=None, scale=None, dres=None, eps=1e-5, out=None, workspace=None, stream=None):
+    """Gradient of ssm_add_norm_fwd for the loss sum(dy * y) + sum(dres * r). dy
+    (rows, D); r the forward's residual_out; x required with a scale. Returns a
+    dict: dx (like dy), dresidual (like r), dweight (D,) float32, dscale (D,)
+    float32 or None. `out` may hold preallocated outputs by those names."""
+    import torch
+    if dy.dim() != 2:
+        raise ValueError("dy must be (rows, D)")
+    rows, D = dy.shape
+    act, f32 = dy.dtype, torch.float32
+    code, rcode = _dtype_code(dy), _res_code(r, dy.dtype)
+    o = dict(out or {})
+    given = set(o)
+    o.setdefault("dx", torch.empty_like(dy))
+    o.setdefault("dresidual", torch.empty_like(r))
+    o.setdefault("dweight", torch.empty((D,), dtype=f32, device=dy.device))
+    o.setdefault("dscale", None if scale is None else torch.empty((D,), dtype=f32, device=dy.device))
+    allocated = [v for k, v in o.items() if k not in given and v is not None]
+    if workspace is None:
+        workspace = torch.empty(max(ssm_norm_bwd_workspace_bytes(rows, D), 16), dtype=torch.uint8, device=dy.device)
+        allocated.append(workspace)
+    _call("ssm_add_norm_bwd", dy, (r, weight, x, scale, dres, workspace, *o.values()), stream, allocated, rows, D, code,
+          rcode, _ptr(dy, "dy", act), _ptr(r, "r", r.dtype, (rows, D)), _ptr(weight, "weight", f32, (D,)),
+          _ptr(x, "x", act, (rows, D)), _ptr(scale, "scale", f32, (D,)), _ptr(dres, "dres", r.dtype, (rows, D)),
+          float(eps), _ptr(o["dx"], "dx", act, (rows, D)), _ptr(o["dresidual"], "dresidual", r.dtype, (rows, D)),
+          _ptr(o["dweight"], "dweight", f32, (D,)), _ptr(o["dscale"], "dscale", f32, (D,)),
+          _ptr(workspace, "workspace"), workspace.numel() * workspace.element_size())
+    return o
+
+
+def ssm_gate_norm_fwd(x, z, weight, groups=1, eps=1e-5, y=None, stream=None):
+    """y = rms_norm(x * silu(z)) * weight over groups of D / groups channels. x, z
+    (rows, D), rows dense but possibly apart (z a slice of the projection);
+    weight (D,) float32; y (rows, D)."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError("x must be (rows, D)")
+    rows, D = x.shape
+    act, f32 = x.dtype, torch.float32
+    code = _dtype_code(x)
+    x_ptr, x_stride = _rows(x, "x", act, (rows, D))
+    z_ptr, z_stride = _rows(z, "z", act, (rows, D))
+    allocated = []
+    if y is None:
+        y = torch.empty((rows, D), dtype=act, device=x.device)
+        allocated.append(y)
+    _call("ssm_gate_norm_fwd", x, (z, weight, y), stream, allocated, rows, D, int(groups), code, x_ptr, x_stride, z_ptr,
+          z_stride, _ptr(weight, "weight", f32, (D,)), float(eps), _ptr(y, "y", act, (rows, D)))
+    return y
+
+
+def ssm_gate_norm_bwd(dy, x, z, weight, groups=1, eps=1e-5, out=None, workspace=None, stream=None):
+    """Gradient of ssm_gate_norm_fwd for the loss sum(dy * y): a dict of dx, dz
+    (rows, D) in x's dtype and dweight (D,) float32. `out` may hold preallocated
+    outputs by those names (dz with rows apart, as z may be)."""
+    import torch
+    if dy.dim() != 2:
+        raise ValueError("dy must be (rows, D)")
+    rows, D = dy.shape
+    act, f32 = dy.dtype, torch.float32
+    code = _dtype_code(dy)
+    o = dict(out or {})
+    given = set(o)
+    o.setdefault("dx", torch.empty_like(dy))
+    o.setdefault("dz", torch.empty_like(dy))
+    o.setdefault("dweight", torch.empty((D,), dtype=f32, device=dy.device))
+    allocated = [v for k, v in o.items() if k not in given]
+    if workspace is None:
+        workspace = torch.empty(max(ssm_norm_bwd_workspace_bytes(rows, D), 16), dtype=torch.uint8, device=dy.device)
+        allocated.append(workspace)
+    x_ptr, x_stride = _rows(x, "x", act, (rows, D))
+    z_ptr, z_stride = _rows(z, "z", act, (rows, D))
+    dz_ptr, dz_stride = _rows(o["dz"], "dz", act, (rows, D))
+    _call("ssm_gate_norm_bwd", dy, (x, z, weight, workspace, *o.values()), stream, allocated, rows, D, int(groups), code,
+          _ptr(dy, "dy", act), x_ptr, x_stride, z_ptr, z_stride, _ptr(weight, "weight", f32, (D,)), float(eps),
+          _ptr(o["dx"], "dx", act, (rows, D)), dz_ptr, dz_stride, _ptr(o["dweight"], "dweight", f32, (D,)),
+          _ptr(workspace, "workspace"), workspace.numel() * workspace.element_size())
+    return o

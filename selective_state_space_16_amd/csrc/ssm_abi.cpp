@@ -77,6 +77,20 @@ size_t workspace_for(int64_t batch, int64_t L, int64_t D, int64_t N, int dtype) 
                                                                : twopass_workspace(batch, L, D, N, &K, &Lc);
 }
 
+constexpr int64_t kMaxRow = (int64_t)1 << 23;  // elements between rows of the cache entry points' inputs
+
+// Sizes the SSD layer on a cache takes: heads of 64 to 256 in whole 64s, N of
+// 64 or 128, rows and sequences that the kernels' offsets and grids reach.
+bool ssd_cache_sizes(int64_t seqs, int64_t rows, int64_t H, int64_t P, int64_t G, int64_t N) {
+    if (P < 64 || P > 256 || P % 64 != 0 || (N != 64 && N != 128)) return false;
+    if (seqs > 65535 || rows > INT32_MAX || H >= kMaxRow / P || G >= kMaxRow / (2 * N)) return false;
+    return H * P + 2 * G * N < kMaxRow && rows / 64 + seqs <= INT32_MAX / ((H * P) / 64 + 1);
+}
+
+// Floats per request in the step's workspace: x | B | C, dt and exp(dt A),
+// in whole 16-byte pieces.
+int64_t ssd_step_row(int64_t H, int64_t P, int64_t G, int64_t N) { return (H * P + 2 * G * N + 2 * H + 3) / 4 * 4; }
+
 }  // namespace
 
 extern "C" {
@@ -87,7 +101,7 @@ const char *ssm_status_string(int status) {
         case SSM_ERR_NULL: return "a required pointer is NULL";
         case SSM_ERR_SHAPE: return "a size is negative or the tensor sizes overflow";
         case SSM_ERR_DTYPE: return "dtype must be SSM_F32 or SSM_BF16";
-        case SSM_ERR_UNSUPPORTED: return "N must be 1, 2, 4, 8 or 16";
+        case SSM_ERR_UNSUPPORTED: return "N (1, 2, 4, 8 or 16 in a selective scan) or another size is not one this entry point supports";
         case SSM_ERR_ALIGN: return "a pointer is not 16-byte aligned";
         case SSM_ERR_WORKSPACE: return "workspace is missing or too small";
         case SSM_ERR_HIP: return "a HIP launch failed";
@@ -704,6 +718,240 @@ int ssm_ssd_fwd(int64_t batch, int64_t L, int64_t H, int64_t P, int64_t G, int64
     a.state_out = state_out;
     a.y = y;
     return ssm::launch_ssd(a, (int)N, s) == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+}
+
+// Sizes and arguments that ssm_ssd_fwd_cache and ssm_ssd_step_cache share;
+// fills `a` when everything is in order.
+static int ssd_cache_check(int64_t seqs, int64_t rows, int64_t H, int64_t P, int64_t G, int64_t N, int dtype,
+                           bool prompt, const int32_t *cu_seqlens, const int32_t *slots, const int32_t *resume,
+                           int64_t num_slots, const void *xBC, int64_t xBC_stride, const float *conv_w,
+                           const float *conv_b, const void *dt_raw, int64_t dt_stride, const float *dt_bias,
+                           const float *A, const float *Dskip, void *conv_cache, float *state_cache, void *y,
+                           const void *workspace, size_t workspace_bytes, ssm::SsdCacheArgs *a) {
+    if (seqs < 0 || rows < 0 || H < 0 || P < 0 || G < 0 || N < 0 || num_slots < 0 || xBC_stride < 0 || dt_stride < 0)
+        return SSM_ERR_SHAPE;
+    if (dtype != SSM_F32 && dtype != SSM_BF16) return SSM_ERR_DTYPE;
+    if ((prompt && dtype != SSM_BF16) || !ssd_cache_sizes(seqs, rows, H, P, G, N)) return SSM_ERR_UNSUPPORTED;
+    if (H > 0 && (G < 1 || H % G != 0)) return SSM_ERR_SHAPE;
+    const int64_t C = H * P + 2 * G * N;
+    if (num_slots > INT32_MAX || xBC_stride < C || dt_stride < H) return SSM_ERR_SHAPE;
+    // 64 rows and the three before them are reached by 32-bit offsets
+    if (xBC_stride >= kMaxRow || dt_stride >= kMaxRow) return SSM_ERR_UNSUPPORTED;
+    if (checked_mul3(checked_mul(num_slots, H), P, N) < 0 || checked_mul3(num_slots, C, 3) < 0) return SSM_ERR_SHAPE;
+    if (seqs == 0 || H == 0) return SSM_OK;
+    if (!slots || !A || !conv_w || !conv_cache || !state_cache || (prompt && !cu_seqlens)) return SSM_ERR_NULL;
+    if (rows > 0 && (!xBC || !dt_raw || !y)) return SSM_ERR_NULL;
+    const void *ptrs[] = {cu_seqlens, slots, resume, xBC, conv_w, conv_b, dt_raw, dt_bias, A, Dskip,
+                          conv_cache, state_cache, y, workspace};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return SSM_ERR_ALIGN;
+    if (xBC_stride * (dtype == SSM_F32 ? 4 : 2) % 16 != 0) return SSM_ERR_ALIGN;
+    const size_t need = prompt ? ssm_ssd_fwd_cache_workspace_bytes(seqs, rows, H, P, G, N, dtype)
+                               : ssm_ssd_step_cache_workspace_bytes(seqs, H, P, G, N);
+    if (!workspace || workspace_bytes < need) return SSM_ERR_WORKSPACE;
+    a->seqs = seqs;
+    a->rows = rows;
+    a->H = H;
+    a->P = P;
+    a->G = G;
+    a->C = C;
+    a->num_slots = num_slots;
+    a->xBC_stride = xBC_stride;
+    a->dt_stride = dt_stride;
+    a->cu_seqlens = cu_seqlens;
+    a->slots = slots;
+    a->resume = resume;
+    a->xBC = xBC;
+    a->dt_raw = dt_raw;
+    a->conv_w = conv_w;
+    a->conv_b = conv_b;
+    a->dt_bias = dt_bias;
+    a->A = A;
+    a->Dskip = Dskip;
+    a->conv_cache = conv_cache;
+    a->state_cache = state_cache;
+    a->y = y;
+    return SSM_OK;
+}
+
+size_t ssm_ssd_fwd_cache_workspace_bytes(int64_t seqs, int64_t rows, int64_t H, int64_t P, int64_t G, int64_t N,
+                                         int dtype) {
+    if (dtype != SSM_BF16 || seqs <= 0 || rows < 0 || H <= 0 || G < 1 || H % G != 0 ||
+        !ssd_cache_sizes(seqs, rows, H, P, G, N))
+        return 0;
+    return ssm::ssd_cache_workspace(seqs, rows, H, P, G, N);
+}
+
+int ssm_ssd_fwd_cache(int64_t seqs, int64_t rows, int64_t H, int64_t P, int64_t G, int64_t N, int dtype,
+                      const int32_t *cu_seqlens, const int32_t *slots, const int32_t *resume, int64_t num_slots,
+                      const void *xBC, int64_t xBC_stride, const float *conv_w, const float *conv_b,
+                      const void *dt_raw, int64_t dt_stride, const float *dt_bias, const float *A,
+                      const float *Dskip, void *conv_cache, float *state_cache, void *y, void *workspace,
+                      size_t workspace_bytes, void *stream) {
+    ssm::SsdCacheArgs a{};
+    const int st = ssd_cache_check(seqs, rows, H, P, G, N, dtype, true, cu_seqlens, slots, resume, num_slots, xBC,
+                                   xBC_stride, conv_w, conv_b, dt_raw, dt_stride, dt_bias, A, Dskip, conv_cache,
+                                   state_cache, y, workspace, workspace_bytes, &a);
+    if (st != SSM_OK || seqs == 0 || H == 0) return st;
+    return ssm::launch_ssd_cache(a, (int)N, workspace, (hipStream_t)stream) == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+}
+
+size_t ssm_ssd_step_cache_workspace_bytes(int64_t batch, int64_t H, int64_t P, int64_t G, int64_t N) {
+    if (batch <= 0 || H <= 0 || G < 1 || H % G != 0 || !ssd_cache_sizes(batch, batch, H, P, G, N)) return 0;
+    return round_up256((size_t)batch * 4) + (size_t)batch * ssd_step_row(H, P, G, N) * 4;
+}
+
+int ssm_ssd_step_cache(int64_t batch, int64_t H, int64_t P, int64_t G, int64_t N, int dtype, const int32_t *slots,
+                       int64_t num_slots, const void *xBC, int64_t xBC_stride, const float *conv_w,
+                       const float *conv_b, const void *dt_raw, int64_t dt_stride, const float *dt_bias,
+                       const float *A, const float *Dskip, void *conv_cache, float *state_cache, void *y,
+                       void *workspace, size_t workspace_bytes, void *stream) {
+    ssm::SsdCacheArgs a{};
+    const int st = ssd_cache_check(batch, batch, H, P, G, N, dtype, false, nullptr, slots, nullptr, num_slots, xBC,
+                                   xBC_stride, conv_w, conv_b, dt_raw, dt_stride, dt_bias, A, Dskip, conv_cache,
+                                   state_cache, y, workspace, workspace_bytes, &a);
+    if (st != SSM_OK || batch == 0 || H == 0) return st;
+    a.ws_slot = (int32_t *)workspace;
+    a.ws_act = (float *)((char *)workspace + round_up256((size_t)batch * 4));
+    a.ws_row = ssd_step_row(H, P, G, N);
+    return ssm::launch_ssd_step_cache(a, (int)N, dtype, (hipStream_t)stream) == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+}
+
+size_t ssm_norm_bwd_workspace_bytes(int64_t rows, int64_t D) {
+    if (rows <= 0 || D <= 0 || checked_mul(rows, D) < 0) return 0;
+    return (size_t)ssm::norm_bwd_blocks(rows) * 2 * (size_t)D * sizeof(float);
+}
+
+// Sizes that every norm entry point takes.
+static int norm_check(int64_t rows, int64_t D, int64_t groups, int dtype) {
+    if (rows < 0 || D < 0 || groups < 0) return SSM_ERR_SHAPE;
+    if (dtype != SSM_F32 && dtype != SSM_BF16) return SSM_ERR_DTYPE;
+    if (D > 0 && (groups < 1 || D % groups != 0)) return SSM_ERR_SHAPE;
+    if (D > 0 && (D / groups > ssm::kNormMaxWidth || groups > 65535)) return SSM_ERR_UNSUPPORTED;
+    return checked_mul(rows, D) < 0 ? SSM_ERR_SHAPE : SSM_OK;
+}
+
+int ssm_add_norm_fwd(int64_t rows, int64_t D, int dtype, int res_dtype, const void *x, const void *residual,
+                     const float *scale, const float *weight, float eps, void *y, void *residual_out, void *stream) {
+    const int st = norm_check(rows, D, 1, dtype);
+    if (st != SSM_OK) return st;
+    if (res_dtype != SSM_F32 && res_dtype != dtype) return SSM_ERR_DTYPE;
+    if (rows == 0 || D == 0) return SSM_OK;
+    if (!x || !weight || !y || !residual_out) return SSM_ERR_NULL;
+    const void *ptrs[] = {x, residual, scale, weight, y, residual_out};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return SSM_ERR_ALIGN;
+    ssm::AddNormArgs a{};
+    a.rows = rows;
+    a.D = D;
+    a.eps = eps;
+    a.x = x;
+    a.residual = residual;
+    a.scale = scale;
+    a.weight = weight;
+    a.y = y;
+    a.residual_out = residual_out;
+    return ssm::launch_add_norm(a, false, dtype, res_dtype, (hipStream_t)stream) == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+}
+
+int ssm_add_norm_bwd(int64_t rows, int64_t D, int dtype, int res_dtype, const void *dy, const void *r,
+                     const float *weight, const void *x, const float *scale, const void *dres, float eps, void *dx,
+                     void *dresidual, float *dweight, float *dscale, void *workspace, size_t workspace_bytes,
+                     void *stream) {
+    const int st = norm_check(rows, D, 1, dtype);
+    if (st != SSM_OK) return st;
+    if (res_dtype != SSM_F32 && res_dtype != dtype) return SSM_ERR_DTYPE;
+    if (D == 0) return SSM_OK;
+    if (!dweight) return SSM_ERR_NULL;
+    if (rows > 0 && (!dy || !r || !weight || !dx || !dresidual || (scale && !x))) return SSM_ERR_NULL;
+    const void *ptrs[] = {dy, r, weight, x, scale, dres, dx, dresidual, dweight, dscale, workspace};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return SSM_ERR_ALIGN;
+    hipStream_t s = (hipStream_t)stream;
+    if (rows == 0) {
+        if (ssm::launch_state_copy(nullptr, dweight, D, s) != hipSuccess) return SSM_ERR_HIP;
+        return !dscale || ssm::launch_state_copy(nullptr, dscale, D, s) == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+    }
+    if (!workspace || workspace_bytes < ssm_norm_bwd_workspace_bytes(rows, D)) return SSM_ERR_WORKSPACE;
+    ssm::AddNormArgs a{};
+    a.rows = rows;
+    a.D = D;
+    a.eps = eps;
+    a.x = x;
+    a.residual = r;
+    a.dy = dy;
+    a.dres = dres;
+    a.scale = scale;
+    a.weight = weight;
+    a.residual_out = dresidual;
+    a.dx = dx;
+    a.dweight = dweight;
+    a.dscale = scale ? dscale : nullptr;
+    a.part = (float *)workspace;
+    return ssm::launch_add_norm(a, true, dtype, res_dtype, s) == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+}
+
+int ssm_gate_norm_fwd(int64_t rows, int64_t D, int64_t groups, int dtype, const void *x, int64_t x_stride,
+                      const void *z, int64_t z_stride, const float *weight, float eps, void *y, void *stream) {
+    const int st = norm_check(rows, D, groups, dtype);
+    if (st != SSM_OK) return st;
+    if (x_stride < D || z_stride < D || checked_mul(rows, x_stride) < 0 || checked_mul(rows, z_stride) < 0)
+        return SSM_ERR_SHAPE;
+    if (rows == 0 || D == 0) return SSM_OK;
+    if (!x || !z || !weight || !y) return SSM_ERR_NULL;
+    const void *ptrs[] = {x, z, weight, y};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return SSM_ERR_ALIGN;
+    ssm::GateNormArgs a{};
+    a.rows = rows;
+    a.D = D;
+    a.groups = groups;
+    a.x_stride = x_stride;
+    a.z_stride = z_stride;
+    a.eps = eps;
+    a.x = x;
+    a.z = z;
+    a.weight = weight;
+    a.y = y;
+    return ssm::launch_gate_norm(a, false, dtype, (hipStream_t)stream) == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+}
+
+int ssm_gate_norm_bwd(int64_t rows, int64_t D, int64_t groups, int dtype, const void *dy, const void *x,
+                      int64_t x_stride, const void *z, int64_t z_stride, const float *weight, float eps, void *dx,
+                      void *dz, int64_t dz_stride, float *dweight, void *workspace, size_t workspace_bytes,
+                      void *stream) {
+    const int st = norm_check(rows, D, groups, dtype);
+    if (st != SSM_OK) return st;
+    if (x_stride < D || z_stride < D || dz_stride < D || checked_mul(rows, x_stride) < 0 ||
+        checked_mul(rows, z_stride) < 0 || checked_mul(rows, dz_stride) < 0)
+        return SSM_ERR_SHAPE;
+    if (D == 0) return SSM_OK;
+    if (!dweight) return SSM_ERR_NULL;
+    if (rows > 0 && (!dy || !x || !z || !weight || !dx || !dz)) return SSM_ERR_NULL;
+    const void *ptrs[] = {dy, x, z, weight, dx, dz, dweight, workspace};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return SSM_ERR_ALIGN;
+    hipStream_t s = (hipStream_t)stream;
+    if (rows == 0)
+        return ssm::launch_state_copy(nullptr, dweight, D, s) == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+    if (!workspace || workspace_bytes < ssm_norm_bwd_workspace_bytes(rows, D)) return SSM_ERR_WORKSPACE;
+    ssm::GateNormArgs a{};
+    a.rows = rows;
+    a.D = D;
+    a.groups = groups;
+    a.x_stride = x_stride;
+    a.z_stride = z_stride;
+    a.dz_stride = dz_stride;
+    a.eps = eps;
+    a.x = x;
+    a.z = z;
+    a.dy = dy;
+    a.weight = weight;
+    a.dx = dx;
+    a.dz = dz;
+    a.dweight = dweight;
+    a.part = (float *)workspace;
+    return ssm::launch_gate_norm(a, true, dtype, s) == hipSuccess ? SSM_OK : SSM_ERR_HIP;
 }
 
 }  // extern "C"

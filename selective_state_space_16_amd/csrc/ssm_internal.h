@@ -214,4 +214,48 @@ int scan_fwd_euler(int64_t batch, int64_t L, int64_t D, int64_t N, int dtype, co
 hipError_t launch_state_copy(const float *src, float *dst, int64_t n, hipStream_t s);
 hipError_t launch_step(const StepArgs &a, int N, int dtype, hipStream_t s);
 
+// The SSD layer behind its convolution on a cache of states: packed prompts
+// (ssm_ssd_cache.hip) and one token per request (ssm_ssd_step_cache.hip).
+struct SsdCacheArgs {
+    int64_t seqs, rows, H, P, G, C, num_slots, xBC_stride, dt_stride;  // C = H P + 2 G N
+    const int32_t *cu_seqlens, *slots, *resume;
+    const void *xBC, *dt_raw;
+    const float *conv_w, *conv_b, *dt_bias, *A, *Dskip;
+    void *conv_cache;
+    float *state_cache;
+    void *y;
+    // workspace
+    int32_t *ws_slot;   // (seqs) the slot a sequence owns, -1 for none
+    uint16_t *ws_win;   // prompts: (seqs, 3, C) raw rows before each sequence
+    float *ws_act;      // step: (seqs, ws_row) x | B | C after the convolution, dt, exp(dt A)
+    int64_t ws_row;
+};
+size_t ssd_cache_workspace(int64_t seqs, int64_t rows, int64_t H, int64_t P, int64_t G, int64_t N);
+hipError_t launch_ssd_cache(SsdCacheArgs a, int N, void *workspace, hipStream_t s);
+hipError_t launch_ssd_step_cache(const SsdCacheArgs &a, int N, int dtype, hipStream_t s);
+
+// The norms of a block (ssm_norm.hip). `residual` and `residual_out` are the
+// sum and its gradient in the backward pass.
+constexpr int64_t kNormMaxWidth = 16384;  // channels of a row (or group) that a workgroup holds
+constexpr int64_t kNormBwdBlocks = 512;   // workgroups of a backward pass: one partial row each
+struct AddNormArgs {
+    int64_t rows, D;
+    float eps;
+    const void *x, *residual, *dy, *dres;
+    const float *scale, *weight;
+    void *y, *residual_out, *dx;
+    float *dweight, *dscale, *part;
+};
+struct GateNormArgs {
+    int64_t rows, D, groups, x_stride, z_stride, dz_stride;
+    float eps;
+    const void *x, *z, *dy;
+    const float *weight;
+    void *y, *dx, *dz;
+    float *dweight, *part;
+};
+int64_t norm_bwd_blocks(int64_t rows);
+hipError_t launch_add_norm(const AddNormArgs &a, bool backward, int dtype, int res_dtype, hipStream_t s);
+hipError_t launch_gate_norm(const GateNormArgs &a, bool backward, int dtype, hipStream_t s);
+
 }  // namespace ssm

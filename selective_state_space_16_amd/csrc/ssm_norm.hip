@@ -1,0 +1,484 @@
+// The norms of a Mamba block for gfx950, forward and backward: the residual
+// sum with the root-mean-square norm ahead of the block's projection, and the
+// gate with the (grouped) root-mean-square norm behind its scan.
+//
+//   add norm    r = residual + scale o x;   y = r rstd w,  rstd = (mean r^2 + eps)^-1/2
+//   gate norm   u = x silu(z);              y = u rstd w   per group of D / groups channels
+//
+// Backward, with g = dy w and hat = r rstd (or u rstd), the norm's chain rule is
+//   dr = rstd (g - hat mean(g hat)),   dw = sum over rows of dy hat,
+// so one reduction per row gives both sums that a row needs (sum r^2 and
+// sum g r). Every kernel reads each input once and writes each output once:
+// HBM bounds them all. A row is held in registers by the lanes that read it
+// (a wave, or a workgroup for long rows), so a row costs one pass.
+//
+// dw (and dscale) sum over all rows: a workgroup keeps its rows' sums in
+// registers, adds its waves' in a fixed order through LDS and writes one
+// partial row; a second kernel adds the partial rows in order. Equal inputs
+// give equal bits.
+#include "ssm_common.h"
+#include "ssm_internal.h"
+
+namespace ssm {
+
+namespace {
+
+typedef float f32x4n __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4n __attribute__((ext_vector_type(4)));
+
+// VEC consecutive elements as floats. VEC = 8: 16-byte pieces; 1: one element.
+template <int VEC>
+__device__ __forceinline__ void ld_vec(const float *p, float (&v)[VEC]) {
+    if constexpr (VEC == 8) {
+        const f32x4n a = *(const f32x4n *)p, b = *(const f32x4n *)(p + 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
+    } else {
+        v[0] = *p;
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void ld_vec(const uint16_t *p, float (&v)[VEC]) {
+    if constexpr (VEC == 8) {
+        const u32x4n a = *(const u32x4n *)p;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(a[i] << 16);
+            v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
+        }
+    } else {
+        v[0] = ld_act(p, 0);
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void st_vec(float *p, const float (&v)[VEC]) {
+    if constexpr (VEC == 8) {
+        *(f32x4n *)p = f32x4n{v[0], v[1], v[2], v[3]};
+        *(f32x4n *)(p + 4) = f32x4n{v[4], v[5], v[6], v[7]};
+    } else {
+        *p = v[0];
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void st_vec(uint16_t *p, const float (&v)[VEC]) {
+    if constexpr (VEC == 8) {
+        typedef __bf16 bf16x8n __attribute__((ext_vector_type(8)));
+        bf16x8n o;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = (__bf16)v[i];
+        *(bf16x8n *)p = o;
+    } else {
+        st_act(p, 0, v[0]);
+    }
+}
+
+// Sums of NV values over the TPR lanes that share a row, in every one of them.
+// A wave adds by lane exchanges; more waves meet through LDS (two buffers in
+// turn, so that one barrier per row is enough).
+template <int TPR, int NV>
+__device__ __forceinline__ void row_sum(float (&v)[NV], float (*sh)[16][NV], int &turn) {
+#pragma unroll
+    for (int m = 1; m < 64; m *= 2)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) v[i] += __shfl_xor(v[i], m);
+    if constexpr (TPR > 64) {
+        const int w = threadIdx.x >> 6;
+        if ((threadIdx.x & 63) == 0)
+#pragma unroll
+            for (int i = 0; i < NV; ++i) sh[turn][w][i] = v[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float s = 0.0f;
+#pragma unroll
+            for (int k = 0; k < TPR / 64; ++k) s += sh[turn][k][i];
+            v[i] = s;
+        }
+        turn ^= 1;
+    }
+}
+
+constexpr int block_threads(int TPR) { return TPR < 256 ? 256 : TPR; }
+
+// Adds a workgroup's column sums (one set per row-sharing group of lanes) in
+// the order of the groups and writes them as one partial row of D columns.
+template <int TPR, int VEC, int ITER>
+__device__ __forceinline__ void write_partial(const float (&acc)[ITER][VEC], float *sh, float *part, int64_t D) {
+    constexpr int RPB = block_threads(TPR) / TPR;
+    const int lane = threadIdx.x % TPR, mine = threadIdx.x / TPR;
+#pragma unroll
+    for (int w = 0; w < RPB; ++w) {
+        if (RPB > 1) __syncthreads();
+        if (mine != w) continue;
+#pragma unroll
+        for (int k = 0; k < ITER; ++k) {
+            const int c = (k * TPR + lane) * VEC;
+            if (c >= D) continue;
+            if (RPB == 1) {
+                st_vec<VEC>(part + c, acc[k]);
+            } else {
+                float t[VEC];
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    t[i] = w == 0 ? acc[k][i] : sh[c + i] + acc[k][i];
+                    sh[c + i] = t[i];
+                }
+                if (w == RPB - 1) st_vec<VEC>(part + c, t);
+            }
+        }
+    }
+    if (RPB > 1) __syncthreads();
+}
+
+template <int TPR, int VEC, int ITER, typename T, typename R>
+__global__ __launch_bounds__(block_threads(TPR)) void add_norm_fwd_kernel(AddNormArgs a) {
+    constexpr int RPB = block_threads(TPR) / TPR;
+    __shared__ float sh[2][16][1];
+    int turn = 0;
+    const int lane = threadIdx.x % TPR;
+    const int64_t D = a.D;
+    const float inv = 1.0f / (float)D;
+    for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; row < a.rows; row += (int64_t)gridDim.x * RPB) {
+        const int64_t base = row * D;
+        float r[ITER][VEC], ss[1] = {0.0f};
+#pragma unroll
+        for (int k = 0; k < ITER; ++k) {
+            const int c = (k * TPR + lane) * VEC;
+            if (c < D) {
+                float x[VEC];
+                ld_vec<VEC>((const T *)a.x + base + c, x);
+                if (a.residual) ld_vec<VEC>((const R *)a.residual + base + c, r[k]);
+                float s[VEC];
+                if (a.scale) ld_vec<VEC>(a.scale + c, s);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const float add = a.scale ? s[i] * x[i] : x[i];
+                    r[k][i] = a.residual ? r[k][i] + add : add;
+                    ss[0] = __builtin_fmaf(r[k][i], r[k][i], ss[0]);
+                }
+            }
+        }
+        row_sum<TPR, 1>(ss, sh, turn);
+        const float rstd = rsqrtf(__builtin_fmaf(ss[0], inv, a.eps));
+#pragma unroll
+        for (int k = 0; k < ITER; ++k) {
+            const int c = (k * TPR + lane) * VEC;
+            if (c < D) {
+                float w[VEC], y[VEC];
+                ld_vec<VEC>(a.weight + c, w);
+                st_vec<VEC>((R *)a.residual_out + base + c, r[k]);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) y[i] = r[k][i] * rstd * w[i];
+                st_vec<VEC>((T *)a.y + base + c, y);
+            }
+        }
+    }
+}
+
+template <int TPR, int VEC, int ITER, typename T, typename R>
+__global__ __launch_bounds__(block_threads(TPR)) void add_norm_bwd_kernel(AddNormArgs a) {
+    constexpr int RPB = block_threads(TPR) / TPR;
+    __shared__ float sh[2][16][2];
+    __shared__ float cols[RPB > 1 ? TPR * VEC * ITER : 1];
+    int turn = 0;
+    const int lane = threadIdx.x % TPR;
+    const int64_t D = a.D;
+    const float inv = 1.0f / (float)D;
+    float dw[ITER][VEC], ds[ITER][VEC];
+#pragma unroll
+    for (int k = 0; k < ITER; ++k)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) dw[k][i] = ds[k][i] = 0.0f;
+    for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; row < a.rows; row += (int64_t)gridDim.x * RPB) {
+        const int64_t base = row * D;
+        float r[ITER][VEC], dy[ITER][VEC], ss[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < ITER; ++k) {
+            const int c = (k * TPR + lane) * VEC;
+            if (c < D) {
+                float w[VEC];
+                ld_vec<VEC>((const R *)a.residual + base + c, r[k]);
+                ld_vec<VEC>((const T *)a.dy + base + c, dy[k]);
+                ld_vec<VEC>(a.weight + c, w);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    ss[0] = __builtin_fmaf(r[k][i], r[k][i], ss[0]);
+                    ss[1] = __builtin_fmaf(dy[k][i] * w[i], r[k][i], ss[1]);
+                }
+            }
+        }
+        row_sum<TPR, 2>(ss, sh, turn);
+        const float rstd = rsqrtf(__builtin_fmaf(ss[0], inv, a.eps));
+        const float m = ss[1] * inv * rstd;  // mean(g hat)
+#pragma unroll
+        for (int k = 0; k < ITER; ++k) {
+            const int c = (k * TPR + lane) * VEC;
+            if (c < D) {
+                float w[VEC], dr[VEC], up[VEC], x[VEC], s[VEC], dx[VEC];
+                ld_vec<VEC>(a.weight + c, w);
+                if (a.dres) ld_vec<VEC>((const R *)a.dres + base + c, up);
+                if (a.scale) {
+                    ld_vec<VEC>((const T *)a.x + base + c, x);
+                    ld_vec<VEC>(a.scale + c, s);
+                }
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const float hat = r[k][i] * rstd;
+                    dw[k][i] = __builtin_fmaf(dy[k][i], hat, dw[k][i]);
+                    float v = rstd * __builtin_fmaf(-m, hat, dy[k][i] * w[i]);
+                    if (a.dres) v += up[i];
+                    dr[i] = v;
+                    if (a.scale) {
+                        dx[i] = v * s[i];
+                        ds[k][i] = __builtin_fmaf(v, x[i], ds[k][i]);
+                    } else {
+                        dx[i] = v;
+                    }
+                }
+                st_vec<VEC>((R *)a.residual_out + base + c, dr);
+                st_vec<VEC>((T *)a.dx + base + c, dx);
+            }
+        }
+    }
+    write_partial<TPR, VEC, ITER>(dw, cols, a.part + (int64_t)blockIdx.x * D, D);
+    if (a.scale) write_partial<TPR, VEC, ITER>(ds, cols, a.part + ((int64_t)gridDim.x + blockIdx.x) * D, D);
+}
+
+// u = x silu(z) and the factors of its gradient.
+__device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + fast_exp2(-z * kLog2e)); }
+
+template <int TPR, int VEC, int ITER, typename T>
+__global__ __launch_bounds__(block_threads(TPR)) void gate_norm_fwd_kernel(GateNormArgs a) {
+    constexpr int RPB = block_threads(TPR) / TPR;
+    __shared__ float sh[2][16][1];
+    int turn = 0;
+    const int lane = threadIdx.x % TPR;
+    const int64_t Dg = a.D / a.groups, g0 = (int64_t)blockIdx.y * Dg;
+    const float inv = 1.0f / (float)Dg;
+    for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; row < a.rows; row += (int64_t)gridDim.x * RPB) {
+        const T *xp = (const T *)a.x + row * a.x_stride + g0, *zp = (const T *)a.z + row * a.z_stride + g0;
+        T *yp = (T *)a.y + row * a.D + g0;
+        float u[ITER][VEC], ss[1] = {0.0f};
+#pragma unroll
+        for (int k = 0; k < ITER; ++k) {
+            const int c = (k * TPR + lane) * VEC;
+            if (c < Dg) {
+                float x[VEC], z[VEC];
+                ld_vec<VEC>(xp + c, x);
+                ld_vec<VEC>(zp + c, z);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    u[k][i] = x[i] * silu(z[i]);
+                    ss[0] = __builtin_fmaf(u[k][i], u[k][i], ss[0]);
+                }
+            }
+        }
+        row_sum<TPR, 1>(ss, sh, turn);
+        const float rstd = rsqrtf(__builtin_fmaf(ss[0], inv, a.eps));
+#pragma unroll
+        for (int k = 0; k < ITER; ++k) {
+            const int c = (k * TPR + lane) * VEC;
+            if (c < Dg) {
+                float w[VEC], y[VEC];
+                ld_vec<VEC>(a.weight + g0 + c, w);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) y[i] = u[k][i] * rstd * w[i];
+                st_vec<VEC>(yp + c, y);
+            }
+        }
+    }
+}
+
+template <int TPR, int VEC, int ITER, typename T>
+__global__ __launch_bounds__(block_threads(TPR)) void gate_norm_bwd_kernel(GateNormArgs a) {
+    constexpr int RPB = block_threads(TPR) / TPR;
+    __shared__ float sh[2][16][2];
+    __shared__ float cols[RPB > 1 ? TPR * VEC * ITER : 1];
+    int turn = 0;
+    const int lane = threadIdx.x % TPR;
+    const int64_t D = a.D, Dg = D / a.groups, g0 = (int64_t)blockIdx.y * Dg;
+    const float inv = 1.0f / (float)Dg;
+    float dw[ITER][VEC];
+#pragma unroll
+    for (int k = 0; k < ITER; ++k)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) dw[k][i] = 0.0f;
+    for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; row < a.rows; row += (int64_t)gridDim.x * RPB) {
+        const T *xp = (const T *)a.x + row * a.x_stride + g0, *zp = (const T *)a.z + row * a.z_stride + g0;
+        const T *dyp = (const T *)a.dy + row * D + g0;
+        float x[ITER][VEC], z[ITER][VEC], dy[ITER][VEC], ss[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < ITER; ++k) {
+            const int c = (k * TPR + lane) * VEC;
+            if (c < Dg) {
+                float w[VEC];
+                ld_vec<VEC>(xp + c, x[k]);
+                ld_vec<VEC>(zp + c, z[k]);
+                ld_vec<VEC>(dyp + c, dy[k]);
+                ld_vec<VEC>(a.weight + g0 + c, w);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const float u = x[k][i] * silu(z[k][i]);
+                    ss[0] = __builtin_fmaf(u, u, ss[0]);
+                    ss[1] = __builtin_fmaf(dy[k][i] * w[i], u, ss[1]);
+                }
+            }
+        }
+        row_sum<TPR, 2>(ss, sh, turn);
+        const float rstd = rsqrtf(__builtin_fmaf(ss[0], inv, a.eps));
+        const float m = ss[1] * inv * rstd;  // mean(g hat)
+#pragma unroll
+        for (int k = 0; k < ITER; ++k) {
+            const int c = (k * TPR + lane) * VEC;
+            if (c < Dg) {
+                float w[VEC], dx[VEC], dz[VEC];
+                ld_vec<VEC>(a.weight + g0 + c, w);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const float s = sigmoid(z[k][i]), gate = z[k][i] * s, u = x[k][i] * gate;
+                    const float hat = u * rstd;
+                    dw[k][i] = __builtin_fmaf(dy[k][i], hat, dw[k][i]);
+                    const float du = rstd * __builtin_fmaf(-m, hat, dy[k][i] * w[i]);
+                    dx[i] = du * gate;
+                    // silu'(z) = s + z s (1 - s)
+                    dz[i] = du * x[k][i] * __builtin_fmaf(gate, 1.0f - s, s);
+                }
+                st_vec<VEC>((T *)a.dx + row * D + g0 + c, dx);
+                st_vec<VEC>((T *)a.dz + row * a.dz_stride + g0 + c, dz);
+            }
+        }
+    }
+    write_partial<TPR, VEC, ITER>(dw, cols, a.part + (int64_t)blockIdx.x * D + g0, Dg);
+}
+
+// out[c] = sum over the partial rows, in order: 64 columns per workgroup, 16
+// slices of the rows, whose sums are added in the order of the slices.
+__global__ __launch_bounds__(1024) void norm_reduce_kernel(const float *part, int64_t nblk, int64_t D, float *out0,
+                                                           float *out1) {
+    __shared__ float sh[16][64];
+    const int64_t c = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
+    const int s = threadIdx.x >> 6;
+    const float *p = part + (int64_t)blockIdx.y * nblk * D;
+    const int64_t per = (nblk + 15) / 16, lo = s * per, hi = lo + per < nblk ? lo + per : nblk;
+    float v = 0.0f;
+    if (c < D)
+#pragma unroll 8
+        for (int64_t i = lo; i < hi; ++i) v += p[i * D + c];
+    sh[s][threadIdx.x & 63] = v;
+    __syncthreads();
+    if (s == 0 && c < D) {
+#pragma unroll
+        for (int k = 1; k < 16; ++k) v += sh[k][threadIdx.x & 63];
+        (blockIdx.y ? out1 : out0)[c] = v;
+    }
+}
+
+// Lanes per row and elements per lane by the row's length: a wave per row as
+// long as it holds at most 40 elements per lane (2560 channels), then a
+// workgroup of 4 or 16 waves. VEC = 1 where rows are not whole 16-byte pieces.
+#define SSM_NORM_DISPATCH(LEN, VEC8, CALL)                      \
+    do {                                                        \
+        const int64_t n_ = (LEN);                               \
+        if (VEC8) {                                             \
+            if (n_ <= 512) return CALL(64, 8, 1);               \
+            if (n_ <= 1024) return CALL(64, 8, 2);              \
+            if (n_ <= 1536) return CALL(64, 8, 3);              \
+            if (n_ <= 2048) return CALL(64, 8, 4);              \
+            if (n_ <= 2560) return CALL(64, 8, 5);              \
+            if (n_ <= 4096) return CALL(256, 8, 2);             \
+            if (n_ <= 6144) return CALL(256, 8, 3);             \
+            if (n_ <= 8192) return CALL(256, 8, 4);             \
+            return CALL(1024, 8, 2);                            \
+        }                                                       \
+        if (n_ <= 256) return CALL(64, 1, 4);                   \
+        if (n_ <= 1024) return CALL(64, 1, 16);                 \
+        if (n_ <= 4096) return CALL(256, 1, 16);                \
+        return CALL(1024, 1, 16);                               \
+    } while (0)
+
+unsigned norm_grid(int64_t rows, int tpr, int64_t cap) {
+    const int64_t rpb = tpr < 256 ? 256 / tpr : 1, b = (rows + rpb - 1) / rpb;
+    return (unsigned)(b < cap ? b : cap);
+}
+
+template <int TPR, int VEC, int ITER, typename T, typename R>
+hipError_t add_fwd_n(const AddNormArgs &a, hipStream_t s) {
+    hipLaunchKernelGGL((add_norm_fwd_kernel<TPR, VEC, ITER, T, R>), dim3(norm_grid(a.rows, TPR, 8192)),
+                       dim3(block_threads(TPR)), 0, s, a);
+    return hipGetLastError();
+}
+template <typename T, typename R>
+hipError_t add_fwd(const AddNormArgs &a, hipStream_t s) {
+#define SSM_CALL(TPR, VEC, ITER) add_fwd_n<TPR, VEC, ITER, T, R>(a, s)
+    SSM_NORM_DISPATCH(a.D, a.D % 8 == 0, SSM_CALL);
+#undef SSM_CALL
+}
+
+hipError_t launch_reduce(const float *part, int64_t nblk, int64_t D, float *o0, float *o1, hipStream_t s) {
+    hipLaunchKernelGGL(norm_reduce_kernel, dim3((unsigned)((D + 63) / 64), o1 ? 2 : 1), dim3(1024), 0, s, part, nblk, D,
+                       o0, o1);
+    return hipGetLastError();
+}
+
+template <int TPR, int VEC, int ITER, typename T, typename R>
+hipError_t add_bwd_n(const AddNormArgs &a, hipStream_t s) {
+    const unsigned g = norm_grid(a.rows, TPR, kNormBwdBlocks);
+    hipLaunchKernelGGL((add_norm_bwd_kernel<TPR, VEC, ITER, T, R>), dim3(g), dim3(block_threads(TPR)), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess ? e : launch_reduce(a.part, g, a.D, a.dweight, a.scale ? a.dscale : nullptr, s);
+}
+template <typename T, typename R>
+hipError_t add_bwd(const AddNormArgs &a, hipStream_t s) {
+#define SSM_CALL(TPR, VEC, ITER) add_bwd_n<TPR, VEC, ITER, T, R>(a, s)
+    SSM_NORM_DISPATCH(a.D, a.D % 8 == 0, SSM_CALL);
+#undef SSM_CALL
+}
+
+template <int TPR, int VEC, int ITER, typename T>
+hipError_t gate_fwd_n(const GateNormArgs &a, hipStream_t s) {
+    hipLaunchKernelGGL((gate_norm_fwd_kernel<TPR, VEC, ITER, T>),
+                       dim3(norm_grid(a.rows, TPR, 8192), (unsigned)a.groups), dim3(block_threads(TPR)), 0, s, a);
+    return hipGetLastError();
+}
+template <int TPR, int VEC, int ITER, typename T>
+hipError_t gate_bwd_n(const GateNormArgs &a, hipStream_t s) {
+    const unsigned g = norm_grid(a.rows, TPR, kNormBwdBlocks);
+    hipLaunchKernelGGL((gate_norm_bwd_kernel<TPR, VEC, ITER, T>), dim3(g, (unsigned)a.groups), dim3(block_threads(TPR)),
+                       0, s, a);
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess ? e : launch_reduce(a.part, g, a.D, a.dweight, nullptr, s);
+}
+// whole 16-byte pieces: the group's width, and the row strides of what is read and written
+bool gate_vec(const GateNormArgs &a) {
+    return (a.D / a.groups) % 8 == 0 && a.x_stride % 8 == 0 && a.z_stride % 8 == 0 && a.dz_stride % 8 == 0;
+}
+template <typename T>
+hipError_t gate_fwd(const GateNormArgs &a, hipStream_t s) {
+#define SSM_CALL(TPR, VEC, ITER) gate_fwd_n<TPR, VEC, ITER, T>(a, s)
+    SSM_NORM_DISPATCH(a.D / a.groups, gate_vec(a), SSM_CALL);
+#undef SSM_CALL
+}
+template <typename T>
+hipError_t gate_bwd(const GateNormArgs &a, hipStream_t s) {
+#define SSM_CALL(TPR, VEC, ITER) gate_bwd_n<TPR, VEC, ITER, T>(a, s)
+    SSM_NORM_DISPATCH(a.D / a.groups, gate_vec(a), SSM_CALL);
+#undef SSM_CALL
+}
+
+}  // namespace
+
+// Workgroups of a backward pass, each of which writes one partial row.
+int64_t norm_bwd_blocks(int64_t rows) { return rows < kNormBwdBlocks ? rows : kNormBwdBlocks; }
+
+hipError_t launch_add_norm(const AddNormArgs &a, bool backward, int dtype, int res_dtype, hipStream_t s) {
+    if (dtype == 0) return backward ? add_bwd<float, float>(a, s) : add_fwd<float, float>(a, s);
+    if (res_dtype == 0) return backward ? add_bwd<uint16_t, float>(a, s) : add_fwd<uint16_t, float>(a, s);
+    return backward ? add_bwd<uint16_t, uint16_t>(a, s) : add_fwd<uint16_t, uint16_t>(a, s);
+}
+
+hipError_t launch_gate_norm(const GateNormArgs &a, bool backward, int dtype, hipStream_t s) {
+    if (dtype == 0) return backward ? gate_bwd<float>(a, s) : gate_fwd<float>(a, s);
+    return backward ? gate_bwd<uint16_t>(a, s) : gate_fwd<uint16_t>(a, s);
+}
+
+}  // namespace ssm
