@@ -7,123 +7,817 @@
 //   dt      = softplus(dt_raw + dt_bias),   a = exp(dt A)
 //   S[p][n] = a S[p][n] + dt x[p] B[n],     y[p] = sum_n C[n] S[p][n] + D x[p]
 //
-// The simple form: one workgroup per (sequence, head, 64 rows of the state)
-// walks the tokens in order; four lanes share a state row.
+// Every sequence is cut into chunks of 64 tokens. With cum_t the log2 decay
+// from the chunk's start through token t, sfx_t from behind t to its end and
+// w_t = dt_t exp2(sfx_t), a chunk is three matrix products on the matrix cores:
+//
+//   y   = diag(exp2(cum)) C S^T + (G o exp2(cum_t - cum_s) dt_s, s <= t) x + D x,   G = C B^T
+//   S^T = exp2(cum_last) S^T + B^T (w o x)
+//
+// Launches, in order:
+//   prepare   per (chunk, group): the convolution of B and C, G, and the layouts
+//             that the products load; per (chunk, head): the decays. B, C and G
+//             are shared by all heads of a group, so they are formed once.
+//   walk<0>   for sequences longer than a segment: every segment but the last
+//             from a zero start, its end state only (no y);
+//   join      those end states in order: the state that enters each segment;
+//   walk<1>   every segment from its entering state: y, and the sequence's last
+//             state and window into the cache.
+// The offsets are read on the device. Chunk i of sequence s has the id cu[s] /
+// 64 + s + i (segments likewise): disjoint ranges without a prefix sum, as
+// ceil(len / 64) <= cu[s+1] / 64 - cu[s] / 64 + 1.
+//
+// Precision. The state must come out as a float32 state would, so the products
+// that update it take both operands as sums of two float16 (22 bits; three
+// products, the product of the two low parts is below 2^-22). The products for
+// y, which is rounded to bfloat16 in the end, take single float16 operands (11
+// bits, against 8 of the result). float16 has little range, so operands carry
+// power-of-two scales: C one per token, B one per chunk, x one per chunk and
+// wave; the state accumulates in units 2^K that follow a running bound of its
+// size. Scales are exact, and they cancel in one factor per token at the end.
 #include "ssm_common.h"
+#include "ssm_device.h"
 #include "ssm_internal.h"
 
 namespace ssm {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kTile = 8;  // tokens convolved at a time
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-// The sequence's rows, kept inside [0, rows] whatever the offsets hold.
-__device__ __forceinline__ void seq_rows(const SsdCacheArgs &a, int64_t s, int64_t &t0, int64_t &len) {
-    const int64_t lo = a.cu_seqlens[s], hi = a.cu_seqlens[s + 1];
-    t0 = lo < 0 ? 0 : lo > a.rows ? a.rows : lo;
-    const int64_t t1 = hi < t0 ? t0 : hi > a.rows ? a.rows : hi;
-    len = t1 - t0;
+constexpr int kQ = 64;            // tokens per chunk
+constexpr int kPrepThreads = 256;
+constexpr int kWaves = 8;         // waves per workgroup of a walk: 4 column blocks of 64, two waves each
+constexpr int kWalkThreads = 64 * kWaves;
+
+// Workspace of one (chunk, group), in float16 elements: B high, B low and C as
+// operand registers (lane-major), G as operand registers, 2^eC per token
+// (float32), filled up to whole 1 KiB pieces.
+constexpr int frag_elems(int N) { return 3 * kQ * N + kQ * kQ + 512; }
+constexpr int kHead = 4 * kQ;  // floats per (chunk, head): cum, cum - log2 dt, w, exp2(cum)
+
+__device__ __forceinline__ f32x4 mfma(f16x8 a, f16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+// Smallest e with |v| < 2^e, for a normal v; -126 for zero.
+__device__ __forceinline__ int exponent(float v) { return (int)((__float_as_uint(v) >> 23) & 255) - 126; }
+__device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
+__device__ __forceinline__ bool finite(float v) { return (__float_as_uint(v) & 0x7f800000u) != 0x7f800000u; }
+__device__ __forceinline__ float finite_abs(float v) { return finite(v) ? __builtin_fabsf(v) : 0.0f; }
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// v plus the value of lane (lane - S) of its row of 16 (0 below it).
+template <int S>
+__device__ __forceinline__ float shr_add(float v) {
+    return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x110 + S, 0xF, 0xF,
+                                                                      false));
+}
+// Inclusive prefix sum over the 64 lanes.
+__device__ __forceinline__ float wave_prefix_sum(float v) {
+    v = shr_add<1>(v);
+    v = shr_add<2>(v);
+    v = shr_add<4>(v);
+    v = shr_add<8>(v);
+    v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x142, 0xA, 0xF, false));
+    v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x143, 0xC, 0xF, false));
+    return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+    for (int m = 1; m < 64; m *= 2) v = __builtin_fmaxf(v, __shfl_xor(v, m));
+    return v;
 }
 
-// Which slot each sequence owns (-1: none), and the windows the sequences
-// start from, copied so that the caches can be written while they are read.
-__global__ __launch_bounds__(kThreads) void seq_start_kernel(SsdCacheArgs a) {
-    const int64_t s = blockIdx.y;
+// The rows of sequence s, kept inside [0, rows] whatever the offsets hold.
+__device__ __forceinline__ uint32_t seq_begin(const SsdCacheArgs &a, uint32_t s) {
+    const int32_t lo = a.cu_seqlens[s], rows = (int32_t)a.rows;
+    return lo < 0 ? 0 : lo > rows ? rows : lo;
+}
+__device__ __forceinline__ uint32_t seq_length(const SsdCacheArgs &a, uint32_t s, uint32_t begin) {
+    const int32_t hi = a.cu_seqlens[s + 1], rows = (int32_t)a.rows, end = hi > rows ? rows : hi;
+    return end < (int32_t)begin ? 0 : end - begin;
+}
+
+// The sequence whose pieces of `unit` tokens include piece `id` (the last s
+// with cu[s] / unit + s <= id), or -1: 64 candidates at a time, one per lane.
+__device__ __forceinline__ int find_seq(const SsdCacheArgs &a, uint32_t id, uint32_t unit) {
+    uint32_t lo = 0, n = (uint32_t)a.seqs;
+    const uint32_t lane = threadIdx.x & 63;
+    do {
+        const uint32_t step = (n + 63) / 64, at = lane * step;
+        const bool below = at < n && seq_begin(a, lo + at) / unit + lo + at <= id;
+        const int cnt = __popcll(__ballot(below));
+        if (cnt == 0) return -1;
+        const uint32_t skip = (cnt - 1) * step;
+        n = n - skip < step ? n - skip : step;
+        lo += skip;
+    } while (n > 1);
+    return uniform((int)lo);
+}
+
+// -------------------------------------------------------------------- prepare
+
+template <int N>
+struct PrepShared {
+    static constexpr int R = N + 8;
+    alignas(16) _Float16 Bh[kQ][R], Bl[kQ][R], Ch[kQ][R], Cl[kQ][R];
+    float maxb[4];
+    int ec[kQ];
+};
+
+// Which slot a sequence owns (-1: none), and the raw rows before its start.
+__device__ __forceinline__ void start_seq(const SsdCacheArgs &a, int64_t s, int64_t part) {
     const int32_t slot = a.slots[s];
     bool dead = slot < 0 || slot >= a.num_slots;
     if (!dead) {
         bool same = false;
-        for (int64_t i = threadIdx.x; i < s; i += kThreads) same |= a.slots[i] == slot;
+        for (int64_t i = threadIdx.x; i < s; i += kPrepThreads) same |= a.slots[i] == slot;
         dead = __syncthreads_or(same);
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.ws_slot[s] = dead ? -1 : slot;
+    if (part == 0 && threadIdx.x == 0) a.ws_slot[s] = dead ? -1 : slot;
     const bool resume = !dead && a.resume && a.resume[s] != 0;
-    const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    const int64_t c = part * kPrepThreads + threadIdx.x;
     if (c < a.C)
         for (int k = 0; k < 3; ++k)
             a.ws_win[(s * 3 + k) * a.C + c] = resume ? ((const uint16_t *)a.conv_cache)[((int64_t)slot * a.C + c) * 3 + k] : 0;
 }
 
 template <int N>
-__global__ __launch_bounds__(kThreads) void seq_walk_kernel(SsdCacheArgs a) {
-    __shared__ float X[kTile][64], Bs[kTile][N], Cs[kTile][N], Dt[kTile];
-    constexpr int E = N / 4;  // state elements per lane
-    const int64_t H = a.H, pb = a.P / 64, C = a.C;
-    const int64_t s = blockIdx.y, hp = blockIdx.x, h = hp / pb, p0 = (hp % pb) * 64, g = h / (H / a.G);
-    const int tid = threadIdx.x, p = tid / 4, n0 = (tid % 4) * E;
-    int64_t t0, len;
-    seq_rows(a, s, t0, len);
-    const int32_t slot = a.ws_slot[s];
-    uint16_t *y = (uint16_t *)a.y + (t0 * H + h) * a.P + p0;
-    if (slot < 0) {
-        for (int64_t i = tid; i < len * 64; i += kThreads) y[(i / 64) * H * a.P + i % 64] = 0;
+__global__ __launch_bounds__(kPrepThreads) void prepare_kernel(SsdCacheArgs a) {
+    __shared__ PrepShared<N> sh;
+    const int64_t nchunk = a.nchunk * a.G;
+    if ((int64_t)blockIdx.x >= nchunk) {
+        const uint32_t parts = (uint32_t)((a.C + kPrepThreads - 1) / kPrepThreads), i = (uint32_t)(blockIdx.x - nchunk);
+        start_seq(a, i / parts, i % parts);
         return;
     }
-    float *st = a.state_cache + (((int64_t)slot * H + h) * a.P + p0 + p) * N + n0;
-    const bool resume = a.resume && a.resume[s] != 0;
-    float S[E];
-    for (int e = 0; e < E; ++e) S[e] = resume ? st[e] : 0.0f;
-    const float A2 = a.A[h] * kLog2e, dsk = a.Dskip ? a.Dskip[h] : 0.0f, bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
-    const uint16_t *raw = (const uint16_t *)a.xBC;
-    // raw row k of the sequence (k >= -3; before 0 the window) of channel c
-    auto at = [&](int64_t k, int64_t c) {
-        return ld_act(k < 0 ? a.ws_win : raw, k < 0 ? (s * 3 + k + 3) * C + c : (t0 + k) * a.xBC_stride + c);
-    };
-    for (int64_t k0 = 0; k0 < len; k0 += kTile) {
-        const int m = len - k0 < kTile ? (int)(len - k0) : kTile;
-        __syncthreads();
-        for (int i = tid; i < m * (64 + 2 * N); i += kThreads) {
-            const int j = i / (64 + 2 * N), q = i % (64 + 2 * N);
-            const int64_t k = k0 + j;
-            const int64_t c = q < 64 ? h * a.P + p0 + q : q < 64 + N ? H * a.P + g * N + q - 64 : H * a.P + (a.G + g) * N + q - 64 - N;
-            const float4 w = *(const float4 *)(a.conv_w + 4 * c);
-            const float v = conv_silu(w.x, w.y, w.z, w.w, a.conv_b ? a.conv_b[c] : 0.0f, at(k - 3, c), at(k - 2, c), at(k - 1, c), at(k, c));
-            if (q < 64) X[j][q] = v;
-            else if (q < 64 + N) Bs[j][q - 64] = v;
-            else Cs[j][q - 64 - N] = v;
-        }
-        if (tid < m) Dt[tid] = softplus(ld_act((const uint16_t *)a.dt_raw, (t0 + k0 + tid) * a.dt_stride + h) + bias);
-        __syncthreads();
-        for (int j = 0; j < m; ++j) {
-            const float av = fast_exp2(Dt[j] * A2), dx = Dt[j] * X[j][p];
-            float acc = 0.0f;
+    const uint32_t id = blockIdx.x / (uint32_t)a.G, g = blockIdx.x % (uint32_t)a.G;
+    const int s = find_seq(a, id, kQ);
+    if (s < 0) return;
+    const uint32_t begin = seq_begin(a, s), len = seq_length(a, s, begin);
+    const uint32_t first = (id - (begin / kQ + s)) * kQ;  // token of the sequence
+    if (first >= len) return;
+    const int rem = len - first < kQ ? (int)(len - first) : kQ;
+    const int32_t slot = a.slots[s];
+    const bool resume = a.resume && a.resume[s] != 0 && slot >= 0 && slot < a.num_slots;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+
+    // The convolution: a lane takes four channels of TPB tokens; N / 4 lanes
+    // hold a token's B, the next N / 4 its C.
+    constexpr int LPR = 2 * N / 4, NB = kPrepThreads / LPR, TPB = kQ / NB;
+    const int cl = tid % LPR, tb = tid / LPR, isC = cl / (N / 4), n0 = (cl % (N / 4)) * 4;
+    const int64_t c0 = a.H * a.P + (isC * a.G + g) * N + n0;
+    float w[4][4], bias[4];
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                S[e] = __builtin_fmaf(av, S[e], dx * Bs[j][n0 + e]);
-                acc = __builtin_fmaf(Cs[j][n0 + e], S[e], acc);
-            }
-            acc += __shfl_xor(acc, 1);
-            acc += __shfl_xor(acc, 2);
-            if (tid % 4 == 0) st_act(y, (k0 + j) * H * a.P + p, __builtin_fmaf(dsk, X[j][p], acc));
+    for (int k = 0; k < 4; ++k) {
+        const f32x4 t = *(const f32x4 *)(a.conv_w + 4 * (c0 + k));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[k][j] = t[j];
+        bias[k] = a.conv_b ? a.conv_b[c0 + k] : 0.0f;
+    }
+    uint2 raw[TPB + 3];
+    const int t0 = tb * TPB;
+    const uint16_t *rows = (const uint16_t *)a.xBC + c0;
+#pragma unroll
+    for (int i = 0; i < TPB + 3; ++i) {
+        const int t = (int)first + t0 + i - 3, last = (int)len - 1;  // token of the sequence
+        if (t >= 0) {
+            raw[i] = *(const uint2 *)(rows + (int64_t)(begin + (t < last ? t : last)) * a.xBC_stride);
+        } else {
+            uint32_t v[4];
+            for (int k = 0; k < 4; ++k)
+                v[k] = resume ? ((const uint16_t *)a.conv_cache)[((int64_t)slot * a.C + c0 + k) * 3 + t + 3] : 0;
+            raw[i] = uint2{v[0] | v[1] << 16, v[2] | v[3] << 16};
         }
     }
-    for (int e = 0; e < E; ++e) st[e] = S[e];
-    // the window the sequence leaves; the first head of a group writes its B and C
-    const bool first = h % (H / a.G) == 0 && p0 == 0;
-    for (int q = tid; q < 64 + (first ? 2 * N : 0); q += kThreads) {
-        const int64_t c = q < 64 ? h * a.P + p0 + q : q < 64 + N ? H * a.P + g * N + q - 64 : H * a.P + (a.G + g) * N + q - 64 - N;
-        for (int k = 0; k < 3; ++k) st_act((uint16_t *)a.conv_cache, ((int64_t)slot * C + c) * 3 + k, at(len - 3 + k, c));
+    float v[TPB][4], big = 0.0f;
+#pragma unroll
+    for (int i = 0; i < TPB; ++i) {
+        float top = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            auto at = [&](int j) {
+                const uint32_t u = k < 2 ? raw[i + j].x : raw[i + j].y;
+                return __uint_as_float(k % 2 ? u & 0xffff0000u : u << 16);
+            };
+            v[i][k] = t0 + i < rem ? conv_silu(w[k][0], w[k][1], w[k][2], w[k][3], bias[k], at(0), at(1), at(2), at(3)) : 0.0f;
+            top = __builtin_fmaxf(top, finite_abs(v[i][k]));
+        }
+        // the largest value of the token's C, and of the chunk's B
+#pragma unroll
+        for (int m = 1; m < N / 4; m *= 2) top = __builtin_fmaxf(top, __shfl_xor(top, m));
+        if (isC) {
+            if (cl == N / 4) sh.ec[t0 + i] = clampi(exponent(top), -100, 120);
+        } else {
+            big = __builtin_fmaxf(big, top);
+        }
     }
+    big = wave_max(big);
+    if (lane == 0) sh.maxb[wave] = big;
+    __syncthreads();
+    const int eB = clampi(exponent(__builtin_fmaxf(__builtin_fmaxf(sh.maxb[0], sh.maxb[1]), __builtin_fmaxf(sh.maxb[2], sh.maxb[3]))), -100, 128);
+#pragma unroll
+    for (int i = 0; i < TPB; ++i) {
+        const int e = isC ? 7 - sh.ec[t0 + i] : 14 - eB;
+        f16x4 hi, lo;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float t = __builtin_ldexpf(v[i][k], e);
+            asm("" : "+v"(t));
+            hi[k] = (_Float16)t;
+            lo[k] = (_Float16)(t - (float)hi[k]);
+        }
+        *(f16x4 *)(isC ? &sh.Ch[t0 + i][n0] : &sh.Bh[t0 + i][n0]) = hi;
+        *(f16x4 *)(isC ? &sh.Cl[t0 + i][n0] : &sh.Bl[t0 + i][n0]) = lo;
+    }
+    __syncthreads();
+
+    _Float16 *out = (_Float16 *)a.ws_frag + ((int64_t)id * a.G + g) * frag_elems(N);
+    const int r = lane & 15, q = lane >> 4;
+    // B^T as A operands, (h, nt): row n = 16 nt + r, k = token 16 q + 8 h + j
+    for (int f = wave; f < 2 * (N / 16); f += 4) {
+        const int h = f / (N / 16), nt = f % (N / 16);
+        f16x8 hi, lo;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            hi[j] = sh.Bh[16 * q + 8 * h + j][16 * nt + r];
+            lo[j] = sh.Bl[16 * q + 8 * h + j][16 * nt + r];
+        }
+        *(f16x8 *)(out + (f * 64 + lane) * 8) = hi;
+        *(f16x8 *)(out + kQ * N + (f * 64 + lane) * 8) = lo;
+    }
+    // C as A operands, (tt, m): row r is token 16 (r / 4) + 4 tt + r % 4, and k
+    // runs over n in the order in which two accumulator tiles hold the state
+    const int row = 16 * (r / 4) + r % 4;
+    for (int f = wave; f < 4 * (N / 32); f += 4) {
+        const int tt = f / (N / 32), m = f % (N / 32);
+        const _Float16 *src = &sh.Ch[row + 4 * tt][32 * m + 4 * q];
+        const f16x4 lo = *(const f16x4 *)src, hi = *(const f16x4 *)(src + 16);
+        *(f16x8 *)(out + 2 * kQ * N + (f * 64 + lane) * 8) = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+    // G as A operands, (tt, h): row r as in C, k = token s = 16 q + 8 h + j. The
+    // wave's tt; a product's row 4 q + e is token 16 q + 8 h + 4 b + e.
+    {
+        const int tt = wave;
+        f16x8 ch[N / 32], clo[N / 32];
+#pragma unroll
+        for (int m = 0; m < N / 32; ++m) {
+            ch[m] = *(const f16x8 *)&sh.Ch[row + 4 * tt][32 * m + 8 * q];
+            clo[m] = *(const f16x8 *)&sh.Cl[row + 4 * tt][32 * m + 8 * q];
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            f16x8 o;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int m = 0; m < N / 32; ++m) {
+                    const f16x8 bh = *(const f16x8 *)&sh.Bh[row + 8 * h + 4 * b][32 * m + 8 * q];
+                    const f16x8 bl = *(const f16x8 *)&sh.Bl[row + 8 * h + 4 * b][32 * m + 8 * q];
+                    acc = mfma(bh, ch[m], acc);
+                    acc = mfma(bl, ch[m], acc);
+                    acc = mfma(bh, clo[m], acc);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    o[4 * b + e] = 16 * q + 8 * h + 4 * b + e <= row + 4 * tt ? (_Float16)(acc[e] * 0x1p-14f) : (_Float16)0.0f;
+            }
+            *(f16x8 *)(out + 3 * kQ * N + ((tt * 2 + h) * 64 + lane) * 8) = o;
+        }
+    }
+    if (tid < kQ) ((float *)(out + 3 * kQ * N + kQ * kQ))[tid] = __builtin_ldexpf(1.0f, sh.ec[tid]);
+    if (tid == 0) a.ws_eb[id * a.G + g] = eB;
+
+    // The decays, a wave per head of the group, a lane per token.
+    const uint32_t hpg = (uint32_t)a.H / (uint32_t)a.G;
+    const int64_t trow = begin + first + (lane < rem ? lane : rem - 1);
+    for (uint32_t k = wave; k < hpg; k += 4) {
+        const int64_t h = g * hpg + k;
+        const float rawdt = ld_act((const uint16_t *)a.dt_raw, trow * a.dt_stride + h);
+        const float dt = lane < rem ? softplus(rawdt + (a.dt_bias ? a.dt_bias[h] : 0.0f)) : 0.0f;
+        const float step = dt * (a.A[h] * kLog2e);
+        const float cum = wave_prefix_sum(step);
+        // from the end, without subtracting: exact where little decays
+        const float back = wave_prefix_sum(__shfl(step, 63 - lane));
+        const float sfx = lane < 63 ? __shfl(back, 62 - lane) : 0.0f;
+        const float wt = dt * fast_exp2(sfx);
+        const float top = wave_max(finite_abs(dt)), wtop = wave_max(finite_abs(wt));
+        const int ed = exponent(top);
+        float *o = a.ws_head + (id * a.H + h) * kHead;
+        o[lane] = cum;
+        o[kQ + lane] = cum - __builtin_amdgcn_logf(dt) + (float)ed;
+        o[2 * kQ + lane] = wt;
+        o[3 * kQ + lane] = fast_exp2(cum);
+        if (lane == 63)
+            *(f32x4 *)(a.ws_meta + (id * a.H + h) * 4) =
+                f32x4{fast_exp2(cum), __int_as_float(exponent(wtop)), __int_as_float(ed), 0.0f};
+    }
+}
+
+// ----------------------------------------------------------------------- walk
+
+template <int N, bool OUT>
+struct WalkShared {
+    static constexpr int kFrag = OUT ? frag_elems(N) : 2 * kQ * N;
+    struct Buffer {
+        alignas(16) _Float16 frag[kFrag];
+        alignas(16) float head[4][kHead];
+    } buf[2];
+    alignas(16) _Float16 M[OUT ? 4 : 1][OUT ? 8 : 1][64][8];
+};
+
+// One workgroup: the segment's chunks in order, for four column blocks (64 rows
+// of a head's state) of one group; two waves share a block, 32 columns each,
+// and each forms half of the block's masked matrix. Lane (r, q) = (l % 16, l /
+// 16) holds the channels p = 2 r + c of the wave's 32 for the tokens 16 q + i
+// of a chunk: what the 16 x 16 x 32 product takes as its B operand (column r,
+// k = 8 consecutive tokens), and, with the output's rows numbered to match, the
+// place where y comes out.
+template <int N, bool OUT>
+__global__ __launch_bounds__(kWalkThreads, 2) void walk_kernel(SsdCacheArgs a) {
+    constexpr int NT = N / 16, KB = N / 32;
+    __shared__ WalkShared<N, OUT> sh;
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int r = lane & 15, q = lane >> 4;
+    // Workgroups are dealt to the 8 XCDs in turn: neighbours in the order of
+    // the work (the column blocks of one segment, which load the same B, C and
+    // G) go to one XCD and its L2.
+    const uint32_t pb = (uint32_t)a.P / 64, G = (uint32_t)a.G, seg = (uint32_t)a.seg;
+    const uint32_t ncb = (uint32_t)a.H / G * pb, nhb = (ncb + 3) / 4;
+    const uint32_t total = (uint32_t)a.nseg * G * nhb, per = (total + 7) / 8;
+    const uint32_t unit = blockIdx.x % 8 * per + blockIdx.x / 8;
+    if (unit >= total) return;
+    const uint32_t sid = unit / (G * nhb), g = unit / nhb % G, hb = unit % nhb;
+    const int s = find_seq(a, sid, seg);
+    if (s < 0) return;
+    const uint32_t begin = seq_begin(a, s), len = seq_length(a, s, begin);
+    const uint32_t k = sid - (begin / seg + s);  // segment of the sequence
+    const uint32_t nseg = len > 0 ? (len + seg - 1) / seg : 1;
+    if (k >= (OUT ? nseg : nseg - 1)) return;
+    const uint32_t from = k * seg, to = len - from < seg ? len : from + seg;
+    const bool last = k == nseg - 1;
+    const uint32_t cb = hb * 4 + wave / 2;
+    const bool on = cb < ncb;
+    const int64_t h = g * ((uint32_t)a.H / G) + (on ? cb / pb : 0);
+    const int64_t ch0 = h * a.P + (on ? cb % pb : 0) * 64 + 32 * (wave % 2);  // the wave's first channel
+    const uint32_t kept = begin / seg + k;  // the segment's place among those that keep a state
+    const int32_t slot = a.ws_slot[s];
+    if (slot < 0) {
+        if (OUT && on)
+            for (uint32_t t = from + q; t < to; t += 4) *(uint32_t *)((uint16_t *)a.y + (int64_t)(begin + t) * a.H * a.P + ch0 + 2 * r) = 0u;
+        return;
+    }
+
+    // the state: acc[nt][c][e] = S[p = 2 r + c][n = 16 nt + 4 q + e] 2^-K
+    f32x4 acc[NT][2];
+    int K = 0;
+    float bound = 0.0f;  // of |acc|
+    const bool resume = a.resume && a.resume[s] != 0;
+    const int64_t off = (ch0 + 2 * r) * N + 4 * q, hpn = a.H * a.P * N;
+    float *const cache = a.state_cache + (int64_t)slot * hpn + off;
+    const float *src = nullptr;
+    if (OUT) src = k > 0 ? a.ws_state + (int64_t)(kept - 1) * hpn + off : resume ? cache : nullptr;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            acc[nt][c] = src && on ? *(const f32x4 *)(src + c * N + 16 * nt) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) bound = __builtin_fmaxf(bound, finite_abs(acc[nt][c][e]));
+        }
+    bound = wave_max(bound);
+    if (bound > 0.0f) {
+        K = uniform(exponent(bound));
+        bound = 1.0f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[nt][c][e] = __builtin_ldexpf(acc[nt][c][e], -K);
+    }
+
+    float w[2][4], bias[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const f32x4 t = *(const f32x4 *)(a.conv_w + 4 * (ch0 + 2 * r + c));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[c][j] = t[j];
+        bias[c] = a.conv_b ? a.conv_b[ch0 + 2 * r + c] : 0.0f;
+    }
+    const float dsk = OUT && a.Dskip ? a.Dskip[h] : 0.0f;
+    float segdec = 1.0f;
+
+    // The raw rows of a chunk: tokens 16 q - 3 .. 16 q + 15, two channels each.
+    // Behind the sequence's end its last row again; before its start the window.
+    uint32_t raw[19];
+    const uint32_t rowb = (uint32_t)a.xBC_stride * 2, chb = (uint32_t)(ch0 + 2 * r) * 2;
+    auto load = [&](uint32_t t) {  // the chunk that starts at token t of the sequence
+        const char *base = (const char *)a.xBC + (int64_t)(begin + t) * rowb;
+        const uint32_t rem = to - t < kQ ? to - t : kQ, end = (rem - 1) * rowb + chb;
+        uint32_t o = 16 * q * rowb + chb;
+        asm volatile("" : "+v"(o));  // one running offset, not sixteen kept between chunks
+        if (t > 0) {
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                const uint32_t at = o + i * rowb, lim = end + 3 * rowb;
+                raw[i] = *(const uint32_t *)(base - 3 * (int64_t)rowb + (at < lim ? at : lim));
+            }
+        } else {
+            const uint16_t *win = a.ws_win + (int64_t)s * 3 * a.C;
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                const uint32_t at = o + i * rowb - 3 * rowb;
+                const char *p = q == 0 ? (const char *)(win + i * a.C) + chb : base + (at < end ? at : end);
+                raw[i] = *(const uint32_t *)p;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            raw[3 + i] = *(const uint32_t *)(base + (o < end ? o : end));
+            o += rowb;
+        }
+    };
+    const uint32_t chunk0 = begin / kQ + s;
+    auto stage = [&](uint32_t t, int b) {  // B, C, G and the decays of that chunk, straight into LDS
+        const uint32_t id = chunk0 + t / kQ;
+        const char *f = (const char *)a.ws_frag + ((int64_t)id * G + g) * (frag_elems(N) * 2);
+        const uint32_t dst = lds_addr(sh.buf[b].frag);
+#pragma unroll
+        for (int i = 0; i < (WalkShared<N, OUT>::kFrag / 512 + kWaves - 1) / kWaves; ++i) {
+            const int piece = i * kWaves + wave;
+            if (piece < WalkShared<N, OUT>::kFrag / 512) dma16_s(f + piece * 1024, lane * 16, dst + piece * 1024);
+        }
+        if (wave % 2 == 0 && on)
+            dma16_s(a.ws_head + (id * a.H + h) * kHead, lane * 16, lds_addr(sh.buf[b].head[wave / 2]));
+    };
+
+    if (from < to) stage(from, 0);
+    if (!on) {  // no columns: the wave only carries its share of the loads
+        for (uint32_t t = from; t < to; t += kQ) {
+            vm_wait();
+            lds_barrier();
+            if (t + kQ < to) stage(t + kQ, (int)((t - from) / kQ & 1) ^ 1);
+            if constexpr (OUT) lds_barrier();
+        }
+    } else {
+    if (from < to) load(from);
+    for (uint32_t t = from; t < to; t += kQ) {
+        const int b = (int)((t - from) / kQ & 1);
+        const uint32_t id = chunk0 + t / kQ;
+        const cf32_ptr meta = (cf32_ptr)(a.ws_meta + (id * a.H + h) * 4);
+        const float dec = meta[0];
+        const int ew = __float_as_int(meta[1]), ed = __float_as_int(meta[2]);
+        const int eB = ((const __attribute__((address_space(4))) int *)a.ws_eb)[(int64_t)id * G + g];
+        vm_wait();
+        lds_barrier();  // the chunk is in LDS, and the other buffer is free
+        if (t + kQ < to) stage(t + kQ, b ^ 1);
+        const auto &buf = sh.buf[b];
+        const float *hd = buf.head[wave / 2];
+        const int rem = to - t < kQ ? (int)(to - t) : kQ;
+
+        // the wave's half of the masked matrix: M[t][s] = G[t][s] exp2(cum_t - cum_s) dt_s
+        if (OUT) {
+            f32x4 cs[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) cs[i] = *(const f32x4 *)(hd + kQ + 16 * q + 4 * i);
+#pragma unroll
+            for (int k2 = 0; k2 < 2; ++k2) {
+                const int tt = 2 * (wave % 2) + k2;
+                const float ct = hd[16 * (r / 4) + r % 4 + 4 * tt];
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    const f16x8 gv = *(const f16x8 *)(buf.frag + 3 * kQ * N + ((tt * 2 + hh) * 64 + lane) * 8);
+                    f16x8 m;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        // G is zero above the diagonal, where the exponent may be large
+                        m[j] = (_Float16)fast_exp2(__builtin_fminf(ct - cs[2 * hh + j / 4][j % 4], 15.0f));
+                    *(f16x8 *)&sh.M[wave / 2][tt * 2 + hh][lane][0] = m * gv;
+                }
+            }
+        }
+        // x, and the scale of its operand
+        float x[2][16], top = 0.0f;
+        uint32_t badm[2] = {0u, 0u};
+        bool anybad = false;
+        {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    auto at = [&](int j) { return __uint_as_float(c ? raw[i + j] & 0xffff0000u : raw[i + j] << 16); };
+                    x[c][i] = conv_silu(w[c][0], w[c][1], w[c][2], w[c][3], bias[c], at(0), at(1), at(2), at(3));
+                }
+            if (rem < kQ) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[c][i] = 16 * q + i < rem ? x[c][i] : 0.0f;
+            }
+            if (t + kQ < to) load(t + kQ);
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int i = 0; i < 16; i += 2)  // keeps a NaN
+                    top = __builtin_elementwise_maximum(__builtin_elementwise_maximum(__builtin_fabsf(x[c][i]), __builtin_fabsf(x[c][i + 1])), top);
+            if (__ballot(!finite(top))) {
+                // A value that is not finite would reach earlier tokens as 0
+                // times itself: the products take zero for it, and what it
+                // reaches (its channel, from its token on) is marked at the end.
+                anybad = true;
+                top = 0.0f;
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        if (!finite(x[c][i])) {
+                            badm[c] |= 1u << i;
+                            x[c][i] = 0.0f;
+                        }
+                        top = __builtin_fmaxf(top, __builtin_fabsf(x[c][i]));
+                    }
+            }
+            top = wave_max(top);
+        }
+        const int ex = clampi(uniform(exponent(top)), -100, 127);
+        const int eb = uniform(exponent(bound));
+        // units of the state after this chunk: S = acc 2^Kn
+        int kv = ex + ew;
+        const int need = K + eb - 100 + 28 - eB;
+        kv = kv > need ? kv : need;
+        const int Kn = kv - 28 + eB;
+        f16x8 vh[2][2], vl[2][2], x16[2][2];
+        int E2 = 0;
+        float dx = 0.0f;
+        f32x4 Y[4][2];
+        {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float wk = __builtin_ldexpf(hd[2 * kQ + 16 * q + i], 14 - kv);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float v = x[c][i] * wk;
+                    // one rounded product: the low part is what the high part leaves of it
+                    asm("" : "+v"(v));
+                    vh[c][i / 8][i % 8] = (_Float16)v;
+                    vl[c][i / 8][i % 8] = (_Float16)(v - (float)vh[c][i / 8][i % 8]);
+                }
+            }
+            if constexpr (OUT) {
+                const int sS = clampi(15 - eb, -127, 100);
+                const int E1 = K - sS - 7;
+                int exx = E1 - 60 - ed - eB + 21;
+                exx = ex > exx ? ex : exx;
+                E2 = exx + ed + eB - 21;
+                const float sx = __builtin_ldexpf(1.0f, 14 - exx);
+                dx = dsk * __builtin_ldexpf(1.0f, exx - 14);
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x16[c][i / 8][i % 8] = (_Float16)(x[c][i] * sx);
+                // C S^T, in units of the masked product
+                const float sf = __builtin_ldexpf(1.0f, sS);
+#pragma unroll
+                for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) Y[tt][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int m = 0; m < KB; ++m) {
+                    f16x8 so[2];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) so[c][e] = (_Float16)(acc[2 * m + e / 4][c][e % 4] * sf);
+#pragma unroll
+                    for (int tt = 0; tt < 4; ++tt) {
+                        const f16x8 co = *(const f16x8 *)(buf.frag + 2 * kQ * N + ((tt * KB + m) * 64 + lane) * 8);
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) Y[tt][c] = mfma(co, so[c], Y[tt][c]);
+                    }
+                }
+#pragma unroll
+                for (int tt = 0; tt < 4; ++tt) {
+                    const f32x4 ec = *(const f32x4 *)(hd + 3 * kQ + 16 * q + 4 * tt);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float al = __builtin_ldexpf(ec[e], E1 - E2);
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) Y[tt][c][e] *= al;
+                    }
+                }
+            }
+        }
+        if constexpr (OUT) lds_barrier();  // M is whole
+        if constexpr (OUT) {
+#pragma unroll
+            for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    const f16x8 mo = *(const f16x8 *)&sh.M[wave / 2][tt * 2 + hh][lane][0];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) Y[tt][c] = mfma(mo, x16[c][hh], Y[tt][c]);
+                }
+            const float *rs = (const float *)(buf.frag + 3 * kQ * N + kQ * kQ);
+            char *yb = (char *)a.y + ((int64_t)(begin + t) * a.H * a.P + ch0) * 2;
+            const uint32_t yrow = (uint32_t)(a.H * a.P) * 2;
+            uint32_t yo = 16 * q * yrow + 4 * r;
+            asm volatile("" : "+v"(yo));
+            bool low[2] = {false, false};
+            if (anybad) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int d = 16; d < 64; d += 16) {
+                        const uint32_t o = __shfl(badm[c], (lane - d) & 63);
+                        low[c] |= lane >= d && o != 0u;
+                    }
+            }
+#pragma unroll
+            for (int tt = 0; tt < 4; ++tt) {
+                const f32x4 rv = *(const f32x4 *)(rs + 16 * q + 4 * tt);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = 4 * tt + e;
+                    const float be = __builtin_ldexpf(rv[e], E2);
+                    float o[2];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        o[c] = __builtin_fmaf((float)x16[c][i / 8][i % 8], dx, Y[tt][c][e] * be);
+                        if (anybad && (low[c] || (badm[c] & ((2u << i) - 1)))) o[c] = __builtin_nanf("");
+                    }
+                    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+                    const bf16x2 pk = {(__bf16)o[0], (__bf16)o[1]};
+                    if (rem == kQ || 16 * q + i < rem) *(bf16x2 *)(yb + yo) = pk;
+                    yo += yrow;
+                }
+            }
+        }
+        // the state
+        const int sh_k = K - Kn;
+        const float f = __builtin_ldexpf(dec, sh_k < 120 ? sh_k : 120);
+        bound = __builtin_fmaf(bound, f, 0x1p34f);
+        if (!finite(bound)) bound = 0x1p34f;
+        segdec *= dec;
+        K = Kn;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) acc[nt][c] *= f;
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const f16x8 bh = *(const f16x8 *)(buf.frag + ((hh * NT + nt) * 64 + lane) * 8);
+                const f16x8 bl = *(const f16x8 *)(buf.frag + kQ * N + ((hh * NT + nt) * 64 + lane) * 8);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    acc[nt][c] = mfma(bh, vh[c][hh], acc[nt][c]);
+                    acc[nt][c] = mfma(bl, vh[c][hh], acc[nt][c]);
+                    acc[nt][c] = mfma(bh, vl[c][hh], acc[nt][c]);
+                }
+            }
+        if (anybad) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t o = badm[c];
+                o |= __shfl_xor(o, 16);
+                o |= __shfl_xor(o, 32);
+                if (o)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[nt][c][e] = __builtin_nanf("");
+            }
+        }
+    }
+    }
+
+    if (!OUT || last) {
+        if (on) {
+            float *dst = OUT ? cache : a.ws_state + (int64_t)kept * hpn + off;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    f32x4 v;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = __builtin_ldexpf(acc[nt][c][e], K);
+                    *(f32x4 *)(dst + c * N + 16 * nt) = v;
+                }
+            if (!OUT && lane == 0) a.ws_segdec[(int64_t)kept * a.H + h] = segdec;
+        }
+        if constexpr (OUT) {
+            // the window: the last three raw rows, of the wave's channels and,
+            // once per group, of its B and C
+            auto row = [&](int t, int64_t c) {
+                return t < 0 ? a.ws_win[((int64_t)s * 3 + t + 3) * a.C + c]
+                             : ((const uint16_t *)a.xBC)[(int64_t)(begin + t) * a.xBC_stride + c];
+            };
+            uint16_t *win = (uint16_t *)a.conv_cache + (int64_t)slot * a.C * 3;
+            if (on && q < 3)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) win[(ch0 + 2 * r + c) * 3 + q] = row((int)len - 3 + q, ch0 + 2 * r + c);
+            if (hb == 0)
+                for (int i = threadIdx.x; i < 2 * N * 3; i += kWalkThreads) {
+                    const int n = i / 3;
+                    const int64_t c = a.H * a.P + ((n / N) * a.G + g) * N + n % N;
+                    win[c * 3 + i % 3] = row((int)len - 3 + i % 3, c);
+                }
+        }
+    }
+}
+
+// ----------------------------------------------------------------------- join
+
+// enter[k+1] = dec[k] enter[k] + end[k], in place of end[k].
+__global__ __launch_bounds__(256) void join_kernel(SsdCacheArgs a, int N) {
+    const uint32_t s = blockIdx.y, begin = seq_begin(a, s), len = seq_length(a, s, begin), seg = (uint32_t)a.seg;
+    const uint32_t nseg = (len + seg - 1) / seg;
+    const int32_t slot = a.ws_slot[s];
+    if (nseg < 2 || slot < 0) return;
+    const int64_t hpn = a.H * a.P * N, i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= hpn) return;
+    const int64_t h = i / (a.P * N), first = begin / seg;
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (a.resume && a.resume[s] != 0) v = *(const f32x4 *)(a.state_cache + slot * hpn + i);
+    for (uint32_t k = 0; k < nseg - 1; ++k) {
+        f32x4 *p = (f32x4 *)(a.ws_state + (first + k) * hpn + i);
+        v = *p + v * a.ws_segdec[(first + k) * a.H + h];
+        *p = v;
+    }
+}
+
+template <int N>
+hipError_t launch_n(const SsdCacheArgs &a, hipStream_t s) {
+    const int64_t parts = (a.C + kPrepThreads - 1) / kPrepThreads;
+    hipLaunchKernelGGL((prepare_kernel<N>), dim3((unsigned)(a.nchunk * a.G + a.seqs * parts)), dim3(kPrepThreads), 0, s, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int64_t ncb = a.H / a.G * (a.P / 64), units = a.nseg * a.G * ((ncb + 3) / 4);
+    const dim3 grid((unsigned)((units + 7) / 8 * 8));
+    if (a.rows > a.seg) {  // some sequence may be longer than a segment
+        hipLaunchKernelGGL((walk_kernel<N, false>), grid, dim3(kWalkThreads), 0, s, a);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        hipLaunchKernelGGL(join_kernel, dim3((unsigned)((a.H * a.P * N + 1023) / 1024), (unsigned)a.seqs), dim3(256), 0, s, a, N);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL((walk_kernel<N, true>), grid, dim3(kWalkThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+// Tokens per segment: enough segments that the walk has about two waves per
+// SIMD (a wave takes 32 of the H P columns), none shorter than 256 tokens.
+int64_t segment_tokens(int64_t rows, int64_t H, int64_t P) {
+    const int64_t want = (2048 * 32 + H * P - 1) / (H * P);
+    const int64_t seg = (rows + want - 1) / want;
+    return (seg < 256 ? 256 : seg + 63) / 64 * 64;
+}
+
+// Cuts the workspace up; returns its size.
+size_t plan(SsdCacheArgs &a, int N, char *base) {
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        char *p = base + at;
+        at += up256(bytes);
+        return p;
+    };
+    a.seg = segment_tokens(a.rows, a.H, a.P);
+    a.nchunk = a.rows / kQ + a.seqs;
+    a.nseg = a.rows / a.seg + a.seqs;
+    const int64_t kept = a.rows / a.seg;
+    a.ws_slot = (int32_t *)take((size_t)a.seqs * 4);
+    a.ws_win = (uint16_t *)take((size_t)a.seqs * 3 * a.C * 2);
+    a.ws_frag = take((size_t)(a.nchunk * a.G) * frag_elems(N) * 2);
+    a.ws_head = (float *)take((size_t)(a.nchunk * a.H) * kHead * 4);
+    a.ws_meta = (float *)take((size_t)(a.nchunk * a.H) * 16);
+    a.ws_eb = (int32_t *)take((size_t)(a.nchunk * a.G) * 4);
+    a.ws_state = (float *)take((size_t)kept * a.H * a.P * N * 4);
+    a.ws_segdec = (float *)take((size_t)kept * a.H * 4);
+    return at;
 }
 
 }  // namespace
 
 size_t ssd_cache_workspace(int64_t seqs, int64_t rows, int64_t H, int64_t P, int64_t G, int64_t N) {
-    return ((size_t)seqs * 4 + 255) / 256 * 256 + (size_t)seqs * 3 * (H * P + 2 * G * N) * 2;
+    SsdCacheArgs a{};
+    a.seqs = seqs;
+    a.rows = rows;
+    a.H = H;
+    a.P = P;
+    a.G = G;
+    a.C = H * P + 2 * G * N;
+    return plan(a, (int)N, nullptr);
 }
 
 hipError_t launch_ssd_cache(SsdCacheArgs a, int N, void *workspace, hipStream_t s) {
-    a.ws_slot = (int32_t *)workspace;
-    a.ws_win = (uint16_t *)((char *)workspace + ((size_t)a.seqs * 4 + 255) / 256 * 256);
-    hipLaunchKernelGGL(seq_start_kernel, dim3((unsigned)((a.C + kThreads - 1) / kThreads), (unsigned)a.seqs), dim3(kThreads), 0, s, a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    const dim3 grid((unsigned)(a.H * (a.P / 64)), (unsigned)a.seqs);
-    if (N == 64) hipLaunchKernelGGL((seq_walk_kernel<64>), grid, dim3(kThreads), 0, s, a);
-    else hipLaunchKernelGGL((seq_walk_kernel<128>), grid, dim3(kThreads), 0, s, a);
-    return hipGetLastError();
+    plan(a, N, (char *)workspace);
+    return N == 64 ? launch_n<64>(a, s) : launch_n<128>(a, s);
 }
 
 }  // namespace ssm
