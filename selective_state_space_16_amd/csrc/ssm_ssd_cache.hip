@@ -45,21 +45,37 @@ namespace {
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kQ = 64;            // tokens per chunk
 constexpr int kPrepThreads = 256;
-constexpr int kWaves = 8;         // waves per workgroup of a walk: 4 column blocks of 64, two waves each
+constexpr int kWaves = 4;         // waves per workgroup of a walk: two column blocks of 64, two waves each
 constexpr int kWalkThreads = 64 * kWaves;
 
 // Workspace of one (chunk, group), in float16 elements: B high, B low and C as
 // operand registers (lane-major), G as operand registers, 2^eC per token
 // (float32), filled up to whole 1 KiB pieces.
 constexpr int frag_elems(int N) { return 3 * kQ * N + kQ * kQ + 512; }
-constexpr int kHead = 4 * kQ;  // floats per (chunk, head): cum, cum - log2 dt, w, exp2(cum)
+constexpr int kHead = 4 * kQ;  // floats per (chunk, head): cum, cum - log2 dt, -ln2 w, exp2(cum)
 
 __device__ __forceinline__ f32x4 mfma(f16x8 a, f16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+// a and b as sums of two float16 each: what rounding leaves of them, exactly
+// (the mixed-precision fma reads the rounded pair as it is).
+__device__ __forceinline__ void split(float a, float b, f16x2 &hi, f16x2 &lo) {
+    float la, lb;
+    hi = f16x2{(_Float16)a, (_Float16)b};
+    asm("v_fma_mix_f32 %0, %1, 1.0, -%2 op_sel_hi:[0,0,1]" : "=v"(la) : "v"(a), "v"(hi));
+    asm("v_fma_mix_f32 %0, %1, 1.0, -%2 op_sel:[0,0,1] op_sel_hi:[0,0,1]" : "=v"(lb) : "v"(b), "v"(hi));
+    lo = f16x2{(_Float16)la, (_Float16)lb};
+}
+// Buffer accesses: bytes from a wave-uniform base, a range that the hardware
+// checks (loads outside it give 0, stores outside it are dropped).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *base, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, bytes, 0x00020000);
 }
 // Smallest e with |v| < 2^e, for a normal v; -126 for zero.
 __device__ __forceinline__ int exponent(float v) { return (int)((__float_as_uint(v) >> 23) & 255) - 126; }
@@ -88,6 +104,21 @@ __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
     for (int m = 1; m < 64; m *= 2) v = __builtin_fmaxf(v, __shfl_xor(v, m));
     return v;
+}
+
+// The largest of the wave's values, none negative (or NaN, which stays): the
+// order of their bits.
+__device__ __forceinline__ float wave_top(float v) {
+    uint32_t u = __float_as_uint(v);
+    auto step = [&](uint32_t o) { u = o > u ? o : u; };
+    step(__builtin_amdgcn_update_dpp(0, u, 0x128, 0xF, 0xF, false));  // row_ror:8, 4, 2, 1
+    step(__builtin_amdgcn_update_dpp(0, u, 0x124, 0xF, 0xF, false));
+    step(__builtin_amdgcn_update_dpp(0, u, 0x122, 0xF, 0xF, false));
+    step(__builtin_amdgcn_update_dpp(0, u, 0x121, 0xF, 0xF, false));
+    const uint32_t a = __builtin_amdgcn_readlane(u, 0), b = __builtin_amdgcn_readlane(u, 16);
+    const uint32_t c = __builtin_amdgcn_readlane(u, 32), d = __builtin_amdgcn_readlane(u, 48);
+    const uint32_t ab = a > b ? a : b, cd = c > d ? c : d;
+    return __uint_as_float(ab > cd ? ab : cd);
 }
 
 // The rows of sequence s, kept inside [0, rows] whatever the offsets hold.
@@ -303,7 +334,7 @@ __global__ __launch_bounds__(kPrepThreads) void prepare_kernel(SsdCacheArgs a) {
         // from the end, without subtracting: exact where little decays
         const float back = wave_prefix_sum(__shfl(step, 63 - lane));
         const float sfx = lane < 63 ? __shfl(back, 62 - lane) : 0.0f;
-        const float wt = dt * fast_exp2(sfx);
+        const float wt = dt * fast_exp2(sfx) * -kLn2;  // the walks hold x as -log2(e) x
         const float top = wave_max(finite_abs(dt)), wtop = wave_max(finite_abs(wt));
         const int ed = exponent(top);
         float *o = a.ws_head + (id * a.H + h) * kHead;
@@ -319,17 +350,21 @@ __global__ __launch_bounds__(kPrepThreads) void prepare_kernel(SsdCacheArgs a) {
 
 // ----------------------------------------------------------------------- walk
 
+// LDS of a walk. For y one chunk at a time: B arrives while the masked matrix is
+// formed, C, G and the decays of the next chunk while the state is updated, so
+// that two workgroups fit a CU and run out of step. For the end states alone B
+// and the decays are held twice.
 template <int N, bool OUT>
 struct WalkShared {
-    static constexpr int kFrag = OUT ? frag_elems(N) : 2 * kQ * N;
-    struct Buffer {
-        alignas(16) _Float16 frag[kFrag];
-        alignas(16) float head[4][kHead];
-    } buf[2];
-    alignas(16) _Float16 M[OUT ? 4 : 1][OUT ? 8 : 1][64][8];
+    static constexpr int kBufs = OUT ? 1 : 2;
+    alignas(16) _Float16 B[kBufs][2 * kQ * N];
+    alignas(16) _Float16 CG[OUT ? kQ * N + kQ * kQ : 8];
+    alignas(16) float scale[2][256];  // 2^eC per token
+    alignas(16) float head[2][2][kHead];
+    alignas(16) _Float16 M[OUT ? 2 : 1][OUT ? 8 : 1][64][8];
 };
 
-// One workgroup: the segment's chunks in order, for four column blocks (64 rows
+// One workgroup: the segment's chunks in order, for two column blocks (64 rows
 // of a head's state) of one group; two waves share a block, 32 columns each,
 // and each forms half of the block's masked matrix. Lane (r, q) = (l % 16, l /
 // 16) holds the channels p = 2 r + c of the wave's 32 for the tokens 16 q + i
@@ -346,7 +381,7 @@ __global__ __launch_bounds__(kWalkThreads, 2) void walk_kernel(SsdCacheArgs a) {
     // the work (the column blocks of one segment, which load the same B, C and
     // G) go to one XCD and its L2.
     const uint32_t pb = (uint32_t)a.P / 64, G = (uint32_t)a.G, seg = (uint32_t)a.seg;
-    const uint32_t ncb = (uint32_t)a.H / G * pb, nhb = (ncb + 3) / 4;
+    const uint32_t ncb = (uint32_t)a.H / G * pb, nhb = (ncb + 1) / 2;
     const uint32_t total = (uint32_t)a.nseg * G * nhb, per = (total + 7) / 8;
     const uint32_t unit = blockIdx.x % 8 * per + blockIdx.x / 8;
     if (unit >= total) return;
@@ -359,7 +394,7 @@ __global__ __launch_bounds__(kWalkThreads, 2) void walk_kernel(SsdCacheArgs a) {
     if (k >= (OUT ? nseg : nseg - 1)) return;
     const uint32_t from = k * seg, to = len - from < seg ? len : from + seg;
     const bool last = k == nseg - 1;
-    const uint32_t cb = hb * 4 + wave / 2;
+    const uint32_t cb = hb * 2 + wave / 2;
     const bool on = cb < ncb;
     const int64_t h = g * ((uint32_t)a.H / G) + (on ? cb / pb : 0);
     const int64_t ch0 = h * a.P + (on ? cb % pb : 0) * 64 + 32 * (wave % 2);  // the wave's first channel
@@ -400,68 +435,88 @@ __global__ __launch_bounds__(kWalkThreads, 2) void walk_kernel(SsdCacheArgs a) {
                 for (int e = 0; e < 4; ++e) acc[nt][c][e] = __builtin_ldexpf(acc[nt][c][e], -K);
     }
 
+    // The convolution times -log2(e): its exp2 is SiLU's exponential, and the
+    // factor comes out again with the scales.
     float w[2][4], bias[2];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
         const f32x4 t = *(const f32x4 *)(a.conv_w + 4 * (ch0 + 2 * r + c));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[c][j] = t[j];
-        bias[c] = a.conv_b ? a.conv_b[ch0 + 2 * r + c] : 0.0f;
+        for (int j = 0; j < 4; ++j) w[c][j] = t[j] * -kLog2e;
+        bias[c] = a.conv_b ? a.conv_b[ch0 + 2 * r + c] * -kLog2e : 0.0f;
     }
     const float dsk = OUT && a.Dskip ? a.Dskip[h] : 0.0f;
     float segdec = 1.0f;
 
     // The raw rows of a chunk: tokens 16 q - 3 .. 16 q + 15, two channels each.
-    // Behind the sequence's end its last row again; before its start the window.
+    // Behind the sequence's end zeros; before its start the window.
     uint32_t raw[19];
     const uint32_t rowb = (uint32_t)a.xBC_stride * 2, chb = (uint32_t)(ch0 + 2 * r) * 2;
+    const uint32_t xlane = 16 * q * rowb + chb;
     auto load = [&](uint32_t t) {  // the chunk that starts at token t of the sequence
         const char *base = (const char *)a.xBC + (int64_t)(begin + t) * rowb;
-        const uint32_t rem = to - t < kQ ? to - t : kQ, end = (rem - 1) * rowb + chb;
-        uint32_t o = 16 * q * rowb + chb;
+        const uint32_t rem = to - t < kQ ? to - t : kQ;
+        const auto rows = buffer(base, rem * rowb);
+        uint32_t o = xlane;
         asm volatile("" : "+v"(o));  // one running offset, not sixteen kept between chunks
         if (t > 0) {
+            const auto before = buffer(base - 3 * (int64_t)rowb, (rem + 3) * rowb);
 #pragma unroll
-            for (int i = 0; i < 3; ++i) {
-                const uint32_t at = o + i * rowb, lim = end + 3 * rowb;
-                raw[i] = *(const uint32_t *)(base - 3 * (int64_t)rowb + (at < lim ? at : lim));
-            }
+            for (int i = 0; i < 3; ++i) raw[i] = __builtin_amdgcn_raw_buffer_load_b32(before, o + i * rowb, 0, 0);
         } else {
             const uint16_t *win = a.ws_win + (int64_t)s * 3 * a.C;
 #pragma unroll
             for (int i = 0; i < 3; ++i) {
-                const uint32_t at = o + i * rowb - 3 * rowb;
-                const char *p = q == 0 ? (const char *)(win + i * a.C) + chb : base + (at < end ? at : end);
-                raw[i] = *(const uint32_t *)p;
+                const uint32_t first = *(const uint32_t *)((const char *)(win + i * a.C) + chb);
+                const uint32_t later = __builtin_amdgcn_raw_buffer_load_b32(rows, o + i * rowb - 3 * rowb, 0, 0);
+                raw[i] = q == 0 ? first : later;
             }
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            raw[3 + i] = *(const uint32_t *)(base + (o < end ? o : end));
+            raw[3 + i] = __builtin_amdgcn_raw_buffer_load_b32(rows, o, 0, 0);
             o += rowb;
         }
     };
     const uint32_t chunk0 = begin / kQ + s;
-    auto stage = [&](uint32_t t, int b) {  // B, C, G and the decays of that chunk, straight into LDS
-        const uint32_t id = chunk0 + t / kQ;
-        const char *f = (const char *)a.ws_frag + ((int64_t)id * G + g) * (frag_elems(N) * 2);
-        const uint32_t dst = lds_addr(sh.buf[b].frag);
+    // Pieces [from, to) of 1 KiB of the chunk's operands, straight into LDS.
+    auto pieces = [&](uint32_t t, int lo, int hi, const void *to_lds) {
+        const char *f = (const char *)a.ws_frag + ((int64_t)(chunk0 + t / kQ) * G + g) * (frag_elems(N) * 2);
+        const uint32_t dst = lds_addr(to_lds);
 #pragma unroll
-        for (int i = 0; i < (WalkShared<N, OUT>::kFrag / 512 + kWaves - 1) / kWaves; ++i) {
-            const int piece = i * kWaves + wave;
-            if (piece < WalkShared<N, OUT>::kFrag / 512) dma16_s(f + piece * 1024, lane * 16, dst + piece * 1024);
+        for (int i = 0; i < (hi - lo + kWaves - 1) / kWaves; ++i) {
+            const int p = i * kWaves + wave;
+            if (p < hi - lo) dma16_s(f + (lo + p) * 1024, lane * 16, dst + p * 1024);
         }
+    };
+    constexpr int kB = 2 * kQ * N / 512, kCG = (kQ * N + kQ * kQ) / 512;
+    auto head = [&](uint32_t t, int b) {
         if (wave % 2 == 0 && on)
-            dma16_s(a.ws_head + (id * a.H + h) * kHead, lane * 16, lds_addr(sh.buf[b].head[wave / 2]));
+            dma16_s(a.ws_head + ((chunk0 + t / kQ) * a.H + h) * kHead, lane * 16, lds_addr(sh.head[b][wave / 2]));
+    };
+    auto stage = [&](uint32_t t) {  // what a chunk needs first
+        const int b = (int)((t - from) / kQ & 1);
+        if constexpr (OUT) {
+            pieces(t, kB, kB + kCG, sh.CG);
+            pieces(t, kB + kCG, kB + kCG + 1, sh.scale[b]);
+            head(t, b);
+        } else {
+            pieces(t, 0, kB, sh.B[b]);
+            head(t, b);
+        }
     };
 
-    if (from < to) stage(from, 0);
+    if (from < to) stage(from);
     if (!on) {  // no columns: the wave only carries its share of the loads
         for (uint32_t t = from; t < to; t += kQ) {
             vm_wait();
             lds_barrier();
-            if (t + kQ < to) stage(t + kQ, (int)((t - from) / kQ & 1) ^ 1);
-            if constexpr (OUT) lds_barrier();
+            if constexpr (OUT) {
+                pieces(t, 0, kB, sh.B[0]);
+                vm_wait();
+                lds_barrier();
+            }
+            if (t + kQ < to) stage(t + kQ);
         }
     } else {
     if (from < to) load(from);
@@ -472,11 +527,15 @@ __global__ __launch_bounds__(kWalkThreads, 2) void walk_kernel(SsdCacheArgs a) {
         const float dec = meta[0];
         const int ew = __float_as_int(meta[1]), ed = __float_as_int(meta[2]);
         const int eB = ((const __attribute__((address_space(4))) int *)a.ws_eb)[(int64_t)id * G + g];
-        vm_wait();
-        lds_barrier();  // the chunk is in LDS, and the other buffer is free
-        if (t + kQ < to) stage(t + kQ, b ^ 1);
-        const auto &buf = sh.buf[b];
-        const float *hd = buf.head[wave / 2];
+        // The chunk's first part is in LDS and every wave is done with the chunk
+        // before. Issued since: that part, the rows, and 16 stores of y, which
+        // may stay in flight (accesses complete in order).
+        if (OUT && t > from) asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
+        else vm_wait();
+        lds_barrier();
+        if constexpr (OUT) pieces(t, 0, kB, sh.B[0]);
+        else if (t + kQ < to) stage(t + kQ);
+        const float *hd = sh.head[b][wave / 2];
         const int rem = to - t < kQ ? (int)(to - t) : kQ;
 
         // the wave's half of the masked matrix: M[t][s] = G[t][s] exp2(cum_t - cum_s) dt_s
@@ -490,7 +549,7 @@ __global__ __launch_bounds__(kWalkThreads, 2) void walk_kernel(SsdCacheArgs a) {
                 const float ct = hd[16 * (r / 4) + r % 4 + 4 * tt];
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
-                    const f16x8 gv = *(const f16x8 *)(buf.frag + 3 * kQ * N + ((tt * 2 + hh) * 64 + lane) * 8);
+                    const f16x8 gv = *(const f16x8 *)(sh.CG + kQ * N + ((tt * 2 + hh) * 64 + lane) * 8);
                     f16x8 m;
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
@@ -510,7 +569,11 @@ __global__ __launch_bounds__(kWalkThreads, 2) void walk_kernel(SsdCacheArgs a) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     auto at = [&](int j) { return __uint_as_float(c ? raw[i + j] & 0xffff0000u : raw[i + j] << 16); };
-                    x[c][i] = conv_silu(w[c][0], w[c][1], w[c][2], w[c][3], bias[c], at(0), at(1), at(2), at(3));
+                    float u = __builtin_fmaf(w[c][0], at(0), bias[c]);
+                    u = __builtin_fmaf(w[c][1], at(1), u);
+                    u = __builtin_fmaf(w[c][2], at(2), u);
+                    u = __builtin_fmaf(w[c][3], at(3), u);
+                    x[c][i] = u * __builtin_amdgcn_rcpf(1.0f + fast_exp2(u));
                 }
             if (rem < kQ) {
 #pragma unroll
@@ -518,13 +581,14 @@ __global__ __launch_bounds__(kWalkThreads, 2) void walk_kernel(SsdCacheArgs a) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) x[c][i] = 16 * q + i < rem ? x[c][i] : 0.0f;
             }
-            if (t + kQ < to) load(t + kQ);
+            if (!OUT && t + kQ < to) load(t + kQ);
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int i = 0; i < 16; i += 2)  // keeps a NaN
                     top = __builtin_elementwise_maximum(__builtin_elementwise_maximum(__builtin_fabsf(x[c][i]), __builtin_fabsf(x[c][i + 1])), top);
-            if (__ballot(!finite(top))) {
+            top = wave_top(top);
+            if (!finite(top)) {
                 // A value that is not finite would reach earlier tokens as 0
                 // times itself: the products take zero for it, and what it
                 // reaches (its channel, from its token on) is marked at the end.
@@ -540,8 +604,8 @@ __global__ __launch_bounds__(kWalkThreads, 2) void walk_kernel(SsdCacheArgs a) {
                         }
                         top = __builtin_fmaxf(top, __builtin_fabsf(x[c][i]));
                     }
+                top = wave_top(top);
             }
-            top = wave_max(top);
         }
         const int ex = clampi(uniform(exponent(top)), -100, 127);
         const int eb = uniform(exponent(bound));
@@ -550,30 +614,18 @@ __global__ __launch_bounds__(kWalkThreads, 2) void walk_kernel(SsdCacheArgs a) {
         const int need = K + eb - 100 + 28 - eB;
         kv = kv > need ? kv : need;
         const int Kn = kv - 28 + eB;
-        f16x8 vh[2][2], vl[2][2], x16[2][2];
+        f16x8 x16[2][2];
         int E2 = 0;
         float dx = 0.0f;
         f32x4 Y[4][2];
         {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float wk = __builtin_ldexpf(hd[2 * kQ + 16 * q + i], 14 - kv);
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float v = x[c][i] * wk;
-                    // one rounded product: the low part is what the high part leaves of it
-                    asm("" : "+v"(v));
-                    vh[c][i / 8][i % 8] = (_Float16)v;
-                    vl[c][i / 8][i % 8] = (_Float16)(v - (float)vh[c][i / 8][i % 8]);
-                }
-            }
             if constexpr (OUT) {
                 const int sS = clampi(15 - eb, -127, 100);
                 const int E1 = K - sS - 7;
                 int exx = E1 - 60 - ed - eB + 21;
                 exx = ex > exx ? ex : exx;
                 E2 = exx + ed + eB - 21;
-                const float sx = __builtin_ldexpf(1.0f, 14 - exx);
+                const float sx = __builtin_ldexpf(-kLn2, 14 - exx);
                 dx = dsk * __builtin_ldexpf(1.0f, exx - 14);
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
@@ -594,7 +646,7 @@ __global__ __launch_bounds__(kWalkThreads, 2) void walk_kernel(SsdCacheArgs a) {
                         for (int e = 0; e < 8; ++e) so[c][e] = (_Float16)(acc[2 * m + e / 4][c][e % 4] * sf);
 #pragma unroll
                     for (int tt = 0; tt < 4; ++tt) {
-                        const f16x8 co = *(const f16x8 *)(buf.frag + 2 * kQ * N + ((tt * KB + m) * 64 + lane) * 8);
+                        const f16x8 co = *(const f16x8 *)(sh.CG + ((tt * KB + m) * 64 + lane) * 8);
 #pragma unroll
                         for (int c = 0; c < 2; ++c) Y[tt][c] = mfma(co, so[c], Y[tt][c]);
                     }
@@ -611,7 +663,14 @@ __global__ __launch_bounds__(kWalkThreads, 2) void walk_kernel(SsdCacheArgs a) {
                 }
             }
         }
-        if constexpr (OUT) lds_barrier();  // M is whole
+        if constexpr (OUT) {
+            vm_wait();
+            lds_barrier();  // M is whole, B is in LDS, and every wave is done with C, G and the decays
+            if (t + kQ < to) {
+                stage(t + kQ);
+                load(t + kQ);
+            }
+        }
         if constexpr (OUT) {
 #pragma unroll
             for (int tt = 0; tt < 4; ++tt)
@@ -621,21 +680,25 @@ __global__ __launch_bounds__(kWalkThreads, 2) void walk_kernel(SsdCacheArgs a) {
 #pragma unroll
                     for (int c = 0; c < 2; ++c) Y[tt][c] = mfma(mo, x16[c][hh], Y[tt][c]);
                 }
-            const float *rs = (const float *)(buf.frag + 3 * kQ * N + kQ * kQ);
-            char *yb = (char *)a.y + ((int64_t)(begin + t) * a.H * a.P + ch0) * 2;
-            const uint32_t yrow = (uint32_t)(a.H * a.P) * 2;
-            uint32_t yo = 16 * q * yrow + 4 * r;
-            asm volatile("" : "+v"(yo));
-            bool low[2] = {false, false};
+            const float *rs = sh.scale[b];
             if (anybad) {
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
+                for (int c = 0; c < 2; ++c) {
+                    bool low = false;  // the channel is marked in an earlier lane's tokens
 #pragma unroll
                     for (int d = 16; d < 64; d += 16) {
                         const uint32_t o = __shfl(badm[c], (lane - d) & 63);
-                        low[c] |= lane >= d && o != 0u;
+                        low |= lane >= d && o != 0u;
                     }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (low || (badm[c] & ((2u << i) - 1))) Y[i / 4][c][i % 4] = __builtin_nanf("");
+                }
             }
+            const uint32_t yrow = (uint32_t)(a.H * a.P) * 2;
+            const auto yb = buffer((const char *)a.y + ((int64_t)(begin + t) * a.H * a.P + ch0) * 2, (rem - 1) * yrow + 64);
+            uint32_t yo = 16 * q * yrow + 4 * r;
+            asm volatile("" : "+v"(yo));
 #pragma unroll
             for (int tt = 0; tt < 4; ++tt) {
                 const f32x4 rv = *(const f32x4 *)(rs + 16 * q + 4 * tt);
@@ -645,13 +708,8 @@ __global__ __launch_bounds__(kWalkThreads, 2) void walk_kernel(SsdCacheArgs a) {
                     const float be = __builtin_ldexpf(rv[e], E2);
                     float o[2];
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        o[c] = __builtin_fmaf((float)x16[c][i / 8][i % 8], dx, Y[tt][c][e] * be);
-                        if (anybad && (low[c] || (badm[c] & ((2u << i) - 1)))) o[c] = __builtin_nanf("");
-                    }
-                    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-                    const bf16x2 pk = {(__bf16)o[0], (__bf16)o[1]};
-                    if (rem == kQ || 16 * q + i < rem) *(bf16x2 *)(yb + yo) = pk;
+                    for (int c = 0; c < 2; ++c) o[c] = __builtin_fmaf((float)x16[c][i / 8][i % 8], dx, Y[tt][c][e] * be);
+                    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, bf16x2{(__bf16)o[0], (__bf16)o[1]}), yb, yo, 0, 0);
                     yo += yrow;
                 }
             }
@@ -668,18 +726,33 @@ __global__ __launch_bounds__(kWalkThreads, 2) void walk_kernel(SsdCacheArgs a) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) acc[nt][c] *= f;
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh)
+        for (int hh = 0; hh < 2; ++hh) {
+            f16x8 vh[2], vl[2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const f16x8 bh = *(const f16x8 *)(buf.frag + ((hh * NT + nt) * 64 + lane) * 8);
-                const f16x8 bl = *(const f16x8 *)(buf.frag + kQ * N + ((hh * NT + nt) * 64 + lane) * 8);
+            for (int j = 0; j < 8; j += 2) {
+                const int i = 8 * hh + j;
+                const float wa = __builtin_ldexpf(hd[2 * kQ + 16 * q + i], 14 - kv);
+                const float wb = __builtin_ldexpf(hd[2 * kQ + 16 * q + i + 1], 14 - kv);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    acc[nt][c] = mfma(bh, vh[c][hh], acc[nt][c]);
-                    acc[nt][c] = mfma(bl, vh[c][hh], acc[nt][c]);
-                    acc[nt][c] = mfma(bh, vl[c][hh], acc[nt][c]);
+                    f16x2 hi, lo;
+                    split(x[c][i] * wa, x[c][i + 1] * wb, hi, lo);
+                    vh[c][j] = hi[0], vh[c][j + 1] = hi[1];
+                    vl[c][j] = lo[0], vl[c][j + 1] = lo[1];
                 }
             }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const f16x8 bh = *(const f16x8 *)(sh.B[OUT ? 0 : b] + ((hh * NT + nt) * 64 + lane) * 8);
+                const f16x8 bl = *(const f16x8 *)(sh.B[OUT ? 0 : b] + kQ * N + ((hh * NT + nt) * 64 + lane) * 8);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    acc[nt][c] = mfma(bh, vh[c], acc[nt][c]);
+                    acc[nt][c] = mfma(bl, vh[c], acc[nt][c]);
+                    acc[nt][c] = mfma(bh, vl[c], acc[nt][c]);
+                }
+            }
+        }
         if (anybad) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
@@ -757,7 +830,7 @@ hipError_t launch_n(const SsdCacheArgs &a, hipStream_t s) {
     hipLaunchKernelGGL((prepare_kernel<N>), dim3((unsigned)(a.nchunk * a.G + a.seqs * parts)), dim3(kPrepThreads), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int64_t ncb = a.H / a.G * (a.P / 64), units = a.nseg * a.G * ((ncb + 3) / 4);
+    const int64_t ncb = a.H / a.G * (a.P / 64), units = a.nseg * a.G * ((ncb + 1) / 2);
     const dim3 grid((unsigned)((units + 7) / 8 * 8));
     if (a.rows > a.seg) {  // some sequence may be longer than a segment
         hipLaunchKernelGGL((walk_kernel<N, false>), grid, dim3(kWalkThreads), 0, s, a);
@@ -771,10 +844,11 @@ hipError_t launch_n(const SsdCacheArgs &a, hipStream_t s) {
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Tokens per segment: enough segments that the walk has about two waves per
-// SIMD (a wave takes 32 of the H P columns), none shorter than 256 tokens.
-int64_t segment_tokens(int64_t rows, int64_t H, int64_t P) {
-    const int64_t want = (2048 * 32 + H * P - 1) / (H * P);
+// Tokens per segment: as many segments as keep the 512 workgroups that the chip
+// holds at once, none shorter than 256 tokens.
+int64_t segment_tokens(int64_t rows, int64_t H, int64_t P, int64_t G) {
+    const int64_t units = G * ((H / G * (P / 64) + 1) / 2);
+    const int64_t want = units >= 512 ? 1 : 512 / units;
     const int64_t seg = (rows + want - 1) / want;
     return (seg < 256 ? 256 : seg + 63) / 64 * 64;
 }
@@ -787,7 +861,7 @@ size_t plan(SsdCacheArgs &a, int N, char *base) {
         at += up256(bytes);
         return p;
     };
-    a.seg = segment_tokens(a.rows, a.H, a.P);
+    a.seg = segment_tokens(a.rows, a.H, a.P, a.G);
     a.nchunk = a.rows / kQ + a.seqs;
     a.nseg = a.rows / a.seg + a.seqs;
     const int64_t kept = a.rows / a.seg;
