@@ -18,22 +18,24 @@
 //   prepare   per (chunk, group): the convolution of B and C, G, and the layouts
 //             that the products load; per (chunk, head): the decays. B, C and G
 //             are shared by all heads of a group, so they are formed once.
-//   walk<0>   for sequences longer than a segment: every segment but the last
-//             from a zero start, its end state only (no y);
-//   join      those end states in order: the state that enters each segment;
-//   walk<1>   every segment from its entering state: y, and the sequence's last
-//             state and window into the cache.
-// The offsets are read on the device. Chunk i of sequence s has the id cu[s] /
-// 64 + s + i (segments likewise): disjoint ranges without a prefix sum, as
-// ceil(len / 64) <= cu[s+1] / 64 - cu[s] / 64 + 1.
+//   walk A    every segment of every sequence: the convolution of x, kept as the
+//             operand of the later products, and the segment's end state, from
+//             zero where the sequence is longer than one segment;
+//   join      those end states in order: the state that enters each segment, and
+//             the sequence's last state into the cache;
+//   walk C    every segment from its entering state: y.
+// A long sequence so keeps the whole chip busy. The offsets are read on the
+// device. Chunk i of sequence s has the id cu[s] / 64 + s + i (segments
+// likewise): disjoint ranges without a prefix sum, as ceil(len / 64) <= cu[s+1]
+// / 64 - cu[s] / 64 + 1.
 //
 // Precision. The state must come out as a float32 state would, so the products
-// that update it take both operands as sums of two float16 (22 bits; three
-// products, the product of the two low parts is below 2^-22). The products for
-// y, which is rounded to bfloat16 in the end, take single float16 operands (11
-// bits, against 8 of the result). float16 has little range, so operands carry
-// power-of-two scales: C one per token, B one per chunk, x one per chunk and
-// wave; the state accumulates in units 2^K that follow a running bound of its
+// of walk A take both operands as sums of two float16 (22 bits; three products,
+// the product of the two low parts is below 2^-22). The products for y, which is
+// rounded to bfloat16 in the end, take single float16 operands (11 bits, against
+// 8 of the result). float16 has little range, so operands carry power-of-two
+// scales: C one per token, B one per chunk, x one per chunk and wave, w one per
+// chunk; the state accumulates in units 2^K that follow a running bound of its
 // size. Scales are exact, and they cancel in one factor per token at the end.
 #include "ssm_common.h"
 #include "ssm_device.h"
@@ -58,7 +60,10 @@ constexpr int kWalkThreads = 64 * kWaves;
 // operand registers (lane-major), G as operand registers, 2^eC per token
 // (float32), filled up to whole 1 KiB pieces.
 constexpr int frag_elems(int N) { return 3 * kQ * N + kQ * kQ + 512; }
-constexpr int kHead = 4 * kQ;  // floats per (chunk, head): cum, cum - log2 dt, -ln2 w, exp2(cum)
+// Floats per (chunk, head) for walk C: cum, cum - log2 dt, exp2(cum), and w as
+// scaled float16, filled up to 1 KiB.
+constexpr int kHead = 4 * kQ;
+constexpr int kDtHeads = 16;  // heads per workgroup of the decays
 
 __device__ __forceinline__ f32x4 mfma(f16x8 a, f16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
@@ -100,12 +105,16 @@ __device__ __forceinline__ float wave_prefix_sum(float v) {
     v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x143, 0xC, 0xF, false));
     return v;
 }
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int m = 1; m < 64; m *= 2) v = __builtin_fmaxf(v, __shfl_xor(v, m));
+
+// The largest of the values in a lane's row of 16, none negative.
+__device__ __forceinline__ float row_top(float v) {
+    auto step = [&](int o) { v = __builtin_fmaxf(v, __int_as_float(o)); };
+    step(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x128, 0xF, 0xF, false));  // row_ror:8, 4, 2, 1
+    step(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x124, 0xF, 0xF, false));
+    step(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x122, 0xF, 0xF, false));
+    step(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x121, 0xF, 0xF, false));
     return v;
 }
-
 // The largest of the wave's values, none negative (or NaN, which stays): the
 // order of their bits.
 __device__ __forceinline__ float wave_top(float v) {
@@ -175,16 +184,57 @@ __device__ __forceinline__ void start_seq(const SsdCacheArgs &a, int64_t s, int6
             a.ws_win[(s * 3 + k) * a.C + c] = resume ? ((const uint16_t *)a.conv_cache)[((int64_t)slot * a.C + c) * 3 + k] : 0;
 }
 
+// The decays of the chunk for a wave's heads h0 .., a lane per token.
+__device__ __forceinline__ void chunk_decays(const SsdCacheArgs &a, uint32_t id, uint32_t row, int rem, uint32_t h0) {
+    constexpr int kPer = kDtHeads / 4;
+    const int lane = threadIdx.x & 63;
+    const uint32_t H = (uint32_t)a.H;
+    const uint16_t *src = (const uint16_t *)a.dt_raw + (int64_t)(row + (lane < rem ? lane : rem - 1)) * a.dt_stride;
+    float raw[kPer], bias[kPer], A2[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const uint32_t h = h0 + k < H ? h0 + k : H - 1;
+        raw[k] = ld_act(src, h);
+        bias[k] = a.dt_bias ? a.dt_bias[h] : 0.0f;
+        A2[k] = a.A[h] * kLog2e;
+    }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        if (h0 + k >= H) break;
+        const int64_t at = (int64_t)id * H + h0 + k;
+        const float dt = lane < rem ? softplus(raw[k] + bias[k]) : 0.0f;
+        const float step = dt * A2[k];
+        const float cum = wave_prefix_sum(step);
+        // from the end, without subtracting: exact where little decays
+        const float back = wave_prefix_sum(__shfl(step, 63 - lane));
+        const float sfx = lane < 63 ? __shfl(back, 62 - lane) : 0.0f;
+        const float wt = dt * fast_exp2(sfx);
+        const int ed = exponent(wave_top(finite_abs(dt))), ew = exponent(wave_top(finite_abs(wt)));
+        float *o = a.ws_head + at * kHead;
+        o[lane] = cum;
+        o[kQ + lane] = cum - __builtin_amdgcn_logf(dt) + (float)ed;
+        o[2 * kQ + lane] = fast_exp2(cum);
+        ((_Float16 *)(o + 3 * kQ))[lane] = (_Float16)__builtin_ldexpf(wt, -ew);
+        a.ws_w[at * kQ + lane] = wt * -kLn2;  // walk A holds x as -log2(e) x
+        if (lane == 63) *(f32x4 *)(a.ws_meta + at * 4) = f32x4{fast_exp2(cum), __int_as_float(ew), __int_as_float(ed), 0.0f};
+    }
+}
+
 template <int N>
 __global__ __launch_bounds__(kPrepThreads) void prepare_kernel(SsdCacheArgs a) {
     __shared__ PrepShared<N> sh;
-    const int64_t nchunk = a.nchunk * a.G;
-    if ((int64_t)blockIdx.x >= nchunk) {
-        const uint32_t parts = (uint32_t)((a.C + kPrepThreads - 1) / kPrepThreads), i = (uint32_t)(blockIdx.x - nchunk);
-        start_seq(a, i / parts, i % parts);
+    uint32_t blk = blockIdx.x;
+    const uint32_t nbc = (uint32_t)(a.nchunk * a.G), per = ((uint32_t)a.H + kDtHeads - 1) / kDtHeads;
+    const uint32_t ndt = (uint32_t)a.nchunk * per;
+    if (blk >= nbc + ndt) {
+        const uint32_t parts = (uint32_t)((a.C + kPrepThreads - 1) / kPrepThreads);
+        blk -= nbc + ndt;
+        start_seq(a, blk / parts, blk % parts);
         return;
     }
-    const uint32_t id = blockIdx.x / (uint32_t)a.G, g = blockIdx.x % (uint32_t)a.G;
+    const bool decays = blk >= nbc;
+    if (decays) blk -= nbc;
+    const uint32_t id = blk / (decays ? per : (uint32_t)a.G), g = blk % (decays ? per : (uint32_t)a.G);
     const int s = find_seq(a, id, kQ);
     if (s < 0) return;
     const uint32_t begin = seq_begin(a, s), len = seq_length(a, s, begin);
@@ -194,6 +244,10 @@ __global__ __launch_bounds__(kPrepThreads) void prepare_kernel(SsdCacheArgs a) {
     const int32_t slot = a.slots[s];
     const bool resume = a.resume && a.resume[s] != 0 && slot >= 0 && slot < a.num_slots;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    if (decays) {
+        chunk_decays(a, id, begin + first, rem, g * kDtHeads + wave * (kDtHeads / 4));
+        return;
+    }
 
     // The convolution: a lane takes four channels of TPB tokens; N / 4 lanes
     // hold a token's B, the next N / 4 its C.
@@ -237,21 +291,21 @@ __global__ __launch_bounds__(kPrepThreads) void prepare_kernel(SsdCacheArgs a) {
             top = __builtin_fmaxf(top, finite_abs(v[i][k]));
         }
         // the largest value of the token's C, and of the chunk's B
-#pragma unroll
-        for (int m = 1; m < N / 4; m *= 2) top = __builtin_fmaxf(top, __shfl_xor(top, m));
+        top = row_top(top);
+        if constexpr (N == 128) top = __builtin_fmaxf(top, __shfl_xor(top, 16));
         if (isC) {
             if (cl == N / 4) sh.ec[t0 + i] = clampi(exponent(top), -100, 120);
         } else {
             big = __builtin_fmaxf(big, top);
         }
     }
-    big = wave_max(big);
+    big = wave_top(big);
     if (lane == 0) sh.maxb[wave] = big;
     __syncthreads();
     const int eB = clampi(exponent(__builtin_fmaxf(__builtin_fmaxf(sh.maxb[0], sh.maxb[1]), __builtin_fmaxf(sh.maxb[2], sh.maxb[3]))), -100, 128);
 #pragma unroll
     for (int i = 0; i < TPB; ++i) {
-        const int e = isC ? 7 - sh.ec[t0 + i] : 14 - eB;
+        const int e = 7 - (isC ? sh.ec[t0 + i] : eB);
         f16x4 hi, lo;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -314,125 +368,128 @@ __global__ __launch_bounds__(kPrepThreads) void prepare_kernel(SsdCacheArgs a) {
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    o[4 * b + e] = 16 * q + 8 * h + 4 * b + e <= row + 4 * tt ? (_Float16)(acc[e] * 0x1p-14f) : (_Float16)0.0f;
+                    o[4 * b + e] = 16 * q + 8 * h + 4 * b + e <= row + 4 * tt ? (_Float16)(acc[e] * 0x1p-7f) : (_Float16)0.0f;
             }
             *(f16x8 *)(out + 3 * kQ * N + ((tt * 2 + h) * 64 + lane) * 8) = o;
         }
     }
     if (tid < kQ) ((float *)(out + 3 * kQ * N + kQ * kQ))[tid] = __builtin_ldexpf(1.0f, sh.ec[tid]);
     if (tid == 0) a.ws_eb[id * a.G + g] = eB;
-
-    // The decays, a wave per head of the group, a lane per token.
-    const uint32_t hpg = (uint32_t)a.H / (uint32_t)a.G;
-    const int64_t trow = begin + first + (lane < rem ? lane : rem - 1);
-    for (uint32_t k = wave; k < hpg; k += 4) {
-        const int64_t h = g * hpg + k;
-        const float rawdt = ld_act((const uint16_t *)a.dt_raw, trow * a.dt_stride + h);
-        const float dt = lane < rem ? softplus(rawdt + (a.dt_bias ? a.dt_bias[h] : 0.0f)) : 0.0f;
-        const float step = dt * (a.A[h] * kLog2e);
-        const float cum = wave_prefix_sum(step);
-        // from the end, without subtracting: exact where little decays
-        const float back = wave_prefix_sum(__shfl(step, 63 - lane));
-        const float sfx = lane < 63 ? __shfl(back, 62 - lane) : 0.0f;
-        const float wt = dt * fast_exp2(sfx) * -kLn2;  // the walks hold x as -log2(e) x
-        const float top = wave_max(finite_abs(dt)), wtop = wave_max(finite_abs(wt));
-        const int ed = exponent(top);
-        float *o = a.ws_head + (id * a.H + h) * kHead;
-        o[lane] = cum;
-        o[kQ + lane] = cum - __builtin_amdgcn_logf(dt) + (float)ed;
-        o[2 * kQ + lane] = wt;
-        o[3 * kQ + lane] = fast_exp2(cum);
-        if (lane == 63)
-            *(f32x4 *)(a.ws_meta + (id * a.H + h) * 4) =
-                f32x4{fast_exp2(cum), __int_as_float(exponent(wtop)), __int_as_float(ed), 0.0f};
-    }
 }
 
-// ----------------------------------------------------------------------- walk
+// ---------------------------------------------------------------------- walks
 
-// LDS of a walk. For y one chunk at a time: B arrives while the masked matrix is
-// formed, C, G and the decays of the next chunk while the state is updated, so
-// that two workgroups fit a CU and run out of step. For the end states alone B
-// and the decays are held twice.
-template <int N, bool OUT>
-struct WalkShared {
-    static constexpr int kBufs = OUT ? 1 : 2;
-    alignas(16) _Float16 B[kBufs][2 * kQ * N];
-    alignas(16) _Float16 CG[OUT ? kQ * N + kQ * kQ : 8];
-    alignas(16) float scale[2][256];  // 2^eC per token
-    alignas(16) float head[2][2][kHead];
-    alignas(16) _Float16 M[OUT ? 2 : 1][OUT ? 8 : 1][64][8];
+// What a workgroup of a walk works on: one segment of one sequence, and two
+// column blocks (64 rows of a head's state each) of one group; two waves share a
+// block, 32 columns each. Lane (r, q) = (l % 16, l / 16) holds the channels p =
+// 2 r + c of the wave's 32 for the tokens 16 q + i of a chunk: what the 16 x 16
+// x 32 product takes as its B operand (column r, k = 8 consecutive tokens), and,
+// with the output's rows numbered to match, the place where y comes out.
+struct Unit {
+    uint32_t begin, len, k, nseg, from, to, g, hb, h, hfirst, ch0, sid, chunk0;
+    int s;
+    bool on;    // the wave has columns
+    bool some;  // there is anything to do
 };
 
-// One workgroup: the segment's chunks in order, for two column blocks (64 rows
-// of a head's state) of one group; two waves share a block, 32 columns each,
-// and each forms half of the block's masked matrix. Lane (r, q) = (l % 16, l /
-// 16) holds the channels p = 2 r + c of the wave's 32 for the tokens 16 q + i
-// of a chunk: what the 16 x 16 x 32 product takes as its B operand (column r,
-// k = 8 consecutive tokens), and, with the output's rows numbered to match, the
-// place where y comes out.
-template <int N, bool OUT>
-__global__ __launch_bounds__(kWalkThreads, 2) void walk_kernel(SsdCacheArgs a) {
-    constexpr int NT = N / 16, KB = N / 32;
-    __shared__ WalkShared<N, OUT> sh;
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const int r = lane & 15, q = lane >> 4;
+__device__ __forceinline__ Unit find_unit(const SsdCacheArgs &a) {
+    Unit u;
+    u.some = false;
+    const uint32_t wave = uniform(threadIdx.x >> 6);
     // Workgroups are dealt to the 8 XCDs in turn: neighbours in the order of
     // the work (the column blocks of one segment, which load the same B, C and
     // G) go to one XCD and its L2.
-    const uint32_t pb = (uint32_t)a.P / 64, G = (uint32_t)a.G, seg = (uint32_t)a.seg;
-    const uint32_t ncb = (uint32_t)a.H / G * pb, nhb = (ncb + 1) / 2;
+    const uint32_t P = (uint32_t)a.P, pb = P / 64, G = (uint32_t)a.G, hpg = (uint32_t)a.H / G, seg = (uint32_t)a.seg;
+    const uint32_t ncb = hpg * pb, nhb = (ncb + 1) / 2;
     const uint32_t total = (uint32_t)a.nseg * G * nhb, per = (total + 7) / 8;
     const uint32_t unit = blockIdx.x % 8 * per + blockIdx.x / 8;
-    if (unit >= total) return;
-    const uint32_t sid = unit / (G * nhb), g = unit / nhb % G, hb = unit % nhb;
-    const int s = find_seq(a, sid, seg);
-    if (s < 0) return;
-    const uint32_t begin = seq_begin(a, s), len = seq_length(a, s, begin);
-    const uint32_t k = sid - (begin / seg + s);  // segment of the sequence
-    const uint32_t nseg = len > 0 ? (len + seg - 1) / seg : 1;
-    if (k >= (OUT ? nseg : nseg - 1)) return;
-    const uint32_t from = k * seg, to = len - from < seg ? len : from + seg;
-    const bool last = k == nseg - 1;
-    const uint32_t cb = hb * 2 + wave / 2;
-    const bool on = cb < ncb;
-    const int64_t h = g * ((uint32_t)a.H / G) + (on ? cb / pb : 0);
-    const int64_t ch0 = h * a.P + (on ? cb % pb : 0) * 64 + 32 * (wave % 2);  // the wave's first channel
-    const uint32_t kept = begin / seg + k;  // the segment's place among those that keep a state
-    const int32_t slot = a.ws_slot[s];
-    if (slot < 0) {
-        if (OUT && on)
-            for (uint32_t t = from + q; t < to; t += 4) *(uint32_t *)((uint16_t *)a.y + (int64_t)(begin + t) * a.H * a.P + ch0 + 2 * r) = 0u;
-        return;
-    }
+    if (unit >= total) return u;
+    u.sid = unit / (G * nhb);
+    u.g = unit / nhb % G;
+    u.hb = unit % nhb;
+    u.s = find_seq(a, u.sid, seg);
+    if (u.s < 0) return u;
+    u.begin = seq_begin(a, u.s);
+    u.len = seq_length(a, u.s, u.begin);
+    u.k = u.sid - (u.begin / seg + u.s);
+    u.nseg = u.len > 0 ? (u.len + seg - 1) / seg : 1;
+    if (u.k >= u.nseg) return u;
+    u.from = u.k * seg;
+    u.to = u.len - u.from < seg ? u.len : u.from + seg;
+    const uint32_t cb = u.hb * 2 + wave / 2;
+    u.on = cb < ncb;
+    u.hfirst = u.g * hpg + u.hb * 2 / pb;
+    u.h = u.g * hpg + (u.on ? cb / pb : 0);
+    u.ch0 = u.h * P + (u.on ? cb % pb : 0) * 64 + 32 * (wave % 2);  // the wave's first channel
+    u.chunk0 = u.begin / kQ + u.s;
+    u.some = true;
+    return u;
+}
 
-    // the state: acc[nt][c][e] = S[p = 2 r + c][n = 16 nt + 4 q + e] 2^-K
+// Pieces of 1 KiB from `src` straight into LDS, dealt to the waves in turn.
+template <int PIECES>
+__device__ __forceinline__ void pieces(const void *src, const void *to_lds, int wave, int lane) {
+    const uint32_t dst = lds_addr(to_lds);
+#pragma unroll
+    for (int i = 0; i < (PIECES + kWaves - 1) / kWaves; ++i) {
+        const int p = i * kWaves + wave;
+        if (p < PIECES) dma16_s((const char *)src + p * 1024, lane * 16, dst + p * 1024);
+    }
+}
+
+constexpr int pieces_b(int N) { return 2 * kQ * N / 512; }
+constexpr int pieces_cg(int N) { return (kQ * N + kQ * kQ) / 512; }
+
+// Walk A: x, and the segment's end state. Bound by the vector ALU (the
+// convolution and SiLU, the splitting of operands); the products run beside it.
+// B of two chunks is held in LDS, so that two workgroups share a CU.
+template <int N>
+__global__ __launch_bounds__(kWalkThreads, 2) void walk_state_kernel(SsdCacheArgs a) {
+    constexpr int NT = N / 16;
+    struct Shared {
+        alignas(16) _Float16 B[2][2 * kQ * N];
+        alignas(16) float w[2][4][kQ];
+    };
+    __shared__ Shared sh;
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), r = lane & 15, q = lane >> 4;
+    const Unit u = find_unit(a);
+    if (!u.some) return;
+    const int32_t slot = a.ws_slot[u.s];
+    if (slot < 0) return;
+    const uint32_t from = u.from, to = u.to, H = (uint32_t)a.H, G = (uint32_t)a.G;
+
+    // the state: acc[nt][c][e] = S[p = 2 r + c][n = 16 nt + 4 q + e] 2^-K, from
+    // the cache where the sequence is one segment and resumes
     f32x4 acc[NT][2];
     int K = 0;
     float bound = 0.0f;  // of |acc|
-    const bool resume = a.resume && a.resume[s] != 0;
-    const int64_t off = (ch0 + 2 * r) * N + 4 * q, hpn = a.H * a.P * N;
+    const int64_t off = (int64_t)(u.ch0 + 2 * r) * N + 4 * q, hpn = a.H * a.P * N;
+    const bool resume = a.resume && a.resume[u.s] != 0, one = u.nseg == 1;
     float *const cache = a.state_cache + (int64_t)slot * hpn + off;
-    const float *src = nullptr;
-    if (OUT) src = k > 0 ? a.ws_state + (int64_t)(kept - 1) * hpn + off : resume ? cache : nullptr;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            acc[nt][c] = src && on ? *(const f32x4 *)(src + c * N + 16 * nt) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) bound = __builtin_fmaxf(bound, finite_abs(acc[nt][c][e]));
-        }
-    bound = wave_max(bound);
-    if (bound > 0.0f) {
-        K = uniform(exponent(bound));
-        bound = 1.0f;
+        for (int c = 0; c < 2; ++c) acc[nt][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (one && resume && u.on) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
+            for (int c = 0; c < 2; ++c) {
+                acc[nt][c] = *(const f32x4 *)(cache + c * N + 16 * nt);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[nt][c][e] = __builtin_ldexpf(acc[nt][c][e], -K);
+                for (int e = 0; e < 4; ++e) bound = __builtin_fmaxf(bound, finite_abs(acc[nt][c][e]));
+            }
+        bound = wave_top(bound);
+        if (bound > 0.0f) {
+            K = uniform(exponent(bound));
+            bound = 1.0f;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[nt][c][e] = __builtin_ldexpf(acc[nt][c][e], -K);
+        }
     }
 
     // The convolution times -log2(e): its exp2 is SiLU's exponential, and the
@@ -440,21 +497,19 @@ __global__ __launch_bounds__(kWalkThreads, 2) void walk_kernel(SsdCacheArgs a) {
     float w[2][4], bias[2];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-        const f32x4 t = *(const f32x4 *)(a.conv_w + 4 * (ch0 + 2 * r + c));
+        const f32x4 t = *(const f32x4 *)(a.conv_w + 4 * (int64_t)(u.ch0 + 2 * r + c));
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[c][j] = t[j] * -kLog2e;
-        bias[c] = a.conv_b ? a.conv_b[ch0 + 2 * r + c] * -kLog2e : 0.0f;
+        bias[c] = a.conv_b ? a.conv_b[u.ch0 + 2 * r + c] * -kLog2e : 0.0f;
     }
-    const float dsk = OUT && a.Dskip ? a.Dskip[h] : 0.0f;
-    float segdec = 1.0f;
 
     // The raw rows of a chunk: tokens 16 q - 3 .. 16 q + 15, two channels each.
     // Behind the sequence's end zeros; before its start the window.
     uint32_t raw[19];
-    const uint32_t rowb = (uint32_t)a.xBC_stride * 2, chb = (uint32_t)(ch0 + 2 * r) * 2;
+    const uint32_t rowb = (uint32_t)a.xBC_stride * 2, chb = (u.ch0 + 2 * r) * 2;
     const uint32_t xlane = 16 * q * rowb + chb;
     auto load = [&](uint32_t t) {  // the chunk that starts at token t of the sequence
-        const char *base = (const char *)a.xBC + (int64_t)(begin + t) * rowb;
+        const char *base = (const char *)a.xBC + (int64_t)(u.begin + t) * rowb;
         const uint32_t rem = to - t < kQ ? to - t : kQ;
         const auto rows = buffer(base, rem * rowb);
         uint32_t o = xlane;
@@ -464,7 +519,7 @@ __global__ __launch_bounds__(kWalkThreads, 2) void walk_kernel(SsdCacheArgs a) {
 #pragma unroll
             for (int i = 0; i < 3; ++i) raw[i] = __builtin_amdgcn_raw_buffer_load_b32(before, o + i * rowb, 0, 0);
         } else {
-            const uint16_t *win = a.ws_win + (int64_t)s * 3 * a.C;
+            const uint16_t *win = a.ws_win + (int64_t)u.s * 3 * a.C;
 #pragma unroll
             for (int i = 0; i < 3; ++i) {
                 const uint32_t first = *(const uint32_t *)((const char *)(win + i * a.C) + chb);
@@ -478,247 +533,112 @@ __global__ __launch_bounds__(kWalkThreads, 2) void walk_kernel(SsdCacheArgs a) {
             o += rowb;
         }
     };
-    const uint32_t chunk0 = begin / kQ + s;
-    // Pieces [from, to) of 1 KiB of the chunk's operands, straight into LDS.
-    auto pieces = [&](uint32_t t, int lo, int hi, const void *to_lds) {
-        const char *f = (const char *)a.ws_frag + ((int64_t)(chunk0 + t / kQ) * G + g) * (frag_elems(N) * 2);
-        const uint32_t dst = lds_addr(to_lds);
-#pragma unroll
-        for (int i = 0; i < (hi - lo + kWaves - 1) / kWaves; ++i) {
-            const int p = i * kWaves + wave;
-            if (p < hi - lo) dma16_s(f + (lo + p) * 1024, lane * 16, dst + p * 1024);
-        }
-    };
-    constexpr int kB = 2 * kQ * N / 512, kCG = (kQ * N + kQ * kQ) / 512;
-    auto head = [&](uint32_t t, int b) {
-        if (wave % 2 == 0 && on)
-            dma16_s(a.ws_head + ((chunk0 + t / kQ) * a.H + h) * kHead, lane * 16, lds_addr(sh.head[b][wave / 2]));
-    };
-    auto stage = [&](uint32_t t) {  // what a chunk needs first
+    auto stage = [&](uint32_t t) {
         const int b = (int)((t - from) / kQ & 1);
-        if constexpr (OUT) {
-            pieces(t, kB, kB + kCG, sh.CG);
-            pieces(t, kB + kCG, kB + kCG + 1, sh.scale[b]);
-            head(t, b);
-        } else {
-            pieces(t, 0, kB, sh.B[b]);
-            head(t, b);
-        }
+        const uint32_t id = u.chunk0 + t / kQ;
+        pieces<pieces_b(N)>((const char *)a.ws_frag + ((int64_t)id * G + u.g) * (frag_elems(N) * 2), sh.B[b], wave, lane);
+        // w of four heads, the first two or all of them needed
+        if (wave == 0) dma16_s(a.ws_w + ((int64_t)id * H + u.hfirst) * kQ, lane * 16, lds_addr(sh.w[b]));
     };
 
-    if (from < to) stage(from);
-    if (!on) {  // no columns: the wave only carries its share of the loads
-        for (uint32_t t = from; t < to; t += kQ) {
-            vm_wait();
-            lds_barrier();
-            if constexpr (OUT) {
-                pieces(t, 0, kB, sh.B[0]);
-                vm_wait();
-                lds_barrier();
-            }
-            if (t + kQ < to) stage(t + kQ);
-        }
-    } else {
-    if (from < to) load(from);
+    float segdec = 1.0f;
+    if (from < to) {
+        stage(from);
+        if (u.on) load(from);
+    }
     for (uint32_t t = from; t < to; t += kQ) {
         const int b = (int)((t - from) / kQ & 1);
-        const uint32_t id = chunk0 + t / kQ;
-        const cf32_ptr meta = (cf32_ptr)(a.ws_meta + (id * a.H + h) * 4);
+        const uint32_t id = u.chunk0 + t / kQ;
+        vm_wait();
+        lds_barrier();  // the chunk is in LDS, and every wave is done with the one before
+        if (t + kQ < to) stage(t + kQ);
+        if (!u.on) continue;
+        const cf32_ptr meta = (cf32_ptr)(a.ws_meta + ((int64_t)id * H + u.h) * 4);
         const float dec = meta[0];
-        const int ew = __float_as_int(meta[1]), ed = __float_as_int(meta[2]);
-        const int eB = ((const __attribute__((address_space(4))) int *)a.ws_eb)[(int64_t)id * G + g];
-        // The chunk's first part is in LDS and every wave is done with the chunk
-        // before. Issued since: that part, the rows, and 16 stores of y, which
-        // may stay in flight (accesses complete in order).
-        if (OUT && t > from) asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
-        else vm_wait();
-        lds_barrier();
-        if constexpr (OUT) pieces(t, 0, kB, sh.B[0]);
-        else if (t + kQ < to) stage(t + kQ);
-        const float *hd = sh.head[b][wave / 2];
+        const int ew = __float_as_int(meta[1]);
+        const int eB = ((const __attribute__((address_space(4))) int *)a.ws_eb)[(int64_t)id * G + u.g];
+        const float *wt = sh.w[b][u.h - u.hfirst] + 16 * q;
         const int rem = to - t < kQ ? (int)(to - t) : kQ;
 
-        // the wave's half of the masked matrix: M[t][s] = G[t][s] exp2(cum_t - cum_s) dt_s
-        if (OUT) {
-            f32x4 cs[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) cs[i] = *(const f32x4 *)(hd + kQ + 16 * q + 4 * i);
-#pragma unroll
-            for (int k2 = 0; k2 < 2; ++k2) {
-                const int tt = 2 * (wave % 2) + k2;
-                const float ct = hd[16 * (r / 4) + r % 4 + 4 * tt];
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    const f16x8 gv = *(const f16x8 *)(sh.CG + kQ * N + ((tt * 2 + hh) * 64 + lane) * 8);
-                    f16x8 m;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        // G is zero above the diagonal, where the exponent may be large
-                        m[j] = (_Float16)fast_exp2(__builtin_fminf(ct - cs[2 * hh + j / 4][j % 4], 15.0f));
-                    *(f16x8 *)&sh.M[wave / 2][tt * 2 + hh][lane][0] = m * gv;
-                }
-            }
-        }
-        // x, and the scale of its operand
+        // x, and the scale of its operands
         float x[2][16], top = 0.0f;
         uint32_t badm[2] = {0u, 0u};
         bool anybad = false;
-        {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                auto at = [&](int j) { return __uint_as_float(c ? raw[i + j] & 0xffff0000u : raw[i + j] << 16); };
+                float v = __builtin_fmaf(w[c][0], at(0), bias[c]);
+                v = __builtin_fmaf(w[c][1], at(1), v);
+                v = __builtin_fmaf(w[c][2], at(2), v);
+                v = __builtin_fmaf(w[c][3], at(3), v);
+                x[c][i] = v * __builtin_amdgcn_rcpf(1.0f + fast_exp2(v));
+            }
+        if (t + kQ < to) load(t + kQ);
+        if (rem < kQ) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[c][i] = 16 * q + i < rem ? x[c][i] : 0.0f;
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < 16; i += 2)  // keeps a NaN
+                top = __builtin_elementwise_maximum(__builtin_elementwise_maximum(__builtin_fabsf(x[c][i]), __builtin_fabsf(x[c][i + 1])), top);
+        top = wave_top(top);
+        if (!finite(top)) {
+            // A value that is not finite would reach earlier tokens as 0 times
+            // itself: the products take zero for it, and what it reaches (its
+            // channel, from its token on) is marked.
+            anybad = true;
+            top = 0.0f;
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    auto at = [&](int j) { return __uint_as_float(c ? raw[i + j] & 0xffff0000u : raw[i + j] << 16); };
-                    float u = __builtin_fmaf(w[c][0], at(0), bias[c]);
-                    u = __builtin_fmaf(w[c][1], at(1), u);
-                    u = __builtin_fmaf(w[c][2], at(2), u);
-                    u = __builtin_fmaf(w[c][3], at(3), u);
-                    x[c][i] = u * __builtin_amdgcn_rcpf(1.0f + fast_exp2(u));
+                    if (!finite(x[c][i])) {
+                        badm[c] |= 1u << i;
+                        x[c][i] = 0.0f;
+                    }
+                    top = __builtin_fmaxf(top, __builtin_fabsf(x[c][i]));
                 }
-            if (rem < kQ) {
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) x[c][i] = 16 * q + i < rem ? x[c][i] : 0.0f;
-            }
-            if (!OUT && t + kQ < to) load(t + kQ);
+            top = wave_top(top);
+        }
+        const int ex = clampi(uniform(exponent(top)), -100, 127);
+        // x as walk C takes it, as its registers; a marked value is a NaN again
+        {
+            const float sx = __builtin_ldexpf(-kLn2, 14 - ex);
+            f16x8 xo[2][2];
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
-                for (int i = 0; i < 16; i += 2)  // keeps a NaN
-                    top = __builtin_elementwise_maximum(__builtin_elementwise_maximum(__builtin_fabsf(x[c][i]), __builtin_fabsf(x[c][i + 1])), top);
-            top = wave_top(top);
-            if (!finite(top)) {
-                // A value that is not finite would reach earlier tokens as 0
-                // times itself: the products take zero for it, and what it
-                // reaches (its channel, from its token on) is marked at the end.
-                anybad = true;
-                top = 0.0f;
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        if (!finite(x[c][i])) {
-                            badm[c] |= 1u << i;
-                            x[c][i] = 0.0f;
-                        }
-                        top = __builtin_fmaxf(top, __builtin_fabsf(x[c][i]));
-                    }
-                top = wave_top(top);
-            }
-        }
-        const int ex = clampi(uniform(exponent(top)), -100, 127);
-        const int eb = uniform(exponent(bound));
-        // units of the state after this chunk: S = acc 2^Kn
-        int kv = ex + ew;
-        const int need = K + eb - 100 + 28 - eB;
-        kv = kv > need ? kv : need;
-        const int Kn = kv - 28 + eB;
-        f16x8 x16[2][2];
-        int E2 = 0;
-        float dx = 0.0f;
-        f32x4 Y[4][2];
-        {
-            if constexpr (OUT) {
-                const int sS = clampi(15 - eb, -127, 100);
-                const int E1 = K - sS - 7;
-                int exx = E1 - 60 - ed - eB + 21;
-                exx = ex > exx ? ex : exx;
-                E2 = exx + ed + eB - 21;
-                const float sx = __builtin_ldexpf(-kLn2, 14 - exx);
-                dx = dsk * __builtin_ldexpf(1.0f, exx - 14);
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) x16[c][i / 8][i % 8] = (_Float16)(x[c][i] * sx);
-                // C S^T, in units of the masked product
-                const float sf = __builtin_ldexpf(1.0f, sS);
-#pragma unroll
-                for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) Y[tt][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int m = 0; m < KB; ++m) {
-                    f16x8 so[2];
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) so[c][e] = (_Float16)(acc[2 * m + e / 4][c][e % 4] * sf);
-#pragma unroll
-                    for (int tt = 0; tt < 4; ++tt) {
-                        const f16x8 co = *(const f16x8 *)(sh.CG + ((tt * KB + m) * 64 + lane) * 8);
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) Y[tt][c] = mfma(co, so[c], Y[tt][c]);
-                    }
-                }
-#pragma unroll
-                for (int tt = 0; tt < 4; ++tt) {
-                    const f32x4 ec = *(const f32x4 *)(hd + 3 * kQ + 16 * q + 4 * tt);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float al = __builtin_ldexpf(ec[e], E1 - E2);
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) Y[tt][c][e] *= al;
-                    }
-                }
-            }
-        }
-        if constexpr (OUT) {
-            vm_wait();
-            lds_barrier();  // M is whole, B is in LDS, and every wave is done with C, G and the decays
-            if (t + kQ < to) {
-                stage(t + kQ);
-                load(t + kQ);
-            }
-        }
-        if constexpr (OUT) {
-#pragma unroll
-            for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    const f16x8 mo = *(const f16x8 *)&sh.M[wave / 2][tt * 2 + hh][lane][0];
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) Y[tt][c] = mfma(mo, x16[c][hh], Y[tt][c]);
-                }
-            const float *rs = sh.scale[b];
+                for (int i = 0; i < 16; ++i) xo[c][i / 8][i % 8] = (_Float16)(x[c][i] * sx);
             if (anybad) {
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    bool low = false;  // the channel is marked in an earlier lane's tokens
-#pragma unroll
-                    for (int d = 16; d < 64; d += 16) {
-                        const uint32_t o = __shfl(badm[c], (lane - d) & 63);
-                        low |= lane >= d && o != 0u;
-                    }
+                for (int c = 0; c < 2; ++c)
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        if (low || (badm[c] & ((2u << i) - 1))) Y[i / 4][c][i % 4] = __builtin_nanf("");
-                }
+                        if (badm[c] >> i & 1) xo[c][i / 8][i % 8] = (_Float16)__builtin_nanf("");
             }
-            const uint32_t yrow = (uint32_t)(a.H * a.P) * 2;
-            const auto yb = buffer((const char *)a.y + ((int64_t)(begin + t) * a.H * a.P + ch0) * 2, (rem - 1) * yrow + 64);
-            uint32_t yo = 16 * q * yrow + 4 * r;
-            asm volatile("" : "+v"(yo));
+            const int64_t at = (int64_t)id * (a.H * a.P / 32) + u.ch0 / 32;
+            f16x8 *dst = (f16x8 *)a.ws_x + at * 256 + lane;
 #pragma unroll
-            for (int tt = 0; tt < 4; ++tt) {
-                const f32x4 rv = *(const f32x4 *)(rs + 16 * q + 4 * tt);
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int i = 4 * tt + e;
-                    const float be = __builtin_ldexpf(rv[e], E2);
-                    float o[2];
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) o[c] = __builtin_fmaf((float)x16[c][i / 8][i % 8], dx, Y[tt][c][e] * be);
-                    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, bf16x2{(__bf16)o[0], (__bf16)o[1]}), yb, yo, 0, 0);
-                    yo += yrow;
-                }
-            }
+                for (int hh = 0; hh < 2; ++hh) dst[(c * 2 + hh) * 64] = xo[c][hh];
+            if (lane == 0) a.ws_ex[at] = ex + (anybad ? 1 << 16 : 0);
         }
-        // the state
-        const int sh_k = K - Kn;
-        const float f = __builtin_ldexpf(dec, sh_k < 120 ? sh_k : 120);
-        bound = __builtin_fmaf(bound, f, 0x1p34f);
-        if (!finite(bound)) bound = 0x1p34f;
+        // units of the state after this chunk: S = acc 2^Kn
+        const int eb = uniform(exponent(bound));
+        int kv = ex + ew;
+        const int need = K + eb - 100 + 21 - eB;
+        kv = kv > need ? kv : need;
+        const int Kn = kv - 21 + eB, by = K - Kn;
+        const float f = __builtin_ldexpf(dec, by < 120 ? by : 120);
+        bound = __builtin_fmaf(bound, f, 0x1p27f);
+        if (!finite(bound)) bound = 0x1p27f;
         segdec *= dec;
         K = Kn;
 #pragma unroll
@@ -731,8 +651,7 @@ __global__ __launch_bounds__(kWalkThreads, 2) void walk_kernel(SsdCacheArgs a) {
 #pragma unroll
             for (int j = 0; j < 8; j += 2) {
                 const int i = 8 * hh + j;
-                const float wa = __builtin_ldexpf(hd[2 * kQ + 16 * q + i], 14 - kv);
-                const float wb = __builtin_ldexpf(hd[2 * kQ + 16 * q + i + 1], 14 - kv);
+                const float wa = __builtin_ldexpf(wt[i], 14 - kv), wb = __builtin_ldexpf(wt[i + 1], 14 - kv);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     f16x2 hi, lo;
@@ -743,8 +662,8 @@ __global__ __launch_bounds__(kWalkThreads, 2) void walk_kernel(SsdCacheArgs a) {
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const f16x8 bh = *(const f16x8 *)(sh.B[OUT ? 0 : b] + ((hh * NT + nt) * 64 + lane) * 8);
-                const f16x8 bl = *(const f16x8 *)(sh.B[OUT ? 0 : b] + kQ * N + ((hh * NT + nt) * 64 + lane) * 8);
+                const f16x8 bh = *(const f16x8 *)(sh.B[b] + ((hh * NT + nt) * 64 + lane) * 8);
+                const f16x8 bl = *(const f16x8 *)(sh.B[b] + kQ * N + ((hh * NT + nt) * 64 + lane) * 8);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     acc[nt][c] = mfma(bh, vh[c], acc[nt][c]);
@@ -767,46 +686,24 @@ __global__ __launch_bounds__(kWalkThreads, 2) void walk_kernel(SsdCacheArgs a) {
             }
         }
     }
-    }
-
-    if (!OUT || last) {
-        if (on) {
-            float *dst = OUT ? cache : a.ws_state + (int64_t)kept * hpn + off;
+    if (!u.on) return;
+    // A sequence of one segment that does not resume is done; one that does is
+    // stored aside, as walk C still reads its first state; others are joined.
+    float *dst = one && !resume ? cache : a.ws_state + (int64_t)u.sid * hpn + off;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    f32x4 v;
+        for (int c = 0; c < 2; ++c) {
+            f32x4 v;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = __builtin_ldexpf(acc[nt][c][e], K);
-                    *(f32x4 *)(dst + c * N + 16 * nt) = v;
-                }
-            if (!OUT && lane == 0) a.ws_segdec[(int64_t)kept * a.H + h] = segdec;
+            for (int e = 0; e < 4; ++e) v[e] = __builtin_ldexpf(acc[nt][c][e], K);
+            *(f32x4 *)(dst + c * N + 16 * nt) = v;
         }
-        if constexpr (OUT) {
-            // the window: the last three raw rows, of the wave's channels and,
-            // once per group, of its B and C
-            auto row = [&](int t, int64_t c) {
-                return t < 0 ? a.ws_win[((int64_t)s * 3 + t + 3) * a.C + c]
-                             : ((const uint16_t *)a.xBC)[(int64_t)(begin + t) * a.xBC_stride + c];
-            };
-            uint16_t *win = (uint16_t *)a.conv_cache + (int64_t)slot * a.C * 3;
-            if (on && q < 3)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) win[(ch0 + 2 * r + c) * 3 + q] = row((int)len - 3 + q, ch0 + 2 * r + c);
-            if (hb == 0)
-                for (int i = threadIdx.x; i < 2 * N * 3; i += kWalkThreads) {
-                    const int n = i / 3;
-                    const int64_t c = a.H * a.P + ((n / N) * a.G + g) * N + n % N;
-                    win[c * 3 + i % 3] = row((int)len - 3 + i % 3, c);
-                }
-        }
-    }
+    if (lane == 0) a.ws_segdec[(int64_t)u.sid * H + u.h] = segdec;
 }
 
-// ----------------------------------------------------------------------- join
-
-// enter[k+1] = dec[k] enter[k] + end[k], in place of end[k].
+// enter[k] in place of end[k]: enter[0] the sequence's first state, enter[k+1] =
+// dec[k] enter[k] + end[k]; the last one goes into the cache.
 __global__ __launch_bounds__(256) void join_kernel(SsdCacheArgs a, int N) {
     const uint32_t s = blockIdx.y, begin = seq_begin(a, s), len = seq_length(a, s, begin), seg = (uint32_t)a.seg;
     const uint32_t nseg = (len + seg - 1) / seg;
@@ -814,31 +711,345 @@ __global__ __launch_bounds__(256) void join_kernel(SsdCacheArgs a, int N) {
     if (nseg < 2 || slot < 0) return;
     const int64_t hpn = a.H * a.P * N, i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
     if (i >= hpn) return;
-    const int64_t h = i / (a.P * N), first = begin / seg;
+    const int64_t h = i / (a.P * N), first = begin / seg + s;
+    float *const cache = a.state_cache + slot * hpn + i;
     f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (a.resume && a.resume[s] != 0) v = *(const f32x4 *)(a.state_cache + slot * hpn + i);
-    for (uint32_t k = 0; k < nseg - 1; ++k) {
+    if (a.resume && a.resume[s] != 0) v = *(const f32x4 *)cache;
+    for (uint32_t k = 0; k < nseg; ++k) {
         f32x4 *p = (f32x4 *)(a.ws_state + (first + k) * hpn + i);
-        v = *p + v * a.ws_segdec[(first + k) * a.H + h];
+        const f32x4 end = *p;
         *p = v;
+        v = end + v * a.ws_segdec[(first + k) * a.H + h];
     }
+    *(f32x4 *)cache = v;
+}
+
+// Walk C: y of a segment. Each wave of a block forms half of the block's masked
+// matrix and puts it into LDS as operand registers. One chunk is held in LDS at
+// a time: B arrives while the masked matrix is formed, C, G and the decays of
+// the next chunk while the state is updated, so that two workgroups fit a CU
+// and run out of step.
+template <int N>
+__global__ __launch_bounds__(kWalkThreads, 2) void walk_out_kernel(SsdCacheArgs a) {
+    constexpr int NT = N / 16, KB = N / 32;
+    struct Shared {
+        alignas(16) _Float16 B[kQ * N];  // the high parts
+        alignas(16) _Float16 CG[kQ * N + kQ * kQ];
+        alignas(16) float scale[2][256];  // 2^eC per token
+        alignas(16) float head[2][2][kHead];
+        alignas(16) _Float16 M[2][8][64][8];
+    };
+    __shared__ Shared sh;
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), r = lane & 15, q = lane >> 4;
+    const Unit u = find_unit(a);
+    if (!u.some) return;
+    const uint32_t from = u.from, to = u.to, H = (uint32_t)a.H, G = (uint32_t)a.G;
+    const int32_t slot = a.ws_slot[u.s];
+    const uint32_t yrow = (uint32_t)(a.H * a.P) * 2;
+    if (slot < 0) {
+        if (u.on)
+            for (uint32_t t = from + q; t < to; t += 4)
+                *(uint32_t *)((char *)a.y + (int64_t)(u.begin + t) * yrow + (u.ch0 + 2 * r) * 2) = 0u;
+        return;
+    }
+
+    // the state: acc[nt][c][e] = S[p = 2 r + c][n = 16 nt + 4 q + e] 2^-K, kept
+    // below 2^15 by its bound, so that its float16 copy needs no scale of its own
+    f32x4 acc[NT][2];
+    int K = 0;
+    float bound = 0.0f;  // of |acc|
+    const int64_t off = (int64_t)(u.ch0 + 2 * r) * N + 4 * q, hpn = a.H * a.P * N;
+    const bool resume = a.resume && a.resume[u.s] != 0, one = u.nseg == 1;
+    float *const cache = a.state_cache + (int64_t)slot * hpn + off;
+    const float *const own = a.ws_state + (int64_t)u.sid * hpn + off;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) acc[nt][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if ((resume || u.k > 0) && u.on) {
+        const float *src = one ? cache : own;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                acc[nt][c] = *(const f32x4 *)(src + c * N + 16 * nt);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) bound = __builtin_fmaxf(bound, finite_abs(acc[nt][c][e]));
+            }
+        bound = wave_top(bound);
+        if (bound > 0.0f) {
+            K = uniform(exponent(bound)) - 14;
+            bound = 0x1p14f;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[nt][c][e] = __builtin_ldexpf(acc[nt][c][e], -K);
+        }
+    }
+    const float dsk = a.Dskip ? a.Dskip[u.h] : 0.0f;
+
+    auto operands = [&](uint32_t t) {
+        return (const char *)a.ws_frag + ((int64_t)(u.chunk0 + t / kQ) * G + u.g) * (frag_elems(N) * 2);
+    };
+    auto stage = [&](uint32_t t) {  // what a chunk needs first
+        const int b = (int)((t - from) / kQ & 1);
+        const char *f = operands(t) + pieces_b(N) * 1024;
+        pieces<pieces_cg(N)>(f, sh.CG, wave, lane);
+        if (wave == 3) dma16_s(f + pieces_cg(N) * 1024, lane * 16, lds_addr(sh.scale[b]));
+        if (wave % 2 == 0 && u.on)
+            dma16_s(a.ws_head + ((int64_t)(u.chunk0 + t / kQ) * H + u.h) * kHead, lane * 16, lds_addr(sh.head[b][wave / 2]));
+    };
+    f16x8 xn[2][2];
+    auto load = [&](uint32_t t) {
+        const f16x8 *src = (const f16x8 *)a.ws_x + ((int64_t)(u.chunk0 + t / kQ) * (a.H * a.P / 32) + u.ch0 / 32) * 256 + lane;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) xn[c][hh] = src[(c * 2 + hh) * 64];
+    };
+
+    if (from < to) stage(from);
+    if (!u.on) {  // no columns: the wave only carries its share of the loads
+        for (uint32_t t = from; t < to; t += kQ) {
+            vm_wait();
+            lds_barrier();
+            pieces<pieces_b(N) / 2>(operands(t), sh.B, wave, lane);
+            vm_wait();
+            lds_barrier();
+            if (t + kQ < to) stage(t + kQ);
+        }
+    } else {
+        if (from < to) load(from);
+        for (uint32_t t = from; t < to; t += kQ) {
+            const int b = (int)((t - from) / kQ & 1);
+            const uint32_t id = u.chunk0 + t / kQ;
+            const cf32_ptr meta = (cf32_ptr)(a.ws_meta + ((int64_t)id * H + u.h) * 4);
+            const float dec = meta[0];
+            const int ew = __float_as_int(meta[1]), ed = __float_as_int(meta[2]);
+            const int eB = ((const __attribute__((address_space(4))) int *)a.ws_eb)[(int64_t)id * G + u.g];
+            const int exb = ((const __attribute__((address_space(4))) int *)a.ws_ex)[(int64_t)id * (a.H * a.P / 32) + u.ch0 / 32];
+            const bool anybad = exb >= 1 << 15;
+            const int ex = anybad ? exb - (1 << 16) : exb;
+            // The chunk's first part is in LDS and every wave is done with the
+            // chunk before. Issued since: that part, x, and 16 stores of y, which
+            // may stay in flight (accesses complete in order).
+            if (t > from) asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
+            else vm_wait();
+            lds_barrier();
+            pieces<pieces_b(N) / 2>(operands(t), sh.B, wave, lane);
+            const float *hd = sh.head[b][wave / 2];
+            const int rem = to - t < kQ ? (int)(to - t) : kQ;
+            f16x8 x16[2][2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) x16[c][hh] = xn[c][hh];
+            uint32_t badm[2] = {0u, 0u};
+            if (anybad) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const _Float16 v = x16[c][i / 8][i % 8];
+                        if (v != v) {
+                            badm[c] |= 1u << i;
+                            x16[c][i / 8][i % 8] = (_Float16)0.0f;
+                        }
+                    }
+            }
+
+            // the wave's half of the masked matrix: M[t][s] = G[t][s] exp2(cum_t - cum_s) dt_s
+            {
+                f32x4 cs[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) cs[i] = *(const f32x4 *)(hd + kQ + 16 * q + 4 * i);
+#pragma unroll
+                for (int k2 = 0; k2 < 2; ++k2) {
+                    const int tt = 2 * (wave % 2) + k2;
+                    const float ct = hd[16 * (r / 4) + r % 4 + 4 * tt];
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+                        const f16x8 gv = *(const f16x8 *)(sh.CG + kQ * N + ((tt * 2 + hh) * 64 + lane) * 8);
+                        f16x8 m;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            // G is zero above the diagonal, where the exponent may be large
+                            m[j] = (_Float16)fast_exp2(__builtin_fminf(ct - cs[2 * hh + j / 4][j % 4], 15.0f));
+                        *(f16x8 *)&sh.M[wave / 2][tt * 2 + hh][lane][0] = m * gv;
+                    }
+                }
+            }
+            // C S^T in units 2^(eC + E1), the masked product in units 2^(eC + E2)
+            const int E1 = K - 7;
+            int E2 = ex + ed + eB - 21;
+            const bool small = E1 - E2 > 60;  // nothing beside the state: the factor below stays in range
+            if (small) E2 = E1 - 60;
+            f32x4 Y[4][2];
+#pragma unroll
+            for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) Y[tt][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int m = 0; m < KB; ++m) {
+                f16x8 so[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) so[c][e] = (_Float16)acc[2 * m + e / 4][c][e % 4];
+#pragma unroll
+                for (int tt = 0; tt < 4; ++tt) {
+                    const f16x8 co = *(const f16x8 *)(sh.CG + ((tt * KB + m) * 64 + lane) * 8);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) Y[tt][c] = mfma(co, so[c], Y[tt][c]);
+                }
+            }
+            {
+                const float al = __builtin_ldexpf(1.0f, E1 - E2);
+#pragma unroll
+                for (int tt = 0; tt < 4; ++tt) {
+                    const f32x4 ec = *(const f32x4 *)(hd + 2 * kQ + 16 * q + 4 * tt) * al;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) Y[tt][c] *= ec;
+                }
+            }
+            vm_wait();
+            lds_barrier();  // M is whole, B is in LDS, and every wave is done with C and G
+            if (t + kQ < to) {
+                stage(t + kQ);
+                load(t + kQ);
+            }
+            if (!small) {
+#pragma unroll
+                for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+                        const f16x8 mo = *(const f16x8 *)&sh.M[wave / 2][tt * 2 + hh][lane][0];
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) Y[tt][c] = mfma(mo, x16[c][hh], Y[tt][c]);
+                    }
+            }
+            if (anybad) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    bool low = false;  // the channel is marked in an earlier lane's tokens
+#pragma unroll
+                    for (int d = 16; d < 64; d += 16) {
+                        const uint32_t o = __shfl(badm[c], (lane - d) & 63);
+                        low |= lane >= d && o != 0u;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (low || (badm[c] & ((2u << i) - 1))) Y[i / 4][c][i % 4] = __builtin_nanf("");
+                }
+            }
+            {
+                const float dx = __builtin_ldexpf(dsk, ex - 14);
+                const auto yb = buffer((const char *)a.y + (int64_t)(u.begin + t) * yrow + u.ch0 * 2, (rem - 1) * yrow + 64);
+                uint32_t yo = 16 * q * yrow + 4 * r;
+                asm volatile("" : "+v"(yo));
+#pragma unroll
+                for (int tt = 0; tt < 4; ++tt) {
+                    const f32x4 rv = *(const f32x4 *)(sh.scale[b] + 16 * q + 4 * tt);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int i = 4 * tt + e;
+                        const float be = __builtin_ldexpf(rv[e], E2);
+                        float o[2];
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) o[c] = __builtin_fmaf((float)x16[c][i / 8][i % 8], dx, Y[tt][c][e] * be);
+                        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, bf16x2{(__bf16)o[0], (__bf16)o[1]}), yb, yo, 0, 0);
+                        yo += yrow;
+                    }
+                }
+            }
+            // the state: x 2^-sc times w (w < 1 as stored) in units that keep
+            // dec |acc| + 64 |x w B| below 2^15
+            const int c0 = ex + ew + eB - 21;
+            int e1 = K - c0 + uniform(exponent(bound * dec));
+            e1 = e1 > 27 ? e1 : 27;
+            const int sc = e1 - 14, Kn = c0 + sc;
+            const float f = __builtin_ldexpf(dec, K - Kn < 120 ? K - Kn : 120);
+            bound = __builtin_fmaf(bound, f, __builtin_ldexpf(1.0f, 27 - sc));
+            if (!finite(bound)) bound = 0x1p14f;
+            K = Kn;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) acc[nt][c] *= f;
+            const _Float16 sf = (_Float16)__builtin_ldexpf(1.0f, sc < 24 ? -sc : -24);
+            const _Float16 sw = (_Float16)__builtin_ldexpf(1.0f, sc < 24 ? 0 : 24 - sc);
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                f16x8 wv = *(const f16x8 *)((const _Float16 *)(hd + 3 * kQ) + 16 * q + 8 * hh);
+                if (sc > 24) wv *= sw;
+                f16x8 v[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) v[c] = (x16[c][hh] * sf) * wv;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const f16x8 bh = *(const f16x8 *)(sh.B + ((hh * NT + nt) * 64 + lane) * 8);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) acc[nt][c] = mfma(bh, v[c], acc[nt][c]);
+                }
+            }
+            if (anybad) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t o = badm[c];
+                    o |= __shfl_xor(o, 16);
+                    o |= __shfl_xor(o, 32);
+                    if (o)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) acc[nt][c][e] = __builtin_nanf("");
+                }
+            }
+        }
+    }
+
+    if (u.k != u.nseg - 1) return;
+    if (u.on && one && resume) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) *(f32x4 *)(cache + c * N + 16 * nt) = *(const f32x4 *)(own + c * N + 16 * nt);
+    }
+    // the window: the last three raw rows, of the wave's channels and, once per
+    // group, of its B and C
+    auto row = [&](int t, int64_t c) {
+        return t < 0 ? a.ws_win[((int64_t)u.s * 3 + t + 3) * a.C + c]
+                     : ((const uint16_t *)a.xBC)[(int64_t)(u.begin + t) * a.xBC_stride + c];
+    };
+    uint16_t *win = (uint16_t *)a.conv_cache + (int64_t)slot * a.C * 3;
+    if (u.on && q < 3)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) win[(int64_t)(u.ch0 + 2 * r + c) * 3 + q] = row((int)u.len - 3 + q, u.ch0 + 2 * r + c);
+    if (u.hb == 0)
+        for (int i = threadIdx.x; i < 2 * N * 3; i += kWalkThreads) {
+            const int n = i / 3;
+            const int64_t c = a.H * a.P + ((n / N) * a.G + u.g) * N + n % N;
+            win[c * 3 + i % 3] = row((int)u.len - 3 + i % 3, c);
+        }
 }
 
 template <int N>
 hipError_t launch_n(const SsdCacheArgs &a, hipStream_t s) {
-    const int64_t parts = (a.C + kPrepThreads - 1) / kPrepThreads;
-    hipLaunchKernelGGL((prepare_kernel<N>), dim3((unsigned)(a.nchunk * a.G + a.seqs * parts)), dim3(kPrepThreads), 0, s, a);
+    const int64_t parts = (a.C + kPrepThreads - 1) / kPrepThreads, dts = (a.H + kDtHeads - 1) / kDtHeads;
+    hipLaunchKernelGGL((prepare_kernel<N>), dim3((unsigned)(a.nchunk * (a.G + dts) + a.seqs * parts)), dim3(kPrepThreads), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t ncb = a.H / a.G * (a.P / 64), units = a.nseg * a.G * ((ncb + 1) / 2);
     const dim3 grid((unsigned)((units + 7) / 8 * 8));
+    hipLaunchKernelGGL((walk_state_kernel<N>), grid, dim3(kWalkThreads), 0, s, a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
     if (a.rows > a.seg) {  // some sequence may be longer than a segment
-        hipLaunchKernelGGL((walk_kernel<N, false>), grid, dim3(kWalkThreads), 0, s, a);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
         hipLaunchKernelGGL(join_kernel, dim3((unsigned)((a.H * a.P * N + 1023) / 1024), (unsigned)a.seqs), dim3(256), 0, s, a, N);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((walk_kernel<N, true>), grid, dim3(kWalkThreads), 0, s, a);
+    hipLaunchKernelGGL((walk_out_kernel<N>), grid, dim3(kWalkThreads), 0, s, a);
     return hipGetLastError();
 }
 
@@ -864,15 +1075,18 @@ size_t plan(SsdCacheArgs &a, int N, char *base) {
     a.seg = segment_tokens(a.rows, a.H, a.P, a.G);
     a.nchunk = a.rows / kQ + a.seqs;
     a.nseg = a.rows / a.seg + a.seqs;
-    const int64_t kept = a.rows / a.seg;
+    const size_t chunks = (size_t)a.nchunk;
     a.ws_slot = (int32_t *)take((size_t)a.seqs * 4);
     a.ws_win = (uint16_t *)take((size_t)a.seqs * 3 * a.C * 2);
-    a.ws_frag = take((size_t)(a.nchunk * a.G) * frag_elems(N) * 2);
-    a.ws_head = (float *)take((size_t)(a.nchunk * a.H) * kHead * 4);
-    a.ws_meta = (float *)take((size_t)(a.nchunk * a.H) * 16);
-    a.ws_eb = (int32_t *)take((size_t)(a.nchunk * a.G) * 4);
-    a.ws_state = (float *)take((size_t)kept * a.H * a.P * N * 4);
-    a.ws_segdec = (float *)take((size_t)kept * a.H * 4);
+    a.ws_frag = take(chunks * a.G * frag_elems(N) * 2);
+    a.ws_head = (float *)take(chunks * a.H * kHead * 4);
+    a.ws_w = (float *)take(chunks * a.H * kQ * 4 + 1024);  // read four heads at a time
+    a.ws_meta = (float *)take(chunks * a.H * 16);
+    a.ws_eb = (int32_t *)take(chunks * a.G * 4);
+    a.ws_ex = (int32_t *)take(chunks * (a.H * a.P / 32) * 4);
+    a.ws_x = take(chunks * (a.H * a.P / 32) * 4096);
+    a.ws_state = (float *)take((size_t)a.nseg * a.H * a.P * N * 4);
+    a.ws_segdec = (float *)take((size_t)a.nseg * a.H * 4);
     return at;
 }
 
