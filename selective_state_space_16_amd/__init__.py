@@ -694,31 +694,72 @@ def ssm_norm_bwd_workspace_bytes(rows: int, D: int) -> int:
     return int(lib().ssm_norm_bwd_workspace_bytes(rows, D))
 
 
-def _rows(t, name, dtype, shape):
-    """Device pointer and row stride (elements) of a 2-D GPU tensor whose rows
-    are dense but may lie apart (a slice of a wider one)."""
+def _refuse(t, name, device, dtype, shape):
+    """The error for a tensor that _arg or _rows does not take."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if shape[1] > 1 and t.stride(1) != 1:
+    if t.get_device() != device:
+        raise ValueError(f"every tensor must be on cuda:{device}, {name} is on {t.device}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _arg(t, name, device, dtype, shape):
+    """Device pointer of a contiguous tensor on GPU number `device` (None ->
+    NULL). One short test on the way of a correct call: a decode step's launches
+    take less time than a row of separate checks."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, name, device, dtype, shape)
+
+
+def _rows(t, name, device, dtype, shape):
+    """Device pointer and row stride (elements) of a 2-D tensor whose rows are
+    dense but may lie apart (a slice of a wider one)."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
+        _refuse(t, name, device, dtype, shape)
+    rs, cs = t.stride()
+    if shape[1] > 1 and cs != 1:
         raise ValueError(f"the rows of {name} must be contiguous")
     # with one row the stride is never used: any allowed one
-    return t.data_ptr(), (t.stride(0) if shape[0] > 1 else -(-shape[1] // 8) * 8)
+    return t.data_ptr(), (rs if shape[0] > 1 else -(-shape[1] // 8) * 8)
 
 
-def _call(name, on, tensors, stream, allocated, *args):
-    """Launch on the device of `on` (which need not be the current one), on its
+def _bytes(workspace, device):
+    """Pointer and size of a workspace tensor on GPU number `device`."""
+    if workspace.get_device() != device or not workspace.is_contiguous():
+        _refuse(workspace, "workspace", device, workspace.dtype, workspace.shape)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _gpu(t, name):
+    """The number of the GPU a tensor is on."""
+    device = t.get_device()
+    if device < 0:
+        raise ValueError(f"{name} must be a GPU tensor")
+    return device
+
+
+def _call(name, device, stream, allocated, *args):
+    """Launch on GPU number `device` (which need not be the current one), on its
     current stream unless one is given."""
     import torch
-    for t in tensors:
-        if t is not None and t.device != on.device:
-            raise ValueError(f"every tensor must be on {on.device}, got one on {t.device}")
-    with torch.cuda.device(on.device):
-        _order_after_alloc(stream, allocated)
-        st = getattr(lib(), name)(*args, _stream(stream))
+    fn = getattr(lib(), name)
+    if device == torch._C._cuda_getDevice():
+        if stream is None:
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(device))
+        else:
+            _order_after_alloc(stream, allocated)
+            st = fn(*args, _stream(stream))
+    else:
+        with torch.cuda.device(device):
+            _order_after_alloc(stream, allocated)
+            st = fn(*args, _stream(stream))
     if st != 0:
         raise SSMError(st, name)
 
@@ -739,31 +780,32 @@ def _ssd_cache(name, xBC, dt_raw, A, conv_w, cu_seqlens, slots, conv_cache, stat
     prompt = name == "ssm_ssd_fwd_cache"
     if not prompt and rows != seqs:
         raise ValueError(f"one row per request: {rows} rows, {seqs} slots")
-    x_ptr, x_stride = _rows(xBC, "xBC", act, (rows, C))
-    dt_ptr, dt_stride = _rows(dt_raw, "dt_raw", act, (rows, H))
+    dev = _gpu(xBC, "xBC")
+    x_ptr, x_stride = _rows(xBC, "xBC", dev, act, (rows, C))
+    dt_ptr, dt_stride = _rows(dt_raw, "dt_raw", dev, act, (rows, H))
     allocated = []
     if y is None:
         # rows outside every sequence are not written
         y = torch.zeros((rows, H, P), dtype=act, device=xBC.device) if prompt else torch.empty(
             (rows, H, P), dtype=act, device=xBC.device)
         allocated.append(y)
-    need = ssm_ssd_fwd_cache_workspace_bytes(seqs, rows, H, P, G, N, code) if prompt else \
-        ssm_ssd_step_cache_workspace_bytes(seqs, H, P, G, N)
     if workspace is None:
+        need = ssm_ssd_fwd_cache_workspace_bytes(seqs, rows, H, P, G, N, code) if prompt else \
+            ssm_ssd_step_cache_workspace_bytes(seqs, H, P, G, N)
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=xBC.device)
         allocated.append(workspace)
-    sizes = [seqs, rows, H, P, G, N, code] if prompt else [seqs, H, P, G, N, code]
-    args = [_ptr(cu_seqlens, "cu_seqlens", i32, (seqs + 1,))] if prompt else []
-    args.append(_ptr(slots, "slots", i32, (seqs,)))
+    args = [seqs, rows, H, P, G, N, code] if prompt else [seqs, H, P, G, N, code]
     if prompt:
-        args.append(_ptr(resume, "resume", i32, (seqs,)))
-    args += [num_slots, x_ptr, x_stride, _ptr(conv_w, "conv_w", f32, (C, 4)), _ptr(conv_b, "conv_b", f32, (C,)),
-             dt_ptr, dt_stride, _ptr(dt_bias, "dt_bias", f32, (H,)), _ptr(A, "A", f32, (H,)),
-             _ptr(Dskip, "Dskip", f32, (H,)), _ptr(conv_cache, "conv_cache", act, (num_slots, C, 3)),
-             _ptr(state_cache, "state_cache", f32, (num_slots, H, P, N)), _ptr(y, "y", act, (rows, H, P)),
-             _ptr(workspace, "workspace"), workspace.numel() * workspace.element_size()]
-    _call(name, xBC, (dt_raw, A, conv_w, cu_seqlens, slots, conv_cache, state_cache, conv_b, dt_bias, Dskip, resume, y,
-                      workspace), stream, allocated, *sizes, *args)
+        args.append(_arg(cu_seqlens, "cu_seqlens", dev, i32, (seqs + 1,)))
+    args.append(_arg(slots, "slots", dev, i32, (seqs,)))
+    if prompt:
+        args.append(_arg(resume, "resume", dev, i32, (seqs,)))
+    _call(name, dev, stream, allocated, *args, num_slots, x_ptr, x_stride, _arg(conv_w, "conv_w", dev, f32, (C, 4)),
+          _arg(conv_b, "conv_b", dev, f32, (C,)), dt_ptr, dt_stride, _arg(dt_bias, "dt_bias", dev, f32, (H,)),
+          _arg(A, "A", dev, f32, (H,)), _arg(Dskip, "Dskip", dev, f32, (H,)),
+          _arg(conv_cache, "conv_cache", dev, act, (num_slots, C, 3)),
+          _arg(state_cache, "state_cache", dev, f32, (num_slots, H, P, N)), _arg(y, "y", dev, act, (rows, H, P)),
+          *_bytes(workspace, dev))
     return y
 
 
@@ -806,7 +848,7 @@ def ssm_add_norm_fwd(x, weight, residual=None, scale=None, eps=1e-5, y=None, res
         raise ValueError("x must be (rows, D)")
     rows, D = x.shape
     act, f32 = x.dtype, torch.float32
-    code = _dtype_code(x)
+    code, dev = _dtype_code(x), _gpu(x, "x")
     allocated = []
     if y is None:
         y = torch.empty_like(x)
@@ -814,11 +856,11 @@ def ssm_add_norm_fwd(x, weight, residual=None, scale=None, eps=1e-5, y=None, res
     if residual_out is None:
         residual_out = torch.empty((rows, D), dtype=f32 if residual is None else residual.dtype, device=x.device)
         allocated.append(residual_out)
-    rcode = _res_code(residual_out, act)
-    _call("ssm_add_norm_fwd", x, (weight, residual, scale, y, residual_out), stream, allocated, rows, D, code, rcode,
-          _ptr(x, "x", act), _ptr(residual, "residual", residual_out.dtype, (rows, D)),
-          _ptr(scale, "scale", f32, (D,)), _ptr(weight, "weight", f32, (D,)), float(eps), _ptr(y, "y", act, (rows, D)),
-          _ptr(residual_out, "residual_out", residual_out.dtype, (rows, D)))
+    rcode, rt, shape = _res_code(residual_out, act), residual_out.dtype, (rows, D)
+    _call("ssm_add_norm_fwd", dev, stream, allocated, rows, D, code, rcode, _arg(x, "x", dev, act, shape),
+          _arg(residual, "residual", dev, rt, shape), _arg(scale, "scale", dev, f32, (D,)),
+          _arg(weight, "weight", dev, f32, (D,)), float(eps), _arg(y, "y", dev, act, shape),
+          _arg(residual_out, "residual_out", dev, rt, shape))
     return y, residual_out
 
 
@@ -832,23 +874,29 @@ def ssm_add_norm_bwd(dy, r, weight, x=None, scale=None, dres=None, eps=1e-5, out
         raise ValueError("dy must be (rows, D)")
     rows, D = dy.shape
     act, f32 = dy.dtype, torch.float32
-    code, rcode = _dtype_code(dy), _res_code(r, dy.dtype)
+    code, rcode, rt, dev = _dtype_code(dy), _res_code(r, act), r.dtype, _gpu(dy, "dy")
     o = dict(out or {})
-    given = set(o)
-    o.setdefault("dx", torch.empty_like(dy))
-    o.setdefault("dresidual", torch.empty_like(r))
-    o.setdefault("dweight", torch.empty((D,), dtype=f32, device=dy.device))
-    o.setdefault("dscale", None if scale is None else torch.empty((D,), dtype=f32, device=dy.device))
-    allocated = [v for k, v in o.items() if k not in given and v is not None]
+    allocated = []
+
+    def new(key, make):
+        if key not in o:
+            o[key] = make()
+            allocated.append(o[key])
+        return o[key]
+
+    dx, dr = new("dx", lambda: torch.empty_like(dy)), new("dresidual", lambda: torch.empty_like(r))
+    dw = new("dweight", lambda: torch.empty((D,), dtype=f32, device=dy.device))
+    ds = new("dscale", lambda: torch.empty((D,), dtype=f32, device=dy.device)) if scale is not None else \
+        o.setdefault("dscale", None)
     if workspace is None:
         workspace = torch.empty(max(ssm_norm_bwd_workspace_bytes(rows, D), 16), dtype=torch.uint8, device=dy.device)
         allocated.append(workspace)
-    _call("ssm_add_norm_bwd", dy, (r, weight, x, scale, dres, workspace, *o.values()), stream, allocated, rows, D, code,
-          rcode, _ptr(dy, "dy", act), _ptr(r, "r", r.dtype, (rows, D)), _ptr(weight, "weight", f32, (D,)),
-          _ptr(x, "x", act, (rows, D)), _ptr(scale, "scale", f32, (D,)), _ptr(dres, "dres", r.dtype, (rows, D)),
-          float(eps), _ptr(o["dx"], "dx", act, (rows, D)), _ptr(o["dresidual"], "dresidual", r.dtype, (rows, D)),
-          _ptr(o["dweight"], "dweight", f32, (D,)), _ptr(o["dscale"], "dscale", f32, (D,)),
-          _ptr(workspace, "workspace"), workspace.numel() * workspace.element_size())
+    shape = (rows, D)
+    _call("ssm_add_norm_bwd", dev, stream, allocated, rows, D, code, rcode, _arg(dy, "dy", dev, act, shape),
+          _arg(r, "r", dev, rt, shape), _arg(weight, "weight", dev, f32, (D,)), _arg(x, "x", dev, act, shape),
+          _arg(scale, "scale", dev, f32, (D,)), _arg(dres, "dres", dev, rt, shape), float(eps),
+          _arg(dx, "dx", dev, act, shape), _arg(dr, "dresidual", dev, rt, shape), _arg(dw, "dweight", dev, f32, (D,)),
+          _arg(ds, "dscale", dev, f32, (D,)), *_bytes(workspace, dev))
     return o
 
 
@@ -862,14 +910,15 @@ def ssm_gate_norm_fwd(x, z, weight, groups=1, eps=1e-5, y=None, stream=None):
     rows, D = x.shape
     act, f32 = x.dtype, torch.float32
     code = _dtype_code(x)
-    x_ptr, x_stride = _rows(x, "x", act, (rows, D))
-    z_ptr, z_stride = _rows(z, "z", act, (rows, D))
+    dev, shape = _gpu(x, "x"), (rows, D)
+    x_ptr, x_stride = _rows(x, "x", dev, act, shape)
+    z_ptr, z_stride = _rows(z, "z", dev, act, shape)
     allocated = []
     if y is None:
-        y = torch.empty((rows, D), dtype=act, device=x.device)
+        y = torch.empty(shape, dtype=act, device=x.device)
         allocated.append(y)
-    _call("ssm_gate_norm_fwd", x, (z, weight, y), stream, allocated, rows, D, int(groups), code, x_ptr, x_stride, z_ptr,
-          z_stride, _ptr(weight, "weight", f32, (D,)), float(eps), _ptr(y, "y", act, (rows, D)))
+    _call("ssm_gate_norm_fwd", dev, stream, allocated, rows, D, int(groups), code, x_ptr, x_stride, z_ptr, z_stride,
+          _arg(weight, "weight", dev, f32, (D,)), float(eps), _arg(y, "y", dev, act, shape))
     return y
 
 
@@ -882,21 +931,21 @@ def ssm_gate_norm_bwd(dy, x, z, weight, groups=1, eps=1e-5, out=None, workspace=
         raise ValueError("dy must be (rows, D)")
     rows, D = dy.shape
     act, f32 = dy.dtype, torch.float32
-    code = _dtype_code(dy)
+    code, dev, shape = _dtype_code(dy), _gpu(dy, "dy"), (rows, D)
     o = dict(out or {})
-    given = set(o)
-    o.setdefault("dx", torch.empty_like(dy))
-    o.setdefault("dz", torch.empty_like(dy))
-    o.setdefault("dweight", torch.empty((D,), dtype=f32, device=dy.device))
-    allocated = [v for k, v in o.items() if k not in given]
+    allocated = []
+    for key, like in (("dx", dy), ("dz", dy), ("dweight", weight)):
+        if key not in o:
+            o[key] = torch.empty_like(like)
+            allocated.append(o[key])
     if workspace is None:
         workspace = torch.empty(max(ssm_norm_bwd_workspace_bytes(rows, D), 16), dtype=torch.uint8, device=dy.device)
         allocated.append(workspace)
-    x_ptr, x_stride = _rows(x, "x", act, (rows, D))
-    z_ptr, z_stride = _rows(z, "z", act, (rows, D))
-    dz_ptr, dz_stride = _rows(o["dz"], "dz", act, (rows, D))
-    _call("ssm_gate_norm_bwd", dy, (x, z, weight, workspace, *o.values()), stream, allocated, rows, D, int(groups), code,
-          _ptr(dy, "dy", act), x_ptr, x_stride, z_ptr, z_stride, _ptr(weight, "weight", f32, (D,)), float(eps),
-          _ptr(o["dx"], "dx", act, (rows, D)), dz_ptr, dz_stride, _ptr(o["dweight"], "dweight", f32, (D,)),
-          _ptr(workspace, "workspace"), workspace.numel() * workspace.element_size())
+    x_ptr, x_stride = _rows(x, "x", dev, act, shape)
+    z_ptr, z_stride = _rows(z, "z", dev, act, shape)
+    dz_ptr, dz_stride = _rows(o["dz"], "dz", dev, act, shape)
+    _call("ssm_gate_norm_bwd", dev, stream, allocated, rows, D, int(groups), code, _arg(dy, "dy", dev, act, shape), x_ptr,
+          x_stride, z_ptr, z_stride, _arg(weight, "weight", dev, f32, (D,)), float(eps),
+          _arg(o["dx"], "dx", dev, act, shape), dz_ptr, dz_stride, _arg(o["dweight"], "dweight", dev, f32, (D,)),
+          *_bytes(workspace, dev))
     return o
