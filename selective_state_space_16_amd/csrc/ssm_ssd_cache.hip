@@ -53,8 +53,8 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kQ = 64;            // tokens per chunk
 constexpr int kPrepThreads = 256;
-constexpr int kWaves = 4;         // waves per workgroup of a walk: two column blocks of 64, two waves each
-constexpr int kWalkThreads = 64 * kWaves;
+constexpr int kBlocksA = 2;       // column blocks of 64 per workgroup of walk A, two waves each
+constexpr int kBlocksC = 4;       // of walk C
 
 // Workspace of one (chunk, group), in float16 elements: B high, B low and C as
 // operand registers (lane-major), G as operand registers, 2^eC per token
@@ -379,7 +379,7 @@ __global__ __launch_bounds__(kPrepThreads) void prepare_kernel(SsdCacheArgs a) {
 
 // ---------------------------------------------------------------------- walks
 
-// What a workgroup of a walk works on: one segment of one sequence, and two
+// What a workgroup of a walk works on: one segment of one sequence, and BLOCKS
 // column blocks (64 rows of a head's state each) of one group; two waves share a
 // block, 32 columns each. Lane (r, q) = (l % 16, l / 16) holds the channels p =
 // 2 r + c of the wave's 32 for the tokens 16 q + i of a chunk: what the 16 x 16
@@ -392,6 +392,7 @@ struct Unit {
     bool some;  // there is anything to do
 };
 
+template <int BLOCKS>
 __device__ __forceinline__ Unit find_unit(const SsdCacheArgs &a) {
     Unit u;
     u.some = false;
@@ -400,7 +401,7 @@ __device__ __forceinline__ Unit find_unit(const SsdCacheArgs &a) {
     // the work (the column blocks of one segment, which load the same B, C and
     // G) go to one XCD and its L2.
     const uint32_t P = (uint32_t)a.P, pb = P / 64, G = (uint32_t)a.G, hpg = (uint32_t)a.H / G, seg = (uint32_t)a.seg;
-    const uint32_t ncb = hpg * pb, nhb = (ncb + 1) / 2;
+    const uint32_t ncb = hpg * pb, nhb = (ncb + BLOCKS - 1) / BLOCKS;
     const uint32_t total = (uint32_t)a.nseg * G * nhb, per = (total + 7) / 8;
     const uint32_t unit = blockIdx.x % 8 * per + blockIdx.x / 8;
     if (unit >= total) return u;
@@ -416,9 +417,9 @@ __device__ __forceinline__ Unit find_unit(const SsdCacheArgs &a) {
     if (u.k >= u.nseg) return u;
     u.from = u.k * seg;
     u.to = u.len - u.from < seg ? u.len : u.from + seg;
-    const uint32_t cb = u.hb * 2 + wave / 2;
+    const uint32_t cb = u.hb * BLOCKS + wave / 2;
     u.on = cb < ncb;
-    u.hfirst = u.g * hpg + u.hb * 2 / pb;
+    u.hfirst = u.g * hpg + u.hb * BLOCKS / pb;
     u.h = u.g * hpg + (u.on ? cb / pb : 0);
     u.ch0 = u.h * P + (u.on ? cb % pb : 0) * 64 + 32 * (wave % 2);  // the wave's first channel
     u.chunk0 = u.begin / kQ + u.s;
@@ -427,12 +428,12 @@ __device__ __forceinline__ Unit find_unit(const SsdCacheArgs &a) {
 }
 
 // Pieces of 1 KiB from `src` straight into LDS, dealt to the waves in turn.
-template <int PIECES>
+template <int PIECES, int WAVES>
 __device__ __forceinline__ void pieces(const void *src, const void *to_lds, int wave, int lane) {
     const uint32_t dst = lds_addr(to_lds);
 #pragma unroll
-    for (int i = 0; i < (PIECES + kWaves - 1) / kWaves; ++i) {
-        const int p = i * kWaves + wave;
+    for (int i = 0; i < (PIECES + WAVES - 1) / WAVES; ++i) {
+        const int p = i * WAVES + wave;
         if (p < PIECES) dma16_s((const char *)src + p * 1024, lane * 16, dst + p * 1024);
     }
 }
@@ -444,7 +445,7 @@ constexpr int pieces_cg(int N) { return (kQ * N + kQ * kQ) / 512; }
 // convolution and SiLU, the splitting of operands); the products run beside it.
 // B of two chunks is held in LDS, so that two workgroups share a CU.
 template <int N>
-__global__ __launch_bounds__(kWalkThreads, 2) void walk_state_kernel(SsdCacheArgs a) {
+__global__ __launch_bounds__(128 * kBlocksA, 2) void walk_state_kernel(SsdCacheArgs a) {
     constexpr int NT = N / 16;
     struct Shared {
         alignas(16) _Float16 B[2][2 * kQ * N];
@@ -452,7 +453,7 @@ __global__ __launch_bounds__(kWalkThreads, 2) void walk_state_kernel(SsdCacheArg
     };
     __shared__ Shared sh;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), r = lane & 15, q = lane >> 4;
-    const Unit u = find_unit(a);
+    const Unit u = find_unit<kBlocksA>(a);
     if (!u.some) return;
     const int32_t slot = a.ws_slot[u.s];
     if (slot < 0) return;
@@ -536,7 +537,7 @@ __global__ __launch_bounds__(kWalkThreads, 2) void walk_state_kernel(SsdCacheArg
     auto stage = [&](uint32_t t) {
         const int b = (int)((t - from) / kQ & 1);
         const uint32_t id = u.chunk0 + t / kQ;
-        pieces<pieces_b(N)>((const char *)a.ws_frag + ((int64_t)id * G + u.g) * (frag_elems(N) * 2), sh.B[b], wave, lane);
+        pieces<pieces_b(N), 2 * kBlocksA>((const char *)a.ws_frag + ((int64_t)id * G + u.g) * (frag_elems(N) * 2), sh.B[b], wave, lane);
         // w of four heads, the first two or all of them needed
         if (wave == 0) dma16_s(a.ws_w + ((int64_t)id * H + u.hfirst) * kQ, lane * 16, lds_addr(sh.w[b]));
     };
@@ -724,24 +725,25 @@ __global__ __launch_bounds__(256) void join_kernel(SsdCacheArgs a, int N) {
     *(f32x4 *)cache = v;
 }
 
-// Walk C: y of a segment. Each wave of a block forms half of the block's masked
-// matrix and puts it into LDS as operand registers. One chunk is held in LDS at
-// a time: B arrives while the masked matrix is formed, C, G and the decays of
-// the next chunk while the state is updated, so that two workgroups fit a CU
-// and run out of step.
+// Walk C: y of a segment. The two waves of a block each form half of the block's
+// masked matrix and put it into LDS as operand registers. An iteration finishes
+// one chunk (the masked product, y, the state) and begins the next one (C S^T and
+// the masked matrix), so that one barrier per chunk is enough and products and
+// vector instructions of both stand side by side; B, C, G and the decays are
+// held twice and loaded a whole iteration ahead. One workgroup fills a CU.
 template <int N>
-__global__ __launch_bounds__(kWalkThreads, 2) void walk_out_kernel(SsdCacheArgs a) {
-    constexpr int NT = N / 16, KB = N / 32;
+__global__ __launch_bounds__(128 * kBlocksC, 2) void walk_out_kernel(SsdCacheArgs a) {
+    constexpr int NT = N / 16, KB = N / 32, WAVES = 2 * kBlocksC;
     struct Shared {
-        alignas(16) _Float16 B[kQ * N];  // the high parts
-        alignas(16) _Float16 CG[kQ * N + kQ * kQ];
-        alignas(16) float scale[2][256];  // 2^eC per token
-        alignas(16) float head[2][2][kHead];
-        alignas(16) _Float16 M[2][8][64][8];
+        alignas(16) _Float16 B[2][kQ * N];  // the high parts
+        alignas(16) _Float16 CG[2][kQ * N + kQ * kQ];
+        alignas(16) float scale[3][256];  // 2^eC per token
+        alignas(16) float head[3][kBlocksC][kHead];
+        alignas(16) _Float16 M[2][kBlocksC][8][64][8];
     };
     __shared__ Shared sh;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), r = lane & 15, q = lane >> 4;
-    const Unit u = find_unit(a);
+    const Unit u = find_unit<kBlocksC>(a);
     if (!u.some) return;
     const uint32_t from = u.from, to = u.to, H = (uint32_t)a.H, G = (uint32_t)a.G;
     const int32_t slot = a.ws_slot[u.s];
@@ -753,186 +755,214 @@ __global__ __launch_bounds__(kWalkThreads, 2) void walk_out_kernel(SsdCacheArgs 
         return;
     }
 
+    auto operands = [&](uint32_t t) {
+        return (const char *)a.ws_frag + ((int64_t)(u.chunk0 + t / kQ) * G + u.g) * (frag_elems(N) * 2);
+    };
+    auto stage_b = [&](uint32_t t) {
+        pieces<pieces_b(N) / 2, WAVES>(operands(t), sh.B[(t - from) / kQ & 1], wave, lane);
+    };
+    auto stage_cg = [&](uint32_t t) {
+        const uint32_t i = (t - from) / kQ, i3 = i % 3;
+        const char *f = operands(t) + pieces_b(N) * 1024;
+        pieces<pieces_cg(N), WAVES>(f, sh.CG[i & 1], wave, lane);
+        if (wave == WAVES - 1) dma16_s(f + pieces_cg(N) * 1024, lane * 16, lds_addr(sh.scale[i3]));
+        if (wave % 2 == 0 && u.on)
+            dma16_s(a.ws_head + ((int64_t)(u.chunk0 + t / kQ) * H + u.h) * kHead, lane * 16, lds_addr(sh.head[i3][wave / 2]));
+    };
+    if (from < to) {
+        stage_b(from);
+        stage_cg(from);
+        if (from + kQ < to) stage_cg(from + kQ);
+    }
+    if (!u.on) {  // no columns: the wave only carries its share of the loads
+        if (from < to) {
+            vm_wait();
+            lds_barrier();
+        }
+        for (uint32_t t = from; t < to; t += kQ) {
+            vm_wait();
+            lds_barrier();
+            if (t + kQ < to) stage_b(t + kQ);
+            if (t + 2 * kQ < to) stage_cg(t + 2 * kQ);
+        }
+    }
+
     // the state: acc[nt][c][e] = S[p = 2 r + c][n = 16 nt + 4 q + e] 2^-K, kept
     // below 2^15 by its bound, so that its float16 copy needs no scale of its own
-    f32x4 acc[NT][2];
-    int K = 0;
-    float bound = 0.0f;  // of |acc|
     const int64_t off = (int64_t)(u.ch0 + 2 * r) * N + 4 * q, hpn = a.H * a.P * N;
     const bool resume = a.resume && a.resume[u.s] != 0, one = u.nseg == 1;
     float *const cache = a.state_cache + (int64_t)slot * hpn + off;
     const float *const own = a.ws_state + (int64_t)u.sid * hpn + off;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) acc[nt][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    if ((resume || u.k > 0) && u.on) {
-        const float *src = one ? cache : own;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                acc[nt][c] = *(const f32x4 *)(src + c * N + 16 * nt);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) bound = __builtin_fmaxf(bound, finite_abs(acc[nt][c][e]));
-            }
-        bound = wave_top(bound);
-        if (bound > 0.0f) {
-            K = uniform(exponent(bound)) - 14;
-            bound = 0x1p14f;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[nt][c][e] = __builtin_ldexpf(acc[nt][c][e], -K);
-        }
-    }
-    const float dsk = a.Dskip ? a.Dskip[u.h] : 0.0f;
-
-    auto operands = [&](uint32_t t) {
-        return (const char *)a.ws_frag + ((int64_t)(u.chunk0 + t / kQ) * G + u.g) * (frag_elems(N) * 2);
-    };
-    auto stage = [&](uint32_t t) {  // what a chunk needs first
-        const int b = (int)((t - from) / kQ & 1);
-        const char *f = operands(t) + pieces_b(N) * 1024;
-        pieces<pieces_cg(N)>(f, sh.CG, wave, lane);
-        if (wave == 3) dma16_s(f + pieces_cg(N) * 1024, lane * 16, lds_addr(sh.scale[b]));
-        if (wave % 2 == 0 && u.on)
-            dma16_s(a.ws_head + ((int64_t)(u.chunk0 + t / kQ) * H + u.h) * kHead, lane * 16, lds_addr(sh.head[b][wave / 2]));
-    };
-    f16x8 xn[2][2];
-    auto load = [&](uint32_t t) {
-        const f16x8 *src = (const f16x8 *)a.ws_x + ((int64_t)(u.chunk0 + t / kQ) * (a.H * a.P / 32) + u.ch0 / 32) * 256 + lane;
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) xn[c][hh] = src[(c * 2 + hh) * 64];
-    };
-
-    if (from < to) stage(from);
-    if (!u.on) {  // no columns: the wave only carries its share of the loads
-        for (uint32_t t = from; t < to; t += kQ) {
-            vm_wait();
-            lds_barrier();
-            pieces<pieces_b(N) / 2>(operands(t), sh.B, wave, lane);
-            vm_wait();
-            lds_barrier();
-            if (t + kQ < to) stage(t + kQ);
-        }
-    } else {
-        if (from < to) load(from);
-        for (uint32_t t = from; t < to; t += kQ) {
-            const int b = (int)((t - from) / kQ & 1);
-            const uint32_t id = u.chunk0 + t / kQ;
-            const cf32_ptr meta = (cf32_ptr)(a.ws_meta + ((int64_t)id * H + u.h) * 4);
-            const float dec = meta[0];
-            const int ew = __float_as_int(meta[1]), ed = __float_as_int(meta[2]);
-            const int eB = ((const __attribute__((address_space(4))) int *)a.ws_eb)[(int64_t)id * G + u.g];
-            const int exb = ((const __attribute__((address_space(4))) int *)a.ws_ex)[(int64_t)id * (a.H * a.P / 32) + u.ch0 / 32];
-            const bool anybad = exb >= 1 << 15;
-            const int ex = anybad ? exb - (1 << 16) : exb;
-            // The chunk's first part is in LDS and every wave is done with the
-            // chunk before. Issued since: that part, x, and 16 stores of y, which
-            // may stay in flight (accesses complete in order).
-            if (t > from) asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
-            else vm_wait();
-            lds_barrier();
-            pieces<pieces_b(N) / 2>(operands(t), sh.B, wave, lane);
-            const float *hd = sh.head[b][wave / 2];
-            const int rem = to - t < kQ ? (int)(to - t) : kQ;
-            f16x8 x16[2][2];
+    if (u.on && from < to) {
+        f32x4 acc[NT][2];
+        int K = 0;
+        float bound = 0.0f;  // of |acc|
+        f16x8 xn[2][2];
+        auto load = [&](uint32_t t) {
+            const f16x8 *src = (const f16x8 *)a.ws_x + ((int64_t)(u.chunk0 + t / kQ) * (a.H * a.P / 32) + u.ch0 / 32) * 256 + lane;
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
-                for (int hh = 0; hh < 2; ++hh) x16[c][hh] = xn[c][hh];
-            uint32_t badm[2] = {0u, 0u};
-            if (anybad) {
+                for (int hh = 0; hh < 2; ++hh) xn[c][hh] = src[(c * 2 + hh) * 64];
+        };
+        load(from);
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const _Float16 v = x16[c][i / 8][i % 8];
-                        if (v != v) {
-                            badm[c] |= 1u << i;
-                            x16[c][i / 8][i % 8] = (_Float16)0.0f;
-                        }
-                    }
-            }
-
-            // the wave's half of the masked matrix: M[t][s] = G[t][s] exp2(cum_t - cum_s) dt_s
-            {
-                f32x4 cs[4];
+            for (int c = 0; c < 2; ++c) acc[nt][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (resume || u.k > 0) {
+            const float *src = one ? cache : own;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) cs[i] = *(const f32x4 *)(hd + kQ + 16 * q + 4 * i);
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int k2 = 0; k2 < 2; ++k2) {
-                    const int tt = 2 * (wave % 2) + k2;
-                    const float ct = hd[16 * (r / 4) + r % 4 + 4 * tt];
+                for (int c = 0; c < 2; ++c) {
+                    acc[nt][c] = *(const f32x4 *)(src + c * N + 16 * nt);
 #pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        const f16x8 gv = *(const f16x8 *)(sh.CG + kQ * N + ((tt * 2 + hh) * 64 + lane) * 8);
-                        f16x8 m;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            // G is zero above the diagonal, where the exponent may be large
-                            m[j] = (_Float16)fast_exp2(__builtin_fminf(ct - cs[2 * hh + j / 4][j % 4], 15.0f));
-                        *(f16x8 *)&sh.M[wave / 2][tt * 2 + hh][lane][0] = m * gv;
-                    }
+                    for (int e = 0; e < 4; ++e) bound = __builtin_fmaxf(bound, finite_abs(acc[nt][c][e]));
                 }
+            bound = wave_top(bound);
+            if (bound > 0.0f) {
+                K = uniform(exponent(bound)) - 14;
+                bound = 0x1p14f;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[nt][c][e] = __builtin_ldexpf(acc[nt][c][e], -K);
             }
+        }
+        const float dsk = a.Dskip ? a.Dskip[u.h] : 0.0f;
+
+        // What a chunk is begun with: its exponents and its decay over all.
+        float dec, decn;
+        int ew, ewn, ed, edn, eB, eBn, exb, exbn;
+        auto scalars = [&](uint32_t t) {
+            const uint32_t id = u.chunk0 + t / kQ;
+            const cf32_ptr meta = (cf32_ptr)(a.ws_meta + ((int64_t)id * H + u.h) * 4);
+            decn = meta[0];
+            ewn = __float_as_int(meta[1]), edn = __float_as_int(meta[2]);
+            eBn = ((const __attribute__((address_space(4))) int *)a.ws_eb)[(int64_t)id * G + u.g];
+            exbn = ((const __attribute__((address_space(4))) int *)a.ws_ex)[(int64_t)id * (a.H * a.P / 32) + u.ch0 / 32];
+        };
+        f32x4 Y[4][2];
+        int E2 = 0, E2n = 0;
+        // C S^T of the chunk with the scalars above and the wave's half of its
+        // masked matrix, M[t][s] = G[t][s] exp2(cum_t - cum_s) dt_s.
+        auto begin_chunk = [&](uint32_t i, int ex, int edx, int eBx) {
+            const float *hd = sh.head[i % 3][wave / 2];
+            const _Float16 *CG = sh.CG[i & 1];
             // C S^T in units 2^(eC + E1), the masked product in units 2^(eC + E2)
             const int E1 = K - 7;
-            int E2 = ex + ed + eB - 21;
-            const bool small = E1 - E2 > 60;  // nothing beside the state: the factor below stays in range
-            if (small) E2 = E1 - 60;
-            f32x4 Y[4][2];
+            E2n = ex + edx + eBx - 21;
+            const bool small = E1 - E2n > 60;  // nothing beside the state: the factor below stays in range
+            if (small) E2n = E1 - 60;
+            const float cap = small ? -200.0f : 15.0f;
+            // operands are read from LDS one group of products ahead
+            f32x4 cs[4], ec[4];
+            float ct[2];
+            f16x8 gv[2][2], co[2][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) cs[j] = *(const f32x4 *)(hd + kQ + 16 * q + 4 * j);
+#pragma unroll
+            for (int k2 = 0; k2 < 2; ++k2) {
+                ct[k2] = hd[16 * (r / 4) + r % 4 + 4 * (2 * (wave % 2) + k2)];
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh)
+                    gv[k2][hh] = *(const f16x8 *)(CG + kQ * N + (((2 * (wave % 2) + k2) * 2 + hh) * 64 + lane) * 8);
+            }
+            auto read_c = [&](int m) {
+#pragma unroll
+                for (int tt = 0; tt < 4; ++tt) co[m & 1][tt] = *(const f16x8 *)(CG + ((tt * KB + m) * 64 + lane) * 8);
+            };
+            read_c(0);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) Y[tt][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int m = 0; m < KB; ++m) {
+                if (m + 1 < KB) {
+                    read_c(m + 1);
+                } else {
+#pragma unroll
+                    for (int tt = 0; tt < 4; ++tt) ec[tt] = *(const f32x4 *)(hd + 2 * kQ + 16 * q + 4 * tt);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                // C S^T, and in between the masked matrix
                 f16x8 so[2];
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) so[c][e] = (_Float16)acc[2 * m + e / 4][c][e % 4];
 #pragma unroll
-                for (int tt = 0; tt < 4; ++tt) {
-                    const f16x8 co = *(const f16x8 *)(sh.CG + ((tt * KB + m) * 64 + lane) * 8);
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) Y[tt][c] = mfma(co, so[c], Y[tt][c]);
-                }
-            }
-            {
-                const float al = __builtin_ldexpf(1.0f, E1 - E2);
-#pragma unroll
-                for (int tt = 0; tt < 4; ++tt) {
-                    const f32x4 ec = *(const f32x4 *)(hd + 2 * kQ + 16 * q + 4 * tt) * al;
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) Y[tt][c] *= ec;
-                }
-            }
-            vm_wait();
-            lds_barrier();  // M is whole, B is in LDS, and every wave is done with C and G
-            if (t + kQ < to) {
-                stage(t + kQ);
-                load(t + kQ);
-            }
-            if (!small) {
-#pragma unroll
                 for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        const f16x8 mo = *(const f16x8 *)&sh.M[wave / 2][tt * 2 + hh][lane][0];
+                    for (int c = 0; c < 2; ++c) Y[tt][c] = mfma(co[m & 1][tt], so[c], Y[tt][c]);
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) Y[tt][c] = mfma(mo, x16[c][hh], Y[tt][c]);
-                    }
+                for (int k = m * 4 / KB; k < (m + 1) * 4 / KB; ++k) {
+                    const int k2 = k / 2, hh = k % 2;
+                    f16x8 me;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        // G is zero above the diagonal, where the exponent may be large
+                        me[j] = (_Float16)fast_exp2(__builtin_fminf(ct[k2] - cs[2 * hh + j / 4][j % 4], cap));
+                    *(f16x8 *)&sh.M[i & 1][wave / 2][(2 * (wave % 2) + k2) * 2 + hh][lane][0] = me * gv[k2][hh];
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
+            const float al = __builtin_ldexpf(1.0f, E1 - E2n);
+#pragma unroll
+            for (int tt = 0; tt < 4; ++tt) {
+                ec[tt] *= al;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) Y[tt][c] *= ec[tt];
+            }
+        };
+        auto of_ex = [](int e) { return e >= 1 << 15 ? e - (1 << 16) : e; };  // without the mark of values that are not finite
+
+        scalars(from);
+        vm_wait();
+        lds_barrier();
+        begin_chunk(0, of_ex(exbn), edn, eBn);
+        for (uint32_t t = from; t < to; t += kQ) {
+            const uint32_t i = (t - from) / kQ;
+            dec = decn, ew = ewn, ed = edn, eB = eBn, exb = exbn, E2 = E2n;
+            const bool anybad = exb >= 1 << 15;
+            const int ex = of_ex(exb), rem = to - t < kQ ? (int)(to - t) : kQ;
+            const bool more = t + kQ < to;
+            if (more) scalars(t + kQ);
+            f16x8 x16[2][2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) x16[c][hh] = xn[c][hh];
+            // Issued since the barrier before: the loads of two chunks ahead, x,
+            // and the last chunk's 16 stores of y, which may stay in flight
+            // (accesses complete in order).
+            if (t > from) asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
+            else vm_wait();
+            lds_barrier();  // M is whole, and the next chunk's C, G and decays and this one's B are in LDS
+            if (more) {
+                stage_b(t + kQ);
+                if (t + 2 * kQ < to) stage_cg(t + 2 * kQ);
+                load(t + kQ);
+            }
+            uint32_t badm[2] = {0u, 0u};
             if (anybad) {
+                // values that are not finite: zero for the products, and what
+                // they reach (their channel, from their token on) becomes NaN
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const _Float16 v = x16[c][j / 8][j % 8];
+                        if (v != v) {
+                            badm[c] |= 1u << j;
+                            x16[c][j / 8][j % 8] = (_Float16)0.0f;
+                        }
+                    }
                     bool low = false;  // the channel is marked in an earlier lane's tokens
 #pragma unroll
                     for (int d = 16; d < 64; d += 16) {
@@ -940,30 +970,20 @@ __global__ __launch_bounds__(kWalkThreads, 2) void walk_out_kernel(SsdCacheArgs 
                         low |= lane >= d && o != 0u;
                     }
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (low || (badm[c] & ((2u << i) - 1))) Y[i / 4][c][i % 4] = __builtin_nanf("");
+                    for (int j = 0; j < 16; ++j)
+                        if (low || (badm[c] & ((2u << j) - 1))) Y[j / 4][c][j % 4] = __builtin_nanf("");
                 }
             }
-            {
-                const float dx = __builtin_ldexpf(dsk, ex - 14);
-                const auto yb = buffer((const char *)a.y + (int64_t)(u.begin + t) * yrow + u.ch0 * 2, (rem - 1) * yrow + 64);
-                uint32_t yo = 16 * q * yrow + 4 * r;
-                asm volatile("" : "+v"(yo));
+            const float *hd = sh.head[i % 3][wave / 2];
+            // LDS reads stand a group of products ahead of their use
+            f16x8 mo[4][2], wv[2], bq[2][4];
 #pragma unroll
-                for (int tt = 0; tt < 4; ++tt) {
-                    const f32x4 rv = *(const f32x4 *)(sh.scale[b] + 16 * q + 4 * tt);
+            for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int i = 4 * tt + e;
-                        const float be = __builtin_ldexpf(rv[e], E2);
-                        float o[2];
+                for (int hh = 0; hh < 2; ++hh) mo[tt][hh] = *(const f16x8 *)&sh.M[i & 1][wave / 2][tt * 2 + hh][lane][0];
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) o[c] = __builtin_fmaf((float)x16[c][i / 8][i % 8], dx, Y[tt][c][e] * be);
-                        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, bf16x2{(__bf16)o[0], (__bf16)o[1]}), yb, yo, 0, 0);
-                        yo += yrow;
-                    }
-                }
-            }
+            for (int hh = 0; hh < 2; ++hh) wv[hh] = *(const f16x8 *)((const _Float16 *)(hd + 3 * kQ) + 16 * q + 8 * hh);
+            __builtin_amdgcn_sched_barrier(0);
             // the state: x 2^-sc times w (w < 1 as stored) in units that keep
             // dec |acc| + 64 |x w B| below 2^15
             const int c0 = ex + ew + eB - 21;
@@ -974,25 +994,63 @@ __global__ __launch_bounds__(kWalkThreads, 2) void walk_out_kernel(SsdCacheArgs 
             bound = __builtin_fmaf(bound, f, __builtin_ldexpf(1.0f, 27 - sc));
             if (!finite(bound)) bound = 0x1p14f;
             K = Kn;
+            const _Float16 sf = (_Float16)__builtin_ldexpf(1.0f, sc < 24 ? -sc : -24);
+            const _Float16 sw = (_Float16)__builtin_ldexpf(1.0f, sc < 24 ? 0 : 24 - sc);
+            auto read_b = [&](int g) {  // four operands in the order (hh, nt)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) bq[g & 1][k] = *(const f16x8 *)(sh.B[i & 1] + ((4 * g + k) * 64 + lane) * 8);
+            };
+            read_b(0);
+            f32x4 rv[4];
+#pragma unroll
+            for (int tt = 0; tt < 4; ++tt) rv[tt] = *(const f32x4 *)(sh.scale[i % 3] + 16 * q + 4 * tt);
+            __builtin_amdgcn_sched_barrier(0);
+            // the masked product
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) Y[tt][c] = mfma(mo[tt][hh], x16[c][hh], Y[tt][c]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) acc[nt][c] *= f;
-            const _Float16 sf = (_Float16)__builtin_ldexpf(1.0f, sc < 24 ? -sc : -24);
-            const _Float16 sw = (_Float16)__builtin_ldexpf(1.0f, sc < 24 ? 0 : 24 - sc);
+            f16x8 v[2][2];
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-                f16x8 wv = *(const f16x8 *)((const _Float16 *)(hd + 3 * kQ) + 16 * q + 8 * hh);
-                if (sc > 24) wv *= sw;
-                f16x8 v[2];
+            for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
-                for (int c = 0; c < 2; ++c) v[c] = (x16[c][hh] * sf) * wv;
+                for (int c = 0; c < 2; ++c) v[c][hh] = (x16[c][hh] * sf) * (wv[hh] * sw);
+            __builtin_amdgcn_sched_barrier(0);
+            // the state's products, and in between y
+            const float dx = __builtin_ldexpf(dsk, ex - 14);
+            const auto yb = buffer((const char *)a.y + (int64_t)(u.begin + t) * yrow + u.ch0 * 2, (rem - 1) * yrow + 64);
+            uint32_t yo = 16 * q * yrow + 4 * r;
+            asm volatile("" : "+v"(yo));
+            constexpr int GB = NT / 2;  // groups of four operands
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const f16x8 bh = *(const f16x8 *)(sh.B + ((hh * NT + nt) * 64 + lane) * 8);
+            for (int g = 0; g < GB; ++g) {
+                if (g + 1 < GB) read_b(g + 1);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) acc[nt][c] = mfma(bh, v[c], acc[nt][c]);
+                for (int k = 0; k < 4; ++k) {
+                    const int hh = (4 * g + k) / NT, nt = (4 * g + k) % NT;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) acc[nt][c] = mfma(bq[g & 1][k], v[c][hh], acc[nt][c]);
                 }
+#pragma unroll
+                for (int tt = g * 4 / GB; tt < (g + 1) * 4 / GB; ++tt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = 4 * tt + e;
+                        const float be = __builtin_ldexpf(rv[tt][e], E2);
+                        float o[2];
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) o[c] = __builtin_fmaf((float)x16[c][j / 8][j % 8], dx, Y[tt][c][e] * be);
+                        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, bf16x2{(__bf16)o[0], (__bf16)o[1]}), yb, yo, 0, 0);
+                        yo += yrow;
+                    }
+                __builtin_amdgcn_sched_barrier(0);
             }
             if (anybad) {
 #pragma unroll
@@ -1007,6 +1065,7 @@ __global__ __launch_bounds__(kWalkThreads, 2) void walk_out_kernel(SsdCacheArgs 
                             for (int e = 0; e < 4; ++e) acc[nt][c][e] = __builtin_nanf("");
                 }
             }
+            if (more) begin_chunk(i + 1, of_ex(exbn), edn, eBn);
         }
     }
 
@@ -1028,7 +1087,7 @@ __global__ __launch_bounds__(kWalkThreads, 2) void walk_out_kernel(SsdCacheArgs 
 #pragma unroll
         for (int c = 0; c < 2; ++c) win[(int64_t)(u.ch0 + 2 * r + c) * 3 + q] = row((int)u.len - 3 + q, u.ch0 + 2 * r + c);
     if (u.hb == 0)
-        for (int i = threadIdx.x; i < 2 * N * 3; i += kWalkThreads) {
+        for (int i = threadIdx.x; i < 2 * N * 3; i += 64 * WAVES) {
             const int n = i / 3;
             const int64_t c = a.H * a.P + ((n / N) * a.G + u.g) * N + n % N;
             win[c * 3 + i % 3] = row((int)u.len - 3 + i % 3, c);
@@ -1041,15 +1100,15 @@ hipError_t launch_n(const SsdCacheArgs &a, hipStream_t s) {
     hipLaunchKernelGGL((prepare_kernel<N>), dim3((unsigned)(a.nchunk * (a.G + dts) + a.seqs * parts)), dim3(kPrepThreads), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int64_t ncb = a.H / a.G * (a.P / 64), units = a.nseg * a.G * ((ncb + 1) / 2);
-    const dim3 grid((unsigned)((units + 7) / 8 * 8));
-    hipLaunchKernelGGL((walk_state_kernel<N>), grid, dim3(kWalkThreads), 0, s, a);
+    const int64_t ncb = a.H / a.G * (a.P / 64);
+    auto grid = [&](int blocks) { return dim3((unsigned)((a.nseg * a.G * ((ncb + blocks - 1) / blocks) + 7) / 8 * 8)); };
+    hipLaunchKernelGGL((walk_state_kernel<N>), grid(kBlocksA), dim3(128 * kBlocksA), 0, s, a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if (a.rows > a.seg) {  // some sequence may be longer than a segment
         hipLaunchKernelGGL(join_kernel, dim3((unsigned)((a.H * a.P * N + 1023) / 1024), (unsigned)a.seqs), dim3(256), 0, s, a, N);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((walk_out_kernel<N>), grid, dim3(kWalkThreads), 0, s, a);
+    hipLaunchKernelGGL((walk_out_kernel<N>), grid(kBlocksC), dim3(128 * kBlocksC), 0, s, a);
     return hipGetLastError();
 }
 
