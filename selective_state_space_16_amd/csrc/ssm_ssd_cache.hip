@@ -162,7 +162,8 @@ __device__ __forceinline__ int find_seq(const SsdCacheArgs &a, uint32_t id, uint
 template <int N>
 struct PrepShared {
     static constexpr int R = N + 8;
-    alignas(16) _Float16 Bh[kQ][R], Bl[kQ][R], Ch[kQ][R], Cl[kQ][R];
+    // high parts, and the low parts of B, then those of C: three of these workgroups fit a CU
+    alignas(16) _Float16 Bh[kQ][R], Ch[kQ][R], lo[kQ][R];
     float maxb[4];
     int ec[kQ];
 };
@@ -186,7 +187,7 @@ __device__ __forceinline__ void start_seq(const SsdCacheArgs &a, int64_t s, int6
 
 // The decays of the chunk for a wave's heads h0 .., a lane per token.
 __device__ __forceinline__ void chunk_decays(const SsdCacheArgs &a, uint32_t id, uint32_t row, int rem, uint32_t h0) {
-    constexpr int kPer = kDtHeads / 4;
+    constexpr int kPer = kDtHeads / 4;  // the loads of all of them before the first use
     const int lane = threadIdx.x & 63;
     const uint32_t H = (uint32_t)a.H;
     const uint16_t *src = (const uint16_t *)a.dt_raw + (int64_t)(row + (lane < rem ? lane : rem - 1)) * a.dt_stride;
@@ -303,19 +304,20 @@ __global__ __launch_bounds__(kPrepThreads) void prepare_kernel(SsdCacheArgs a) {
     if (lane == 0) sh.maxb[wave] = big;
     __syncthreads();
     const int eB = clampi(exponent(__builtin_fmaxf(__builtin_fmaxf(sh.maxb[0], sh.maxb[1]), __builtin_fmaxf(sh.maxb[2], sh.maxb[3]))), -100, 128);
+    f16x4 low[TPB];
 #pragma unroll
     for (int i = 0; i < TPB; ++i) {
         const int e = 7 - (isC ? sh.ec[t0 + i] : eB);
-        f16x4 hi, lo;
+        f16x4 hi;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             float t = __builtin_ldexpf(v[i][k], e);
             asm("" : "+v"(t));
             hi[k] = (_Float16)t;
-            lo[k] = (_Float16)(t - (float)hi[k]);
+            low[i][k] = (_Float16)(t - (float)hi[k]);
         }
         *(f16x4 *)(isC ? &sh.Ch[t0 + i][n0] : &sh.Bh[t0 + i][n0]) = hi;
-        *(f16x4 *)(isC ? &sh.Cl[t0 + i][n0] : &sh.Bl[t0 + i][n0]) = lo;
+        if (!isC) *(f16x4 *)&sh.lo[t0 + i][n0] = low[i];
     }
     __syncthreads();
 
@@ -328,7 +330,7 @@ __global__ __launch_bounds__(kPrepThreads) void prepare_kernel(SsdCacheArgs a) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             hi[j] = sh.Bh[16 * q + 8 * h + j][16 * nt + r];
-            lo[j] = sh.Bl[16 * q + 8 * h + j][16 * nt + r];
+            lo[j] = sh.lo[16 * q + 8 * h + j][16 * nt + r];
         }
         *(f16x8 *)(out + (f * 64 + lane) * 8) = hi;
         *(f16x8 *)(out + kQ * N + (f * 64 + lane) * 8) = lo;
@@ -344,34 +346,48 @@ __global__ __launch_bounds__(kPrepThreads) void prepare_kernel(SsdCacheArgs a) {
     }
     // G as A operands, (tt, h): row r as in C, k = token s = 16 q + 8 h + j. The
     // wave's tt; a product's row 4 q + e is token 16 q + 8 h + 4 b + e.
-    {
-        const int tt = wave;
-        f16x8 ch[N / 32], clo[N / 32];
+    const int tt = wave;
+    f32x4 acc[2][2];
 #pragma unroll
-        for (int m = 0; m < N / 32; ++m) {
-            ch[m] = *(const f16x8 *)&sh.Ch[row + 4 * tt][32 * m + 8 * q];
-            clo[m] = *(const f16x8 *)&sh.Cl[row + 4 * tt][32 * m + 8 * q];
-        }
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            f16x8 o;
+        for (int b = 0; b < 2; ++b) acc[h][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int m = 0; m < N / 32; ++m) {
+        const f16x8 ch = *(const f16x8 *)&sh.Ch[row + 4 * tt][32 * m + 8 * q];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int m = 0; m < N / 32; ++m) {
-                    const f16x8 bh = *(const f16x8 *)&sh.Bh[row + 8 * h + 4 * b][32 * m + 8 * q];
-                    const f16x8 bl = *(const f16x8 *)&sh.Bl[row + 8 * h + 4 * b][32 * m + 8 * q];
-                    acc = mfma(bh, ch[m], acc);
-                    acc = mfma(bl, ch[m], acc);
-                    acc = mfma(bh, clo[m], acc);
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    o[4 * b + e] = 16 * q + 8 * h + 4 * b + e <= row + 4 * tt ? (_Float16)(acc[e] * 0x1p-7f) : (_Float16)0.0f;
+                const f16x8 bh = *(const f16x8 *)&sh.Bh[row + 8 * h + 4 * b][32 * m + 8 * q];
+                const f16x8 bl = *(const f16x8 *)&sh.lo[row + 8 * h + 4 * b][32 * m + 8 * q];
+                acc[h][b] = mfma(bh, ch, acc[h][b]);
+                acc[h][b] = mfma(bl, ch, acc[h][b]);
             }
-            *(f16x8 *)(out + 3 * kQ * N + ((tt * 2 + h) * 64 + lane) * 8) = o;
-        }
+    }
+    __syncthreads();
+    if (isC)
+#pragma unroll
+        for (int i = 0; i < TPB; ++i) *(f16x4 *)&sh.lo[t0 + i][n0] = low[i];
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < N / 32; ++m) {
+        const f16x8 cl2 = *(const f16x8 *)&sh.lo[row + 4 * tt][32 * m + 8 * q];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+                acc[h][b] = mfma(*(const f16x8 *)&sh.Bh[row + 8 * h + 4 * b][32 * m + 8 * q], cl2, acc[h][b]);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        f16x8 o;
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                o[4 * b + e] = 16 * q + 8 * h + 4 * b + e <= row + 4 * tt ? (_Float16)(acc[h][b][e] * 0x1p-7f) : (_Float16)0.0f;
+        *(f16x8 *)(out + 3 * kQ * N + ((tt * 2 + h) * 64 + lane) * 8) = o;
     }
     if (tid < kQ) ((float *)(out + 3 * kQ * N + kQ * kQ))[tid] = __builtin_ldexpf(1.0f, sh.ec[tid]);
     if (tid == 0) a.ws_eb[id * a.G + g] = eB;
@@ -1114,13 +1130,27 @@ hipError_t launch_n(const SsdCacheArgs &a, hipStream_t s) {
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Tokens per segment: as many segments as keep the 512 workgroups that the chip
-// holds at once, none shorter than 256 tokens.
-int64_t segment_tokens(int64_t rows, int64_t H, int64_t P, int64_t G) {
-    const int64_t units = G * ((H / G * (P / 64) + 1) / 2);
-    const int64_t want = units >= 512 ? 1 : 512 / units;
-    const int64_t seg = (rows + want - 1) / want;
-    return (seg < 256 ? 256 : seg + 63) / 64 * 64;
+// Tokens per segment. The chip holds 512 workgroups of walk A at once; a round of
+// them costs a segment's chunks and about two more (the first loads, the states),
+// so the segment is the one that costs least over 1 to 8 rounds, with at most
+// (rows + seqs (seg - 1)) / seg segments of sequences whose lengths only the device
+// knows. Measured (80 heads, N = 128): one prompt of 16384 tokens in one round
+// 270 us, in two 287; eight of 4096 in two rounds 623, in four 574, in eight 687.
+// At most 2048 where there are several sequences, one of which may be long.
+int64_t segment_tokens(int64_t seqs, int64_t rows, int64_t H, int64_t P, int64_t G) {
+    const int64_t units = G * ((H / G * (P / 64) + kBlocksA - 1) / kBlocksA);
+    const int64_t mean = (rows / seqs + kQ - 1) / kQ;  // chunks of a sequence
+    int64_t best = seqs > 1 ? 2048 : (rows + kQ - 1) / kQ * kQ, cost = INT64_MAX;
+    for (int64_t rounds = 1; rounds <= 8; ++rounds) {
+        const int64_t most = 512 * rounds / units;  // segments
+        if (most <= seqs && !(seqs == 1 && most == 1)) continue;
+        // the smallest segment with that many of them at most
+        int64_t seg = seqs == 1 ? (rows + most - 1) / most : (rows - seqs + most - seqs) / (most - seqs);
+        seg = (seg < kQ ? kQ : seg + kQ - 1) / kQ * kQ;
+        const int64_t chunks = seg / kQ < mean ? seg / kQ : mean, c = rounds * (chunks + 2);
+        if (c < cost && (seqs == 1 || seg <= 2048)) cost = c, best = seg;
+    }
+    return best < kQ ? kQ : best;
 }
 
 // Cuts the workspace up; returns its size.
@@ -1131,7 +1161,7 @@ size_t plan(SsdCacheArgs &a, int N, char *base) {
         at += up256(bytes);
         return p;
     };
-    a.seg = segment_tokens(a.rows, a.H, a.P, a.G);
+    a.seg = segment_tokens(a.seqs, a.rows, a.H, a.P, a.G);
     a.nchunk = a.rows / kQ + a.seqs;
     a.nseg = a.rows / a.seg + a.seqs;
     const size_t chunks = (size_t)a.nchunk;
