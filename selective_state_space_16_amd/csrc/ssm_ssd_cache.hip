@@ -52,7 +52,9 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kQ = 64;            // tokens per chunk
-constexpr int kPrepThreads = 256;
+// Threads of a workgroup ahead of the walks: a lane convolves four channels of
+// four tokens (256 threads and 16 tokens: 11.8 us for one chunk against 7).
+constexpr int prep_threads(int N) { return 8 * N; }
 constexpr int kBlocksA = 2;       // column blocks of 64 per workgroup of walk A, two waves each
 constexpr int kBlocksC = 4;       // of walk C
 
@@ -63,7 +65,7 @@ constexpr int frag_elems(int N) { return 3 * kQ * N + kQ * kQ + 512; }
 // Floats per (chunk, head) for walk C: cum, cum - log2 dt, exp2(cum), and w as
 // scaled float16, filled up to 1 KiB.
 constexpr int kHead = 4 * kQ;
-constexpr int kDtHeads = 16;  // heads per workgroup of the decays
+constexpr int dt_heads(int N) { return prep_threads(N) / 32; }  // heads per workgroup of the decays, two a wave
 
 __device__ __forceinline__ f32x4 mfma(f16x8 a, f16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
@@ -164,30 +166,31 @@ struct PrepShared {
     static constexpr int R = N + 8;
     // high parts, and the low parts of B, then those of C: three of these workgroups fit a CU
     alignas(16) _Float16 Bh[kQ][R], Ch[kQ][R], lo[kQ][R];
-    float maxb[4];
+    float maxb[16];
     int ec[kQ];
 };
 
 // Which slot a sequence owns (-1: none), and the raw rows before its start.
+template <int THREADS>
 __device__ __forceinline__ void start_seq(const SsdCacheArgs &a, int64_t s, int64_t part) {
     const int32_t slot = a.slots[s];
     bool dead = slot < 0 || slot >= a.num_slots;
     if (!dead) {
         bool same = false;
-        for (int64_t i = threadIdx.x; i < s; i += kPrepThreads) same |= a.slots[i] == slot;
+        for (int64_t i = threadIdx.x; i < s; i += THREADS) same |= a.slots[i] == slot;
         dead = __syncthreads_or(same);
     }
     if (part == 0 && threadIdx.x == 0) a.ws_slot[s] = dead ? -1 : slot;
     const bool resume = !dead && a.resume && a.resume[s] != 0;
-    const int64_t c = part * kPrepThreads + threadIdx.x;
+    const int64_t c = part * THREADS + threadIdx.x;
     if (c < a.C)
         for (int k = 0; k < 3; ++k)
             a.ws_win[(s * 3 + k) * a.C + c] = resume ? ((const uint16_t *)a.conv_cache)[((int64_t)slot * a.C + c) * 3 + k] : 0;
 }
 
-// The decays of the chunk for a wave's heads h0 .., a lane per token.
+// The decays of the chunk for a wave's two heads h0 .., a lane per token.
 __device__ __forceinline__ void chunk_decays(const SsdCacheArgs &a, uint32_t id, uint32_t row, int rem, uint32_t h0) {
-    constexpr int kPer = kDtHeads / 4;  // the loads of all of them before the first use
+    constexpr int kPer = 2;
     const int lane = threadIdx.x & 63;
     const uint32_t H = (uint32_t)a.H;
     const uint16_t *src = (const uint16_t *)a.dt_raw + (int64_t)(row + (lane < rem ? lane : rem - 1)) * a.dt_stride;
@@ -222,15 +225,16 @@ __device__ __forceinline__ void chunk_decays(const SsdCacheArgs &a, uint32_t id,
 }
 
 template <int N>
-__global__ __launch_bounds__(kPrepThreads) void prepare_kernel(SsdCacheArgs a) {
+__global__ __launch_bounds__(prep_threads(N)) void prepare_kernel(SsdCacheArgs a) {
     __shared__ PrepShared<N> sh;
+    constexpr int THREADS = prep_threads(N), WAVES = THREADS / 64, HEADS = dt_heads(N);
     uint32_t blk = blockIdx.x;
-    const uint32_t nbc = (uint32_t)(a.nchunk * a.G), per = ((uint32_t)a.H + kDtHeads - 1) / kDtHeads;
+    const uint32_t nbc = (uint32_t)(a.nchunk * a.G), per = ((uint32_t)a.H + HEADS - 1) / HEADS;
     const uint32_t ndt = (uint32_t)a.nchunk * per;
     if (blk >= nbc + ndt) {
-        const uint32_t parts = (uint32_t)((a.C + kPrepThreads - 1) / kPrepThreads);
+        const uint32_t parts = (uint32_t)((a.C + THREADS - 1) / THREADS);
         blk -= nbc + ndt;
-        start_seq(a, blk / parts, blk % parts);
+        start_seq<THREADS>(a, blk / parts, blk % parts);
         return;
     }
     const bool decays = blk >= nbc;
@@ -246,13 +250,13 @@ __global__ __launch_bounds__(kPrepThreads) void prepare_kernel(SsdCacheArgs a) {
     const bool resume = a.resume && a.resume[s] != 0 && slot >= 0 && slot < a.num_slots;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     if (decays) {
-        chunk_decays(a, id, begin + first, rem, g * kDtHeads + wave * (kDtHeads / 4));
+        chunk_decays(a, id, begin + first, rem, g * HEADS + wave * 2);
         return;
     }
 
     // The convolution: a lane takes four channels of TPB tokens; N / 4 lanes
     // hold a token's B, the next N / 4 its C.
-    constexpr int LPR = 2 * N / 4, NB = kPrepThreads / LPR, TPB = kQ / NB;
+    constexpr int LPR = 2 * N / 4, NB = THREADS / LPR, TPB = kQ / NB;
     const int cl = tid % LPR, tb = tid / LPR, isC = cl / (N / 4), n0 = (cl % (N / 4)) * 4;
     const int64_t c0 = a.H * a.P + (isC * a.G + g) * N + n0;
     float w[4][4], bias[4];
@@ -303,7 +307,9 @@ __global__ __launch_bounds__(kPrepThreads) void prepare_kernel(SsdCacheArgs a) {
     big = wave_top(big);
     if (lane == 0) sh.maxb[wave] = big;
     __syncthreads();
-    const int eB = clampi(exponent(__builtin_fmaxf(__builtin_fmaxf(sh.maxb[0], sh.maxb[1]), __builtin_fmaxf(sh.maxb[2], sh.maxb[3]))), -100, 128);
+#pragma unroll
+    for (int k = 0; k < WAVES; ++k) big = __builtin_fmaxf(big, sh.maxb[k]);
+    const int eB = clampi(exponent(big), -100, 128);
     f16x4 low[TPB];
 #pragma unroll
     for (int i = 0; i < TPB; ++i) {
@@ -324,7 +330,7 @@ __global__ __launch_bounds__(kPrepThreads) void prepare_kernel(SsdCacheArgs a) {
     _Float16 *out = (_Float16 *)a.ws_frag + ((int64_t)id * a.G + g) * frag_elems(N);
     const int r = lane & 15, q = lane >> 4;
     // B^T as A operands, (h, nt): row n = 16 nt + r, k = token 16 q + 8 h + j
-    for (int f = wave; f < 2 * (N / 16); f += 4) {
+    for (int f = wave; f < 2 * (N / 16); f += WAVES) {
         const int h = f / (N / 16), nt = f % (N / 16);
         f16x8 hi, lo;
 #pragma unroll
@@ -338,32 +344,27 @@ __global__ __launch_bounds__(kPrepThreads) void prepare_kernel(SsdCacheArgs a) {
     // C as A operands, (tt, m): row r is token 16 (r / 4) + 4 tt + r % 4, and k
     // runs over n in the order in which two accumulator tiles hold the state
     const int row = 16 * (r / 4) + r % 4;
-    for (int f = wave; f < 4 * (N / 32); f += 4) {
+    for (int f = wave; f < 4 * (N / 32); f += WAVES) {
         const int tt = f / (N / 32), m = f % (N / 32);
         const _Float16 *src = &sh.Ch[row + 4 * tt][32 * m + 4 * q];
         const f16x4 lo = *(const f16x4 *)src, hi = *(const f16x4 *)(src + 16);
         *(f16x8 *)(out + 2 * kQ * N + (f * 64 + lane) * 8) = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     }
-    // G as A operands, (tt, h): row r as in C, k = token s = 16 q + 8 h + j. The
-    // wave's tt; a product's row 4 q + e is token 16 q + 8 h + 4 b + e.
-    const int tt = wave;
-    f32x4 acc[2][2];
+    // G as A operands, (tt, h): row r as in C, k = token s = 16 q + 8 h + j. A
+    // wave forms one or two of the sixteen products (tt, h, b), whose row 4 q + e
+    // is token 16 q + 8 h + 4 b + e.
+    constexpr int PER = 16 / WAVES;
+    f32x4 acc[PER];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int k = 0; k < PER; ++k) {
+        const int f = wave * PER + k, tt = f / 4, sr = row + 4 * (f % 4);
+        acc[k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int b = 0; b < 2; ++b) acc[h][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int m = 0; m < N / 32; ++m) {
-        const f16x8 ch = *(const f16x8 *)&sh.Ch[row + 4 * tt][32 * m + 8 * q];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const f16x8 bh = *(const f16x8 *)&sh.Bh[row + 8 * h + 4 * b][32 * m + 8 * q];
-                const f16x8 bl = *(const f16x8 *)&sh.lo[row + 8 * h + 4 * b][32 * m + 8 * q];
-                acc[h][b] = mfma(bh, ch, acc[h][b]);
-                acc[h][b] = mfma(bl, ch, acc[h][b]);
-            }
+        for (int m = 0; m < N / 32; ++m) {
+            const f16x8 ch = *(const f16x8 *)&sh.Ch[row + 4 * tt][32 * m + 8 * q];
+            acc[k] = mfma(*(const f16x8 *)&sh.Bh[sr][32 * m + 8 * q], ch, acc[k]);
+            acc[k] = mfma(*(const f16x8 *)&sh.lo[sr][32 * m + 8 * q], ch, acc[k]);
+        }
     }
     __syncthreads();
     if (isC)
@@ -371,23 +372,15 @@ __global__ __launch_bounds__(kPrepThreads) void prepare_kernel(SsdCacheArgs a) {
         for (int i = 0; i < TPB; ++i) *(f16x4 *)&sh.lo[t0 + i][n0] = low[i];
     __syncthreads();
 #pragma unroll
-    for (int m = 0; m < N / 32; ++m) {
-        const f16x8 cl2 = *(const f16x8 *)&sh.lo[row + 4 * tt][32 * m + 8 * q];
+    for (int k = 0; k < PER; ++k) {
+        const int f = wave * PER + k, tt = f / 4, sr = row + 4 * (f % 4), s0 = 16 * q + 4 * (f % 4);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int m = 0; m < N / 32; ++m)
+            acc[k] = mfma(*(const f16x8 *)&sh.Bh[sr][32 * m + 8 * q], *(const f16x8 *)&sh.lo[row + 4 * tt][32 * m + 8 * q], acc[k]);
+        f16x4 o;
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
-                acc[h][b] = mfma(*(const f16x8 *)&sh.Bh[row + 8 * h + 4 * b][32 * m + 8 * q], cl2, acc[h][b]);
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        f16x8 o;
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                o[4 * b + e] = 16 * q + 8 * h + 4 * b + e <= row + 4 * tt ? (_Float16)(acc[h][b][e] * 0x1p-7f) : (_Float16)0.0f;
-        *(f16x8 *)(out + 3 * kQ * N + ((tt * 2 + h) * 64 + lane) * 8) = o;
+        for (int e = 0; e < 4; ++e) o[e] = s0 + e <= row + 4 * tt ? (_Float16)(acc[k][e] * 0x1p-7f) : (_Float16)0.0f;
+        *(f16x4 *)(out + 3 * kQ * N + ((f / 2) * 64 + lane) * 8 + 4 * (f % 2)) = o;
     }
     if (tid < kQ) ((float *)(out + 3 * kQ * N + kQ * kQ))[tid] = __builtin_ldexpf(1.0f, sh.ec[tid]);
     if (tid == 0) a.ws_eb[id * a.G + g] = eB;
@@ -1112,8 +1105,9 @@ __global__ __launch_bounds__(128 * kBlocksC, 2) void walk_out_kernel(SsdCacheArg
 
 template <int N>
 hipError_t launch_n(const SsdCacheArgs &a, hipStream_t s) {
-    const int64_t parts = (a.C + kPrepThreads - 1) / kPrepThreads, dts = (a.H + kDtHeads - 1) / kDtHeads;
-    hipLaunchKernelGGL((prepare_kernel<N>), dim3((unsigned)(a.nchunk * (a.G + dts) + a.seqs * parts)), dim3(kPrepThreads), 0, s, a);
+    constexpr int64_t threads = prep_threads(N);
+    const int64_t parts = (a.C + threads - 1) / threads, dts = (a.H + dt_heads(N) - 1) / dt_heads(N);
+    hipLaunchKernelGGL((prepare_kernel<N>), dim3((unsigned)(a.nchunk * (a.G + dts) + a.seqs * parts)), dim3(threads), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t ncb = a.H / a.G * (a.P / 64);
