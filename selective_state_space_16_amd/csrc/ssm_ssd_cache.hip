@@ -218,8 +218,8 @@ __device__ __forceinline__ void chunk_decays(const SsdCacheArgs &a, uint32_t id,
         o[lane] = cum;
         o[kQ + lane] = cum - __builtin_amdgcn_logf(dt) + (float)ed;
         o[2 * kQ + lane] = fast_exp2(cum);
-        ((_Float16 *)(o + 3 * kQ))[lane] = (_Float16)__builtin_ldexpf(wt, -ew);
-        a.ws_w[at * kQ + lane] = wt * -kLn2;  // walk A holds x as -log2(e) x
+        ((_Float16 *)(o + 3 * kQ))[lane] = (_Float16)__builtin_ldexpf(wt, -ew);  // below 1, as for walk A below
+        a.ws_w[at * kQ + lane] = __builtin_ldexpf(wt, -ew);
         if (lane == 63) *(f32x4 *)(a.ws_meta + at * 4) = f32x4{fast_exp2(cum), __int_as_float(ew), __int_as_float(ed), 0.0f};
     }
 }
@@ -617,29 +617,20 @@ __global__ __launch_bounds__(128 * kBlocksA, 2) void walk_state_kernel(SsdCacheA
             top = wave_top(top);
         }
         const int ex = clampi(uniform(exponent(top)), -100, 127);
-        // x as walk C takes it, as its registers; a marked value is a NaN again
-        {
-            const float sx = __builtin_ldexpf(-kLn2, 14 - ex);
-            f16x8 xo[2][2];
+        // B of the first products, ahead of their use
+        f16x8 bh[2][2], bl[2][2];
+        auto read_b = [&](int g) {  // two operands, high and low, in the order (hh, nt)
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) xo[c][i / 8][i % 8] = (_Float16)(x[c][i] * sx);
-            if (anybad) {
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (badm[c] >> i & 1) xo[c][i / 8][i % 8] = (_Float16)__builtin_nanf("");
+            for (int j = 0; j < 2; ++j) {
+                bh[g & 1][j] = *(const f16x8 *)(sh.B[b] + ((2 * g + j) * 64 + lane) * 8);
+                bl[g & 1][j] = *(const f16x8 *)(sh.B[b] + kQ * N + ((2 * g + j) * 64 + lane) * 8);
             }
-            const int64_t at = (int64_t)id * (a.H * a.P / 32) + u.ch0 / 32;
-            f16x8 *dst = (f16x8 *)a.ws_x + at * 256 + lane;
+        };
+        read_b(0);
+        f32x4 wq[4];
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) dst[(c * 2 + hh) * 64] = xo[c][hh];
-            if (lane == 0) a.ws_ex[at] = ex + (anybad ? 1 << 16 : 0);
-        }
+        for (int j = 0; j < 4; ++j) wq[j] = *(const f32x4 *)(wt + 4 * j);
+        __builtin_amdgcn_sched_barrier(0);
         // units of the state after this chunk: S = acc 2^Kn
         const int eb = uniform(exponent(bound));
         int kv = ex + ew;
@@ -651,36 +642,67 @@ __global__ __launch_bounds__(128 * kBlocksA, 2) void walk_state_kernel(SsdCacheA
         if (!finite(bound)) bound = 0x1p27f;
         segdec *= dec;
         K = Kn;
+        // x times 2^(14 - ex): walk C's operand as float16, and with w times
+        // 2^(ex + ew - kv) (both exact) the state's
+        const float sx = __builtin_ldexpf(-kLn2, 14 - ex), sw = __builtin_ldexpf(1.0f, ex + ew - kv);
+        f16x8 xo[2][2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                x[c][i] *= sx;
+                xo[c][i / 8][i % 8] = (_Float16)x[c][i];
+            }
+        const int64_t at = (int64_t)id * (a.H * a.P / 32) + u.ch0 / 32;
+        if (lane == 0) a.ws_ex[at] = ex + (anybad ? 1 << 16 : 0);
+        if (anybad) {  // a marked value is a NaN again
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (badm[c] >> i & 1) xo[c][i / 8][i % 8] = (_Float16)__builtin_nanf("");
+        }
+        {
+            f16x8 *dst = (f16x8 *)a.ws_x + at * 256 + lane;
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) dst[(c * 2 + hh) * 64] = xo[c][hh];
+        }
+        f16x8 vh[2][2], vl[2][2];
+        auto split_x = [&](int hh) {
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                const int i = 8 * hh + j;
+                const float wa = wq[i / 4][i % 4] * sw, wb = wq[i / 4][i % 4 + 1] * sw;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    f16x2 hi, lo;
+                    split(x[c][i] * wa, x[c][i + 1] * wb, hi, lo);
+                    vh[c][hh][j] = hi[0], vh[c][hh][j + 1] = hi[1];
+                    vl[c][hh][j] = lo[0], vl[c][hh][j + 1] = lo[1];
+                }
+            }
+        };
+        split_x(0);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) acc[nt][c] *= f;
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-            f16x8 vh[2], vl[2];
+        for (int g = 0; g < NT; ++g) {
+            if (g + 1 < NT) read_b(g + 1);
+            __builtin_amdgcn_sched_barrier(0);
+            const int hh = g / (NT / 2), nt = 2 * g % NT;
+            if (g == 0) split_x(1);
 #pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-                const int i = 8 * hh + j;
-                const float wa = __builtin_ldexpf(wt[i], 14 - kv), wb = __builtin_ldexpf(wt[i + 1], 14 - kv);
+            for (int k = 0; k < 3; ++k)  // the small products first
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    f16x2 hi, lo;
-                    split(x[c][i] * wa, x[c][i + 1] * wb, hi, lo);
-                    vh[c][j] = hi[0], vh[c][j + 1] = hi[1];
-                    vl[c][j] = lo[0], vl[c][j + 1] = lo[1];
-                }
-            }
+                for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const f16x8 bh = *(const f16x8 *)(sh.B[b] + ((hh * NT + nt) * 64 + lane) * 8);
-                const f16x8 bl = *(const f16x8 *)(sh.B[b] + kQ * N + ((hh * NT + nt) * 64 + lane) * 8);
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    acc[nt][c] = mfma(bh, vh[c], acc[nt][c]);
-                    acc[nt][c] = mfma(bl, vh[c], acc[nt][c]);
-                    acc[nt][c] = mfma(bh, vl[c], acc[nt][c]);
-                }
-            }
+                    for (int c = 0; c < 2; ++c)
+                        acc[nt + j][c] = mfma(k == 0 ? bl[g & 1][j] : bh[g & 1][j], k == 1 ? vl[c][hh] : vh[c][hh], acc[nt + j][c]);
+            __builtin_amdgcn_sched_barrier(0);
         }
         if (anybad) {
 #pragma unroll
