@@ -26,21 +26,27 @@ namespace {
 typedef float f32x4n __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4n __attribute__((ext_vector_type(4)));
 
+// Rows beyond the last-level cache (256 MB) that a kernel passes over once are
+// loaded and stored as data without reuse (STREAM).
+constexpr int64_t kStreamBytes = 256ll << 20;
+
 // VEC consecutive elements as floats. VEC = 8: 16-byte pieces; 1: one element.
-template <int VEC>
+template <int VEC, bool STREAM = false>
 __device__ __forceinline__ void ld_vec(const float *p, float (&v)[VEC]) {
     if constexpr (VEC == 8) {
-        const f32x4n a = *(const f32x4n *)p, b = *(const f32x4n *)(p + 4);
+        const f32x4n *q = (const f32x4n *)p;
+        const f32x4n a = STREAM ? __builtin_nontemporal_load(q) : q[0];
+        const f32x4n b = STREAM ? __builtin_nontemporal_load(q + 1) : q[1];
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
     } else {
         v[0] = *p;
     }
 }
-template <int VEC>
+template <int VEC, bool STREAM = false>
 __device__ __forceinline__ void ld_vec(const uint16_t *p, float (&v)[VEC]) {
     if constexpr (VEC == 8) {
-        const u32x4n a = *(const u32x4n *)p;
+        const u32x4n a = STREAM ? __builtin_nontemporal_load((const u32x4n *)p) : *(const u32x4n *)p;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             v[2 * i] = __uint_as_float(a[i] << 16);
@@ -50,23 +56,31 @@ __device__ __forceinline__ void ld_vec(const uint16_t *p, float (&v)[VEC]) {
         v[0] = ld_act(p, 0);
     }
 }
-template <int VEC>
+template <int VEC, bool STREAM = false>
 __device__ __forceinline__ void st_vec(float *p, const float (&v)[VEC]) {
     if constexpr (VEC == 8) {
-        *(f32x4n *)p = f32x4n{v[0], v[1], v[2], v[3]};
-        *(f32x4n *)(p + 4) = f32x4n{v[4], v[5], v[6], v[7]};
+        const f32x4n a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
+        f32x4n *q = (f32x4n *)p;
+        if constexpr (STREAM) {
+            __builtin_nontemporal_store(a, q);
+            __builtin_nontemporal_store(b, q + 1);
+        } else {
+            q[0] = a;
+            q[1] = b;
+        }
     } else {
         *p = v[0];
     }
 }
-template <int VEC>
+template <int VEC, bool STREAM = false>
 __device__ __forceinline__ void st_vec(uint16_t *p, const float (&v)[VEC]) {
     if constexpr (VEC == 8) {
         typedef __bf16 bf16x8n __attribute__((ext_vector_type(8)));
         bf16x8n o;
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] = (__bf16)v[i];
-        *(bf16x8n *)p = o;
+        if constexpr (STREAM) __builtin_nontemporal_store(o, (bf16x8n *)p);
+        else *(bf16x8n *)p = o;
     } else {
         st_act(p, 0, v[0]);
     }
@@ -247,7 +261,7 @@ __global__ __launch_bounds__(block_threads(TPR)) void add_norm_bwd_kernel(AddNor
 // u = x silu(z) and the factors of its gradient.
 __device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + fast_exp2(-z * kLog2e)); }
 
-template <int TPR, int VEC, int ITER, typename T>
+template <int TPR, int VEC, int ITER, typename T, bool STREAM>
 __global__ __launch_bounds__(block_threads(TPR)) void gate_norm_fwd_kernel(GateNormArgs a) {
     constexpr int RPB = block_threads(TPR) / TPR;
     __shared__ float sh[2][16][1];
@@ -264,8 +278,8 @@ __global__ __launch_bounds__(block_threads(TPR)) void gate_norm_fwd_kernel(GateN
             const int c = (k * TPR + lane) * VEC;
             if (c < Dg) {
                 float x[VEC], z[VEC];
-                ld_vec<VEC>(xp + c, x);
-                ld_vec<VEC>(zp + c, z);
+                ld_vec<VEC, STREAM>(xp + c, x);
+                ld_vec<VEC, STREAM>(zp + c, z);
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
                     u[k][i] = x[i] * silu(z[i]);
@@ -283,7 +297,7 @@ __global__ __launch_bounds__(block_threads(TPR)) void gate_norm_fwd_kernel(GateN
                 ld_vec<VEC>(a.weight + g0 + c, w);
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) y[i] = u[k][i] * rstd * w[i];
-                st_vec<VEC>(yp + c, y);
+                st_vec<VEC, STREAM>(yp + c, y);
             }
         }
     }
@@ -436,8 +450,11 @@ hipError_t add_bwd(const AddNormArgs &a, hipStream_t s) {
 
 template <int TPR, int VEC, int ITER, typename T>
 hipError_t gate_fwd_n(const GateNormArgs &a, hipStream_t s) {
-    hipLaunchKernelGGL((gate_norm_fwd_kernel<TPR, VEC, ITER, T>),
-                       dim3(norm_grid(a.rows, TPR, 8192), (unsigned)a.groups), dim3(block_threads(TPR)), 0, s, a);
+    const dim3 grid(norm_grid(a.rows, TPR, 8192), (unsigned)a.groups);
+    if (VEC == 8 && a.rows * a.D * (int64_t)sizeof(T) > kStreamBytes)
+        hipLaunchKernelGGL((gate_norm_fwd_kernel<TPR, VEC, ITER, T, VEC == 8>), grid, dim3(block_threads(TPR)), 0, s, a);
+    else
+        hipLaunchKernelGGL((gate_norm_fwd_kernel<TPR, VEC, ITER, T, false>), grid, dim3(block_threads(TPR)), 0, s, a);
     return hipGetLastError();
 }
 template <int TPR, int VEC, int ITER, typename T>
