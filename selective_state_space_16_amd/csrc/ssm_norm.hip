@@ -388,21 +388,39 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(const float *part, in
 }
 
 // Lanes per row and elements per lane by the row's length: a wave per row as
-// long as it holds at most 40 elements per lane (2560 channels), then a
-// workgroup of 4 or 16 waves. VEC = 1 where rows are not whole 16-byte pieces.
-#define SSM_NORM_DISPATCH(LEN, VEC8, CALL)                      \
+// long as it holds at most 24 elements per lane (1536 channels), then a
+// workgroup of as many waves as give each lane 8. VEC = 1 where rows are not
+// whole 16-byte pieces.
+//
+// Both sides at rows of 84 MB of bfloat16 (float32 residual), us: add norm
+// forward / backward, gate norm forward / backward,
+//   1536   a wave, 24 per lane       99 133  42  96     3 waves, 8 per lane    97 144  40 135
+//   2048   a wave, 32 per lane      103 134  49  98     4 waves                94 132  42 102
+//   2560   a wave, 40 per lane      103 137  44 102     5 waves                94 134  40  98
+//   4096   4 waves, 16 per lane      94 136  43 107     8 waves                90 133  42  92
+//   5120   4 waves, 24 per lane      98 141  44 120     10 waves               93 141  48  93
+//   8192   4 waves, 32 per lane     100 138  42 105     16 waves               95 137  41  97
+// Only the gate norm's forward pass keeps 4 waves for rows above 4096 (FEW):
+// 32768 rows of 5120 channels take 173 us so and 182 with 10 waves.
+#define SSM_NORM_DISPATCH(LEN, VEC8, FEW, CALL)                 \
     do {                                                        \
         const int64_t n_ = (LEN);                               \
         if (VEC8) {                                             \
             if (n_ <= 512) return CALL(64, 8, 1);               \
             if (n_ <= 1024) return CALL(64, 8, 2);              \
             if (n_ <= 1536) return CALL(64, 8, 3);              \
-            if (n_ <= 2048) return CALL(64, 8, 4);              \
-            if (n_ <= 2560) return CALL(64, 8, 5);              \
-            if (n_ <= 4096) return CALL(256, 8, 2);             \
-            if (n_ <= 6144) return CALL(256, 8, 3);             \
-            if (n_ <= 8192) return CALL(256, 8, 4);             \
-            return CALL(1024, 8, 2);                            \
+            if (n_ <= 2048) return CALL(256, 8, 1);             \
+            if (n_ <= 2560) return CALL(320, 8, 1);             \
+            if (n_ <= 4096) return CALL(512, 8, 1);             \
+            if (n_ > 8192) return CALL(1024, 8, 2);             \
+            if constexpr (FEW) {                                \
+                if (n_ <= 6144) return CALL(256, 8, 3);         \
+                return CALL(256, 8, 4);                         \
+            } else {                                            \
+                if (n_ <= 5120) return CALL(640, 8, 1);         \
+                if (n_ <= 6144) return CALL(768, 8, 1);         \
+                return CALL(1024, 8, 1);                        \
+            }                                                   \
         }                                                       \
         if (n_ <= 256) return CALL(64, 1, 4);                   \
         if (n_ <= 1024) return CALL(64, 1, 16);                 \
@@ -424,7 +442,7 @@ hipError_t add_fwd_n(const AddNormArgs &a, hipStream_t s) {
 template <typename T, typename R>
 hipError_t add_fwd(const AddNormArgs &a, hipStream_t s) {
 #define SSM_CALL(TPR, VEC, ITER) add_fwd_n<TPR, VEC, ITER, T, R>(a, s)
-    SSM_NORM_DISPATCH(a.D, a.D % 8 == 0, SSM_CALL);
+    SSM_NORM_DISPATCH(a.D, a.D % 8 == 0, false, SSM_CALL);
 #undef SSM_CALL
 }
 
@@ -444,7 +462,7 @@ hipError_t add_bwd_n(const AddNormArgs &a, hipStream_t s) {
 template <typename T, typename R>
 hipError_t add_bwd(const AddNormArgs &a, hipStream_t s) {
 #define SSM_CALL(TPR, VEC, ITER) add_bwd_n<TPR, VEC, ITER, T, R>(a, s)
-    SSM_NORM_DISPATCH(a.D, a.D % 8 == 0, SSM_CALL);
+    SSM_NORM_DISPATCH(a.D, a.D % 8 == 0, false, SSM_CALL);
 #undef SSM_CALL
 }
 
@@ -472,13 +490,13 @@ bool gate_vec(const GateNormArgs &a) {
 template <typename T>
 hipError_t gate_fwd(const GateNormArgs &a, hipStream_t s) {
 #define SSM_CALL(TPR, VEC, ITER) gate_fwd_n<TPR, VEC, ITER, T>(a, s)
-    SSM_NORM_DISPATCH(a.D / a.groups, gate_vec(a), SSM_CALL);
+    SSM_NORM_DISPATCH(a.D / a.groups, gate_vec(a), true, SSM_CALL);
 #undef SSM_CALL
 }
 template <typename T>
 hipError_t gate_bwd(const GateNormArgs &a, hipStream_t s) {
 #define SSM_CALL(TPR, VEC, ITER) gate_bwd_n<TPR, VEC, ITER, T>(a, s)
-    SSM_NORM_DISPATCH(a.D / a.groups, gate_vec(a), SSM_CALL);
+    SSM_NORM_DISPATCH(a.D / a.groups, gate_vec(a), false, SSM_CALL);
 #undef SSM_CALL
 }
 
