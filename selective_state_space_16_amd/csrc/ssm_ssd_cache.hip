@@ -164,7 +164,8 @@ __device__ __forceinline__ int find_seq(const SsdCacheArgs &a, uint32_t id, uint
 template <int N>
 struct PrepShared {
     static constexpr int R = N + 8;
-    // high parts, and the low parts of B, then those of C: three of these workgroups fit a CU
+    // high parts, and the low parts of B, then those of C: with one array less
+    // than operands two workgroups of 1024 threads share a CU beside their LDS
     alignas(16) _Float16 Bh[kQ][R], Ch[kQ][R], lo[kQ][R];
     float maxb[16];
     int ec[kQ];
@@ -224,6 +225,11 @@ __device__ __forceinline__ void chunk_decays(const SsdCacheArgs &a, uint32_t id,
     }
 }
 
+// Bound by latency and by its stores of 1.3 KB per (chunk, head) and 58 KB per
+// (chunk, group) together: 10 us for one chunk, 22 us for 16384 tokens of 80
+// heads (52 MB), 39 us for 32768. The heads' decays have workgroups of their
+// own, so that a short prompt waits for neither: done by the workgroups that
+// convolve B and C, one chunk took 11.4 us, 16384 tokens 22.9 and 32768 tokens 44.
 template <int N>
 __global__ __launch_bounds__(prep_threads(N)) void prepare_kernel(SsdCacheArgs a) {
     __shared__ PrepShared<N> sh;
@@ -450,9 +456,16 @@ __device__ __forceinline__ void pieces(const void *src, const void *to_lds, int 
 constexpr int pieces_b(int N) { return 2 * kQ * N / 512; }
 constexpr int pieces_cg(int N) { return (kQ * N + kQ * kQ) / 512; }
 
-// Walk A: x, and the segment's end state. Bound by the vector ALU (the
-// convolution and SiLU, the splitting of operands); the products run beside it.
-// B of two chunks is held in LDS, so that two workgroups share a CU.
+// Walk A: x, and the segment's end state. B of two chunks is held in LDS, so that
+// two workgroups share a CU, two waves a SIMD.
+//
+// Bound by instruction issue: per chunk and wave the convolution and SiLU of 32
+// values a lane, their split into two float16 and 96 products (N = 128), from
+// two waves per SIMD, which is what the state's 64 registers and the operands
+// leave room for (225 of 256). 16384 tokens of 80 heads: 124 us for 168 MB of x
+// read and as much written, half the rate of a copy. Workgroups of 6 waves (which
+// do not pair up on a CU) took 197 us, of 12 waves 155; B read just ahead of its
+// use 126.
 template <int N>
 __global__ __launch_bounds__(128 * kBlocksA, 2) void walk_state_kernel(SsdCacheArgs a) {
     constexpr int NT = N / 16;
@@ -734,6 +747,8 @@ __global__ __launch_bounds__(128 * kBlocksA, 2) void walk_state_kernel(SsdCacheA
     if (lane == 0) a.ws_segdec[(int64_t)u.sid * H + u.h] = segdec;
 }
 
+// Bound by HBM: 63 MB of segment states in 13 us (16384 tokens, 80 heads, 12
+// segments), 267 MB in 41 us (eight prompts of 4096).
 // enter[k] in place of end[k]: enter[0] the sequence's first state, enter[k+1] =
 // dec[k] enter[k] + end[k]; the last one goes into the cache.
 __global__ __launch_bounds__(256) void join_kernel(SsdCacheArgs a, int N) {
@@ -761,7 +776,13 @@ __global__ __launch_bounds__(256) void join_kernel(SsdCacheArgs a, int N) {
 // one chunk (the masked product, y, the state) and begins the next one (C S^T and
 // the masked matrix), so that one barrier per chunk is enough and products and
 // vector instructions of both stand side by side; B, C, G and the decays are
-// held twice and loaded a whole iteration ahead. One workgroup fills a CU.
+// held twice and loaded a whole iteration ahead. One workgroup fills a CU (160 KB
+// of LDS at N = 128).
+//
+// Bound by instruction issue, as walk A: 48 products for y and 32 for the state
+// per chunk and wave, the masked matrix's exponentials (16 per lane), the
+// operands' LDS reads. 16384 tokens of 80 heads: 112 us; with two barriers per
+// chunk and operands read at their use 126. 6 waves per workgroup 188, 12 waves 140.
 template <int N>
 __global__ __launch_bounds__(128 * kBlocksC, 2) void walk_out_kernel(SsdCacheArgs a) {
     constexpr int NT = N / 16, KB = N / 32, WAVES = 2 * kBlocksC;
