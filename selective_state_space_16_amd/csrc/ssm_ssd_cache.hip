@@ -146,6 +146,7 @@ __device__ __forceinline__ uint32_t seq_length(const SsdCacheArgs &a, uint32_t s
 // with cu[s] / unit + s <= id), or -1: 64 candidates at a time, one per lane.
 __device__ __forceinline__ int find_seq(const SsdCacheArgs &a, uint32_t id, uint32_t unit) {
     uint32_t lo = 0, n = (uint32_t)a.seqs;
+    if (n == 1) return 0;
     const uint32_t lane = threadIdx.x & 63;
     do {
         const uint32_t step = (n + 63) / 64, at = lane * step;
@@ -164,9 +165,7 @@ __device__ __forceinline__ int find_seq(const SsdCacheArgs &a, uint32_t id, uint
 template <int N>
 struct PrepShared {
     static constexpr int R = N + 8;
-    // high parts, and the low parts of B, then those of C: with one array less
-    // than operands two workgroups of 1024 threads share a CU beside their LDS
-    alignas(16) _Float16 Bh[kQ][R], Ch[kQ][R], lo[kQ][R];
+    alignas(16) _Float16 Bh[kQ][R], Bl[kQ][R], Ch[kQ][R], Cl[kQ][R];  // high and low parts
     float maxb[16];
     int ec[kQ];
 };
@@ -226,10 +225,12 @@ __device__ __forceinline__ void chunk_decays(const SsdCacheArgs &a, uint32_t id,
 }
 
 // Bound by latency and by its stores of 1.3 KB per (chunk, head) and 58 KB per
-// (chunk, group) together: 10 us for one chunk, 22 us for 16384 tokens of 80
-// heads (52 MB), 39 us for 32768. The heads' decays have workgroups of their
-// own, so that a short prompt waits for neither: done by the workgroups that
-// convolve B and C, one chunk took 11.4 us, 16384 tokens 22.9 and 32768 tokens 44.
+// (chunk, group) together: 9.1 us for one chunk (3 of them an empty launch, 1.6
+// the loads and the convolution, the rest LDS and its barriers: with the low
+// parts of B and C in one array in turn 10.0), 22 us for 16384 tokens of 80 heads
+// (52 MB), 38 us for 32768. The heads' decays have workgroups of their own, so
+// that a short prompt waits for neither: done by the workgroups that convolve B
+// and C, one chunk took 2 us more, 16384 tokens the same and 32768 tokens 5 more.
 template <int N>
 __global__ __launch_bounds__(prep_threads(N)) void prepare_kernel(SsdCacheArgs a) {
     __shared__ PrepShared<N> sh;
@@ -248,13 +249,14 @@ __global__ __launch_bounds__(prep_threads(N)) void prepare_kernel(SsdCacheArgs a
     const uint32_t id = blk / (decays ? per : (uint32_t)a.G), g = blk % (decays ? per : (uint32_t)a.G);
     const int s = find_seq(a, id, kQ);
     if (s < 0) return;
+    // all of the sequence's words at once, ahead of the branches
+    const int32_t slot = a.slots[s], flag = a.resume ? a.resume[s] : 0;
     const uint32_t begin = seq_begin(a, s), len = seq_length(a, s, begin);
     const uint32_t first = (id - (begin / kQ + s)) * kQ;  // token of the sequence
     if (first >= len) return;
     const int rem = len - first < kQ ? (int)(len - first) : kQ;
-    const int32_t slot = a.slots[s];
-    const bool resume = a.resume && a.resume[s] != 0 && slot >= 0 && slot < a.num_slots;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const bool resume = flag != 0 && slot >= 0 && slot < a.num_slots;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     if (decays) {
         chunk_decays(a, id, begin + first, rem, g * HEADS + wave * 2);
         return;
@@ -316,76 +318,65 @@ __global__ __launch_bounds__(prep_threads(N)) void prepare_kernel(SsdCacheArgs a
 #pragma unroll
     for (int k = 0; k < WAVES; ++k) big = __builtin_fmaxf(big, sh.maxb[k]);
     const int eB = clampi(exponent(big), -100, 128);
-    f16x4 low[TPB];
 #pragma unroll
     for (int i = 0; i < TPB; ++i) {
         const int e = 7 - (isC ? sh.ec[t0 + i] : eB);
-        f16x4 hi;
+        f16x4 hi, low;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             float t = __builtin_ldexpf(v[i][k], e);
             asm("" : "+v"(t));
             hi[k] = (_Float16)t;
-            low[i][k] = (_Float16)(t - (float)hi[k]);
+            low[k] = (_Float16)(t - (float)hi[k]);
         }
         *(f16x4 *)(isC ? &sh.Ch[t0 + i][n0] : &sh.Bh[t0 + i][n0]) = hi;
-        if (!isC) *(f16x4 *)&sh.lo[t0 + i][n0] = low[i];
+        *(f16x4 *)(isC ? &sh.Cl[t0 + i][n0] : &sh.Bl[t0 + i][n0]) = low;
     }
     __syncthreads();
 
     _Float16 *out = (_Float16 *)a.ws_frag + ((int64_t)id * a.G + g) * frag_elems(N);
     const int r = lane & 15, q = lane >> 4;
-    // B^T as A operands, (h, nt): row n = 16 nt + r, k = token 16 q + 8 h + j
-    for (int f = wave; f < 2 * (N / 16); f += WAVES) {
-        const int h = f / (N / 16), nt = f % (N / 16);
+    // Each wave forms one of B^T's operands, (h, nt): row n = 16 nt + r, k = token
+    // 16 q + 8 h + j;
+    static_assert(2 * (N / 16) == WAVES && 4 * (N / 32) == WAVES);
+    {
+        const int h = wave / (N / 16), nt = wave % (N / 16);
         f16x8 hi, lo;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             hi[j] = sh.Bh[16 * q + 8 * h + j][16 * nt + r];
-            lo[j] = sh.lo[16 * q + 8 * h + j][16 * nt + r];
+            lo[j] = sh.Bl[16 * q + 8 * h + j][16 * nt + r];
         }
-        *(f16x8 *)(out + (f * 64 + lane) * 8) = hi;
-        *(f16x8 *)(out + kQ * N + (f * 64 + lane) * 8) = lo;
+        *(f16x8 *)(out + (wave * 64 + lane) * 8) = hi;
+        *(f16x8 *)(out + kQ * N + (wave * 64 + lane) * 8) = lo;
     }
-    // C as A operands, (tt, m): row r is token 16 (r / 4) + 4 tt + r % 4, and k
-    // runs over n in the order in which two accumulator tiles hold the state
+    // one of C's, (tt, m): row r is token 16 (r / 4) + 4 tt + r % 4, and k runs
+    // over n in the order in which two accumulator tiles hold the state;
     const int row = 16 * (r / 4) + r % 4;
-    for (int f = wave; f < 4 * (N / 32); f += WAVES) {
-        const int tt = f / (N / 32), m = f % (N / 32);
+    {
+        const int tt = wave / (N / 32), m = wave % (N / 32);
         const _Float16 *src = &sh.Ch[row + 4 * tt][32 * m + 4 * q];
         const f16x4 lo = *(const f16x4 *)src, hi = *(const f16x4 *)(src + 16);
-        *(f16x8 *)(out + 2 * kQ * N + (f * 64 + lane) * 8) = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        *(f16x8 *)(out + 2 * kQ * N + (wave * 64 + lane) * 8) = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     }
-    // G as A operands, (tt, h): row r as in C, k = token s = 16 q + 8 h + j. A
-    // wave forms one or two of the sixteen products (tt, h, b), whose row 4 q + e
-    // is token 16 q + 8 h + 4 b + e.
+    // and of G's, (tt, h) with row r as in C and k = token s = 16 q + 8 h + j, one
+    // or two of the sixteen products (tt, h, b), whose row 4 q + e is token
+    // 16 q + 8 h + 4 b + e.
     constexpr int PER = 16 / WAVES;
-    f32x4 acc[PER];
-#pragma unroll
-    for (int k = 0; k < PER; ++k) {
-        const int f = wave * PER + k, tt = f / 4, sr = row + 4 * (f % 4);
-        acc[k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int m = 0; m < N / 32; ++m) {
-            const f16x8 ch = *(const f16x8 *)&sh.Ch[row + 4 * tt][32 * m + 8 * q];
-            acc[k] = mfma(*(const f16x8 *)&sh.Bh[sr][32 * m + 8 * q], ch, acc[k]);
-            acc[k] = mfma(*(const f16x8 *)&sh.lo[sr][32 * m + 8 * q], ch, acc[k]);
-        }
-    }
-    __syncthreads();
-    if (isC)
-#pragma unroll
-        for (int i = 0; i < TPB; ++i) *(f16x4 *)&sh.lo[t0 + i][n0] = low[i];
-    __syncthreads();
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
         const int f = wave * PER + k, tt = f / 4, sr = row + 4 * (f % 4), s0 = 16 * q + 4 * (f % 4);
+        f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int m = 0; m < N / 32; ++m)
-            acc[k] = mfma(*(const f16x8 *)&sh.Bh[sr][32 * m + 8 * q], *(const f16x8 *)&sh.lo[row + 4 * tt][32 * m + 8 * q], acc[k]);
+        for (int m = 0; m < N / 32; ++m) {
+            const f16x8 ch = *(const f16x8 *)&sh.Ch[row + 4 * tt][32 * m + 8 * q], bh = *(const f16x8 *)&sh.Bh[sr][32 * m + 8 * q];
+            acc = mfma(bh, *(const f16x8 *)&sh.Cl[row + 4 * tt][32 * m + 8 * q], acc);
+            acc = mfma(*(const f16x8 *)&sh.Bl[sr][32 * m + 8 * q], ch, acc);
+            acc = mfma(bh, ch, acc);
+        }
         f16x4 o;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = s0 + e <= row + 4 * tt ? (_Float16)(acc[k][e] * 0x1p-7f) : (_Float16)0.0f;
+        for (int e = 0; e < 4; ++e) o[e] = s0 + e <= row + 4 * tt ? (_Float16)(acc[e] * 0x1p-7f) : (_Float16)0.0f;
         *(f16x4 *)(out + 3 * kQ * N + ((f / 2) * 64 + lane) * 8 + 4 * (f % 2)) = o;
     }
     if (tid < kQ) ((float *)(out + 3 * kQ * N + kQ * kQ))[tid] = __builtin_ldexpf(1.0f, sh.ec[tid]);
@@ -403,6 +394,8 @@ __global__ __launch_bounds__(prep_threads(N)) void prepare_kernel(SsdCacheArgs a
 struct Unit {
     uint32_t begin, len, k, nseg, from, to, g, hb, h, hfirst, ch0, sid, chunk0;
     int s;
+    int32_t slot;
+    bool resume;
     bool on;    // the wave has columns
     bool some;  // there is anything to do
 };
@@ -425,6 +418,9 @@ __device__ __forceinline__ Unit find_unit(const SsdCacheArgs &a) {
     u.hb = unit % nhb;
     u.s = find_seq(a, u.sid, seg);
     if (u.s < 0) return u;
+    // all of the sequence's words at once, ahead of the branches
+    u.slot = a.ws_slot[u.s];
+    u.resume = a.resume && a.resume[u.s] != 0;
     u.begin = seq_begin(a, u.s);
     u.len = seq_length(a, u.s, u.begin);
     u.k = u.sid - (u.begin / seg + u.s);
@@ -477,43 +473,9 @@ __global__ __launch_bounds__(128 * kBlocksA, 2) void walk_state_kernel(SsdCacheA
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), r = lane & 15, q = lane >> 4;
     const Unit u = find_unit<kBlocksA>(a);
     if (!u.some) return;
-    const int32_t slot = a.ws_slot[u.s];
+    const int32_t slot = u.slot;
     if (slot < 0) return;
     const uint32_t from = u.from, to = u.to, H = (uint32_t)a.H, G = (uint32_t)a.G;
-
-    // the state: acc[nt][c][e] = S[p = 2 r + c][n = 16 nt + 4 q + e] 2^-K, from
-    // the cache where the sequence is one segment and resumes
-    f32x4 acc[NT][2];
-    int K = 0;
-    float bound = 0.0f;  // of |acc|
-    const int64_t off = (int64_t)(u.ch0 + 2 * r) * N + 4 * q, hpn = a.H * a.P * N;
-    const bool resume = a.resume && a.resume[u.s] != 0, one = u.nseg == 1;
-    float *const cache = a.state_cache + (int64_t)slot * hpn + off;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) acc[nt][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    if (one && resume && u.on) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                acc[nt][c] = *(const f32x4 *)(cache + c * N + 16 * nt);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) bound = __builtin_fmaxf(bound, finite_abs(acc[nt][c][e]));
-            }
-        bound = wave_top(bound);
-        if (bound > 0.0f) {
-            K = uniform(exponent(bound));
-            bound = 1.0f;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[nt][c][e] = __builtin_ldexpf(acc[nt][c][e], -K);
-        }
-    }
 
     // The convolution times -log2(e): its exp2 is SiLU's exponential, and the
     // factor comes out again with the scales.
@@ -568,6 +530,40 @@ __global__ __launch_bounds__(128 * kBlocksA, 2) void walk_state_kernel(SsdCacheA
     if (from < to) {
         stage(from);
         if (u.on) load(from);
+    }
+
+    // the state: acc[nt][c][e] = S[p = 2 r + c][n = 16 nt + 4 q + e] 2^-K, from
+    // the cache where the sequence is one segment and resumes
+    f32x4 acc[NT][2];
+    int K = 0;
+    float bound = 0.0f;  // of |acc|
+    const int64_t off = (int64_t)(u.ch0 + 2 * r) * N + 4 * q, hpn = a.H * a.P * N;
+    const bool resume = u.resume, one = u.nseg == 1;
+    float *const cache = a.state_cache + (int64_t)slot * hpn + off;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) acc[nt][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (one && resume && u.on) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                acc[nt][c] = *(const f32x4 *)(cache + c * N + 16 * nt);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) bound = __builtin_fmaxf(bound, finite_abs(acc[nt][c][e]));
+            }
+        bound = wave_top(bound);
+        if (bound > 0.0f) {
+            K = uniform(exponent(bound));
+            bound = 1.0f;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[nt][c][e] = __builtin_ldexpf(acc[nt][c][e], -K);
+        }
     }
     for (uint32_t t = from; t < to; t += kQ) {
         const int b = (int)((t - from) / kQ & 1);
@@ -798,7 +794,7 @@ __global__ __launch_bounds__(128 * kBlocksC, 2) void walk_out_kernel(SsdCacheArg
     const Unit u = find_unit<kBlocksC>(a);
     if (!u.some) return;
     const uint32_t from = u.from, to = u.to, H = (uint32_t)a.H, G = (uint32_t)a.G;
-    const int32_t slot = a.ws_slot[u.s];
+    const int32_t slot = u.slot;
     const uint32_t yrow = (uint32_t)(a.H * a.P) * 2;
     if (slot < 0) {
         if (u.on)
@@ -842,7 +838,7 @@ __global__ __launch_bounds__(128 * kBlocksC, 2) void walk_out_kernel(SsdCacheArg
     // the state: acc[nt][c][e] = S[p = 2 r + c][n = 16 nt + 4 q + e] 2^-K, kept
     // below 2^15 by its bound, so that its float16 copy needs no scale of its own
     const int64_t off = (int64_t)(u.ch0 + 2 * r) * N + 4 * q, hpn = a.H * a.P * N;
-    const bool resume = a.resume && a.resume[u.s] != 0, one = u.nseg == 1;
+    const bool resume = u.resume, one = u.nseg == 1;
     float *const cache = a.state_cache + (int64_t)slot * hpn + off;
     const float *const own = a.ws_state + (int64_t)u.sid * hpn + off;
     if (u.on && from < to) {
