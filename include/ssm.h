@@ -634,8 +634,9 @@ size_t ssm_ssd_fwd_cache_workspace_bytes(int64_t seqs, int64_t rows, int64_t H, 
  * tensors; what such a call computes is otherwise unspecified.
  *
  * Supported: dtype SSM_BF16, P = 64, 128, 192 or 256, N = 64 or 128, at most
- * 65535 sequences, rows within 2^31 - 1, strides below 2^23 elements; anything
- * else returns SSM_ERR_UNSUPPORTED. H must be a multiple of G, strides at
+ * 65535 sequences, rows within 2^31 - 1, strides below 2^23 elements, launches
+ * of less than 2^32 threads (80 heads: 10^7 tokens); anything else returns
+ * SSM_ERR_UNSUPPORTED. H must be a multiple of G, strides at
  * least the row's width (else SSM_ERR_SHAPE), rows of xBC whole 16-byte pieces
  * apart (else SSM_ERR_ALIGN). Conventions otherwise as above.
  */
@@ -734,8 +735,8 @@ int ssm_add_norm_bwd(int64_t rows, int64_t D, int dtype, int res_dtype, const vo
  *   y             (rows, D)      dtype      written, dense; may equal a dense x
  *
  * D must be a multiple of groups and the strides at least D (else
- * SSM_ERR_SHAPE); D / groups at most 16384 and groups at most 65535 (else
- * SSM_ERR_UNSUPPORTED).
+ * SSM_ERR_SHAPE); D / groups at most 16384, groups at most 65535 and D
+ * below 2^28 (else SSM_ERR_UNSUPPORTED).
  */
 int ssm_gate_norm_fwd(int64_t rows, int64_t D, int64_t groups, int dtype, const void *x, int64_t x_stride,
                       const void *z, int64_t z_stride, const float *weight, float eps, void *y, void *stream);

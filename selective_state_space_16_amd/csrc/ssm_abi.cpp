@@ -77,6 +77,7 @@ size_t workspace_for(int64_t batch, int64_t L, int64_t D, int64_t N, int dtype) 
                                                                : twopass_workspace(batch, L, D, N, &K, &Lc);
 }
 
+constexpr int64_t kMaxNorm = (int64_t)1 << 28;  // channels that one launch of the gradients' reduction reaches
 constexpr int64_t kMaxRow = (int64_t)1 << 23;  // elements between rows of the cache entry points' inputs
 
 // Sizes the SSD layer on a cache takes: heads of 64 to 256 in whole 64s, N of
@@ -84,7 +85,11 @@ constexpr int64_t kMaxRow = (int64_t)1 << 23;  // elements between rows of the c
 bool ssd_cache_sizes(int64_t seqs, int64_t rows, int64_t H, int64_t P, int64_t G, int64_t N) {
     if (P < 64 || P > 256 || P % 64 != 0 || (N != 64 && N != 128)) return false;
     if (seqs > 65535 || rows > INT32_MAX || H >= kMaxRow / P || G >= kMaxRow / (2 * N)) return false;
-    return H * P + 2 * G * N < kMaxRow && rows / 64 + seqs <= INT32_MAX / ((H * P) / 64 + 1);
+    const int64_t C = H * P + 2 * G * N, chunks = rows / 64 + seqs;
+    // threads of a launch: per chunk of 64 tokens (or request) and group, 16
+    // heads, or 64 rows of a head's state
+    return C < kMaxRow && (chunks * (G + H / 16 + 1) + seqs * (C / 512 + 1)) * 1024 <= UINT32_MAX &&
+           chunks * (H * P / 64 * 256 + G * 512) <= UINT32_MAX;
 }
 
 // Floats per request in the step's workspace: x | B | C, dt and exp(dt A),
@@ -827,7 +832,7 @@ static int norm_check(int64_t rows, int64_t D, int64_t groups, int dtype) {
     if (rows < 0 || D < 0 || groups < 0) return SSM_ERR_SHAPE;
     if (dtype != SSM_F32 && dtype != SSM_BF16) return SSM_ERR_DTYPE;
     if (D > 0 && (groups < 1 || D % groups != 0)) return SSM_ERR_SHAPE;
-    if (D > 0 && (D / groups > ssm::kNormMaxWidth || groups > 65535)) return SSM_ERR_UNSUPPORTED;
+    if (D > 0 && (D / groups > ssm::kNormMaxWidth || groups > 65535 || D >= kMaxNorm)) return SSM_ERR_UNSUPPORTED;
     return checked_mul(rows, D) < 0 ? SSM_ERR_SHAPE : SSM_OK;
 }
 

@@ -207,7 +207,12 @@ __device__ __forceinline__ void chunk_decays(const SsdCacheArgs &a, uint32_t id,
         if (h0 + k >= H) break;
         const int64_t at = (int64_t)id * H + h0 + k;
         const float dt = lane < rem ? softplus(raw[k] + bias[k]) : 0.0f;
-        const float step = dt * A2[k];
+        // A decay of 2^-256 leaves nothing of a float32 state: no more than that,
+        // so that the sums keep bits for the tokens behind (2^14 at most). A step
+        // that is not finite is a NaN from here on, not a decay to nothing.
+        float step = dt * A2[k];
+        step = step < -256.0f ? -256.0f : step;
+        if (!finite(dt)) step = __builtin_nanf("");
         const float cum = wave_prefix_sum(step);
         // from the end, without subtracting: exact where little decays
         const float back = wave_prefix_sum(__shfl(step, 63 - lane));
@@ -729,7 +734,8 @@ __global__ __launch_bounds__(128 * kBlocksA, 2) void walk_state_kernel(SsdCacheA
     }
     if (!u.on) return;
     // A sequence of one segment that does not resume is done; one that does is
-    // stored aside, as walk C still reads its first state; others are joined.
+    // stored aside, as walk C still reads its first state (without tokens it
+    // keeps its bits); others are joined.
     float *dst = one && !resume ? cache : a.ws_state + (int64_t)u.sid * hpn + off;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -1118,7 +1124,7 @@ __global__ __launch_bounds__(128 * kBlocksC, 2) void walk_out_kernel(SsdCacheArg
     }
 
     if (u.k != u.nseg - 1) return;
-    if (u.on && one && resume) {
+    if (u.on && one && resume && from < to) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

@@ -148,3 +148,12 @@ def test_binding_refuses_cpu_tensors():
                                torch.zeros(2, dtype=i32), torch.zeros(3, 314, 3), torch.zeros(3, 1, 64, 128))
     with pytest.raises(TypeError):
         ssm.ssm_add_norm_fwd(torch.zeros(3, 64, dtype=torch.float16), w)
+
+
+def test_grids_that_no_launch_reaches():
+    """Sizes within every other limit whose launches would have 2^32 threads."""
+    assert fwd(rows=(1 << 31) - 1, H=1, P=64, G=1, N=128, xs=320) == -4
+    assert step(batch=65535, H=16384, G=1, xs=16384 * 64 + 256, ds=16384) == -4
+    assert gate_bwd(rows=1, D=1 << 28, groups=1 << 15, xs=1 << 28, zs=1 << 28, dzs=1 << 28) == -4
+    assert ssm.ssm_ssd_fwd_cache_workspace_bytes(1, (1 << 31) - 1, 1, 64, 1, 128, 1) == 0
+    assert ssm.ssm_ssd_step_cache_workspace_bytes(65535, 16384, 64, 1, 128) == 0

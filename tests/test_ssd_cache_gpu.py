@@ -362,3 +362,74 @@ def test_large_cache_offsets():
     assert torch.equal(ys[0], ys[1]) and torch.equal(zs[0], zs[1]) and ys[0].abs().max() > 0
     assert torch.equal(st[0], st[-1]) and torch.equal(win[0], win[-1]) and not st[1:-1].any()
     del d
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("where", ["B", "C", "dt"])
+def test_nonfinite_shared_inputs(where, value):
+    """A NaN or infinity in one token's B, C or step size: the tokens before it,
+    the sequences around it and the heads that do not read it keep their bits;
+    its own y is not finite, and neither is the state that takes it up."""
+    say(f"case {where} {value}")
+    d = ssd_inputs([50, 100, 30], 2, 64, 2, 128, seed=21)
+    y0 = before(d)
+    g0 = to_gpu(d)
+    ref = prompt(g0, y0.cuda()).cpu()
+    d2 = dict(d, proj=d["proj"].clone())
+    col = {"B": 64 + 128 + 128 + 9, "C": 64 + 128 + 256 + 128 + 9, "dt": 64 + d["C"] + 1}[where]  # of group (head) 1
+    d2["proj"][50 + 40, col] = value  # sequence 1, token 40
+    g = to_gpu(d2)
+    y = prompt(g, y0.cuda()).cpu()
+    torch.cuda.synchronize()
+    assert torch.equal(y[:90], ref[:90]) and torch.equal(y[150:], ref[150:]) and torch.equal(y[:, 0], ref[:, 0])
+    slot = int(d["slots"][1])
+    if where == "C":  # three tokens more, through the convolution
+        assert not torch.isfinite(y[90:94, 1]).any() and torch.isfinite(y[94:]).all()
+        assert torch.equal(g["state_cache"].cpu(), g0["state_cache"].cpu())
+    elif where == "B":  # state column 9 of the head
+        assert not torch.isfinite(y[90:150, 1]).any()
+        assert not torch.isfinite(g["state_cache"][slot, 1, :, 9]).any()
+    else:
+        assert not torch.isfinite(y[90:150, 1]).any() and not torch.isfinite(g["state_cache"][slot, 1]).any()
+    assert torch.equal(g["state_cache"][slot, 0].cpu(), g0["state_cache"][slot, 0].cpu())
+
+
+def test_steps_that_forget_everything():
+    """Steps of 50 to 2000, whose summed decays have no bits left for a token's
+    own: a decay below 2^-256 leaves nothing of any float32 state, so summed
+    exponents of at most 2^14 are exact to 2^-10, one and a half of the eight
+    roundings of 2^-11 (the diagonal has six more). So tight a bound takes the
+    terms as they are behind the SiLU, (C . B) dt x + D x, and 32 float32
+    roundings of the convolution's absolute terms ahead of it."""
+    say("case forgetting steps")
+    d = ssd_inputs([200, 65], 4, 64, 2, 128, seed=22, step=(50.0, 2000.0))
+    g, y0 = to_gpu(d), before(d)
+    y = prompt(g, y0.cuda())
+    torch.cuda.synchronize()
+    compare(d, g, y, y0)
+    yr, _, _, ya, _ = ssd_reference(d, y0)
+    raw, dt = (t.double() for t in views(d))
+    u = sum(raw[j:j + 197] * d["conv_w"][:, j].double() for j in range(4)) + d["conv_b"].double()  # tokens 3 .. of the first
+    v = u * torch.sigmoid(u)
+    x, B, Cm = v[:, :256].view(-1, 4, 64), v[:, 256:512].view(-1, 2, 128), v[:, 512:].view(-1, 2, 128)
+    cb = (Cm * B).abs().sum(2).repeat_interleave(2, 1)[:, :, None]
+    step_size = torch.nn.functional.softplus(dt[3:200] + d["dt_bias"].double())[:, :, None]
+    terms = (cb * step_size + d["Dskip"].double()[:, None]) * x.abs()
+    err = (y[3:200].cpu().double() - yr[3:200]).abs()
+    tol = 2.0 ** -8 * yr[3:200].abs() + 8 * 2.0 ** -11 * terms + 32 * U * ya[3:200]
+    say(f"  worst of the tight bound {float((err / tol).max()):.2f}")
+    assert (err <= tol).all()
+
+
+def test_no_tokens_keep_the_slot():
+    """A resumed sequence of no tokens leaves its slot's bits, whatever it holds."""
+    say("case no tokens")
+    d = ssd_inputs([0, 5], 2, 64, 1, 64, seed=23)
+    d["resume"][:] = 1
+    s = int(d["slots"][0])
+    d["state_cache"][s, 0, 0, :4] = torch.tensor([1e-40, 1e30, float("nan"), -3e-39])
+    g, y0 = to_gpu(d), before(d)
+    prompt(g, y0.cuda())
+    torch.cuda.synchronize()
+    assert torch.equal(g["state_cache"][s].cpu().view(torch.int32), d["state_cache"][s].view(torch.int32))
+    assert torch.equal(g["conv_cache"][s].cpu().view(torch.int16), d["conv_cache"][s].view(torch.int16))
