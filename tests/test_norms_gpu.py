@@ -256,3 +256,12 @@ def test_many_elements():
     torch.cuda.synchronize()
     assert torch.equal(y[-1000:], tail) and torch.equal(y[:1000], tail)
     assert rows == x.shape[0]
+
+
+@pytest.mark.parametrize("dtype", [BF, FL])
+@pytest.mark.parametrize("rows,D", [(70, 24), (33, 61), (257, 65), (40, 128), (41, 129), (31, 200), (5, 255), (600, 256), (9, 257)])
+def test_short_rows(rows, D, dtype):
+    """Rows that share a wave, in workgroups that they fill in part."""
+    test_add_norm(rows, D, dtype, True)
+    test_add_norm_gradient(rows, D, dtype, True)
+    test_gate_norm(rows, D, 2, dtype)
