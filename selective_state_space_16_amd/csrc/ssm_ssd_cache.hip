@@ -749,26 +749,39 @@ __global__ __launch_bounds__(128 * kBlocksA, 2) void walk_state_kernel(SsdCacheA
     if (lane == 0) a.ws_segdec[(int64_t)u.sid * H + u.h] = segdec;
 }
 
-// Bound by HBM: 63 MB of segment states in 13 us (16384 tokens, 80 heads, 12
-// segments), 267 MB in 41 us (eight prompts of 4096).
+// Bound by HBM where there are many heads: 63 MB of segment states in 13 us (16384
+// tokens, 80 heads, 12 segments), 267 MB in 41 us (eight prompts of 4096). With
+// few heads there are many segments, and the loads of one after the other are:
+// four ahead take a prompt batch of 21507 tokens, 8 heads, from 70 to 64 us.
 // enter[k] in place of end[k]: enter[0] the sequence's first state, enter[k+1] =
 // dec[k] enter[k] + end[k]; the last one goes into the cache.
 __global__ __launch_bounds__(256) void join_kernel(SsdCacheArgs a, int N) {
-    const uint32_t s = blockIdx.y, begin = seq_begin(a, s), len = seq_length(a, s, begin), seg = (uint32_t)a.seg;
-    const uint32_t nseg = (len + seg - 1) / seg;
-    const int32_t slot = a.ws_slot[s];
+    constexpr uint32_t kAhead = 4;  // segments loaded ahead of the chain
+    const uint32_t s = blockIdx.y, seg = (uint32_t)a.seg;
+    const int32_t slot = a.ws_slot[s], flag = a.resume ? a.resume[s] : 0;
+    const uint32_t begin = seq_begin(a, s), len = seq_length(a, s, begin), nseg = (len + seg - 1) / seg;
     if (nseg < 2 || slot < 0) return;
     const int64_t hpn = a.H * a.P * N, i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
     if (i >= hpn) return;
     const int64_t h = i / (a.P * N), first = begin / seg + s;
     float *const cache = a.state_cache + slot * hpn + i;
     f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (a.resume && a.resume[s] != 0) v = *(const f32x4 *)cache;
-    for (uint32_t k = 0; k < nseg; ++k) {
-        f32x4 *p = (f32x4 *)(a.ws_state + (first + k) * hpn + i);
-        const f32x4 end = *p;
-        *p = v;
-        v = end + v * a.ws_segdec[(first + k) * a.H + h];
+    if (flag != 0) v = *(const f32x4 *)cache;
+    for (uint32_t k0 = 0; k0 < nseg; k0 += kAhead) {
+        f32x4 end[kAhead];
+        float dec[kAhead];
+#pragma unroll
+        for (uint32_t j = 0; j < kAhead; ++j) {
+            const int64_t k = first + (k0 + j < nseg ? k0 + j : nseg - 1);
+            end[j] = *(const f32x4 *)(a.ws_state + k * hpn + i);
+            dec[j] = a.ws_segdec[k * a.H + h];
+        }
+#pragma unroll
+        for (uint32_t j = 0; j < kAhead; ++j) {
+            if (k0 + j >= nseg) break;
+            *(f32x4 *)(a.ws_state + (first + k0 + j) * hpn + i) = v;
+            v = end[j] + v * dec[j];
+        }
     }
     *(f32x4 *)cache = v;
 }
