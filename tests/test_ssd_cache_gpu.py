@@ -433,3 +433,23 @@ def test_no_tokens_keep_the_slot():
     torch.cuda.synchronize()
     assert torch.equal(g["state_cache"][s].cpu().view(torch.int32), d["state_cache"][s].view(torch.int32))
     assert torch.equal(g["conv_cache"][s].cpu().view(torch.int16), d["conv_cache"][s].view(torch.int16))
+
+
+@pytest.mark.parametrize("batch,N,dtype", [(161, 128, torch.bfloat16), (322, 64, torch.float32)])
+def test_steps_on_more_state_than_the_caches_hold(batch, N, dtype):
+    """A batch whose states pass through the caches equals its halves, whose stay."""
+    say(f"case step streamed batch={batch} N={N} {dtype}")
+    gen = torch.Generator(device="cuda").manual_seed(24)
+    H, P, G = 80, 64, 2
+    C, half = H * P + 2 * G * N, batch // 2
+    rnd = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    x, dt = rnd(batch, C).to(dtype), rnd(batch, H).to(dtype)
+    conv, state = rnd(batch, C, 3).to(dtype), rnd(batch, H, P, N)
+    slots = torch.randperm(batch, generator=gen, device="cuda").to(torch.int32)
+    A, w = -torch.rand(H, generator=gen, device="cuda") - 0.5, rnd(C, 4) * 0.3
+    conv2, state2 = conv.clone(), state.clone()
+    y = ssm.ssm_ssd_step_cache(x, dt, A, w, slots, conv, state)
+    parts = [ssm.ssm_ssd_step_cache(x[k].contiguous(), dt[k].contiguous(), A, w, slots[k].clone(), conv2, state2)
+             for k in (slice(0, half), slice(half, batch))]
+    torch.cuda.synchronize()
+    assert torch.equal(y, torch.cat(parts)) and torch.equal(conv, conv2) and torch.equal(state, state2)
