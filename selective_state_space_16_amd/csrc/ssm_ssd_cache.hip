@@ -463,10 +463,11 @@ constexpr int pieces_cg(int N) { return (kQ * N + kQ * kQ) / 512; }
 // Bound by instruction issue: per chunk and wave the convolution and SiLU of 32
 // values a lane, their split into two float16 and 96 products (N = 128), from
 // two waves per SIMD, which is what the state's 64 registers and the operands
-// leave room for (225 of 256). 16384 tokens of 80 heads: 124 us for 168 MB of x
+// leave room for (225 of 256). 16384 tokens of 80 heads: 117 us for 168 MB of x
 // read and as much written, half the rate of a copy. Workgroups of 6 waves (which
 // do not pair up on a CU) took 197 us, of 12 waves 155; B read just ahead of its
-// use 126.
+// use 126. Its SIMDs issue vector instructions (a fifth of their time exponentials
+// and reciprocals) in two thirds of the cycles and run products in a third.
 template <int N>
 __global__ __launch_bounds__(128 * kBlocksA, 2) void walk_state_kernel(SsdCacheArgs a) {
     constexpr int NT = N / 16;
@@ -698,6 +699,10 @@ __global__ __launch_bounds__(128 * kBlocksA, 2) void walk_state_kernel(SsdCacheA
                 }
             }
         };
+        // The convolution stands before the products of the SIMD's other wave: the
+        // matrix cores are then fed while it runs (16384 tokens 124 -> 117 us; the
+        // products first: 123).
+        __builtin_amdgcn_s_setprio(0);
         split_x(0);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -718,6 +723,7 @@ __global__ __launch_bounds__(128 * kBlocksA, 2) void walk_state_kernel(SsdCacheA
                         acc[nt + j][c] = mfma(k == 0 ? bl[g & 1][j] : bh[g & 1][j], k == 1 ? vl[c][hh] : vh[c][hh], acc[nt + j][c]);
             __builtin_amdgcn_sched_barrier(0);
         }
+        __builtin_amdgcn_s_setprio(1);
         if (anybad) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
@@ -1089,7 +1095,9 @@ __global__ __launch_bounds__(128 * kBlocksC, 2) void walk_out_kernel(SsdCacheArg
 #pragma unroll
                 for (int c = 0; c < 2; ++c) v[c][hh] = (x16[c][hh] * sf) * (wv[hh] * sw);
             __builtin_amdgcn_sched_barrier(0);
-            // the state's products, and in between y
+            // the state's products, and in between y: ahead of what the SIMD's other
+            // wave begins (eight prompts of 4096 tokens 255 -> 249 us)
+            __builtin_amdgcn_s_setprio(1);
             const float dx = __builtin_ldexpf(dsk, ex - 14);
             const auto yb = buffer((const char *)a.y + (int64_t)(u.begin + t) * yrow + u.ch0 * 2, (rem - 1) * yrow + 64);
             uint32_t yo = 16 * q * yrow + 4 * r;
@@ -1132,6 +1140,7 @@ __global__ __launch_bounds__(128 * kBlocksC, 2) void walk_out_kernel(SsdCacheArg
                             for (int e = 0; e < 4; ++e) acc[nt][c][e] = __builtin_nanf("");
                 }
             }
+            __builtin_amdgcn_s_setprio(0);
             if (more) begin_chunk(i + 1, of_ex(exbn), edn, eBn);
         }
     }
