@@ -65,7 +65,10 @@ constexpr int frag_elems(int N) { return 3 * kQ * N + kQ * kQ + 512; }
 // Floats per (chunk, head) for walk C: cum, cum - log2 dt, exp2(cum), and w as
 // scaled float16, filled up to 1 KiB.
 constexpr int kHead = 4 * kQ;
-constexpr int dt_heads(int N) { return prep_threads(N) / 32; }  // heads per workgroup of the decays, two a wave
+// Heads of a wave that forms decays (80 heads then take one workgroup per chunk at
+// N = 128: 16384 tokens 22.2 -> 18.5 us against two heads, a short prompt the same).
+constexpr int kDtHeads = 5;
+constexpr int dt_heads(int N) { return prep_threads(N) / 64 * kDtHeads; }
 
 __device__ __forceinline__ f32x4 mfma(f16x8 a, f16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
@@ -188,22 +191,21 @@ __device__ __forceinline__ void start_seq(const SsdCacheArgs &a, int64_t s, int6
             a.ws_win[(s * 3 + k) * a.C + c] = resume ? ((const uint16_t *)a.conv_cache)[((int64_t)slot * a.C + c) * 3 + k] : 0;
 }
 
-// The decays of the chunk for a wave's two heads h0 .., a lane per token.
+// The decays of the chunk for a wave's heads h0 .., a lane per token.
 __device__ __forceinline__ void chunk_decays(const SsdCacheArgs &a, uint32_t id, uint32_t row, int rem, uint32_t h0) {
-    constexpr int kPer = 2;
     const int lane = threadIdx.x & 63;
     const uint32_t H = (uint32_t)a.H;
     const uint16_t *src = (const uint16_t *)a.dt_raw + (int64_t)(row + (lane < rem ? lane : rem - 1)) * a.dt_stride;
-    float raw[kPer], bias[kPer], A2[kPer];
+    float raw[kDtHeads], bias[kDtHeads], A2[kDtHeads];
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
+    for (int k = 0; k < kDtHeads; ++k) {
         const uint32_t h = h0 + k < H ? h0 + k : H - 1;
         raw[k] = ld_act(src, h);
         bias[k] = a.dt_bias ? a.dt_bias[h] : 0.0f;
         A2[k] = a.A[h] * kLog2e;
     }
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
+    for (int k = 0; k < kDtHeads; ++k) {
         if (h0 + k >= H) break;
         const int64_t at = (int64_t)id * H + h0 + k;
         const float dt = lane < rem ? softplus(raw[k] + bias[k]) : 0.0f;
@@ -232,10 +234,10 @@ __device__ __forceinline__ void chunk_decays(const SsdCacheArgs &a, uint32_t id,
 // Bound by latency and by its stores of 1.3 KB per (chunk, head) and 58 KB per
 // (chunk, group) together: 9.1 us for one chunk (3 of them an empty launch, 1.6
 // the loads and the convolution, the rest LDS and its barriers: with the low
-// parts of B and C in one array in turn 10.0), 22 us for 16384 tokens of 80 heads
-// (52 MB), 38 us for 32768. The heads' decays have workgroups of their own, so
-// that a short prompt waits for neither: done by the workgroups that convolve B
-// and C, one chunk took 2 us more, 16384 tokens the same and 32768 tokens 5 more.
+// parts of B and C in one array in turn 10.0), 19 us for 16384 tokens of 80 heads
+// (52 MB). The heads' decays have workgroups of their own, so that a short
+// prompt waits for neither: done by the workgroups that convolve B and C, one
+// chunk took 2 us more and 16384 tokens 23 in all.
 template <int N>
 __global__ __launch_bounds__(prep_threads(N)) void prepare_kernel(SsdCacheArgs a) {
     __shared__ PrepShared<N> sh;
@@ -263,7 +265,7 @@ __global__ __launch_bounds__(prep_threads(N)) void prepare_kernel(SsdCacheArgs a
     const bool resume = flag != 0 && slot >= 0 && slot < a.num_slots;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     if (decays) {
-        chunk_decays(a, id, begin + first, rem, g * HEADS + wave * 2);
+        chunk_decays(a, id, begin + first, rem, g * HEADS + wave * kDtHeads);
         return;
     }
 
