@@ -227,7 +227,8 @@ struct SsdCacheArgs {
     // workspace
     int32_t *ws_slot;   // (seqs) the slot a sequence owns, -1 for none
     uint16_t *ws_win;   // prompts: (seqs, 3, C) raw rows before each sequence
-    int64_t seg, nchunk, nseg;          // prompts: tokens per segment, ids of chunks and of segments
+    int64_t seg, nchunk, nseg;          // prompts: least tokens per segment, ids of chunks and of segments
+    int32_t *ws_plan;                   // tokens per segment, from the lengths, and each sequence's first segment (NULL: seg)
     void *ws_frag;                      // per (chunk, group): B, C and G as operands, the scales of C
     float *ws_head, *ws_w, *ws_meta;    // per (chunk, head): decays per token, and of the whole chunk
     int32_t *ws_eb, *ws_ex;             // exponents of the scales of B per (chunk, group), of x per (chunk, wave)

@@ -25,9 +25,10 @@
 //             the sequence's last state into the cache;
 //   walk C    every segment from its entering state: y.
 // A long sequence so keeps the whole chip busy. The offsets are read on the
-// device. Chunk i of sequence s has the id cu[s] / 64 + s + i (segments
-// likewise): disjoint ranges without a prefix sum, as ceil(len / 64) <= cu[s+1]
-// / 64 - cu[s] / 64 + 1.
+// device. Chunk i of sequence s has the id cu[s] / 64 + s + i: disjoint ranges
+// without a prefix sum, as ceil(len / 64) <= cu[s+1] / 64 - cu[s] / 64 + 1. The
+// segments of several sequences are chosen and numbered on the device, by one wave
+// of the first launch; otherwise their length is the host's and their ids as above.
 //
 // Precision. The state must come out as a float32 state would, so the products
 // of walk A take both operands as sums of two float16 (22 bits; three products,
@@ -145,15 +146,15 @@ __device__ __forceinline__ uint32_t seq_length(const SsdCacheArgs &a, uint32_t s
     return end < (int32_t)begin ? 0 : end - begin;
 }
 
-// The sequence whose pieces of `unit` tokens include piece `id` (the last s
-// with cu[s] / unit + s <= id), or -1: 64 candidates at a time, one per lane.
-__device__ __forceinline__ int find_seq(const SsdCacheArgs &a, uint32_t id, uint32_t unit) {
-    uint32_t lo = 0, n = (uint32_t)a.seqs;
-    if (n == 1) return 0;
+// The last s < n with key(s) <= id, or -1, for a key that does not decrease: 64
+// candidates at a time, one per lane.
+template <typename Key>
+__device__ __forceinline__ int find(uint32_t id, uint32_t n, Key key) {
+    uint32_t lo = 0;
     const uint32_t lane = threadIdx.x & 63;
     do {
         const uint32_t step = (n + 63) / 64, at = lane * step;
-        const bool below = at < n && seq_begin(a, lo + at) / unit + lo + at <= id;
+        const bool below = at < n && key(lo + at) <= id;
         const int cnt = __popcll(__ballot(below));
         if (cnt == 0) return -1;
         const uint32_t skip = (cnt - 1) * step;
@@ -163,7 +164,89 @@ __device__ __forceinline__ int find_seq(const SsdCacheArgs &a, uint32_t id, uint
     return uniform((int)lo);
 }
 
+// The sequence whose pieces of `unit` tokens include piece `id`: the last s with
+// cu[s] / unit + s <= id.
+__device__ __forceinline__ int find_seq(const SsdCacheArgs &a, uint32_t id, uint32_t unit) {
+    if (a.seqs == 1) return 0;
+    return find(id, (uint32_t)a.seqs, [&](uint32_t s) { return seq_begin(a, s) / unit + s; });
+}
+
+// Tokens per segment.
+__device__ __forceinline__ uint32_t segment(const SsdCacheArgs &a) {
+    return a.ws_plan ? (uint32_t)uniform(a.ws_plan[0]) : (uint32_t)a.seg;
+}
+
+// Segments of a sequence (one without tokens has one too), the id of its first
+// and the number of ids. From the device's plan the ids have no gaps; offsets that
+// overlap may ask for more of them than the workspace holds, which are left out.
+__device__ __forceinline__ uint32_t segments(uint32_t len, uint32_t seg) { return len > 0 ? (len + seg - 1) / seg : 1; }
+__device__ __forceinline__ uint32_t first_segment(const SsdCacheArgs &a, uint32_t s, uint32_t begin, uint32_t seg) {
+    return a.ws_plan ? (uint32_t)a.ws_plan[1 + s] : begin / seg + s;
+}
+__device__ __forceinline__ uint32_t segment_ids(const SsdCacheArgs &a) {
+    if (!a.ws_plan) return (uint32_t)a.nseg;
+    const uint32_t n = (uint32_t)uniform(a.ws_plan[1 + a.seqs]);
+    return n < (uint32_t)a.nseg ? n : (uint32_t)a.nseg;
+}
+
 // -------------------------------------------------------------------- prepare
+
+// The segment length, a lane per candidate, and the ids of the segments. The chip
+// holds 512 workgroups of walk A and 256 of walk C at once. A workgroup costs its
+// chunks and about two more (the first loads, the states); all of them either
+// rounds of the longest (walk A's last round two thirds where it leaves every
+// second place empty) or their sum over the places and one longest, whichever is
+// less; a segment's state passes through the join besides. Against a length that
+// suits the worst case of as many tokens, whole calls (us): eight prompts of 3600
+// to 4900 tokens, 80 heads 548 -> 528, 13 of 4099, 32 heads 56 -> 53, 9 of 4148 tokens, 68 heads 118 -> 99, 3 of
+// 19798 tokens, 34 heads 159 -> 139; 45 of 5143 tokens, 4 heads 56 -> 62.
+__device__ __forceinline__ void plan_segments(const SsdCacheArgs &a) {
+    if (threadIdx.x >= 64) return;
+    const int lane = threadIdx.x, least = (int)(a.seg / kQ);
+    const float m = (float)(least + lane), inv = 1.0f / m, seqs = (float)a.seqs;
+    float n = 0.0f, all = 0.0f, longest = 0.0f;
+    for (int64_t s0 = 0; s0 < a.seqs; s0 += 64) {
+        float c = 0.0f;
+        if (s0 + lane < a.seqs) c = (float)((seq_length(a, s0 + lane, seq_begin(a, s0 + lane)) + kQ - 1) / kQ);
+        const int many = a.seqs - s0 < 64 ? (int)(a.seqs - s0) : 64;
+        for (int k = 0; k < many; ++k) {
+            const float ck = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(c), k));
+            n += __builtin_fmaxf(__builtin_ceilf(__builtin_fmaf(ck, inv, -1e-3f)), 1.0f);
+            all += ck;
+            longest = __builtin_fmaxf(longest, ck);
+        }
+    }
+    const int64_t ncb = a.H / a.G * (a.P / 64);
+    const float ua = (float)(a.G * ((ncb + kBlocksA - 1) / kBlocksA)) * (1.0f / 512.0f);
+    const float uc = (float)(a.G * ((ncb + kBlocksC - 1) / kBlocksC)) * (1.0f / 256.0f);
+    const float one = __builtin_fminf(m, longest) + 2.0f, work = all + 2.0f * n;
+    const float whole = __builtin_floorf(n * ua), rest = n * ua - whole;
+    const float ra = whole + (rest > 0.5f ? 1.0f : rest > 0.0f ? 0.67f : 0.0f);
+    const float cost = __builtin_fminf(ra * one, work * ua + one) + __builtin_fminf(__builtin_ceilf(n * uc) * one, work * uc + one) +
+                       (n > seqs ? 2.2f * n * ua : 0.0f);
+    float best = cost;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) best = __builtin_fminf(best, __shfl_xor(best, d));
+    const int first = __ffsll((unsigned long long)__ballot(cost == best)) - 1;
+    const uint32_t seg = uniform((least + (first < 0 ? 0 : first)) * kQ);
+    uint32_t base = 0;
+    for (int64_t s0 = 0; s0 < a.seqs; s0 += 64) {
+        uint32_t k = 0;
+        if (s0 + lane < a.seqs) k = segments(seq_length(a, s0 + lane, seq_begin(a, s0 + lane)), seg);
+        uint32_t sum = k;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const uint32_t below = __shfl_up(sum, d);
+            sum += lane >= d ? below : 0;
+        }
+        if (s0 + lane < a.seqs) a.ws_plan[1 + s0 + lane] = base + sum - k;
+        base += __shfl(sum, 63);
+    }
+    if (lane == 0) {
+        a.ws_plan[0] = seg;
+        a.ws_plan[1 + a.seqs] = base;
+    }
+}
 
 template <int N>
 struct PrepShared {
@@ -238,11 +321,19 @@ __device__ __forceinline__ void chunk_decays(const SsdCacheArgs &a, uint32_t id,
 // (52 MB). The heads' decays have workgroups of their own, so that a short
 // prompt waits for neither: done by the workgroups that convolve B and C, one
 // chunk took 2 us more and 16384 tokens 23 in all.
-template <int N>
+// PLAN: one workgroup more, the first, chooses the segments (in every launch, its
+// code alone took 3 of those 19 us).
+template <int N, bool PLAN>
 __global__ __launch_bounds__(prep_threads(N)) void prepare_kernel(SsdCacheArgs a) {
     __shared__ PrepShared<N> sh;
     constexpr int THREADS = prep_threads(N), WAVES = THREADS / 64, HEADS = dt_heads(N);
     uint32_t blk = blockIdx.x;
+    if constexpr (PLAN) {
+        if (blk-- == 0) {
+            plan_segments(a);
+            return;
+        }
+    }
     const uint32_t nbc = (uint32_t)(a.nchunk * a.G), per = ((uint32_t)a.H + HEADS - 1) / HEADS;
     const uint32_t ndt = (uint32_t)a.nchunk * per;
     if (blk >= nbc + ndt) {
@@ -415,23 +506,23 @@ __device__ __forceinline__ Unit find_unit(const SsdCacheArgs &a) {
     // Workgroups are dealt to the 8 XCDs in turn: neighbours in the order of
     // the work (the column blocks of one segment, which load the same B, C and
     // G) go to one XCD and its L2.
-    const uint32_t P = (uint32_t)a.P, pb = P / 64, G = (uint32_t)a.G, hpg = (uint32_t)a.H / G, seg = (uint32_t)a.seg;
+    const uint32_t P = (uint32_t)a.P, pb = P / 64, G = (uint32_t)a.G, hpg = (uint32_t)a.H / G, seg = segment(a);
     const uint32_t ncb = hpg * pb, nhb = (ncb + BLOCKS - 1) / BLOCKS;
-    const uint32_t total = (uint32_t)a.nseg * G * nhb, per = (total + 7) / 8;
+    const uint32_t total = segment_ids(a) * G * nhb, per = (total + 7) / 8;
     const uint32_t unit = blockIdx.x % 8 * per + blockIdx.x / 8;
-    if (unit >= total) return u;
+    if (blockIdx.x / 8 >= per || unit >= total) return u;
     u.sid = unit / (G * nhb);
     u.g = unit / nhb % G;
     u.hb = unit % nhb;
-    u.s = find_seq(a, u.sid, seg);
+    u.s = a.ws_plan ? find(u.sid, (uint32_t)a.seqs, [&](uint32_t s) { return (uint32_t)a.ws_plan[1 + s]; }) : find_seq(a, u.sid, seg);
     if (u.s < 0) return u;
     // all of the sequence's words at once, ahead of the branches
     u.slot = a.ws_slot[u.s];
     u.resume = a.resume && a.resume[u.s] != 0;
     u.begin = seq_begin(a, u.s);
     u.len = seq_length(a, u.s, u.begin);
-    u.k = u.sid - (u.begin / seg + u.s);
-    u.nseg = u.len > 0 ? (u.len + seg - 1) / seg : 1;
+    u.k = u.sid - first_segment(a, u.s, u.begin, seg);
+    u.nseg = segments(u.len, seg);
     if (u.k >= u.nseg) return u;
     u.from = u.k * seg;
     u.to = u.len - u.from < seg ? u.len : u.from + seg;
@@ -765,13 +856,14 @@ __global__ __launch_bounds__(128 * kBlocksA, 2) void walk_state_kernel(SsdCacheA
 // dec[k] enter[k] + end[k]; the last one goes into the cache.
 __global__ __launch_bounds__(256) void join_kernel(SsdCacheArgs a, int N) {
     constexpr uint32_t kAhead = 4;  // segments loaded ahead of the chain
-    const uint32_t s = blockIdx.y, seg = (uint32_t)a.seg;
+    const uint32_t s = blockIdx.y, seg = segment(a);
     const int32_t slot = a.ws_slot[s], flag = a.resume ? a.resume[s] : 0;
-    const uint32_t begin = seq_begin(a, s), len = seq_length(a, s, begin), nseg = (len + seg - 1) / seg;
+    const uint32_t begin = seq_begin(a, s), len = seq_length(a, s, begin), nseg = segments(len, seg);
     if (nseg < 2 || slot < 0) return;
     const int64_t hpn = a.H * a.P * N, i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
     if (i >= hpn) return;
-    const int64_t h = i / (a.P * N), first = begin / seg + s;
+    const int64_t h = i / (a.P * N), first = first_segment(a, s, begin, seg);
+    if (first + nseg > a.nseg) return;
     float *const cache = a.state_cache + slot * hpn + i;
     f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
     if (flag != 0) v = *(const f32x4 *)cache;
@@ -1176,14 +1268,16 @@ template <int N>
 hipError_t launch_n(const SsdCacheArgs &a, hipStream_t s) {
     constexpr int64_t threads = prep_threads(N);
     const int64_t parts = (a.C + threads - 1) / threads, dts = (a.H + dt_heads(N) - 1) / dt_heads(N);
-    hipLaunchKernelGGL((prepare_kernel<N>), dim3((unsigned)(a.nchunk * (a.G + dts) + a.seqs * parts)), dim3(threads), 0, s, a);
+    const unsigned prep = (unsigned)(a.nchunk * (a.G + dts) + a.seqs * parts);
+    if (a.ws_plan) hipLaunchKernelGGL((prepare_kernel<N, true>), dim3(prep + 1), dim3(threads), 0, s, a);
+    else hipLaunchKernelGGL((prepare_kernel<N, false>), dim3(prep), dim3(threads), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t ncb = a.H / a.G * (a.P / 64);
     auto grid = [&](int blocks) { return dim3((unsigned)((a.nseg * a.G * ((ncb + blocks - 1) / blocks) + 7) / 8 * 8)); };
     hipLaunchKernelGGL((walk_state_kernel<N>), grid(kBlocksA), dim3(128 * kBlocksA), 0, s, a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    if (a.rows > a.seg) {  // some sequence may be longer than a segment
+    if (a.rows > a.seg) {  // some sequence may be longer than a segment: at least this long
         hipLaunchKernelGGL(join_kernel, dim3((unsigned)((a.H * a.P * N + 1023) / 1024), (unsigned)a.seqs), dim3(256), 0, s, a, N);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
@@ -1193,25 +1287,32 @@ hipError_t launch_n(const SsdCacheArgs &a, hipStream_t s) {
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Tokens per segment. The chip holds 512 workgroups of walk A at once; a round of
-// them costs a segment's chunks and about two more (the first loads, the states),
-// so the segment is the one that costs least over 1 to 8 rounds, with at most
-// (rows + seqs (seg - 1)) / seg segments of sequences whose lengths only the device
-// knows. Measured (80 heads, N = 128): one prompt of 16384 tokens in one round
-// 270 us, in two 287; eight of 4096 in two rounds 623, in four 574, in eight 687.
-// At most 2048 where there are several sequences, one of which may be long.
+// Whether the segment length is chosen on the device, which knows the lengths: a
+// wave looks at every sequence in turn, up to 5 us for this many.
+bool planned(int64_t seqs) { return seqs > 1 && seqs <= 256; }
+
+// Tokens per segment, the least of them where the device chooses: at most 4
+// rounds of 512 workgroups of walk A whatever the lengths are, (rows + seqs (seg -
+// 1)) / seg segments in the worst case, for the workspace and the launches. One
+// sequence: the length that costs least over 1 to 8 rounds, a round costing a
+// segment's chunks and about two more (16384 tokens of 80 heads in one round 270
+// us, in two 287).
 int64_t segment_tokens(int64_t seqs, int64_t rows, int64_t H, int64_t P, int64_t G) {
     const int64_t units = G * ((H / G * (P / 64) + kBlocksA - 1) / kBlocksA);
-    const int64_t mean = (rows / seqs + kQ - 1) / kQ;  // chunks of a sequence
-    int64_t best = seqs > 1 ? 2048 : (rows + kQ - 1) / kQ * kQ, cost = INT64_MAX;
+    if (seqs > 1) {
+        const int64_t most = 512 * 4 / units;  // segments
+        if (most <= seqs) return 2048;
+        const int64_t seg = (rows - seqs + most - seqs) / (most - seqs);
+        return seg > 2048 ? 2048 : seg < kQ ? kQ : (seg + kQ - 1) / kQ * kQ;
+    }
+    int64_t best = (rows + kQ - 1) / kQ * kQ, cost = INT64_MAX;
     for (int64_t rounds = 1; rounds <= 8; ++rounds) {
-        const int64_t most = 512 * rounds / units;  // segments
-        if (most <= seqs && !(seqs == 1 && most == 1)) continue;
-        // the smallest segment with that many of them at most
-        int64_t seg = seqs == 1 ? (rows + most - 1) / most : (rows - seqs + most - seqs) / (most - seqs);
+        const int64_t most = 512 * rounds / units;
+        if (most < 1) continue;
+        int64_t seg = (rows + most - 1) / most;
         seg = (seg < kQ ? kQ : seg + kQ - 1) / kQ * kQ;
-        const int64_t chunks = seg / kQ < mean ? seg / kQ : mean, c = rounds * (chunks + 2);
-        if (c < cost && (seqs == 1 || seg <= 2048)) cost = c, best = seg;
+        const int64_t c = rounds * (seg / kQ + 2);
+        if (c < cost) cost = c, best = seg;
     }
     return best < kQ ? kQ : best;
 }
@@ -1229,6 +1330,7 @@ size_t plan(SsdCacheArgs &a, int N, char *base) {
     a.nseg = a.rows / a.seg + a.seqs;
     const size_t chunks = (size_t)a.nchunk;
     a.ws_slot = (int32_t *)take((size_t)a.seqs * 4);
+    a.ws_plan = planned(a.seqs) ? (int32_t *)take((size_t)(a.seqs + 2) * 4) : nullptr;
     a.ws_win = (uint16_t *)take((size_t)a.seqs * 3 * a.C * 2);
     a.ws_frag = take(chunks * a.G * frag_elems(N) * 2);
     a.ws_head = (float *)take(chunks * a.H * kHead * 4);

@@ -453,3 +453,20 @@ def test_steps_on_more_state_than_the_caches_hold(batch, N, dtype):
              for k in (slice(0, half), slice(half, batch))]
     torch.cuda.synchronize()
     assert torch.equal(y, torch.cat(parts)) and torch.equal(conv, conv2) and torch.equal(state, state2)
+
+
+def test_overlapping_offsets_stay_inside():
+    """Offsets that go back take more segments than the workspace is for: the
+    caches' other slots and what lies behind the workspace keep their bits."""
+    say("case overlapping offsets")
+    d = ssd_inputs([100, 100, 0, 0, 0, 0, 0, 0, 0], 2, 64, 1, 64, seed=25)
+    g = to_gpu(d)
+    g["cu"] = torch.tensor([0, 200, 0, 200, 0, 200, 0, 200, 0, 200], dtype=torch.int32, device="cuda")
+    need = ssm.ssm_ssd_fwd_cache_workspace_bytes(9, 200, 2, 64, 1, 64, ssm.SSM_BF16)
+    ws = torch.full((need + 65536,), 77, dtype=torch.uint8, device="cuda")
+    xBC, dt = views(g)
+    prompt(g, torch.zeros(200, 2, 64, dtype=torch.bfloat16, device="cuda"), workspace=ws[:need])
+    torch.cuda.synchronize()
+    assert (ws[need:] == 77).all()
+    free = [k for k in range(11) if k not in d["slots"].tolist()]
+    assert torch.equal(g["state_cache"][free].cpu(), d["state_cache"][free])
