@@ -556,7 +556,7 @@ constexpr int pieces_cg(int N) { return (kQ * N + kQ * kQ) / 512; }
 // Bound by instruction issue: per chunk and wave the convolution and SiLU of 32
 // values a lane, their split into two float16 and 96 products (N = 128), from
 // two waves per SIMD, which is what the state's 64 registers and the operands
-// leave room for (225 of 256). 16384 tokens of 80 heads: 117 us for 168 MB of x
+// leave room for (225 of 256). 16384 tokens of 80 heads: 114 us for 168 MB of x
 // read and as much written, half the rate of a copy. Workgroups of 6 waves (which
 // do not pair up on a CU) took 197 us, of 12 waves 155; B read just ahead of its
 // use 126. Its SIMDs issue vector instructions (a fifth of their time exponentials
@@ -849,7 +849,7 @@ __global__ __launch_bounds__(128 * kBlocksA, 2) void walk_state_kernel(SsdCacheA
 }
 
 // Bound by HBM where there are many heads: 63 MB of segment states in 13 us (16384
-// tokens, 80 heads, 12 segments), 267 MB in 41 us (eight prompts of 4096). With
+// tokens, 80 heads, 12 segments), 131 MB in 25 us (eight prompts of 4096). With
 // few heads there are many segments, and the loads of one after the other are:
 // four ahead take a prompt batch of 21507 tokens, 8 heads, from 70 to 64 us.
 // enter[k] in place of end[k]: enter[0] the sequence's first state, enter[k+1] =
