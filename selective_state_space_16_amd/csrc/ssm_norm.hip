@@ -12,8 +12,8 @@
 // HBM bounds them all. A row is held in registers by the lanes that read it
 // (a wave, or a workgroup for long rows), so a row costs one pass. Measured, with
 // bfloat16 activations and a float32 residual, against 5.4 TB/s of a large copy:
-//   gate norm 32768 x 5120    forward  173 us, 1.01 GB, 5.8 TB/s
-//   add norm  32768 x 2560    backward 289 us, 1.51 GB, 5.2 TB/s (its reduction 4 us of it)
+//   gate norm 32768 x 5120    forward  174 us, 1.01 GB, 5.8 TB/s
+//   add norm  32768 x 2560    backward 291 us, 1.51 GB, 5.2 TB/s (its reduction 4 us of it)
 //   add norm  16384 x 2560    forward   95 us, 0.50 GB, 5.3 TB/s
 //   gate norm 8193 x 1536/2   backward  30 us, 0.13 GB (reduction 4 us)
 //   add norm  4097 x 1001     forward   14 us, float32, 66 MB
@@ -120,9 +120,14 @@ __device__ __forceinline__ void st_vec(uint16_t *p, int left, const float (&v)[8
 
 // Sums of NV values over the TPR lanes that share a row, in every one of them.
 // A wave adds by lane exchanges; more waves meet through LDS (two buffers in
-// turn, so that one barrier per row is enough).
+// turn, so that one barrier per row is enough). In double precision: what rounds
+// in the last steps of a tree is a whole row's error, and no other row averages it
+// (two rows of 3088 channels, 40 seeds: at most 6.0e-8 of y, 8.0e-8 with float32
+// sums and the hardware's root as it is; 1 % of the time of large batches).
 template <int TPR, int NV>
-__device__ __forceinline__ void row_sum(float (&v)[NV], float (*sh)[16][NV], int &turn) {
+__device__ __forceinline__ void row_sum(const float (&part)[NV], double (&v)[NV], double (*sh)[16][NV], int &turn) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] = (double)part[i];
 #pragma unroll
     for (int m = 1; m < (TPR < 64 ? TPR : 64); m *= 2)
 #pragma unroll
@@ -133,15 +138,36 @@ __device__ __forceinline__ void row_sum(float (&v)[NV], float (*sh)[16][NV], int
 #pragma unroll
             for (int i = 0; i < NV; ++i) sh[turn][w][i] = v[i];
         __syncthreads();
+        if constexpr (TPR <= 512) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            float s = 0.0f;
+            for (int i = 0; i < NV; ++i) {
+                v[i] = 0.0;
 #pragma unroll
-            for (int k = 0; k < TPR / 64; ++k) s += sh[turn][k][i];
-            v[i] = s;
+                for (int k = 0; k < TPR / 64; ++k) v[i] += sh[turn][k][i];
+            }
+        } else {  // a lane per wave, four times over: 16 pairs at once cost registers that a workgroup of 16 waves has not
+            const int k = threadIdx.x & 15;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) v[i] = k < TPR / 64 ? sh[turn][k][i] : 0.0;
+#pragma unroll
+            for (int m = 1; m < 16; m *= 2)
+#pragma unroll
+                for (int i = 0; i < NV; ++i) v[i] += __shfl_xor(v[i], m);
         }
         turn ^= 1;
     }
+}
+
+__device__ __forceinline__ bool finite(float v) { return (__float_as_uint(v) & 0x7f800000u) != 0x7f800000u; }
+
+// (sum / n + eps)^-1/2 rounded once: its error is a whole row's. The hardware's
+// reciprocal root and one step of Newton's in double precision, four
+// instructions per row.
+__device__ __forceinline__ float inv_rms(double sum, double inv, float eps) {
+    const double v = __builtin_fma(sum, inv, (double)eps);
+    const double r = (double)rsqrtf((float)v);
+    const float rstd = (float)__builtin_fma(0.5 * r, __builtin_fma(-v * r, r, 1.0), r);
+    return finite(rstd) ? rstd : (float)r;  // of zero, infinity and NaN
 }
 
 constexpr int block_threads(int TPR) { return TPR < 256 ? 256 : TPR; }
@@ -178,11 +204,11 @@ __device__ __forceinline__ void write_partial(const float (&acc)[ITER][kVec], fl
 template <int TPR, bool ODD, int ITER, typename T, typename R>
 __global__ __launch_bounds__(block_threads(TPR)) void add_norm_fwd_kernel(AddNormArgs a) {
     constexpr int RPB = block_threads(TPR) / TPR;
-    __shared__ float sh[2][16][1];
+    __shared__ double sh[2][16][1];
     int turn = 0;
     const int lane = threadIdx.x % TPR;
     const int64_t D = a.D;
-    const float inv = 1.0f / (float)D;
+    const double inv = 1.0 / (double)D;
     for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; row < a.rows; row += (int64_t)gridDim.x * RPB) {
         const int64_t base = row * D;
         float r[ITER][kVec], ss[1] = {0.0f};
@@ -203,8 +229,9 @@ __global__ __launch_bounds__(block_threads(TPR)) void add_norm_fwd_kernel(AddNor
                 }
             }
         }
-        row_sum<TPR, 1>(ss, sh, turn);
-        const float rstd = rsqrtf(__builtin_fmaf(ss[0], inv, a.eps));
+        double sum[1];
+        row_sum<TPR, 1>(ss, sum, sh, turn);
+        const float rstd = inv_rms(sum[0], inv, a.eps);
 #pragma unroll
         for (int k = 0; k < ITER; ++k) {
             const int c = (k * TPR + lane) * kVec, left = (int)D - c;
@@ -223,12 +250,12 @@ __global__ __launch_bounds__(block_threads(TPR)) void add_norm_fwd_kernel(AddNor
 template <int TPR, bool ODD, int ITER, typename T, typename R>
 __global__ __launch_bounds__(block_threads(TPR)) void add_norm_bwd_kernel(AddNormArgs a) {
     constexpr int RPB = block_threads(TPR) / TPR;
-    __shared__ float sh[2][16][2];
+    __shared__ double sh[2][16][2];
     __shared__ float cols[RPB > 1 ? TPR * kVec * ITER : 1];
     int turn = 0;
     const int lane = threadIdx.x % TPR;
     const int64_t D = a.D;
-    const float inv = 1.0f / (float)D;
+    const double inv = 1.0 / (double)D;
     float dw[ITER][kVec], ds[ITER][kVec];
 #pragma unroll
     for (int k = 0; k < ITER; ++k)
@@ -252,9 +279,10 @@ __global__ __launch_bounds__(block_threads(TPR)) void add_norm_bwd_kernel(AddNor
                 }
             }
         }
-        row_sum<TPR, 2>(ss, sh, turn);
-        const float rstd = rsqrtf(__builtin_fmaf(ss[0], inv, a.eps));
-        const float m = ss[1] * inv * rstd;  // mean(g hat)
+        double sum[2];
+        row_sum<TPR, 2>(ss, sum, sh, turn);
+        const float rstd = inv_rms(sum[0], inv, a.eps);
+        const float m = (float)(sum[1] * inv) * rstd;  // mean(g hat)
 #pragma unroll
         for (int k = 0; k < ITER; ++k) {
             const int c = (k * TPR + lane) * kVec, left = (int)D - c;
@@ -295,11 +323,11 @@ __device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf
 template <int TPR, bool ODD, int ITER, typename T, bool STREAM>
 __global__ __launch_bounds__(block_threads(TPR)) void gate_norm_fwd_kernel(GateNormArgs a) {
     constexpr int RPB = block_threads(TPR) / TPR;
-    __shared__ float sh[2][16][1];
+    __shared__ double sh[2][16][1];
     int turn = 0;
     const int lane = threadIdx.x % TPR;
     const int64_t Dg = a.D / a.groups, g0 = (int64_t)blockIdx.y * Dg;
-    const float inv = 1.0f / (float)Dg;
+    const double inv = 1.0 / (double)Dg;
     for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; row < a.rows; row += (int64_t)gridDim.x * RPB) {
         const T *xp = (const T *)a.x + row * a.x_stride + g0, *zp = (const T *)a.z + row * a.z_stride + g0;
         T *yp = (T *)a.y + row * a.D + g0;
@@ -318,8 +346,9 @@ __global__ __launch_bounds__(block_threads(TPR)) void gate_norm_fwd_kernel(GateN
                 }
             }
         }
-        row_sum<TPR, 1>(ss, sh, turn);
-        const float rstd = rsqrtf(__builtin_fmaf(ss[0], inv, a.eps));
+        double sum[1];
+        row_sum<TPR, 1>(ss, sum, sh, turn);
+        const float rstd = inv_rms(sum[0], inv, a.eps);
 #pragma unroll
         for (int k = 0; k < ITER; ++k) {
             const int c = (k * TPR + lane) * kVec, left = (int)Dg - c;
@@ -337,12 +366,12 @@ __global__ __launch_bounds__(block_threads(TPR)) void gate_norm_fwd_kernel(GateN
 template <int TPR, bool ODD, int ITER, typename T>
 __global__ __launch_bounds__(block_threads(TPR)) void gate_norm_bwd_kernel(GateNormArgs a) {
     constexpr int RPB = block_threads(TPR) / TPR;
-    __shared__ float sh[2][16][2];
+    __shared__ double sh[2][16][2];
     __shared__ float cols[RPB > 1 ? TPR * kVec * ITER : 1];
     int turn = 0;
     const int lane = threadIdx.x % TPR;
     const int64_t D = a.D, Dg = D / a.groups, g0 = (int64_t)blockIdx.y * Dg;
-    const float inv = 1.0f / (float)Dg;
+    const double inv = 1.0 / (double)Dg;
     float dw[ITER][kVec];
 #pragma unroll
     for (int k = 0; k < ITER; ++k)
@@ -369,9 +398,10 @@ __global__ __launch_bounds__(block_threads(TPR)) void gate_norm_bwd_kernel(GateN
                 }
             }
         }
-        row_sum<TPR, 2>(ss, sh, turn);
-        const float rstd = rsqrtf(__builtin_fmaf(ss[0], inv, a.eps));
-        const float m = ss[1] * inv * rstd;  // mean(g hat)
+        double sum[2];
+        row_sum<TPR, 2>(ss, sum, sh, turn);
+        const float rstd = inv_rms(sum[0], inv, a.eps);
+        const float m = (float)(sum[1] * inv) * rstd;  // mean(g hat)
 #pragma unroll
         for (int k = 0; k < ITER; ++k) {
             const int c = (k * TPR + lane) * kVec, left = (int)Dg - c;
