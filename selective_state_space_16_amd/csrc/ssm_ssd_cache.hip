@@ -31,12 +31,14 @@
 // of the first launch; otherwise their length is the host's and their ids as above.
 //
 // Precision. The state must come out as a float32 state would, so the products
-// of walk A take both operands as sums of two float16 (22 bits; three products,
-// the product of the two low parts is below 2^-22). The products for y, which is
+// of walk A take both operands as sums of three bfloat16 (24 bits; six products,
+// those left out are below 2^-24 of the whole). bfloat16 has float32's range, so
+// no scale is needed that channels, columns or tokens of unlike size would share.
+// The products for y, which is
 // rounded to bfloat16 in the end, take single float16 operands (11 bits, against
-// 8 of the result). float16 has little range, so operands carry power-of-two
+// 8 of the result). float16 has little range, so they carry power-of-two
 // scales: C one per token, B one per chunk, x one per chunk and wave, w one per
-// chunk; the state accumulates in units 2^K that follow a running bound of its
+// chunk; walk C's state accumulates in units 2^K that follow a running bound of its
 // size. Scales are exact, and they cancel in one factor per token at the end.
 #include "ssm_common.h"
 #include "ssm_device.h"
@@ -51,6 +53,9 @@ typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kQ = 64;            // tokens per chunk
 // Threads of a workgroup ahead of the walks: a lane convolves four channels of
@@ -59,10 +64,10 @@ constexpr int prep_threads(int N) { return 8 * N; }
 constexpr int kBlocksA = 2;       // column blocks of 64 per workgroup of walk A, two waves each
 constexpr int kBlocksC = 4;       // of walk C
 
-// Workspace of one (chunk, group), in float16 elements: B high, B low and C as
-// operand registers (lane-major), G as operand registers, 2^eC per token
-// (float32), filled up to whole 1 KiB pieces.
-constexpr int frag_elems(int N) { return 3 * kQ * N + kQ * kQ + 512; }
+// Workspace of one (chunk, group), in 16-bit elements: B in three parts as operand
+// registers (lane-major; half, part, n tile), B and C in float16, G as operand
+// registers, 2^eC per token (float32), filled up to whole 1 KiB pieces.
+constexpr int frag_elems(int N) { return 5 * kQ * N + kQ * kQ + 512; }
 // Floats per (chunk, head) for walk C: cum, cum - log2 dt, exp2(cum), and w as
 // scaled float16, filled up to 1 KiB.
 constexpr int kHead = 4 * kQ;
@@ -74,15 +79,29 @@ constexpr int dt_heads(int N) { return prep_threads(N) / 64 * kDtHeads; }
 __device__ __forceinline__ f32x4 mfma(f16x8 a, f16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
-// a and b as sums of two float16 each: what rounding leaves of them, exactly
-// (the mixed-precision fma reads the rounded pair as it is).
-__device__ __forceinline__ void split(float a, float b, f16x2 &hi, f16x2 &lo) {
-    float la, lb;
-    hi = f16x2{(_Float16)a, (_Float16)b};
-    asm("v_fma_mix_f32 %0, %1, 1.0, -%2 op_sel_hi:[0,0,1]" : "=v"(la) : "v"(a), "v"(hi));
-    asm("v_fma_mix_f32 %0, %1, 1.0, -%2 op_sel:[0,0,1] op_sel_hi:[0,0,1]" : "=v"(lb) : "v"(b), "v"(hi));
-    lo = f16x2{(_Float16)la, (_Float16)lb};
+__device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
+// a and b rounded to bfloat16, and what that leaves of them, exactly.
+__device__ __forceinline__ uint32_t bf16_pair(float &a, float &b) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
+    a -= __uint_as_float(u << 16);
+    b -= __uint_as_float(u & 0xffff0000u);
+    return u;
+}
+// Eight values as sums of PARTS bfloat16 each, 8 bits a part.
+template <int PARTS>
+__device__ __forceinline__ void split(float (&v)[8], bf16x8 (&out)[PARTS]) {
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) {
+        u32x4 u;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) u[j] = bf16_pair(v[2 * j], v[2 * j + 1]);
+        out[p] = __builtin_bit_cast(bf16x8, u);
+    }
+}
+// The product of two operands of three parts each, as six, the small ones first.
+constexpr int kTerm[6][2] = {{2, 0}, {0, 2}, {1, 1}, {1, 0}, {0, 1}, {0, 0}};
 // Buffer accesses: bytes from a wave-uniform base, a range that the hardware
 // checks (loads outside it give 0, stores outside it are dropped).
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *base, uint32_t bytes) {
@@ -250,8 +269,8 @@ __device__ __forceinline__ void plan_segments(const SsdCacheArgs &a) {
 
 template <int N>
 struct PrepShared {
-    static constexpr int R = N + 8;
-    alignas(16) _Float16 Bh[kQ][R], Bl[kQ][R], Ch[kQ][R], Cl[kQ][R];  // high and low parts
+    static constexpr int R = N + 4;
+    alignas(16) float B[kQ][R], C[kQ][R];
     float maxb[16];
     int ec[kQ];
 };
@@ -309,7 +328,7 @@ __device__ __forceinline__ void chunk_decays(const SsdCacheArgs &a, uint32_t id,
         o[kQ + lane] = cum - __builtin_amdgcn_logf(dt) + (float)ed;
         o[2 * kQ + lane] = fast_exp2(cum);
         ((_Float16 *)(o + 3 * kQ))[lane] = (_Float16)__builtin_ldexpf(wt, -ew);  // below 1, as for walk A below
-        a.ws_w[at * kQ + lane] = __builtin_ldexpf(wt, -ew);
+        a.ws_w[at * kQ + lane] = wt;
         if (lane == 63) *(f32x4 *)(a.ws_meta + at * 4) = f32x4{fast_exp2(cum), __int_as_float(ew), __int_as_float(ed), 0.0f};
     }
 }
@@ -417,19 +436,7 @@ __global__ __launch_bounds__(prep_threads(N)) void prepare_kernel(SsdCacheArgs a
     for (int k = 0; k < WAVES; ++k) big = __builtin_fmaxf(big, sh.maxb[k]);
     const int eB = clampi(exponent(big), -100, 128);
 #pragma unroll
-    for (int i = 0; i < TPB; ++i) {
-        const int e = 7 - (isC ? sh.ec[t0 + i] : eB);
-        f16x4 hi, low;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            float t = __builtin_ldexpf(v[i][k], e);
-            asm("" : "+v"(t));
-            hi[k] = (_Float16)t;
-            low[k] = (_Float16)(t - (float)hi[k]);
-        }
-        *(f16x4 *)(isC ? &sh.Ch[t0 + i][n0] : &sh.Bh[t0 + i][n0]) = hi;
-        *(f16x4 *)(isC ? &sh.Cl[t0 + i][n0] : &sh.Bl[t0 + i][n0]) = low;
-    }
+    for (int i = 0; i < TPB; ++i) *(f32x4 *)(isC ? &sh.C[t0 + i][n0] : &sh.B[t0 + i][n0]) = f32x4{v[i][0], v[i][1], v[i][2], v[i][3]};
     __syncthreads();
 
     _Float16 *out = (_Float16 *)a.ws_frag + ((int64_t)id * a.G + g) * frag_elems(N);
@@ -437,25 +444,34 @@ __global__ __launch_bounds__(prep_threads(N)) void prepare_kernel(SsdCacheArgs a
     // Each wave forms one of B^T's operands, (h, nt): row n = 16 nt + r, k = token
     // 16 q + 8 h + j;
     static_assert(2 * (N / 16) == WAVES && 4 * (N / 32) == WAVES);
+    _Float16 *const out16 = out + 3 * kQ * N;
     {
-        const int h = wave / (N / 16), nt = wave % (N / 16);
-        f16x8 hi, lo;
+        constexpr int NT = N / 16;
+        const int h = wave / NT, nt = wave % NT;
+        float t[8];
+        f16x8 hi;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            hi[j] = sh.Bh[16 * q + 8 * h + j][16 * nt + r];
-            lo[j] = sh.Bl[16 * q + 8 * h + j][16 * nt + r];
+            t[j] = sh.B[16 * q + 8 * h + j][16 * nt + r];
+            hi[j] = (_Float16)__builtin_ldexpf(t[j], 7 - eB);
         }
-        *(f16x8 *)(out + (wave * 64 + lane) * 8) = hi;
-        *(f16x8 *)(out + kQ * N + (wave * 64 + lane) * 8) = lo;
+        *(f16x8 *)(out16 + (wave * 64 + lane) * 8) = hi;
+        bf16x8 part[3];
+        split(t, part);
+#pragma unroll
+        for (int p = 0; p < 3; ++p) *((bf16x8 *)out + ((h * 3 + p) * NT + nt) * 64 + lane) = part[p];
     }
     // one of C's, (tt, m): row r is token 16 (r / 4) + 4 tt + r % 4, and k runs
     // over n in the order in which two accumulator tiles hold the state;
     const int row = 16 * (r / 4) + r % 4;
     {
-        const int tt = wave / (N / 32), m = wave % (N / 32);
-        const _Float16 *src = &sh.Ch[row + 4 * tt][32 * m + 4 * q];
-        const f16x4 lo = *(const f16x4 *)src, hi = *(const f16x4 *)(src + 16);
-        *(f16x8 *)(out + 2 * kQ * N + (wave * 64 + lane) * 8) = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        const int tt = wave / (N / 32), m = wave % (N / 32), e = 7 - sh.ec[row + 4 * tt];
+        const float *src = &sh.C[row + 4 * tt][32 * m + 4 * q];
+        const f32x4 lo = *(const f32x4 *)src, hi = *(const f32x4 *)(src + 16);
+        f16x8 o;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = (_Float16)__builtin_ldexpf(lo[j], e), o[4 + j] = (_Float16)__builtin_ldexpf(hi[j], e);
+        *(f16x8 *)(out16 + kQ * N + (wave * 64 + lane) * 8) = o;
     }
     // and of G's, (tt, h) with row r as in C and k = token s = 16 q + 8 h + j, one
     // or two of the sixteen products (tt, h, b), whose row 4 q + e is token
@@ -467,17 +483,25 @@ __global__ __launch_bounds__(prep_threads(N)) void prepare_kernel(SsdCacheArgs a
         f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int m = 0; m < N / 32; ++m) {
-            const f16x8 ch = *(const f16x8 *)&sh.Ch[row + 4 * tt][32 * m + 8 * q], bh = *(const f16x8 *)&sh.Bh[sr][32 * m + 8 * q];
-            acc = mfma(bh, *(const f16x8 *)&sh.Cl[row + 4 * tt][32 * m + 8 * q], acc);
-            acc = mfma(*(const f16x8 *)&sh.Bl[sr][32 * m + 8 * q], ch, acc);
-            acc = mfma(bh, ch, acc);
+            float cv[8], bv[8];
+#pragma unroll
+            for (int j = 0; j < 8; j += 4) {
+                *(f32x4 *)(cv + j) = *(const f32x4 *)&sh.C[row + 4 * tt][32 * m + 8 * q + j];
+                *(f32x4 *)(bv + j) = *(const f32x4 *)&sh.B[sr][32 * m + 8 * q + j];
+            }
+            bf16x8 cp[3], bp[3];
+            split(cv, cp);
+            split(bv, bp);
+#pragma unroll
+            for (int p = 0; p < 6; ++p) acc = mfma(bp[kTerm[p][0]], cp[kTerm[p][1]], acc);
         }
         f16x4 o;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = s0 + e <= row + 4 * tt ? (_Float16)(acc[e] * 0x1p-7f) : (_Float16)0.0f;
-        *(f16x4 *)(out + 3 * kQ * N + ((f / 2) * 64 + lane) * 8 + 4 * (f % 2)) = o;
+        for (int e = 0; e < 4; ++e)
+            o[e] = s0 + e <= row + 4 * tt ? (_Float16)__builtin_ldexpf(acc[e], 7 - sh.ec[row + 4 * tt] - eB) : (_Float16)0.0f;
+        *(f16x4 *)(out16 + 2 * kQ * N + ((f / 2) * 64 + lane) * 8 + 4 * (f % 2)) = o;
     }
-    if (tid < kQ) ((float *)(out + 3 * kQ * N + kQ * kQ))[tid] = __builtin_ldexpf(1.0f, sh.ec[tid]);
+    if (tid < kQ) ((float *)(out16 + 2 * kQ * N + kQ * kQ))[tid] = __builtin_ldexpf(1.0f, sh.ec[tid]);
     if (tid == 0) a.ws_eb[id * a.G + g] = eB;
 }
 
@@ -547,25 +571,27 @@ __device__ __forceinline__ void pieces(const void *src, const void *to_lds, int 
     }
 }
 
-constexpr int pieces_b(int N) { return 2 * kQ * N / 512; }
+constexpr int pieces_b(int N) { return 3 * kQ * N / 512; }
 constexpr int pieces_cg(int N) { return (kQ * N + kQ * kQ) / 512; }
 
-// Walk A: x, and the segment's end state. B of two chunks is held in LDS, so that
-// two workgroups share a CU, two waves a SIMD.
+// Walk A: x, and the segment's end state. B lies in LDS by halves of a chunk (48 KB
+// of three parts each chunk at N = 128), three of them in turn, so that two
+// workgroups share a CU, two waves a SIMD; a barrier before each half's products
+// says that it has come and that the one before it may be overwritten.
 //
 // Bound by instruction issue: per chunk and wave the convolution and SiLU of 32
-// values a lane, their split into two float16 and 96 products (N = 128), from
+// values a lane, their split into three bfloat16 and 192 products (N = 128), from
 // two waves per SIMD, which is what the state's 64 registers and the operands
-// leave room for (225 of 256). 16384 tokens of 80 heads: 114 us for 168 MB of x
-// read and as much written, half the rate of a copy. Workgroups of 6 waves (which
-// do not pair up on a CU) took 197 us, of 12 waves 155; B read just ahead of its
-// use 126. Its SIMDs issue vector instructions (a fifth of their time exponentials
-// and reciprocals) in two thirds of the cycles and run products in a third.
+// leave room for (249 of 256). 16384 tokens of 80 heads: 148 us for 168 MB of x
+// read and as much written. Operands of two float16 (22 bits, three products, 114
+// us) need scales that channels, columns and tokens share, and lose what is small
+// beside a neighbour. Workgroups of 6 waves (which do not pair up on a CU) and of 12
+// took 1.7 and 1.35 times as long.
 template <int N>
 __global__ __launch_bounds__(128 * kBlocksA, 2) void walk_state_kernel(SsdCacheArgs a) {
     constexpr int NT = N / 16;
     struct Shared {
-        alignas(16) _Float16 B[2][2 * kQ * N];
+        alignas(16) __bf16 B[3][3 * kQ / 2 * N];  // halves of a chunk, in turn
         alignas(16) float w[2][4][kQ];
     };
     __shared__ Shared sh;
@@ -617,25 +643,25 @@ __global__ __launch_bounds__(128 * kBlocksA, 2) void walk_state_kernel(SsdCacheA
             o += rowb;
         }
     };
-    auto stage = [&](uint32_t t) {
-        const int b = (int)((t - from) / kQ & 1);
+    auto stage = [&](uint32_t t, int half, int slot) {
         const uint32_t id = u.chunk0 + t / kQ;
-        pieces<pieces_b(N), 2 * kBlocksA>((const char *)a.ws_frag + ((int64_t)id * G + u.g) * (frag_elems(N) * 2), sh.B[b], wave, lane);
+        pieces<pieces_b(N) / 2, 2 * kBlocksA>((const char *)a.ws_frag + ((int64_t)id * G + u.g) * (frag_elems(N) * 2) + half * (pieces_b(N) / 2 * 1024),
+                                              sh.B[slot], wave, lane);
         // w of four heads, the first two or all of them needed
-        if (wave == 0) dma16_s(a.ws_w + ((int64_t)id * H + u.hfirst) * kQ, lane * 16, lds_addr(sh.w[b]));
+        if (half == 0 && wave == 0) dma16_s(a.ws_w + ((int64_t)id * H + u.hfirst) * kQ, lane * 16, lds_addr(sh.w[(t - from) / kQ & 1]));
     };
+    int at0 = 0;  // where the chunk's first half lies
 
     float segdec = 1.0f;
     if (from < to) {
-        stage(from);
+        stage(from, 0, 0);
+        stage(from, 1, 1);
         if (u.on) load(from);
     }
 
-    // the state: acc[nt][c][e] = S[p = 2 r + c][n = 16 nt + 4 q + e] 2^-K, from
-    // the cache where the sequence is one segment and resumes
+    // the state: acc[nt][c][e] = S[p = 2 r + c][n = 16 nt + 4 q + e], from the
+    // cache where the sequence is one segment and resumes
     f32x4 acc[NT][2];
-    int K = 0;
-    float bound = 0.0f;  // of |acc|
     const int64_t off = (int64_t)(u.ch0 + 2 * r) * N + 4 * q, hpn = a.H * a.P * N;
     const bool resume = u.resume, one = u.nseg == 1;
     float *const cache = a.state_cache + (int64_t)slot * hpn + off;
@@ -647,189 +673,133 @@ __global__ __launch_bounds__(128 * kBlocksA, 2) void walk_state_kernel(SsdCacheA
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                acc[nt][c] = *(const f32x4 *)(cache + c * N + 16 * nt);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) bound = __builtin_fmaxf(bound, finite_abs(acc[nt][c][e]));
-            }
-        bound = wave_top(bound);
-        if (bound > 0.0f) {
-            K = uniform(exponent(bound));
-            bound = 1.0f;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[nt][c][e] = __builtin_ldexpf(acc[nt][c][e], -K);
-        }
+            for (int c = 0; c < 2; ++c) acc[nt][c] = *(const f32x4 *)(cache + c * N + 16 * nt);
     }
     for (uint32_t t = from; t < to; t += kQ) {
-        const int b = (int)((t - from) / kQ & 1);
         const uint32_t id = u.chunk0 + t / kQ;
-        vm_wait();
-        lds_barrier();  // the chunk is in LDS, and every wave is done with the one before
-        if (t + kQ < to) stage(t + kQ);
-        if (!u.on) continue;
-        const cf32_ptr meta = (cf32_ptr)(a.ws_meta + ((int64_t)id * H + u.h) * 4);
-        const float dec = meta[0];
-        const int ew = __float_as_int(meta[1]);
-        const int eB = ((const __attribute__((address_space(4))) int *)a.ws_eb)[(int64_t)id * G + u.g];
-        const float *wt = sh.w[b][u.h - u.hfirst] + 16 * q;
         const int rem = to - t < kQ ? (int)(to - t) : kQ;
+        const bool more = t + kQ < to;
+        const int at1 = at0 == 2 ? 0 : at0 + 1, at2 = at1 == 2 ? 0 : at1 + 1;
 
-        // x, and the scale of its operands
         float x[2][16], top = 0.0f;
-        uint32_t badm[2] = {0u, 0u};
-        bool anybad = false;
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                auto at = [&](int j) { return __uint_as_float(c ? raw[i + j] & 0xffff0000u : raw[i + j] << 16); };
-                float v = __builtin_fmaf(w[c][0], at(0), bias[c]);
-                v = __builtin_fmaf(w[c][1], at(1), v);
-                v = __builtin_fmaf(w[c][2], at(2), v);
-                v = __builtin_fmaf(w[c][3], at(3), v);
-                x[c][i] = v * __builtin_amdgcn_rcpf(1.0f + fast_exp2(v));
-            }
-        if (t + kQ < to) load(t + kQ);
-        if (rem < kQ) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) x[c][i] = 16 * q + i < rem ? x[c][i] : 0.0f;
-        }
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int i = 0; i < 16; i += 2)  // keeps a NaN
-                top = __builtin_elementwise_maximum(__builtin_elementwise_maximum(__builtin_fabsf(x[c][i]), __builtin_fabsf(x[c][i + 1])), top);
-        top = wave_top(top);
-        if (!finite(top)) {
-            // A value that is not finite would reach earlier tokens as 0 times
-            // itself: the products take zero for it, and what it reaches (its
-            // channel, from its token on) is marked.
-            anybad = true;
-            top = 0.0f;
+        if (u.on) {
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    if (!finite(x[c][i])) {
-                        badm[c] |= 1u << i;
-                        x[c][i] = 0.0f;
-                    }
-                    top = __builtin_fmaxf(top, __builtin_fabsf(x[c][i]));
+                    auto at = [&](int j) { return __uint_as_float(c ? raw[i + j] & 0xffff0000u : raw[i + j] << 16); };
+                    float v = __builtin_fmaf(w[c][0], at(0), bias[c]);
+                    v = __builtin_fmaf(w[c][1], at(1), v);
+                    v = __builtin_fmaf(w[c][2], at(2), v);
+                    v = __builtin_fmaf(w[c][3], at(3), v);
+                    x[c][i] = v * __builtin_amdgcn_rcpf(1.0f + fast_exp2(v)) * -kLn2;
                 }
-            top = wave_top(top);
-        }
-        const int ex = clampi(uniform(exponent(top)), -100, 127);
-        // B of the first products, ahead of their use
-        f16x8 bh[2][2], bl[2][2];
-        auto read_b = [&](int g) {  // two operands, high and low, in the order (hh, nt)
+            if (rem < kQ) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                bh[g & 1][j] = *(const f16x8 *)(sh.B[b] + ((2 * g + j) * 64 + lane) * 8);
-                bl[g & 1][j] = *(const f16x8 *)(sh.B[b] + kQ * N + ((2 * g + j) * 64 + lane) * 8);
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[c][i] = 16 * q + i < rem ? x[c][i] : 0.0f;
+            }
+        }
+        vm_wait();
+        lds_barrier();  // the chunk is in LDS, and every wave is done with the one before
+        if (more) stage(t + kQ, 0, at2);
+        float dec = 0.0f;
+        const float *wt = sh.w[(t - from) / kQ & 1][u.h - u.hfirst] + 16 * q;
+        bf16x8 bo[2][3][2], v[2][3];
+        auto read_b = [&](int slot, int g) {  // two operands, in three parts each
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) bo[g & 1][p][j] = *(const bf16x8 *)(sh.B[slot] + ((p * NT + 2 * g + j) * 64 + lane) * 8);
+        };
+        // w o x of eight tokens a lane, and their products with B
+        auto products = [&](int hh, int slot) {
+            read_b(slot, 0);
+            f32x4 wq[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) wq[j] = *(const f32x4 *)(wt + 8 * hh + 4 * j);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float wx[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) wx[j] = x[c][8 * hh + j] * wq[j / 4][j % 4];
+                split(wx, v[c]);
+            }
+            if (hh == 0) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) acc[nt][c] *= dec;
+            }
+#pragma unroll
+            for (int g = 0; g < NT / 2; ++g) {
+                if (g + 1 < NT / 2) read_b(slot, g + 1);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int k = 0; k < 6; ++k)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            acc[2 * g + j][c] = mfma(bo[g & 1][kTerm[k][0]][j], v[c][kTerm[k][1]], acc[2 * g + j][c]);
+                __builtin_amdgcn_sched_barrier(0);
             }
         };
-        read_b(0);
-        f32x4 wq[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) wq[j] = *(const f32x4 *)(wt + 4 * j);
-        __builtin_amdgcn_sched_barrier(0);
-        // units of the state after this chunk: S = acc 2^Kn
-        const int eb = uniform(exponent(bound));
-        int kv = ex + ew;
-        const int need = K + eb - 100 + 21 - eB;
-        kv = kv > need ? kv : need;
-        const int Kn = kv - 21 + eB, by = K - Kn;
-        const float f = __builtin_ldexpf(dec, by < 120 ? by : 120);
-        bound = __builtin_fmaf(bound, f, 0x1p27f);
-        if (!finite(bound)) bound = 0x1p27f;
-        segdec *= dec;
-        K = Kn;
-        // x times 2^(14 - ex): walk C's operand as float16, and with w times
-        // 2^(ex + ew - kv) (both exact) the state's
-        const float sx = __builtin_ldexpf(-kLn2, 14 - ex), sw = __builtin_ldexpf(1.0f, ex + ew - kv);
-        f16x8 xo[2][2];
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                x[c][i] *= sx;
-                xo[c][i / 8][i % 8] = (_Float16)x[c][i];
-            }
-        const int64_t at = (int64_t)id * (a.H * a.P / 32) + u.ch0 / 32;
-        if (lane == 0) a.ws_ex[at] = ex + (anybad ? 1 << 16 : 0);
-        if (anybad) {  // a marked value is a NaN again
+        if (u.on) {
+            if (more) load(t + kQ);
+            dec = ((cf32_ptr)(a.ws_meta + ((int64_t)id * H + u.h) * 4))[0];
+            segdec *= dec;
+            // x as walk C's operand: float16 times 2^(14 - ex). A value that is not
+            // finite would reach earlier tokens there as 0 times itself: it is marked.
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (badm[c] >> i & 1) xo[c][i / 8][i % 8] = (_Float16)__builtin_nanf("");
-        }
-        {
-            f16x8 *dst = (f16x8 *)a.ws_x + at * 256 + lane;
+                for (int i = 0; i < 16; ++i) top = __builtin_elementwise_maximum(__builtin_fabsf(x[c][i]), top);  // keeps a NaN
+            top = wave_top(top);
+            const bool anybad = !finite(top);
+            if (anybad) {
+                top = 0.0f;
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, finite_abs(x[c][i]));
+                top = wave_top(top);
+            }
+            const int ex = clampi(uniform(exponent(top)), -100, 127);
+            const float sx = __builtin_ldexpf(1.0f, 14 - ex);
+            const int64_t at = (int64_t)id * (a.H * a.P / 32) + u.ch0 / 32;
+            if (lane == 0) a.ws_ex[at] = ex + (anybad ? 1 << 16 : 0);
+            f16x8 xo[2][2], *dst = (f16x8 *)a.ws_x + at * 256 + lane;
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) xo[c][i / 8][i % 8] = (_Float16)(x[c][i] * sx);
+            if (anybad) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (!finite(x[c][i])) xo[c][i / 8][i % 8] = (_Float16)__builtin_nanf("");
+            }
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) dst[(c * 2 + hh) * 64] = xo[c][hh];
+            // The convolution stands before the products of the SIMD's other wave: the
+            // matrix cores are then fed while it runs (16384 tokens 124 -> 117 us; the
+            // products first: 123).
+            __builtin_amdgcn_s_setprio(0);
+            products(0, at0);
         }
-        f16x8 vh[2][2], vl[2][2];
-        auto split_x = [&](int hh) {
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-                const int i = 8 * hh + j;
-                const float wa = wq[i / 4][i % 4] * sw, wb = wq[i / 4][i % 4 + 1] * sw;
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    f16x2 hi, lo;
-                    split(x[c][i] * wa, x[c][i + 1] * wb, hi, lo);
-                    vh[c][hh][j] = hi[0], vh[c][hh][j + 1] = hi[1];
-                    vl[c][hh][j] = lo[0], vl[c][hh][j + 1] = lo[1];
-                }
-            }
-        };
-        // The convolution stands before the products of the SIMD's other wave: the
-        // matrix cores are then fed while it runs (16384 tokens 124 -> 117 us; the
-        // products first: 123).
-        __builtin_amdgcn_s_setprio(0);
-        split_x(0);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) acc[nt][c] *= f;
-#pragma unroll
-        for (int g = 0; g < NT; ++g) {
-            if (g + 1 < NT) read_b(g + 1);
-            __builtin_amdgcn_sched_barrier(0);
-            const int hh = g / (NT / 2), nt = 2 * g % NT;
-            if (g == 0) split_x(1);
-#pragma unroll
-            for (int k = 0; k < 3; ++k)  // the small products first
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        acc[nt + j][c] = mfma(k == 0 ? bl[g & 1][j] : bh[g & 1][j], k == 1 ? vl[c][hh] : vh[c][hh], acc[nt + j][c]);
-            __builtin_amdgcn_sched_barrier(0);
+        lds_barrier();  // every wave is done with the chunk's first half
+        if (more) stage(t + kQ, 1, at0);
+        if (u.on) {
+            products(1, at1);
+            __builtin_amdgcn_s_setprio(1);
         }
-        __builtin_amdgcn_s_setprio(1);
-        if (anybad) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t o = badm[c];
-                o |= __shfl_xor(o, 16);
-                o |= __shfl_xor(o, 32);
-                if (o)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[nt][c][e] = __builtin_nanf("");
-            }
-        }
+        at0 = at2;
     }
     if (!u.on) return;
     // A sequence of one segment that does not resume is done; one that does is
@@ -839,12 +809,7 @@ __global__ __launch_bounds__(128 * kBlocksA, 2) void walk_state_kernel(SsdCacheA
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            f32x4 v;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = __builtin_ldexpf(acc[nt][c][e], K);
-            *(f32x4 *)(dst + c * N + 16 * nt) = v;
-        }
+        for (int c = 0; c < 2; ++c) *(f32x4 *)(dst + c * N + 16 * nt) = acc[nt][c];
     if (lane == 0) a.ws_segdec[(int64_t)u.sid * H + u.h] = segdec;
 }
 
@@ -922,15 +887,15 @@ __global__ __launch_bounds__(128 * kBlocksC, 2) void walk_out_kernel(SsdCacheArg
         return;
     }
 
-    auto operands = [&](uint32_t t) {
-        return (const char *)a.ws_frag + ((int64_t)(u.chunk0 + t / kQ) * G + u.g) * (frag_elems(N) * 2);
+    auto operands = [&](uint32_t t) {  // in float16
+        return (const char *)a.ws_frag + ((int64_t)(u.chunk0 + t / kQ) * G + u.g) * (frag_elems(N) * 2) + pieces_b(N) * 1024;
     };
     auto stage_b = [&](uint32_t t) {
-        pieces<pieces_b(N) / 2, WAVES>(operands(t), sh.B[(t - from) / kQ & 1], wave, lane);
+        pieces<pieces_b(N) / 3, WAVES>(operands(t), sh.B[(t - from) / kQ & 1], wave, lane);
     };
     auto stage_cg = [&](uint32_t t) {
         const uint32_t i = (t - from) / kQ, i3 = i % 3;
-        const char *f = operands(t) + pieces_b(N) * 1024;
+        const char *f = operands(t) + pieces_b(N) / 3 * 1024;
         pieces<pieces_cg(N), WAVES>(f, sh.CG[i & 1], wave, lane);
         if (wave == WAVES - 1) dma16_s(f + pieces_cg(N) * 1024, lane * 16, lds_addr(sh.scale[i3]));
         if (wave % 2 == 0 && u.on)
