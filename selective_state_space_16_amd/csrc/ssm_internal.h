@@ -229,9 +229,9 @@ struct SsdCacheArgs {
     uint16_t *ws_win;   // prompts: (seqs, 3, C) raw rows before each sequence
     int64_t seg, nchunk, nseg;          // prompts: least tokens per segment, ids of chunks and of segments
     int32_t *ws_plan;                   // tokens per segment, from the lengths, and each sequence's first segment (NULL: seg)
-    void *ws_frag;                      // per (chunk, group): B, C and G as operands, the scales of C
-    float *ws_head, *ws_w, *ws_meta;    // per (chunk, head): decays per token, and of the whole chunk
-    int32_t *ws_eb, *ws_ex;             // exponents of the scales of B per (chunk, group), of x per (chunk, wave)
+    void *ws_frag;                      // per (chunk, group): B, C and G as operands
+    float *ws_head, *ws_w, *ws_dec;     // per (chunk, head): decays per token, and of the whole chunk
+    int32_t *ws_bad;                    // per (chunk, wave): whether x holds what is not finite
     void *ws_x;                         // per (chunk, wave): x as an operand
     float *ws_state, *ws_segdec;        // per segment: end state, then entering state; decay
     float *ws_act;      // step: (seqs, ws_row) x | B | C after the convolution, dt, exp(dt A)

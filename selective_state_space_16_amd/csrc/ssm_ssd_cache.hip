@@ -30,16 +30,16 @@
 // segments of several sequences are chosen and numbered on the device, by one wave
 // of the first launch; otherwise their length is the host's and their ids as above.
 //
-// Precision. The state must come out as a float32 state would, so the products
-// of walk A take both operands as sums of three bfloat16 (24 bits; six products,
-// those left out are below 2^-24 of the whole). bfloat16 has float32's range, so
-// no scale is needed that channels, columns or tokens of unlike size would share.
-// The products for y, which is
-// rounded to bfloat16 in the end, take single float16 operands (11 bits, against
-// 8 of the result). float16 has little range, so they carry power-of-two
-// scales: C one per token, B one per chunk, x one per chunk and wave, w one per
-// chunk; walk C's state accumulates in units 2^K that follow a running bound of its
-// size. Scales are exact, and they cancel in one factor per token at the end.
+// Precision. Operands are sums of bfloat16, 8 bits a part: bfloat16 has float32's
+// range, so nothing carries a scale that channels, columns or tokens of unlike size
+// would share. The state must come out as a float32 state would, so the products
+// of walk A take both operands in three parts (24 bits; six products, those left
+// out are below 2^-24 of the whole). The products for y, which is rounded to
+// bfloat16 (8 bits) in the end, take them in two (16 bits; three products): the
+// state as walk C reads it, C, the masked matrix (with D on its diagonal), x and,
+// for walk C's own copy of the state, B and w o x. G, the decays, every sum and
+// the state itself are float32. x goes through as x times -log2(e), which SiLU's
+// exponential needs; the other factor, -ln(2), stands in w, in dt and in D.
 #include "ssm_common.h"
 #include "ssm_device.h"
 #include "ssm_internal.h"
@@ -48,9 +48,6 @@ namespace ssm {
 
 namespace {
 
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -64,21 +61,20 @@ constexpr int prep_threads(int N) { return 8 * N; }
 constexpr int kBlocksA = 2;       // column blocks of 64 per workgroup of walk A, two waves each
 constexpr int kBlocksC = 4;       // of walk C
 
-// Workspace of one (chunk, group), in 16-bit elements: B in three parts as operand
-// registers (lane-major; half, part, n tile), B and C in float16, G as operand
-// registers, 2^eC per token (float32), filled up to whole 1 KiB pieces.
-constexpr int frag_elems(int N) { return 5 * kQ * N + kQ * kQ + 512; }
-// Floats per (chunk, head) for walk C: cum, cum - log2 dt, exp2(cum), and w as
-// scaled float16, filled up to 1 KiB.
+// Workspace of one (chunk, group), in pieces of 1 KiB, a register of 16 bytes of
+// each lane: B (half, part of 3, n tile), C (part of 2, token tile, 32 of n), G in
+// float32 (token tile, half, four tokens).
+constexpr int pieces_b(int N) { return 6 * N / 16; }
+constexpr int pieces_c(int N) { return 8 * N / 32; }
+constexpr int pieces_g() { return 16; }
+constexpr int64_t frag_bytes(int N) { return (pieces_b(N) + pieces_c(N) + pieces_g()) * 1024; }
+// Floats per (chunk, head) for walk C: cum, -ln(2) dt, exp2(cum), filled up to 1 KiB.
 constexpr int kHead = 4 * kQ;
 // Heads of a wave that forms decays (80 heads then take one workgroup per chunk at
 // N = 128: 16384 tokens 22.2 -> 18.5 us against two heads, a short prompt the same).
 constexpr int kDtHeads = 5;
 constexpr int dt_heads(int N) { return prep_threads(N) / 64 * kDtHeads; }
 
-__device__ __forceinline__ f32x4 mfma(f16x8 a, f16x8 b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
-}
 __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
@@ -100,18 +96,16 @@ __device__ __forceinline__ void split(float (&v)[8], bf16x8 (&out)[PARTS]) {
         out[p] = __builtin_bit_cast(bf16x8, u);
     }
 }
-// The product of two operands of three parts each, as six, the small ones first.
+// The product of two operands of three parts each, as six, the small ones first;
+// the last three are that of two parts each.
 constexpr int kTerm[6][2] = {{2, 0}, {0, 2}, {1, 1}, {1, 0}, {0, 1}, {0, 0}};
+constexpr int kTwo = 3;
 // Buffer accesses: bytes from a wave-uniform base, a range that the hardware
 // checks (loads outside it give 0, stores outside it are dropped).
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *base, uint32_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, bytes, 0x00020000);
 }
-// Smallest e with |v| < 2^e, for a normal v; -126 for zero.
-__device__ __forceinline__ int exponent(float v) { return (int)((__float_as_uint(v) >> 23) & 255) - 126; }
-__device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
 __device__ __forceinline__ bool finite(float v) { return (__float_as_uint(v) & 0x7f800000u) != 0x7f800000u; }
-__device__ __forceinline__ float finite_abs(float v) { return finite(v) ? __builtin_fabsf(v) : 0.0f; }
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // v plus the value of lane (lane - S) of its row of 16 (0 below it).
@@ -129,30 +123,6 @@ __device__ __forceinline__ float wave_prefix_sum(float v) {
     v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x142, 0xA, 0xF, false));
     v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x143, 0xC, 0xF, false));
     return v;
-}
-
-// The largest of the values in a lane's row of 16, none negative.
-__device__ __forceinline__ float row_top(float v) {
-    auto step = [&](int o) { v = __builtin_fmaxf(v, __int_as_float(o)); };
-    step(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x128, 0xF, 0xF, false));  // row_ror:8, 4, 2, 1
-    step(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x124, 0xF, 0xF, false));
-    step(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x122, 0xF, 0xF, false));
-    step(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x121, 0xF, 0xF, false));
-    return v;
-}
-// The largest of the wave's values, none negative (or NaN, which stays): the
-// order of their bits.
-__device__ __forceinline__ float wave_top(float v) {
-    uint32_t u = __float_as_uint(v);
-    auto step = [&](uint32_t o) { u = o > u ? o : u; };
-    step(__builtin_amdgcn_update_dpp(0, u, 0x128, 0xF, 0xF, false));  // row_ror:8, 4, 2, 1
-    step(__builtin_amdgcn_update_dpp(0, u, 0x124, 0xF, 0xF, false));
-    step(__builtin_amdgcn_update_dpp(0, u, 0x122, 0xF, 0xF, false));
-    step(__builtin_amdgcn_update_dpp(0, u, 0x121, 0xF, 0xF, false));
-    const uint32_t a = __builtin_amdgcn_readlane(u, 0), b = __builtin_amdgcn_readlane(u, 16);
-    const uint32_t c = __builtin_amdgcn_readlane(u, 32), d = __builtin_amdgcn_readlane(u, 48);
-    const uint32_t ab = a > b ? a : b, cd = c > d ? c : d;
-    return __uint_as_float(ab > cd ? ab : cd);
 }
 
 // The rows of sequence s, kept inside [0, rows] whatever the offsets hold.
@@ -271,8 +241,6 @@ template <int N>
 struct PrepShared {
     static constexpr int R = N + 4;
     alignas(16) float B[kQ][R], C[kQ][R];
-    float maxb[16];
-    int ec[kQ];
 };
 
 // Which slot a sequence owns (-1: none), and the raw rows before its start.
@@ -321,29 +289,25 @@ __device__ __forceinline__ void chunk_decays(const SsdCacheArgs &a, uint32_t id,
         // from the end, without subtracting: exact where little decays
         const float back = wave_prefix_sum(__shfl(step, 63 - lane));
         const float sfx = lane < 63 ? __shfl(back, 62 - lane) : 0.0f;
-        const float wt = dt * fast_exp2(sfx);
-        const int ed = exponent(wave_top(finite_abs(dt))), ew = exponent(wave_top(finite_abs(wt)));
         float *o = a.ws_head + at * kHead;
         o[lane] = cum;
-        o[kQ + lane] = cum - __builtin_amdgcn_logf(dt) + (float)ed;
+        o[kQ + lane] = finite(dt) ? dt * -kLn2 : 0.0f;  // stands beside zeros of G for the tokens before
         o[2 * kQ + lane] = fast_exp2(cum);
-        ((_Float16 *)(o + 3 * kQ))[lane] = (_Float16)__builtin_ldexpf(wt, -ew);  // below 1, as for walk A below
-        a.ws_w[at * kQ + lane] = wt;
-        if (lane == 63) *(f32x4 *)(a.ws_meta + at * 4) = f32x4{fast_exp2(cum), __int_as_float(ew), __int_as_float(ed), 0.0f};
+        a.ws_w[at * kQ + lane] = dt * -kLn2 * fast_exp2(sfx);
+        if (lane == 63) a.ws_dec[at] = fast_exp2(cum);
     }
 }
 
-// Bound by latency and by its stores of 1.3 KB per (chunk, head) and 58 KB per
-// (chunk, group) together: 9.1 us for one chunk (3 of them an empty launch, 1.6
-// the loads and the convolution, the rest LDS and its barriers: with the low
-// parts of B and C in one array in turn 10.0), 19 us for 16384 tokens of 80 heads
-// (52 MB). The heads' decays have workgroups of their own, so that a short
-// prompt waits for neither: done by the workgroups that convolve B and C, one
-// chunk took 2 us more and 16384 tokens 23 in all.
+// Bound by latency and by its stores of 1.3 KB per (chunk, head) and 96 KB per
+// (chunk, group) together: 8.2 us for one chunk (3 of them an empty launch), 18.5 us
+// for 16384 tokens of 80 heads (52 MB). B and C are held as float32 in LDS and split
+// where they are read. The heads' decays have workgroups of their own, so that a
+// short prompt waits for neither: done by the workgroups that convolve B and C, one
+// chunk took 2 us more and 16384 tokens 4.
 // PLAN: one workgroup more, the first, chooses the segments (in every launch, its
 // code alone took 3 of those 19 us).
 template <int N, bool PLAN>
-__global__ __launch_bounds__(prep_threads(N)) void prepare_kernel(SsdCacheArgs a) {
+__global__ __launch_bounds__(prep_threads(N), 8) void prepare_kernel(SsdCacheArgs a) {
     __shared__ PrepShared<N> sh;
     constexpr int THREADS = prep_threads(N), WAVES = THREADS / 64, HEADS = dt_heads(N);
     uint32_t blk = blockIdx.x;
@@ -407,71 +371,49 @@ __global__ __launch_bounds__(prep_threads(N)) void prepare_kernel(SsdCacheArgs a
             raw[i] = uint2{v[0] | v[1] << 16, v[2] | v[3] << 16};
         }
     }
-    float v[TPB][4], big = 0.0f;
 #pragma unroll
     for (int i = 0; i < TPB; ++i) {
-        float top = 0.0f;
+        f32x4 v;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             auto at = [&](int j) {
                 const uint32_t u = k < 2 ? raw[i + j].x : raw[i + j].y;
                 return __uint_as_float(k % 2 ? u & 0xffff0000u : u << 16);
             };
-            v[i][k] = t0 + i < rem ? conv_silu(w[k][0], w[k][1], w[k][2], w[k][3], bias[k], at(0), at(1), at(2), at(3)) : 0.0f;
-            top = __builtin_fmaxf(top, finite_abs(v[i][k]));
+            v[k] = t0 + i < rem ? conv_silu(w[k][0], w[k][1], w[k][2], w[k][3], bias[k], at(0), at(1), at(2), at(3)) : 0.0f;
         }
-        // the largest value of the token's C, and of the chunk's B
-        top = row_top(top);
-        if constexpr (N == 128) top = __builtin_fmaxf(top, __shfl_xor(top, 16));
-        if (isC) {
-            if (cl == N / 4) sh.ec[t0 + i] = clampi(exponent(top), -100, 120);
-        } else {
-            big = __builtin_fmaxf(big, top);
-        }
+        *(f32x4 *)(isC ? &sh.C[t0 + i][n0] : &sh.B[t0 + i][n0]) = v;
     }
-    big = wave_top(big);
-    if (lane == 0) sh.maxb[wave] = big;
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < WAVES; ++k) big = __builtin_fmaxf(big, sh.maxb[k]);
-    const int eB = clampi(exponent(big), -100, 128);
-#pragma unroll
-    for (int i = 0; i < TPB; ++i) *(f32x4 *)(isC ? &sh.C[t0 + i][n0] : &sh.B[t0 + i][n0]) = f32x4{v[i][0], v[i][1], v[i][2], v[i][3]};
     __syncthreads();
 
-    _Float16 *out = (_Float16 *)a.ws_frag + ((int64_t)id * a.G + g) * frag_elems(N);
+    constexpr int NT = N / 16, KB = N / 32;
+    char *const out = (char *)a.ws_frag + ((int64_t)id * a.G + g) * frag_bytes(N);
     const int r = lane & 15, q = lane >> 4;
     // Each wave forms one of B^T's operands, (h, nt): row n = 16 nt + r, k = token
     // 16 q + 8 h + j;
-    static_assert(2 * (N / 16) == WAVES && 4 * (N / 32) == WAVES);
-    _Float16 *const out16 = out + 3 * kQ * N;
+    static_assert(2 * NT == WAVES && 4 * KB == WAVES);
     {
-        constexpr int NT = N / 16;
         const int h = wave / NT, nt = wave % NT;
         float t[8];
-        f16x8 hi;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            t[j] = sh.B[16 * q + 8 * h + j][16 * nt + r];
-            hi[j] = (_Float16)__builtin_ldexpf(t[j], 7 - eB);
-        }
-        *(f16x8 *)(out16 + (wave * 64 + lane) * 8) = hi;
+        for (int j = 0; j < 8; ++j) t[j] = sh.B[16 * q + 8 * h + j][16 * nt + r];
         bf16x8 part[3];
         split(t, part);
 #pragma unroll
-        for (int p = 0; p < 3; ++p) *((bf16x8 *)out + ((h * 3 + p) * NT + nt) * 64 + lane) = part[p];
+        for (int p = 0; p < 3; ++p) ((bf16x8 *)out)[((h * 3 + p) * NT + nt) * 64 + lane] = part[p];
     }
     // one of C's, (tt, m): row r is token 16 (r / 4) + 4 tt + r % 4, and k runs
     // over n in the order in which two accumulator tiles hold the state;
     const int row = 16 * (r / 4) + r % 4;
     {
-        const int tt = wave / (N / 32), m = wave % (N / 32), e = 7 - sh.ec[row + 4 * tt];
-        const float *src = &sh.C[row + 4 * tt][32 * m + 4 * q];
-        const f32x4 lo = *(const f32x4 *)src, hi = *(const f32x4 *)(src + 16);
-        f16x8 o;
+        const int tt = wave / KB, m = wave % KB;
+        float t[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = (_Float16)__builtin_ldexpf(lo[j], e), o[4 + j] = (_Float16)__builtin_ldexpf(hi[j], e);
-        *(f16x8 *)(out16 + kQ * N + (wave * 64 + lane) * 8) = o;
+        for (int j = 0; j < 8; j += 4) *(f32x4 *)(t + j) = *(const f32x4 *)&sh.C[row + 4 * tt][32 * m + 4 * q + 4 * j];
+        bf16x8 part[2];
+        split(t, part);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) ((bf16x8 *)(out + pieces_b(N) * 1024))[(p * 4 * KB + wave) * 64 + lane] = part[p];
     }
     // and of G's, (tt, h) with row r as in C and k = token s = 16 q + 8 h + j, one
     // or two of the sixteen products (tt, h, b), whose row 4 q + e is token
@@ -482,7 +424,7 @@ __global__ __launch_bounds__(prep_threads(N)) void prepare_kernel(SsdCacheArgs a
         const int f = wave * PER + k, tt = f / 4, sr = row + 4 * (f % 4), s0 = 16 * q + 4 * (f % 4);
         f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int m = 0; m < N / 32; ++m) {
+        for (int m = 0; m < KB; ++m) {
             float cv[8], bv[8];
 #pragma unroll
             for (int j = 0; j < 8; j += 4) {
@@ -495,14 +437,10 @@ __global__ __launch_bounds__(prep_threads(N)) void prepare_kernel(SsdCacheArgs a
 #pragma unroll
             for (int p = 0; p < 6; ++p) acc = mfma(bp[kTerm[p][0]], cp[kTerm[p][1]], acc);
         }
-        f16x4 o;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            o[e] = s0 + e <= row + 4 * tt ? (_Float16)__builtin_ldexpf(acc[e], 7 - sh.ec[row + 4 * tt] - eB) : (_Float16)0.0f;
-        *(f16x4 *)(out16 + 2 * kQ * N + ((f / 2) * 64 + lane) * 8 + 4 * (f % 2)) = o;
+        for (int e = 0; e < 4; ++e) acc[e] = s0 + e <= row + 4 * tt ? acc[e] : 0.0f;
+        ((f32x4 *)(out + (pieces_b(N) + pieces_c(N)) * 1024))[f * 64 + lane] = acc;
     }
-    if (tid < kQ) ((float *)(out16 + 2 * kQ * N + kQ * kQ))[tid] = __builtin_ldexpf(1.0f, sh.ec[tid]);
-    if (tid == 0) a.ws_eb[id * a.G + g] = eB;
 }
 
 // ---------------------------------------------------------------------- walks
@@ -567,12 +505,9 @@ __device__ __forceinline__ void pieces(const void *src, const void *to_lds, int 
 #pragma unroll
     for (int i = 0; i < (PIECES + WAVES - 1) / WAVES; ++i) {
         const int p = i * WAVES + wave;
-        if (p < PIECES) dma16_s((const char *)src + p * 1024, lane * 16, dst + p * 1024);
+        if (PIECES % WAVES == 0 || p < PIECES) dma16_s((const char *)src + p * 1024, lane * 16, dst + p * 1024);
     }
 }
-
-constexpr int pieces_b(int N) { return 3 * kQ * N / 512; }
-constexpr int pieces_cg(int N) { return (kQ * N + kQ * kQ) / 512; }
 
 // Walk A: x, and the segment's end state. B lies in LDS by halves of a chunk (48 KB
 // of three parts each chunk at N = 128), three of them in turn, so that two
@@ -582,8 +517,8 @@ constexpr int pieces_cg(int N) { return (kQ * N + kQ * kQ) / 512; }
 // Bound by instruction issue: per chunk and wave the convolution and SiLU of 32
 // values a lane, their split into three bfloat16 and 192 products (N = 128), from
 // two waves per SIMD, which is what the state's 64 registers and the operands
-// leave room for (249 of 256). 16384 tokens of 80 heads: 148 us for 168 MB of x
-// read and as much written. Operands of two float16 (22 bits, three products, 114
+// leave room for (235 of 256). 16384 tokens of 80 heads: 155 us for 168 MB of x
+// read and twice as much written. Operands of two float16 (22 bits, three products, 114
 // us) need scales that channels, columns and tokens share, and lose what is small
 // beside a neighbour. Workgroups of 6 waves (which do not pair up on a CU) and of 12
 // took 1.7 and 1.35 times as long.
@@ -602,8 +537,7 @@ __global__ __launch_bounds__(128 * kBlocksA, 2) void walk_state_kernel(SsdCacheA
     if (slot < 0) return;
     const uint32_t from = u.from, to = u.to, H = (uint32_t)a.H, G = (uint32_t)a.G;
 
-    // The convolution times -log2(e): its exp2 is SiLU's exponential, and the
-    // factor comes out again with the scales.
+    // The convolution times -log2(e): its exp2 is SiLU's exponential.
     float w[2][4], bias[2];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
@@ -645,7 +579,7 @@ __global__ __launch_bounds__(128 * kBlocksA, 2) void walk_state_kernel(SsdCacheA
     };
     auto stage = [&](uint32_t t, int half, int slot) {
         const uint32_t id = u.chunk0 + t / kQ;
-        pieces<pieces_b(N) / 2, 2 * kBlocksA>((const char *)a.ws_frag + ((int64_t)id * G + u.g) * (frag_elems(N) * 2) + half * (pieces_b(N) / 2 * 1024),
+        pieces<pieces_b(N) / 2, 2 * kBlocksA>((const char *)a.ws_frag + ((int64_t)id * G + u.g) * frag_bytes(N) + half * (pieces_b(N) / 2 * 1024),
                                               sh.B[slot], wave, lane);
         // w of four heads, the first two or all of them needed
         if (half == 0 && wave == 0) dma16_s(a.ws_w + ((int64_t)id * H + u.hfirst) * kQ, lane * 16, lds_addr(sh.w[(t - from) / kQ & 1]));
@@ -692,7 +626,7 @@ __global__ __launch_bounds__(128 * kBlocksA, 2) void walk_state_kernel(SsdCacheA
                     v = __builtin_fmaf(w[c][1], at(1), v);
                     v = __builtin_fmaf(w[c][2], at(2), v);
                     v = __builtin_fmaf(w[c][3], at(3), v);
-                    x[c][i] = v * __builtin_amdgcn_rcpf(1.0f + fast_exp2(v)) * -kLn2;
+                    x[c][i] = v * __builtin_amdgcn_rcpf(1.0f + fast_exp2(v));
                 }
             if (rem < kQ) {
 #pragma unroll
@@ -749,44 +683,30 @@ __global__ __launch_bounds__(128 * kBlocksA, 2) void walk_state_kernel(SsdCacheA
         };
         if (u.on) {
             if (more) load(t + kQ);
-            dec = ((cf32_ptr)(a.ws_meta + ((int64_t)id * H + u.h) * 4))[0];
+            dec = ((cf32_ptr)a.ws_dec)[(int64_t)id * H + u.h];
             segdec *= dec;
-            // x as walk C's operand: float16 times 2^(14 - ex). A value that is not
-            // finite would reach earlier tokens there as 0 times itself: it is marked.
+            // x as walk C's operand, in two parts. One whose first is not finite would
+            // reach earlier tokens there as 0 times itself: that is marked.
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) top = __builtin_elementwise_maximum(__builtin_fabsf(x[c][i]), top);  // keeps a NaN
-            top = wave_top(top);
-            const bool anybad = !finite(top);
-            if (anybad) {
-                top = 0.0f;
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, finite_abs(x[c][i]));
-                top = wave_top(top);
-            }
-            const int ex = clampi(uniform(exponent(top)), -100, 127);
-            const float sx = __builtin_ldexpf(1.0f, 14 - ex);
             const int64_t at = (int64_t)id * (a.H * a.P / 32) + u.ch0 / 32;
-            if (lane == 0) a.ws_ex[at] = ex + (anybad ? 1 << 16 : 0);
-            f16x8 xo[2][2], *dst = (f16x8 *)a.ws_x + at * 256 + lane;
+            const bool anybad = __ballot(!(top < 0x1.ffp127f)) != 0;
+            if (lane == 0) a.ws_bad[at] = anybad;
+            bf16x8 *dst = (bf16x8 *)a.ws_x + at * 512 + lane;
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) xo[c][i / 8][i % 8] = (_Float16)(x[c][i] * sx);
-            if (anybad) {
+                for (int hh = 0; hh < 2; ++hh) {
+                    float t[8];
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
+                    for (int j = 0; j < 8; ++j) t[j] = x[c][8 * hh + j];
+                    bf16x8 part[2];
+                    split(t, part);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (!finite(x[c][i])) xo[c][i / 8][i % 8] = (_Float16)__builtin_nanf("");
-            }
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) dst[(c * 2 + hh) * 64] = xo[c][hh];
+                    for (int p = 0; p < 2; ++p) dst[((p * 2 + c) * 2 + hh) * 64] = part[p];
+                }
             // The convolution stands before the products of the SIMD's other wave: the
             // matrix cores are then fed while it runs (16384 tokens 124 -> 117 us; the
             // products first: 123).
@@ -852,26 +772,29 @@ __global__ __launch_bounds__(256) void join_kernel(SsdCacheArgs a, int N) {
 }
 
 // Walk C: y of a segment. The two waves of a block each form half of the block's
-// masked matrix and put it into LDS as operand registers. An iteration finishes
-// one chunk (the masked product, y, the state) and begins the next one (C S^T and
-// the masked matrix), so that one barrier per chunk is enough and products and
-// vector instructions of both stand side by side; B, C, G and the decays are
-// held twice and loaded a whole iteration ahead. One workgroup fills a CU (160 KB
-// of LDS at N = 128).
+// masked matrix and put it into LDS as operand registers. A chunk is begun (C S^T
+// and the masked matrix, from C, G and the decays in LDS) and finished (the masked
+// product, y, the state, from B), with a barrier behind each; what one phase has
+// read is loaded again for the next chunk during the other. One workgroup fills a
+// CU (154 KB of LDS at N = 128).
 //
-// Bound by instruction issue, as walk A: 48 products for y and 32 for the state
-// per chunk and wave, the masked matrix's exponentials (16 per lane), the
-// operands' LDS reads. 16384 tokens of 80 heads: 112 us; with two barriers per
-// chunk and operands read at their use 126. 6 waves per workgroup 188, 12 waves 140.
+// Two waves per SIMD run 240 products each per chunk (N = 128) in 0.38 of its cycles
+// and issue vector instructions (the splits of the state, of the masked matrix and
+// of w o x, its exponentials) in 0.44; the rest waits for LDS and at the barriers.
+// 16384 tokens of 80 heads: 208 us. With single float16 operands (80 products, no
+// splits, one barrier per chunk) 113, but those hold 11 bits and need scales that
+// channels and tokens share. Steps interleaved by hand, priorities and x loaded a
+// phase earlier changed nothing.
 template <int N>
 __global__ __launch_bounds__(128 * kBlocksC, 2) void walk_out_kernel(SsdCacheArgs a) {
     constexpr int NT = N / 16, KB = N / 32, WAVES = 2 * kBlocksC;
     struct Shared {
-        alignas(16) _Float16 B[2][kQ * N];  // the high parts
-        alignas(16) _Float16 CG[2][kQ * N + kQ * kQ];
-        alignas(16) float scale[3][256];  // 2^eC per token
-        alignas(16) float head[3][kBlocksC][kHead];
-        alignas(16) _Float16 M[2][kBlocksC][8][64][8];
+        bf16x8 B[2][2][NT][64];  // half, part, n tile
+        bf16x8 C[2][4][KB][64];  // part, token tile, 32 of n
+        f32x4 G[4][2][2][64];    // token tile, half, four tokens
+        f32x4 head[2][kBlocksC][kHead / 4];
+        f32x4 w[2][4][kQ / 4];
+        bf16x8 M[kBlocksC][2][4][2][64];  // part, token tile, half
     };
     __shared__ Shared sh;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), r = lane & 15, q = lane >> 4;
@@ -887,57 +810,47 @@ __global__ __launch_bounds__(128 * kBlocksC, 2) void walk_out_kernel(SsdCacheArg
         return;
     }
 
-    auto operands = [&](uint32_t t) {  // in float16
-        return (const char *)a.ws_frag + ((int64_t)(u.chunk0 + t / kQ) * G + u.g) * (frag_elems(N) * 2) + pieces_b(N) * 1024;
+    auto operands = [&](uint32_t t) {
+        return (const char *)a.ws_frag + ((int64_t)(u.chunk0 + t / kQ) * G + u.g) * frag_bytes(N);
     };
-    auto stage_b = [&](uint32_t t) {
-        pieces<pieces_b(N) / 3, WAVES>(operands(t), sh.B[(t - from) / kQ & 1], wave, lane);
+    auto stage_b = [&](uint32_t t) {  // two parts of the three
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) pieces<2 * NT, WAVES>(operands(t) + hh * 3 * NT * 1024, sh.B[hh], wave, lane);
     };
     auto stage_cg = [&](uint32_t t) {
-        const uint32_t i = (t - from) / kQ, i3 = i % 3;
-        const char *f = operands(t) + pieces_b(N) / 3 * 1024;
-        pieces<pieces_cg(N), WAVES>(f, sh.CG[i & 1], wave, lane);
-        if (wave == WAVES - 1) dma16_s(f + pieces_cg(N) * 1024, lane * 16, lds_addr(sh.scale[i3]));
-        if (wave % 2 == 0 && u.on)
-            dma16_s(a.ws_head + ((int64_t)(u.chunk0 + t / kQ) * H + u.h) * kHead, lane * 16, lds_addr(sh.head[i3][wave / 2]));
+        const int b = (int)((t - from) / kQ & 1);
+        const uint32_t first = (u.chunk0 + t / kQ) * H;  // chunks times heads: below 2^24
+        static_assert(offsetof(Shared, G) == offsetof(Shared, C) + pieces_c(N) * 1024);
+        pieces<pieces_c(N) + pieces_g(), WAVES>(operands(t) + pieces_b(N) * 1024, sh.C, wave, lane);
+        if (wave % 2 == 0 && u.on) dma16_s(a.ws_head + (int64_t)uniform(first + u.h) * kHead, lane * 16, lds_addr(sh.head[b][wave / 2]));
+        // w of four heads, the first one or all of them needed
+        if (wave == WAVES - 1) dma16_s(a.ws_w + (int64_t)uniform(first + u.hfirst) * kQ, lane * 16, lds_addr(sh.w[b]));
     };
     if (from < to) {
-        stage_b(from);
         stage_cg(from);
-        if (from + kQ < to) stage_cg(from + kQ);
-    }
-    if (!u.on) {  // no columns: the wave only carries its share of the loads
-        if (from < to) {
+        stage_b(from);
+        if (!u.on) {  // no columns: the wave only carries its share of the loads
             vm_wait();
             lds_barrier();
-        }
-        for (uint32_t t = from; t < to; t += kQ) {
-            vm_wait();
-            lds_barrier();
-            if (t + kQ < to) stage_b(t + kQ);
-            if (t + 2 * kQ < to) stage_cg(t + 2 * kQ);
+            for (uint32_t t = from; t < to; t += kQ) {
+                vm_wait();
+                lds_barrier();
+                if (t + kQ >= to) break;
+                stage_cg(t + kQ);
+                vm_wait();
+                lds_barrier();
+                stage_b(t + kQ);
+            }
         }
     }
 
-    // the state: acc[nt][c][e] = S[p = 2 r + c][n = 16 nt + 4 q + e] 2^-K, kept
-    // below 2^15 by its bound, so that its float16 copy needs no scale of its own
+    // the state: acc[nt][c][e] = S[p = 2 r + c][n = 16 nt + 4 q + e]
     const int64_t off = (int64_t)(u.ch0 + 2 * r) * N + 4 * q, hpn = a.H * a.P * N;
     const bool resume = u.resume, one = u.nseg == 1;
     float *const cache = a.state_cache + (int64_t)slot * hpn + off;
     const float *const own = a.ws_state + (int64_t)u.sid * hpn + off;
     if (u.on && from < to) {
         f32x4 acc[NT][2];
-        int K = 0;
-        float bound = 0.0f;  // of |acc|
-        f16x8 xn[2][2];
-        auto load = [&](uint32_t t) {
-            const f16x8 *src = (const f16x8 *)a.ws_x + ((int64_t)(u.chunk0 + t / kQ) * (a.H * a.P / 32) + u.ch0 / 32) * 256 + lane;
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) xn[c][hh] = src[(c * 2 + hh) * 64];
-        };
-        load(from);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -947,140 +860,112 @@ __global__ __launch_bounds__(128 * kBlocksC, 2) void walk_out_kernel(SsdCacheArg
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    acc[nt][c] = *(const f32x4 *)(src + c * N + 16 * nt);
+                for (int c = 0; c < 2; ++c) acc[nt][c] = *(const f32x4 *)(src + c * N + 16 * nt);
+        }
+        // D on the diagonal of the masked matrix, for the wave's half: of the token
+        // tiles tt = 2 (wave % 2) + k2 the elements (h = wave % 2, j = 4 k2 + r % 4)
+        // of the lanes with q = r / 4
+        const float dsk = a.Dskip && q == r / 4 ? a.Dskip[u.h] * -kLn2 : 0.0f;
+        float diag[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) bound = __builtin_fmaxf(bound, finite_abs(acc[nt][c][e]));
-                }
-            bound = wave_top(bound);
-            if (bound > 0.0f) {
-                K = uniform(exponent(bound)) - 14;
-                bound = 0x1p14f;
+        for (int j = 0; j < 4; ++j) diag[j] = j == r % 4 ? dsk : 0.0f;
+        const int mine = wave % 2;
+
+        vm_wait();
+        lds_barrier();  // the first chunk is in LDS
+        for (uint32_t t = from; t < to; t += kQ) {
+            const int b = (int)((t - from) / kQ & 1), rem = to - t < kQ ? (int)(to - t) : kQ;
+            const bool more = t + kQ < to;
+            const int64_t id = u.chunk0 + t / kQ, at = id * (a.H * a.P / 32) + u.ch0 / 32;
+            const f32x4 *hd = sh.head[b][wave / 2];
+            const float *hf = (const float *)hd;
+
+            bf16x8 x[2][2][2];  // part, c, half
+            {
+                const bf16x8 *src = (const bf16x8 *)a.ws_x + at * 512 + lane;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int p = 0; p < 2; ++p)
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[nt][c][e] = __builtin_ldexpf(acc[nt][c][e], -K);
+                        for (int hh = 0; hh < 2; ++hh) x[p][c][hh] = src[((p * 2 + c) * 2 + hh) * 64];
             }
-        }
-        const float dsk = a.Dskip ? a.Dskip[u.h] : 0.0f;
+            const bool anybad = ((const __attribute__((address_space(4))) int *)a.ws_bad)[at] != 0;
+            const float dec = hf[2 * kQ + kQ - 1];
 
-        // What a chunk is begun with: its exponents and its decay over all.
-        float dec, decn;
-        int ew, ewn, ed, edn, eB, eBn, exb, exbn;
-        auto scalars = [&](uint32_t t) {
-            const uint32_t id = u.chunk0 + t / kQ;
-            const cf32_ptr meta = (cf32_ptr)(a.ws_meta + ((int64_t)id * H + u.h) * 4);
-            decn = meta[0];
-            ewn = __float_as_int(meta[1]), edn = __float_as_int(meta[2]);
-            eBn = ((const __attribute__((address_space(4))) int *)a.ws_eb)[(int64_t)id * G + u.g];
-            exbn = ((const __attribute__((address_space(4))) int *)a.ws_ex)[(int64_t)id * (a.H * a.P / 32) + u.ch0 / 32];
-        };
-        f32x4 Y[4][2];
-        int E2 = 0, E2n = 0;
-        // C S^T of the chunk with the scalars above and the wave's half of its
-        // masked matrix, M[t][s] = G[t][s] exp2(cum_t - cum_s) dt_s.
-        auto begin_chunk = [&](uint32_t i, int ex, int edx, int eBx) {
-            const float *hd = sh.head[i % 3][wave / 2];
-            const _Float16 *CG = sh.CG[i & 1];
-            // C S^T in units 2^(eC + E1), the masked product in units 2^(eC + E2)
-            const int E1 = K - 7;
-            E2n = ex + edx + eBx - 21;
-            const bool small = E1 - E2n > 60;  // nothing beside the state: the factor below stays in range
-            if (small) E2n = E1 - 60;
-            const float cap = small ? -200.0f : 15.0f;
-            // operands are read from LDS one group of products ahead
-            f32x4 cs[4], ec[4];
-            float ct[2];
-            f16x8 gv[2][2], co[2][4];
+            // C S^T of the chunk, and in between the wave's half of the masked matrix,
+            // M[t][s] = G[t][s] exp2(cum_t - cum_s) dt_s: steps of two token tiles and 32
+            // of n, their operands read from LDS one step ahead
+            f32x4 Y[4][2];
+            bf16x8 co[2][2][2];  // step, part, tile
+            auto read_c = [&](int i) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) cs[j] = *(const f32x4 *)(hd + kQ + 16 * q + 4 * j);
+                for (int p = 0; p < 2; ++p)
 #pragma unroll
-            for (int k2 = 0; k2 < 2; ++k2) {
-                ct[k2] = hd[16 * (r / 4) + r % 4 + 4 * (2 * (wave % 2) + k2)];
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh)
-                    gv[k2][hh] = *(const f16x8 *)(CG + kQ * N + (((2 * (wave % 2) + k2) * 2 + hh) * 64 + lane) * 8);
-            }
-            auto read_c = [&](int m) {
-#pragma unroll
-                for (int tt = 0; tt < 4; ++tt) co[m & 1][tt] = *(const f16x8 *)(CG + ((tt * KB + m) * 64 + lane) * 8);
+                    for (int k = 0; k < 2; ++k) co[i & 1][p][k] = sh.C[p][2 * (i & 1) + k][i / 2][lane];
             };
             read_c(0);
-            __builtin_amdgcn_sched_barrier(0);
+            const float ct[2] = {hf[16 * (r / 4) + r % 4 + 8 * mine], hf[16 * (r / 4) + r % 4 + 8 * mine + 4]};
 #pragma unroll
             for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) Y[tt][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            __builtin_amdgcn_sched_barrier(0);
+            bf16x8 so[2][2];  // part, c
 #pragma unroll
-            for (int m = 0; m < KB; ++m) {
-                if (m + 1 < KB) {
-                    read_c(m + 1);
-                } else {
-#pragma unroll
-                    for (int tt = 0; tt < 4; ++tt) ec[tt] = *(const f32x4 *)(hd + 2 * kQ + 16 * q + 4 * tt);
-                }
+            for (int i = 0; i < 2 * KB; ++i) {
+                const int m = i / 2;
+                if (i + 1 < 2 * KB) read_c(i + 1);
                 __builtin_amdgcn_sched_barrier(0);
-                // C S^T, and in between the masked matrix
-                f16x8 so[2];
+                if (i % 2 == 0)
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
+                    for (int c = 0; c < 2; ++c) {
+                        float v[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) so[c][e] = (_Float16)acc[2 * m + e / 4][c][e % 4];
+                        for (int e = 0; e < 8; ++e) v[e] = acc[2 * m + e / 4][c][e % 4];
+                        bf16x8 part[2];
+                        split(v, part);
+                        so[0][c] = part[0], so[1][c] = part[1];
+                    }
 #pragma unroll
-                for (int tt = 0; tt < 4; ++tt)
+                for (int p = kTwo; p < 6; ++p)
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) Y[tt][c] = mfma(co[m & 1][tt], so[c], Y[tt][c]);
+                    for (int k = 0; k < 2; ++k)
 #pragma unroll
-                for (int k = m * 4 / KB; k < (m + 1) * 4 / KB; ++k) {
-                    const int k2 = k / 2, hh = k % 2;
-                    f16x8 me;
+                        for (int c = 0; c < 2; ++c)
+                            Y[2 * (i & 1) + k][c] = mfma(co[i & 1][kTerm[p][0]][k], so[kTerm[p][1]][c], Y[2 * (i & 1) + k][c]);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        // G is zero above the diagonal, where the exponent may be large
-                        me[j] = (_Float16)fast_exp2(__builtin_fminf(ct[k2] - cs[2 * hh + j / 4][j % 4], cap));
-                    *(f16x8 *)&sh.M[i & 1][wave / 2][(2 * (wave % 2) + k2) * 2 + hh][lane][0] = me * gv[k2][hh];
+                for (int o = i * 4 / (2 * KB); o < (i + 1) * 4 / (2 * KB); ++o) {
+                    const int k2 = o / 2, hh = o % 2, tt = 2 * mine + k2;
+                    float v[8];
+#pragma unroll
+                    for (int h4 = 0; h4 < 2; ++h4) {
+                        const f32x4 gv = sh.G[tt][hh][h4][lane], cs = hd[4 * q + 2 * hh + h4], dt = hd[kQ / 4 + 4 * q + 2 * hh + h4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            // G is zero above the diagonal, where the exponent may be large
+                            v[4 * h4 + j] = gv[j] * dt[j] * fast_exp2(__builtin_fminf(ct[k2] - cs[j], 126.0f));
+                    }
+                    const float dg = hh == mine ? 1.0f : 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[4 * k2 + j] = __builtin_fmaf(diag[j], dg, v[4 * k2 + j]);
+                    bf16x8 part[2];
+                    split(v, part);
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) sh.M[wave / 2][p][tt][hh][lane] = part[p];
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
-            const float al = __builtin_ldexpf(1.0f, E1 - E2n);
 #pragma unroll
             for (int tt = 0; tt < 4; ++tt) {
-                ec[tt] *= al;
+                const f32x4 ec = hd[2 * kQ / 4 + 4 * q + tt];
 #pragma unroll
-                for (int c = 0; c < 2; ++c) Y[tt][c] *= ec[tt];
+                for (int c = 0; c < 2; ++c) Y[tt][c] *= ec;
             }
-        };
-        auto of_ex = [](int e) { return e >= 1 << 15 ? e - (1 << 16) : e; };  // without the mark of values that are not finite
 
-        scalars(from);
-        vm_wait();
-        lds_barrier();
-        begin_chunk(0, of_ex(exbn), edn, eBn);
-        for (uint32_t t = from; t < to; t += kQ) {
-            const uint32_t i = (t - from) / kQ;
-            dec = decn, ew = ewn, ed = edn, eB = eBn, exb = exbn, E2 = E2n;
-            const bool anybad = exb >= 1 << 15;
-            const int ex = of_ex(exb), rem = to - t < kQ ? (int)(to - t) : kQ;
-            const bool more = t + kQ < to;
-            if (more) scalars(t + kQ);
-            f16x8 x16[2][2];
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) x16[c][hh] = xn[c][hh];
-            // Issued since the barrier before: the loads of two chunks ahead, x,
-            // and the last chunk's 16 stores of y, which may stay in flight
-            // (accesses complete in order).
-            if (t > from) asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
-            else vm_wait();
-            lds_barrier();  // M is whole, and the next chunk's C, G and decays and this one's B are in LDS
-            if (more) {
-                stage_b(t + kQ);
-                if (t + 2 * kQ < to) stage_cg(t + 2 * kQ);
-                load(t + kQ);
-            }
+            vm_wait();
+            lds_barrier();  // M is whole, B is in LDS, and every wave is done with C, G and the decays
+            if (more) stage_cg(t + kQ);
             uint32_t badm[2] = {0u, 0u};
             if (anybad) {
                 // values that are not finite: zero for the products, and what
@@ -1088,12 +973,19 @@ __global__ __launch_bounds__(128 * kBlocksC, 2) void walk_out_kernel(SsdCacheArg
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const _Float16 v = x16[c][j / 8][j % 8];
-                        if (v != v) {
-                            badm[c] |= 1u << j;
-                            x16[c][j / 8][j % 8] = (_Float16)0.0f;
+                    for (int hh = 0; hh < 2; ++hh) {
+                        u32x4 v[2] = {__builtin_bit_cast(u32x4, x[0][c][hh]), __builtin_bit_cast(u32x4, x[1][c][hh])};
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const uint32_t bits = 0x7f80u << 16 * (j % 2);
+                            if ((v[0][j / 2] & bits) == bits) {
+                                badm[c] |= 1u << (8 * hh + j);
+                                v[0][j / 2] &= ~(0xffffu << 16 * (j % 2));
+                                v[1][j / 2] &= ~(0xffffu << 16 * (j % 2));
+                            }
                         }
+                        x[0][c][hh] = __builtin_bit_cast(bf16x8, v[0]);
+                        x[1][c][hh] = __builtin_bit_cast(bf16x8, v[1]);
                     }
                     bool low = false;  // the channel is marked in an earlier lane's tokens
 #pragma unroll
@@ -1106,84 +998,79 @@ __global__ __launch_bounds__(128 * kBlocksC, 2) void walk_out_kernel(SsdCacheArg
                         if (low || (badm[c] & ((2u << j) - 1))) Y[j / 4][c][j % 4] = __builtin_nanf("");
                 }
             }
-            const float *hd = sh.head[i % 3][wave / 2];
-            // LDS reads stand a group of products ahead of their use
-            f16x8 mo[4][2], wv[2], bq[2][4];
+            // the masked product; steps of two token tiles and a half, as above. In
+            // between w o x and the state's decay.
+            bf16x8 mo[2][2][2], v[2][2][2];  // step, part, tile; part, c, half
+            auto read_m = [&](int i) {
 #pragma unroll
-            for (int tt = 0; tt < 4; ++tt)
+                for (int p = 0; p < 2; ++p)
 #pragma unroll
-                for (int hh = 0; hh < 2; ++hh) mo[tt][hh] = *(const f16x8 *)&sh.M[i & 1][wave / 2][tt * 2 + hh][lane][0];
+                    for (int k = 0; k < 2; ++k) mo[i & 1][p][k] = sh.M[wave / 2][p][2 * (i & 1) + k][i / 2][lane];
+            };
+            read_m(0);
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) wv[hh] = *(const f16x8 *)((const _Float16 *)(hd + 3 * kQ) + 16 * q + 8 * hh);
-            __builtin_amdgcn_sched_barrier(0);
-            // the state: x 2^-sc times w (w < 1 as stored) in units that keep
-            // dec |acc| + 64 |x w B| below 2^15
-            const int c0 = ex + ew + eB - 21;
-            int e1 = K - c0 + uniform(exponent(bound * dec));
-            e1 = e1 > 27 ? e1 : 27;
-            const int sc = e1 - 14, Kn = c0 + sc;
-            const float f = __builtin_ldexpf(dec, K - Kn < 120 ? K - Kn : 120);
-            bound = __builtin_fmaf(bound, f, __builtin_ldexpf(1.0f, 27 - sc));
-            if (!finite(bound)) bound = 0x1p14f;
-            K = Kn;
-            const _Float16 sf = (_Float16)__builtin_ldexpf(1.0f, sc < 24 ? -sc : -24);
-            const _Float16 sw = (_Float16)__builtin_ldexpf(1.0f, sc < 24 ? 0 : 24 - sc);
-            auto read_b = [&](int g) {  // four operands in the order (hh, nt)
+            for (int i = 0; i < 4; ++i) {
+                const int hh = i / 2;
+                if (i + 1 < 4) read_m(i + 1);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) bq[g & 1][k] = *(const f16x8 *)(sh.B[i & 1] + ((4 * g + k) * 64 + lane) * 8);
+                for (int p = kTwo; p < 6; ++p)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            Y[2 * (i & 1) + k][c] = mfma(mo[i & 1][kTerm[p][0]][k], x[kTerm[p][1]][c][hh], Y[2 * (i & 1) + k][c]);
+                {
+                    const int c = i & 1;
+                    const f32x4 *wt = sh.w[b][u.h - u.hfirst] + 4 * q + 2 * hh;
+                    const f32x4 w0 = wt[0], w1 = wt[1];
+                    const u32x4 hi = __builtin_bit_cast(u32x4, x[0][c][hh]), lo = __builtin_bit_cast(u32x4, x[1][c][hh]);
+                    float wx[8];
+#pragma unroll
+                    for (int j = 0; j < 8; j += 2) {
+                        wx[j] = (__uint_as_float(hi[j / 2] << 16) + __uint_as_float(lo[j / 2] << 16)) * (j < 4 ? w0[j % 4] : w1[j % 4]);
+                        wx[j + 1] = (__uint_as_float(hi[j / 2] & 0xffff0000u) + __uint_as_float(lo[j / 2] & 0xffff0000u)) *
+                                    (j < 4 ? w0[j % 4 + 1] : w1[j % 4 + 1]);
+                    }
+                    bf16x8 part[2];
+                    split(wx, part);
+                    v[0][c][hh] = part[0], v[1][c][hh] = part[1];
+                }
+#pragma unroll
+                for (int nt = i * NT / 4; nt < (i + 1) * NT / 4; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) acc[nt][c] *= dec;
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            // the state's products, and in between y
+            bf16x8 bo[2][2][2];  // step, part, tile
+            auto read_b = [&](int i) {
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) bo[i & 1][p][k] = sh.B[i / (NT / 2)][p][2 * (i % (NT / 2)) + k][lane];
             };
             read_b(0);
-            f32x4 rv[4];
-#pragma unroll
-            for (int tt = 0; tt < 4; ++tt) rv[tt] = *(const f32x4 *)(sh.scale[i % 3] + 16 * q + 4 * tt);
-            __builtin_amdgcn_sched_barrier(0);
-            // the masked product
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-                for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) Y[tt][c] = mfma(mo[tt][hh], x16[c][hh], Y[tt][c]);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) acc[nt][c] *= f;
-            f16x8 v[2][2];
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) v[c][hh] = (x16[c][hh] * sf) * (wv[hh] * sw);
-            __builtin_amdgcn_sched_barrier(0);
-            // the state's products, and in between y: ahead of what the SIMD's other
-            // wave begins (eight prompts of 4096 tokens 255 -> 249 us)
-            __builtin_amdgcn_s_setprio(1);
-            const float dx = __builtin_ldexpf(dsk, ex - 14);
             const auto yb = buffer((const char *)a.y + (int64_t)(u.begin + t) * yrow + u.ch0 * 2, (rem - 1) * yrow + 64);
             uint32_t yo = 16 * q * yrow + 4 * r;
             asm volatile("" : "+v"(yo));
-            constexpr int GB = NT / 2;  // groups of four operands
 #pragma unroll
-            for (int g = 0; g < GB; ++g) {
-                if (g + 1 < GB) read_b(g + 1);
+            for (int i = 0; i < NT; ++i) {
+                const int hh = i / (NT / 2), nt = 2 * (i % (NT / 2));
+                if (i + 1 < NT) read_b(i + 1);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int hh = (4 * g + k) / NT, nt = (4 * g + k) % NT;
+                for (int p = kTwo; p < 6; ++p)
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) acc[nt][c] = mfma(bq[g & 1][k], v[c][hh], acc[nt][c]);
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) acc[nt + k][c] = mfma(bo[i & 1][kTerm[p][0]][k], v[kTerm[p][1]][c][hh], acc[nt + k][c]);
+#pragma unroll
+                for (int j = i * 16 / NT; j < (i + 1) * 16 / NT; ++j) {
+                    __builtin_amdgcn_raw_buffer_store_b32(
+                        __builtin_bit_cast(uint32_t, bf16x2{(__bf16)Y[j / 4][0][j % 4], (__bf16)Y[j / 4][1][j % 4]}), yb, yo, 0, 0);
+                    yo += yrow;
                 }
-#pragma unroll
-                for (int tt = g * 4 / GB; tt < (g + 1) * 4 / GB; ++tt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int j = 4 * tt + e;
-                        const float be = __builtin_ldexpf(rv[tt][e], E2);
-                        float o[2];
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) o[c] = __builtin_fmaf((float)x16[c][j / 8][j % 8], dx, Y[tt][c][e] * be);
-                        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, bf16x2{(__bf16)o[0], (__bf16)o[1]}), yb, yo, 0, 0);
-                        yo += yrow;
-                    }
                 __builtin_amdgcn_sched_barrier(0);
             }
             if (anybad) {
@@ -1199,8 +1086,12 @@ __global__ __launch_bounds__(128 * kBlocksC, 2) void walk_out_kernel(SsdCacheArg
                             for (int e = 0; e < 4; ++e) acc[nt][c][e] = __builtin_nanf("");
                 }
             }
-            __builtin_amdgcn_s_setprio(0);
-            if (more) begin_chunk(i + 1, of_ex(exbn), edn, eBn);
+            if (!more) break;
+            // Issued since the barrier before: the next chunk's C, G and decays, then the
+            // 16 stores of y, which may stay in flight (accesses complete in order).
+            asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
+            lds_barrier();  // they are in LDS, and every wave is done with B and M
+            stage_b(t + kQ);
         }
     }
 
@@ -1297,13 +1188,12 @@ size_t plan(SsdCacheArgs &a, int N, char *base) {
     a.ws_slot = (int32_t *)take((size_t)a.seqs * 4);
     a.ws_plan = planned(a.seqs) ? (int32_t *)take((size_t)(a.seqs + 2) * 4) : nullptr;
     a.ws_win = (uint16_t *)take((size_t)a.seqs * 3 * a.C * 2);
-    a.ws_frag = take(chunks * a.G * frag_elems(N) * 2);
+    a.ws_frag = take(chunks * a.G * frag_bytes(N));
     a.ws_head = (float *)take(chunks * a.H * kHead * 4);
     a.ws_w = (float *)take(chunks * a.H * kQ * 4 + 1024);  // read four heads at a time
-    a.ws_meta = (float *)take(chunks * a.H * 16);
-    a.ws_eb = (int32_t *)take(chunks * a.G * 4);
-    a.ws_ex = (int32_t *)take(chunks * (a.H * a.P / 32) * 4);
-    a.ws_x = take(chunks * (a.H * a.P / 32) * 4096);
+    a.ws_dec = (float *)take(chunks * a.H * 4);
+    a.ws_bad = (int32_t *)take(chunks * (a.H * a.P / 32) * 4);
+    a.ws_x = take(chunks * (a.H * a.P / 32) * 8192);
     a.ws_state = (float *)take((size_t)a.nseg * a.H * a.P * N * 4);
     a.ws_segdec = (float *)take((size_t)a.nseg * a.H * 4);
     return at;
