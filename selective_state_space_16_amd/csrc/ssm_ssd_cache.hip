@@ -38,7 +38,7 @@
 // bfloat16 (8 bits) in the end, take them in two (16 bits; three products): the
 // state as walk C reads it, C, the masked matrix (with D on its diagonal), x and,
 // for walk C's own copy of the state, B and w o x. G, the decays, every sum and
-// the state itself are float32. x goes through as x times -log2(e), which SiLU's
+// the state itself are float32, the summed exponents of the decays float64. x goes through as x times -log2(e), which SiLU's
 // exponential needs; the other factor, -ln(2), stands in w, in dt and in D.
 #include "ssm_common.h"
 #include "ssm_device.h"
@@ -68,7 +68,8 @@ constexpr int pieces_b(int N) { return 6 * N / 16; }
 constexpr int pieces_c(int N) { return 8 * N / 32; }
 constexpr int pieces_g() { return 16; }
 constexpr int64_t frag_bytes(int N) { return (pieces_b(N) + pieces_c(N) + pieces_g()) * 1024; }
-// Floats per (chunk, head) for walk C: cum, -ln(2) dt, exp2(cum), filled up to 1 KiB.
+// Floats per (chunk, head) for walk C: cum rounded to float32, -ln(2) dt 2^-rest,
+// exp2(cum), 2^rest, where rest is what that rounding leaves of cum.
 constexpr int kHead = 4 * kQ;
 // Heads of a wave that forms decays (80 heads then take one workgroup per chunk at
 // N = 128: 16384 tokens 22.2 -> 18.5 us against two heads, a short prompt the same).
@@ -108,21 +109,24 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *base, uint3
 __device__ __forceinline__ bool finite(float v) { return (__float_as_uint(v) & 0x7f800000u) != 0x7f800000u; }
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// v plus the value of lane (lane - S) of its row of 16 (0 below it).
-template <int S>
-__device__ __forceinline__ float shr_add(float v) {
-    return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x110 + S, 0xF, 0xF,
-                                                                      false));
+// v plus the value of another lane (0 where DPP control CTRL gives none, or in the
+// rows that ROWS leaves out).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_add(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (uint32_t)u, CTRL, ROWS, 0xF, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (uint32_t)(u >> 32), CTRL, ROWS, 0xF, false);
+    return v + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
-// Inclusive prefix sum over the 64 lanes.
-__device__ __forceinline__ float wave_prefix_sum(float v) {
-    v = shr_add<1>(v);
-    v = shr_add<2>(v);
-    v = shr_add<4>(v);
-    v = shr_add<8>(v);
-    v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x142, 0xA, 0xF, false));
-    v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x143, 0xC, 0xF, false));
-    return v;
+// Inclusive prefix sum over the 64 lanes: within rows of 16 (shifts by 1, 2, 4 and
+// 8), then row 0 to row 1 and 2 to 3, then the lower half to the upper.
+__device__ __forceinline__ double wave_prefix_sum(double v) {
+    v = dpp_add<0x111, 0xF>(v);
+    v = dpp_add<0x112, 0xF>(v);
+    v = dpp_add<0x114, 0xF>(v);
+    v = dpp_add<0x118, 0xF>(v);
+    v = dpp_add<0x142, 0xA>(v);
+    return dpp_add<0x143, 0xC>(v);
 }
 
 // The rows of sequence s, kept inside [0, rows] whatever the offsets hold.
@@ -266,35 +270,37 @@ __device__ __forceinline__ void chunk_decays(const SsdCacheArgs &a, uint32_t id,
     const int lane = threadIdx.x & 63;
     const uint32_t H = (uint32_t)a.H;
     const uint16_t *src = (const uint16_t *)a.dt_raw + (int64_t)(row + (lane < rem ? lane : rem - 1)) * a.dt_stride;
-    float raw[kDtHeads], bias[kDtHeads], A2[kDtHeads];
+    float raw[kDtHeads], bias[kDtHeads];
+    double A2[kDtHeads];
 #pragma unroll
     for (int k = 0; k < kDtHeads; ++k) {
         const uint32_t h = h0 + k < H ? h0 + k : H - 1;
         raw[k] = ld_act(src, h);
         bias[k] = a.dt_bias ? a.dt_bias[h] : 0.0f;
-        A2[k] = a.A[h] * kLog2e;
+        A2[k] = (double)a.A[h] * 1.4426950408889634;
     }
 #pragma unroll
     for (int k = 0; k < kDtHeads; ++k) {
         if (h0 + k >= H) break;
         const int64_t at = (int64_t)id * H + h0 + k;
         const float dt = lane < rem ? softplus(raw[k] + bias[k]) : 0.0f;
-        // A decay of 2^-256 leaves nothing of a float32 state: no more than that,
-        // so that the sums keep bits for the tokens behind (2^14 at most). A step
-        // that is not finite is a NaN from here on, not a decay to nothing.
-        float step = dt * A2[k];
-        step = step < -256.0f ? -256.0f : step;
-        if (!finite(dt)) step = __builtin_nanf("");
-        const float cum = wave_prefix_sum(step);
-        // from the end, without subtracting: exact where little decays
-        const float back = wave_prefix_sum(__shfl(step, 63 - lane));
-        const float sfx = lane < 63 ? __shfl(back, 62 - lane) : 0.0f;
+        // A decay of 2^-256 leaves nothing of a float32 state: no more than that. The
+        // sums reach 2^14 and are differenced, so they are held in double precision
+        // and handed on in two parts. A step that is not finite is a NaN from here on,
+        // not a decay to nothing.
+        double step = (double)dt * A2[k];
+        step = step < -256.0 ? -256.0 : step;
+        if (!finite(dt)) step = __builtin_nan("");
+        const double cum = wave_prefix_sum(step), total = __shfl(cum, 63);
+        const float top = (float)cum, rest = (float)(cum - (double)top);
+        const float own = dt * -kLn2 * fast_exp2(-rest), decay = fast_exp2(top) * fast_exp2(rest);
         float *o = a.ws_head + at * kHead;
-        o[lane] = cum;
-        o[kQ + lane] = finite(dt) ? dt * -kLn2 : 0.0f;  // stands beside zeros of G for the tokens before
-        o[2 * kQ + lane] = fast_exp2(cum);
-        a.ws_w[at * kQ + lane] = dt * -kLn2 * fast_exp2(sfx);
-        if (lane == 63) a.ws_dec[at] = fast_exp2(cum);
+        o[lane] = top;
+        o[kQ + lane] = finite(own) ? own : 0.0f;  // stands beside zeros of G for the tokens before
+        o[2 * kQ + lane] = decay;
+        o[3 * kQ + lane] = fast_exp2(rest);
+        a.ws_w[at * kQ + lane] = dt * -kLn2 * fast_exp2((float)(total - cum));
+        if (lane == 63) a.ws_dec[at] = decay;
     }
 }
 
@@ -905,7 +911,8 @@ __global__ __launch_bounds__(128 * kBlocksC, 2) void walk_out_kernel(SsdCacheArg
                     for (int k = 0; k < 2; ++k) co[i & 1][p][k] = sh.C[p][2 * (i & 1) + k][i / 2][lane];
             };
             read_c(0);
-            const float ct[2] = {hf[16 * (r / 4) + r % 4 + 8 * mine], hf[16 * (r / 4) + r % 4 + 8 * mine + 4]};
+            const float *hrow = hf + 16 * (r / 4) + r % 4 + 8 * mine;
+            const float ct[2] = {hrow[0], hrow[4]}, rest[2] = {hrow[3 * kQ], hrow[3 * kQ + 4]};
 #pragma unroll
             for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
@@ -944,7 +951,7 @@ __global__ __launch_bounds__(128 * kBlocksC, 2) void walk_out_kernel(SsdCacheArg
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
                             // G is zero above the diagonal, where the exponent may be large
-                            v[4 * h4 + j] = gv[j] * dt[j] * fast_exp2(__builtin_fminf(ct[k2] - cs[j], 126.0f));
+                            v[4 * h4 + j] = gv[j] * dt[j] * fast_exp2(__builtin_fminf(ct[k2] - cs[j], 126.0f)) * rest[k2];
                     }
                     const float dg = hh == mine ? 1.0f : 0.0f;
 #pragma unroll

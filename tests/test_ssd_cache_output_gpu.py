@@ -54,7 +54,16 @@ def terms_behind_silu(d):
     return out
 
 
-def output_within(d, what, average=False):
+def positive(d):
+    """Makes every term of y positive."""
+    d["proj"][:, 64:64 + d["C"]].abs_()
+    for k in ("conv_w", "conv_b", "conv_cache", "state_cache"):
+        d[k].abs_()
+
+
+def output_within(d, what, average=None):
+    """Each element's error; and over the rows `average`, if given, that from the
+    definition's rounding."""
     g, y0 = to_gpu(d), before(d)
     got = prompt(g, y0.cuda()).cpu().double()
     torch.cuda.synchronize()
@@ -67,7 +76,8 @@ def output_within(d, what, average=False):
     say(f"  {what}: y worst of bound {float((err / tol.clamp_min(1e-300)).max()):.3f}")
     assert torch.isfinite(got).all()
     assert (err <= tol).all(), what
-    if average:
+    if average is not None:
+        got, y, terms, ya = got[average], y[average], terms[average], ya[average]
         exact = y.bfloat16().double()
         step = torch.exp2(torch.floor(torch.log2(y.abs().clamp_min(2.0 ** -100))) - 7)
         off, most = (got - exact).norm(), torch.sqrt(((2 * 2.0 ** -16 * terms + 32 * U * ya) * step).sum())
@@ -81,10 +91,8 @@ def test_bits(lens, H, P, G, N, step):
     """Every term positive; y is D x with steps of nothing, and mostly the sums with others."""
     say(f"case bits {lens} H={H} P={P} G={G} N={N} {step}")
     d = ssd_inputs(lens, H, P, G, N, seed=41, spare=2, step=step)
-    d["proj"][:, 64:64 + d["C"]].abs_()
-    for k in ("conv_w", "conv_b", "conv_cache", "state_cache"):
-        d[k].abs_()
-    output_within(d, "all", average=True)
+    positive(d)
+    output_within(d, "all", average=slice(None))
 
 
 @pytest.mark.parametrize("lens", [[60, 9, 130], [1400]])
@@ -144,3 +152,14 @@ def test_tokens_of_unlike_size():
     for row in (25, 50, 140):
         d["proj"][row, 64:64 + d["C"]] *= 2.0 ** 30
     output_within(d, "tokens")
+
+
+def test_decays_behind_steps_that_forget():
+    """Ordinary tokens behind ones whose steps leave nothing (a decay of 2^-256 or
+    less each): the decays between them are differences of sums of thousands."""
+    say("case behind forgetting steps")
+    d = ssd_inputs([64] * 4, 2, 64, 1, 64, seed=47, dskip=False)
+    for row in range(0, 256, 64):
+        d["proj"][row:row + 50, 64 + d["C"]:64 + d["C"] + 2] = 300.0
+    positive(d)
+    output_within(d, "behind", average=torch.arange(256) % 64 >= 50)
