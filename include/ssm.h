@@ -578,8 +578,9 @@ int ssm_scan_bwd_trap(int64_t batch, int64_t L, int64_t D, int64_t N, int dtype,
 
 /*
  * Scratch bytes ssm_ssd_fwd_cache needs for these sizes (0 for invalid or
- * empty sizes). It needs no clearing; calls that share a workspace must not
- * run at the same time.
+ * empty sizes), never fewer for more rows or sequences: a workspace for the
+ * largest batch serves any smaller one. It needs no clearing; calls that share a
+ * workspace must not run at the same time.
  */
 size_t ssm_ssd_fwd_cache_workspace_bytes(int64_t seqs, int64_t rows, int64_t H, int64_t P, int64_t G, int64_t N,
                                          int dtype);

@@ -1154,6 +1154,9 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 // wave looks at every sequence in turn, up to 5 us for this many.
 bool planned(int64_t seqs) { return seqs > 1 && seqs <= 256; }
 
+// Workgroups of walk A per segment.
+int64_t segment_units(int64_t H, int64_t P, int64_t G) { return G * ((H / G * (P / 64) + kBlocksA - 1) / kBlocksA); }
+
 // Tokens per segment, the least of them where the device chooses: at most 4
 // rounds of 512 workgroups of walk A whatever the lengths are, (rows + seqs (seg -
 // 1)) / seg segments in the worst case, for the workspace and the launches. One
@@ -1161,7 +1164,7 @@ bool planned(int64_t seqs) { return seqs > 1 && seqs <= 256; }
 // segment's chunks and about two more (16384 tokens of 80 heads in one round 270
 // us, in two 287).
 int64_t segment_tokens(int64_t seqs, int64_t rows, int64_t H, int64_t P, int64_t G) {
-    const int64_t units = G * ((H / G * (P / 64) + kBlocksA - 1) / kBlocksA);
+    const int64_t units = segment_units(H, P, G);
     if (seqs > 1) {
         const int64_t most = 512 * 4 / units;  // segments
         if (most <= seqs) return 2048;
@@ -1178,6 +1181,38 @@ int64_t segment_tokens(int64_t seqs, int64_t rows, int64_t H, int64_t P, int64_t
         if (c < cost) cost = c, best = seg;
     }
     return best < kQ ? kQ : best;
+}
+
+// The segments that the workspace holds: at least as many as the length above gives,
+// and never fewer for more rows or sequences, although that length goes by steps; so
+// that a workspace made for the largest batch serves any smaller one.
+//
+// One sequence in k rounds of m_k workgroups has m_k + 1 at most. k rounds are
+// chosen before the first j that fit only if k (c / m_k + 2) < j (c / m_j + 3), c =
+// rows / 64, which for large c stays true once it is; then m_k counts. Several
+// sequences: the length is above (rows - seqs) / (most - seqs) wherever it is not
+// 2048, and so rows / seg is below most - seqs + seqs / 64.
+int64_t most_segments(int64_t seqs, int64_t rows, int64_t H, int64_t P, int64_t G) {
+    const int64_t units = segment_units(H, P, G), chunks = rows / kQ + 1;
+    int64_t one = 1, j = 0, mj = 0;
+    for (int64_t k = 1; k <= 8; ++k) {
+        const int64_t m = 512 * k / units;
+        if (m < 1) continue;
+        if (j == 0) {
+            j = k, one = mj = m;
+            continue;
+        }
+        const int64_t gain = j * m - k * mj, cost = (2 * k - 3 * j) * mj * m;
+        if ((gain > 0 ? chunks * gain > cost : cost < 0) && m > one) one = m;
+    }
+    int64_t n = one + 1;
+    if (seqs > 1) {
+        const int64_t most = 512 * 4 / units + seqs / kQ + 1, whole = rows / 2048 + seqs;
+        n = n > most ? n : most;
+        n = n > whole ? n : whole;
+    }
+    const int64_t all = rows / kQ + seqs;
+    return n < all ? n : all;
 }
 
 // Cuts the workspace up; returns its size.
@@ -1201,8 +1236,9 @@ size_t plan(SsdCacheArgs &a, int N, char *base) {
     a.ws_dec = (float *)take(chunks * a.H * 4);
     a.ws_bad = (int32_t *)take(chunks * (a.H * a.P / 32) * 4);
     a.ws_x = take(chunks * (a.H * a.P / 32) * 8192);
-    a.ws_state = (float *)take((size_t)a.nseg * a.H * a.P * N * 4);
-    a.ws_segdec = (float *)take((size_t)a.nseg * a.H * 4);
+    const size_t most = (size_t)most_segments(a.seqs, a.rows, a.H, a.P, a.G);
+    a.ws_state = (float *)take(most * a.H * a.P * N * 4);
+    a.ws_segdec = (float *)take(most * a.H * 4);
     return at;
 }
 
