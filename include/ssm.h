@@ -737,7 +737,7 @@ int ssm_add_norm_bwd(int64_t rows, int64_t D, int dtype, int res_dtype, const vo
  *
  * D must be a multiple of groups and the strides at least D (else
  * SSM_ERR_SHAPE); D / groups at most 16384, groups at most 65535 and D
- * below 2^28 (else SSM_ERR_UNSUPPORTED).
+ * at most 2^28 - 64 (else SSM_ERR_UNSUPPORTED).
  */
 int ssm_gate_norm_fwd(int64_t rows, int64_t D, int64_t groups, int dtype, const void *x, int64_t x_stride,
                       const void *z, int64_t z_stride, const float *weight, float eps, void *y, void *stream);

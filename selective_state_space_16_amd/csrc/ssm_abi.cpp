@@ -77,7 +77,7 @@ size_t workspace_for(int64_t batch, int64_t L, int64_t D, int64_t N, int dtype) 
                                                                : twopass_workspace(batch, L, D, N, &K, &Lc);
 }
 
-constexpr int64_t kMaxNorm = (int64_t)1 << 28;  // channels that one launch of the gradients' reduction reaches
+constexpr int64_t kMaxNorm = ((int64_t)1 << 28) - 64;  // channels that one launch of the gradients' reduction reaches
 constexpr int64_t kMaxRow = (int64_t)1 << 23;  // elements between rows of the cache entry points' inputs
 
 // Sizes the SSD layer on a cache takes: heads of 64 to 256 in whole 64s, N of
@@ -832,7 +832,7 @@ static int norm_check(int64_t rows, int64_t D, int64_t groups, int dtype) {
     if (rows < 0 || D < 0 || groups < 0) return SSM_ERR_SHAPE;
     if (dtype != SSM_F32 && dtype != SSM_BF16) return SSM_ERR_DTYPE;
     if (D > 0 && (groups < 1 || D % groups != 0)) return SSM_ERR_SHAPE;
-    if (D > 0 && (D / groups > ssm::kNormMaxWidth || groups > 65535 || D >= kMaxNorm)) return SSM_ERR_UNSUPPORTED;
+    if (D > 0 && (D / groups > ssm::kNormMaxWidth || groups > 65535 || D > kMaxNorm)) return SSM_ERR_UNSUPPORTED;
     return checked_mul(rows, D) < 0 ? SSM_ERR_SHAPE : SSM_OK;
 }
 
