@@ -634,6 +634,12 @@ size_t ssm_ssd_fwd_cache_workspace_bytes(int64_t seqs, int64_t rows, int64_t H, 
  * [0, rows] or decreasing ones are cut to the range, so no access leaves the
  * tensors; what such a call computes is otherwise unspecified.
  *
+ * Products take operands of 24 significant bits for the state and of 16 for y,
+ * sums are float32. Equal calls give equal bits. The lengths and the number of a
+ * call's sequences choose where long ones are cut, and with it the order of their
+ * sums: another batch around a sequence may change its last bits, a captured call
+ * replayed with the same contents does not.
+ *
  * Supported: dtype SSM_BF16, P = 64, 128, 192 or 256, N = 64 or 128, at most
  * 65535 sequences, rows within 2^31 - 1, strides below 2^23 elements, launches
  * of less than 2^32 threads (80 heads: 10^7 tokens); anything else returns
@@ -655,8 +661,10 @@ size_t ssm_ssd_step_cache_workspace_bytes(int64_t batch, int64_t H, int64_t P, i
 /*
  * One decode token per request on the cache of ssm_ssd_fwd_cache: row b is one
  * more token of the sequence whose window and state slot slots[b] holds, both
- * updated in place. Equal to ssm_ssd_fwd_cache over sequences of one token
- * that resume (up to rounding).
+ * updated in place. With SSM_BF16 equal to ssm_ssd_fwd_cache over sequences of
+ * one token that resume (up to rounding). With SSM_F32 the windows are float32
+ * too: ssm_ssd_fwd_cache, which writes bfloat16 ones, cannot fill such a cache; it
+ * starts from cleared slots, a token at a time, or from a converted copy.
  *
  *   slots         (batch)        int32
  *   xBC           (batch, C_all) dtype      rows xBC_stride elements apart

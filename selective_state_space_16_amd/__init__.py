@@ -817,7 +817,9 @@ def ssm_ssd_fwd_cache(xBC, dt_raw, A, conv_w, cu_seqlens, slots, conv_cache, sta
     (C, 4), conv_b (C,) float32; cu_seqlens (seqs + 1,), slots, resume (seqs,)
     int32 on the device; conv_cache (slots, C, 3) bfloat16 and state_cache
     (slots, H, P, N) float32, updated in place; y (rows, H, P). A y that the call
-    allocates is zero in rows outside every sequence; a given one keeps them."""
+    allocates is zero in rows outside every sequence; a given one keeps them. A
+    workspace for the largest batch serves smaller ones. Equal calls give equal
+    bits; other sequences in the call may change a long one's last bits."""
     return _ssd_cache("ssm_ssd_fwd_cache", xBC, dt_raw, A, conv_w, cu_seqlens, slots, conv_cache, state_cache, conv_b,
                       dt_bias, Dskip, resume, y, workspace, stream)
 
@@ -827,7 +829,8 @@ def ssm_ssd_step_cache(xBC, dt_raw, A, conv_w, slots, conv_cache, state_cache, c
     """One decode token per request on the cache of ssm_ssd_fwd_cache: xBC
     (batch, C) and dt_raw (batch, H), float32 or bfloat16; slots (batch,) int32,
     a slot outside the cache (or named by an earlier row) marking a padding row
-    whose y is zeros."""
+    whose y is zeros. float32 activations take a float32 conv_cache, which
+    ssm_ssd_fwd_cache does not fill."""
     return _ssd_cache("ssm_ssd_step_cache", xBC, dt_raw, A, conv_w, None, slots, conv_cache, state_cache, conv_b,
                       dt_bias, Dskip, None, y, workspace, stream)
 

@@ -56,7 +56,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kQ = 64;            // tokens per chunk
 // Threads of a workgroup ahead of the walks: a lane convolves four channels of
-// four tokens (256 threads and 16 tokens: 11.8 us for one chunk against 7).
+// four tokens (256 threads and 16 tokens took 1.6 times as long for one chunk).
 constexpr int prep_threads(int N) { return 8 * N; }
 constexpr int kBlocksA = 2;       // column blocks of 64 per workgroup of walk A, two waves each
 constexpr int kBlocksC = 4;       // of walk C
@@ -72,7 +72,7 @@ constexpr int64_t frag_bytes(int N) { return (pieces_b(N) + pieces_c(N) + pieces
 // exp2(cum), 2^rest, where rest is what that rounding leaves of cum.
 constexpr int kHead = 4 * kQ;
 // Heads of a wave that forms decays (80 heads then take one workgroup per chunk at
-// N = 128: 16384 tokens 22.2 -> 18.5 us against two heads, a short prompt the same).
+// N = 128: 16384 tokens 21.9 -> 18.9 us against two heads, a short prompt the same).
 constexpr int kDtHeads = 5;
 constexpr int dt_heads(int N) { return prep_threads(N) / 64 * kDtHeads; }
 
@@ -191,8 +191,9 @@ __device__ __forceinline__ uint32_t segment_ids(const SsdCacheArgs &a) {
 // second place empty) or their sum over the places and one longest, whichever is
 // less; a segment's state passes through the join besides. Against a length that
 // suits the worst case of as many tokens, whole calls (us): eight prompts of 3600
-// to 4900 tokens, 80 heads 548 -> 528, 13 of 4099, 32 heads 56 -> 53, 9 of 4148 tokens, 68 heads 118 -> 99, 3 of
-// 19798 tokens, 34 heads 159 -> 139; 45 of 5143 tokens, 4 heads 56 -> 62.
+// to 4900 tokens, 80 heads 830 -> 786, 13 of 4099, 32 heads 81 -> 64, 9 of 4148
+// tokens, 68 heads 162 -> 128, 3 of 19798 tokens, 34 heads 300 -> 228; 45 of 5143
+// tokens, 4 heads 50 both ways.
 __device__ __forceinline__ void plan_segments(const SsdCacheArgs &a) {
     if (threadIdx.x >= 64) return;
     const int lane = threadIdx.x, least = (int)(a.seg / kQ);
@@ -305,13 +306,13 @@ __device__ __forceinline__ void chunk_decays(const SsdCacheArgs &a, uint32_t id,
 }
 
 // Bound by latency and by its stores of 1.3 KB per (chunk, head) and 96 KB per
-// (chunk, group) together: 8.2 us for one chunk (3 of them an empty launch), 18.5 us
+// (chunk, group) together: 8.2 us for one chunk (3 of them an empty launch), 18.9 us
 // for 16384 tokens of 80 heads (52 MB). B and C are held as float32 in LDS and split
 // where they are read. The heads' decays have workgroups of their own, so that a
 // short prompt waits for neither: done by the workgroups that convolve B and C, one
 // chunk took 2 us more and 16384 tokens 4.
 // PLAN: one workgroup more, the first, chooses the segments (in every launch, its
-// code alone took 3 of those 19 us).
+// code alone takes 3 us more).
 template <int N, bool PLAN>
 __global__ __launch_bounds__(prep_threads(N), 8) void prepare_kernel(SsdCacheArgs a) {
     __shared__ PrepShared<N> sh;
@@ -523,7 +524,7 @@ __device__ __forceinline__ void pieces(const void *src, const void *to_lds, int 
 // Bound by instruction issue: per chunk and wave the convolution and SiLU of 32
 // values a lane, their split into three bfloat16 and 192 products (N = 128), from
 // two waves per SIMD, which is what the state's 64 registers and the operands
-// leave room for (235 of 256). 16384 tokens of 80 heads: 155 us for 168 MB of x
+// leave room for (235 of 256). 16384 tokens of 80 heads: 153 us for 168 MB of x
 // read and twice as much written. Operands of two float16 (22 bits, three products, 114
 // us) need scales that channels, columns and tokens share, and lose what is small
 // beside a neighbour. Workgroups of 6 waves (which do not pair up on a CU) and of 12
@@ -714,8 +715,7 @@ __global__ __launch_bounds__(128 * kBlocksA, 2) void walk_state_kernel(SsdCacheA
                     for (int p = 0; p < 2; ++p) dst[((p * 2 + c) * 2 + hh) * 64] = part[p];
                 }
             // The convolution stands before the products of the SIMD's other wave: the
-            // matrix cores are then fed while it runs (16384 tokens 124 -> 117 us; the
-            // products first: 123).
+            // matrix cores are then fed while it runs (16384 tokens 171 -> 153 us).
             __builtin_amdgcn_s_setprio(0);
             products(0, at0);
         }
@@ -742,7 +742,7 @@ __global__ __launch_bounds__(128 * kBlocksA, 2) void walk_state_kernel(SsdCacheA
 // Bound by HBM where there are many heads: 63 MB of segment states in 13 us (16384
 // tokens, 80 heads, 12 segments), 131 MB in 25 us (eight prompts of 4096). With
 // few heads there are many segments, and the loads of one after the other are:
-// four ahead take a prompt batch of 21507 tokens, 8 heads, from 70 to 64 us.
+// four ahead take a prompt of 21507 tokens, 8 heads, from 117 to 100 us.
 // enter[k] in place of end[k]: enter[0] the sequence's first state, enter[k+1] =
 // dec[k] enter[k] + end[k]; the last one goes into the cache.
 __global__ __launch_bounds__(256) void join_kernel(SsdCacheArgs a, int N) {
@@ -787,7 +787,7 @@ __global__ __launch_bounds__(256) void join_kernel(SsdCacheArgs a, int N) {
 // Two waves per SIMD run 240 products each per chunk (N = 128) in 0.38 of its cycles
 // and issue vector instructions (the splits of the state, of the masked matrix and
 // of w o x, its exponentials) in 0.44; the rest waits for LDS and at the barriers.
-// 16384 tokens of 80 heads: 208 us. With single float16 operands (80 products, no
+// 16384 tokens of 80 heads: 207 us. With single float16 operands (80 products, no
 // splits, one barrier per chunk) 113, but those hold 11 bits and need scales that
 // channels and tokens share. Steps interleaved by hand, priorities and x loaded a
 // phase earlier changed nothing.
@@ -1161,8 +1161,8 @@ int64_t segment_units(int64_t H, int64_t P, int64_t G) { return G * ((H / G * (P
 // rounds of 512 workgroups of walk A whatever the lengths are, (rows + seqs (seg -
 // 1)) / seg segments in the worst case, for the workspace and the launches. One
 // sequence: the length that costs least over 1 to 8 rounds, a round costing a
-// segment's chunks and about two more (16384 tokens of 80 heads in one round 270
-// us, in two 287).
+// segment's chunks and about two more (16384 tokens of 80 heads in one round 386
+// us, in two 409).
 int64_t segment_tokens(int64_t seqs, int64_t rows, int64_t H, int64_t P, int64_t G) {
     const int64_t units = segment_units(H, P, G);
     if (seqs > 1) {
