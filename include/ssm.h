@@ -768,6 +768,181 @@ int ssm_gate_norm_bwd(int64_t rows, int64_t D, int64_t groups, int dtype, const 
                       void *dz, int64_t dz_stride, float *dweight, void *workspace, size_t workspace_bytes,
                       void *stream);
 
+/*
+ * Scratch bytes ssm_delta_fwd_cache needs for these sizes (0 for invalid or
+ * empty sizes), never fewer for more rows or sequences: a workspace for the
+ * largest batch serves any smaller one. It needs no clearing; calls that share a
+ * workspace must not run at the same time.
+ */
+size_t ssm_delta_fwd_cache_workspace_bytes(int64_t seqs, int64_t rows, int64_t H, int64_t P, int64_t G, int64_t N,
+                                           int dtype);
+
+/*
+ * The gated delta rule over packed prompts of different lengths, on a cache of
+ * states. It is the recurrence of the SSD layer (ssm_ssd_fwd_cache) with another
+ * update: a token first takes from the state what its key already stores, then
+ * adds its value. (The pages describe the SSD layer only; the delta rule is from
+ * its published definition.) Sequence s takes rows cu_seqlens[s] ..
+ * cu_seqlens[s+1] - 1. Per token and head, with g = h / (H / G):
+ *
+ *   q'      = scale * q[g] / sqrt(sum_n q[g][n]^2 + norm_eps)
+ *   k'      = k[g] / sqrt(sum_n k[g][n]^2 + norm_eps)
+ *   a       = exp(softplus(dt_raw[h] + dt_bias[h]) * A[h])
+ *   beta    = 1 / (1 + exp(-beta_raw[h]))
+ *   u[p]    = beta * (v[h][p] - a * sum_n S[p][n] * k'[n])
+ *   S[p][n] = a * S[p][n] + u[p] * k'[n]
+ *   y[h][p] = sum_n S[p][n] * q'[n]
+ *
+ * norm_eps < 0 takes queries and keys as they are (q' = scale * q, k' = k); the
+ * recurrence is then stable only while beta |k|^2 stays below 2.
+ *
+ * A sequence with resume[s] != 0 starts from its slot's state, any other from
+ * zeros (whatever the slot holds); after the call the slot holds the state behind
+ * the sequence's last token. A sequence of no tokens leaves its slot as it is, or
+ * clears it if it does not resume.
+ *
+ *   cu_seqlens    (seqs + 1)     int32      row offsets, not decreasing, from
+ *                                           0 to at most `rows`
+ *   slots         (seqs)         int32      cache slot per sequence
+ *   resume        (seqs)         int32      NULL = every sequence starts from zero
+ *   num_slots                               slots of the cache
+ *   q, k          (rows, G, N)   dtype      rows q_stride, k_stride elements apart
+ *   v             (rows, H, P)   dtype      rows v_stride elements apart
+ *   dt_raw        (rows, H)      dtype      rows dt_stride elements apart
+ *   dt_bias       (H)            float      NULL = zero
+ *   beta_raw      (rows, H)      dtype      rows beta_stride elements apart
+ *   A             (H)            float      negative scalar per head
+ *   state_cache   (num_slots, H, P, N)    float   read and written
+ *   y             (rows, H, P)   dtype      written
+ *   workspace     ssm_delta_fwd_cache_workspace_bytes() bytes
+ *
+ * The offsets, slots and flags are read on the device, so a call may be
+ * captured and replayed with other values in them. A slot outside
+ * [0, num_slots), or one that an earlier sequence of the call names, marks a
+ * sequence to leave out: its rows of y are zeros and no cache entry is
+ * touched. Rows of y outside every sequence are not written. Offsets outside
+ * [0, rows] or decreasing ones are cut to the range, so no access leaves the
+ * tensors; what such a call computes is otherwise unspecified.
+ *
+ * Sums are float32; the state is carried as a float32 recurrence carries it.
+ * Equal calls give equal bits.
+ *
+ * Supported: dtype SSM_BF16, P = 64, 128, 192 or 256, N = 64 or 128, at most
+ * 65535 sequences and heads, rows within 2^31 - 1, strides below 2^23 elements,
+ * launches of less than 2^32 threads; anything else returns
+ * SSM_ERR_UNSUPPORTED. H must be a multiple of G, strides at least the row's
+ * width (else SSM_ERR_SHAPE). Rows of q, k and v lie whole 16-byte pieces apart;
+ * dt_raw and beta_raw need only their element's alignment (else SSM_ERR_ALIGN).
+ * y overlaps no input. Conventions otherwise as above.
+ */
+int ssm_delta_fwd_cache(int64_t seqs, int64_t rows, int64_t H, int64_t P, int64_t G, int64_t N, int dtype,
+                        const int32_t *cu_seqlens, const int32_t *slots, const int32_t *resume, int64_t num_slots,
+                        const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                        int64_t v_stride, const void *dt_raw, int64_t dt_stride, const float *dt_bias,
+                        const void *beta_raw, int64_t beta_stride, const float *A, float scale, float norm_eps,
+                        float *state_cache, void *y, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One decode token per request on the cache of ssm_delta_fwd_cache: row b is one
+ * more token of the sequence whose state slot slots[b] holds, updated in place.
+ * Equal to ssm_delta_fwd_cache over sequences of one token that resume (up to
+ * rounding). No workspace.
+ *
+ *   slots         (batch)        int32
+ *   q, k, v, dt_raw, beta_raw, y          `batch` rows of them
+ *
+ * Every other argument as there; dtype SSM_F32 or SSM_BF16. A slot outside
+ * [0, num_slots), or one that an earlier row names, marks a padding row: its y
+ * is zeros and no cache entry is touched.
+ */
+int ssm_delta_step_cache(int64_t batch, int64_t H, int64_t P, int64_t G, int64_t N, int dtype, const int32_t *slots,
+                         int64_t num_slots, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                         const void *v, int64_t v_stride, const void *dt_raw, int64_t dt_stride,
+                         const float *dt_bias, const void *beta_raw, int64_t beta_stride, const float *A, float scale,
+                         float norm_eps, float *state_cache, void *y, void *stream);
+
+/*
+ * The short causal convolution and SiLU ahead of a layer ("Notas sobre Mamba",
+ * section "O bloco Mamba"), over packed prompts on a cache of windows, for layers
+ * that take their channels from it in other ways than the SSD layer, which has it
+ * built in (ssm_ssd_fwd_cache). Per sequence, with raw[t] its rows of x:
+ *
+ *   u[t,c] = conv_b[c] + sum_{j=0..3} conv_w[c,j] * raw[t-3+j, c]
+ *   y[t,c] = u / (1 + exp(-u))
+ *
+ * The rows before token 0 are those of the slot's window where resume[s] != 0 and
+ * zeros elsewhere; after the call the slot holds the sequence's last three raw
+ * rows, oldest first. Sequences, slots, flags, empty and left-out sequences as in
+ * ssm_ssd_fwd_cache.
+ *
+ *   x             (rows, C)      dtype      rows x_stride elements apart
+ *   conv_w        (C, 4)         float      taps; conv_w[c,3] on the token itself
+ *   conv_b        (C)            float      NULL = zero
+ *   conv_cache    (num_slots, C, 3)  dtype  read and written
+ *   y             (rows, C)      dtype      written, dense; overlaps no input
+ *
+ * dtype SSM_F32 or SSM_BF16, any C below 2^23. No workspace. Status codes as
+ * there.
+ */
+int ssm_conv_fwd_cache(int64_t seqs, int64_t rows, int64_t C, int dtype, const int32_t *cu_seqlens,
+                       const int32_t *slots, const int32_t *resume, int64_t num_slots, const void *x,
+                       int64_t x_stride, const float *conv_w, const float *conv_b, void *conv_cache, void *y,
+                       void *stream);
+
+/*
+ * One token per request on the cache of ssm_conv_fwd_cache: row b is one more
+ * token of the sequence whose window slot slots[b] holds, shifted in place. A slot
+ * outside [0, num_slots), or one that an earlier row names, marks a padding row:
+ * its y is zeros and no cache entry is touched. Every argument as there, `batch`
+ * rows of x and y; y may equal a dense x.
+ */
+int ssm_conv_step_cache(int64_t batch, int64_t C, int dtype, const int32_t *slots, int64_t num_slots, const void *x,
+                        int64_t x_stride, const float *conv_w, const float *conv_b, void *conv_cache, void *y,
+                        void *stream);
+
+/*
+ * The residual sum and the layer norm ahead of a block, per row: ssm_add_norm_fwd
+ * with the mean taken off and a bias,
+ *
+ *   r = residual + scale * x          (r = scale * x where residual is NULL)
+ *   y = (r - mean(r)) / sqrt(mean((r - mean(r))^2) + eps) * weight + bias
+ *
+ *   bias          (D)            float      NULL = zeros
+ *   residual_out  (rows, D)      res_dtype  r (written); may equal residual;
+ *                                           NULL = not written
+ *
+ * Every other argument, the sizes and the status codes as in ssm_add_norm_fwd.
+ */
+int ssm_add_layer_norm_fwd(int64_t rows, int64_t D, int dtype, int res_dtype, const void *x, const void *residual,
+                           const float *scale, const float *weight, const float *bias, float eps, void *y,
+                           void *residual_out, void *stream);
+
+/* Scratch bytes ssm_add_layer_norm_bwd needs (0 for empty or invalid sizes); no
+ * clearing, not shared by calls that run at the same time. */
+size_t ssm_add_layer_norm_bwd_workspace_bytes(int64_t rows, int64_t D);
+
+/*
+ * Gradient of ssm_add_layer_norm_fwd, for the loss sum(dy * y) + sum(dres * r).
+ * With rstd = 1 / sqrt(mean((r - mean(r))^2) + eps), hat = (r - mean(r)) rstd and
+ * g = dy weight:
+ *
+ *   dresidual = rstd * (g - mean(g) - hat * mean(g * hat)) + dres     dx = scale * dresidual
+ *   dweight   = sum over rows of dy * hat      dbias = sum over rows of dy
+ *   dscale    = sum over rows of dresidual * x
+ *
+ *   dresidual     (rows, D)      res_dtype  written; may equal dres or r;
+ *                                           NULL = not written
+ *   dweight,dbias (D)            float      written
+ *   workspace     ssm_add_layer_norm_bwd_workspace_bytes() bytes
+ *
+ * Every other argument as in ssm_add_norm_bwd. Every sum runs in a fixed order, so
+ * equal inputs give equal bits. rows = 0 writes zeros to dweight, dbias and dscale.
+ */
+int ssm_add_layer_norm_bwd(int64_t rows, int64_t D, int dtype, int res_dtype, const void *dy, const void *r,
+                           const float *weight, const void *x, const float *scale, const void *dres, float eps,
+                           void *dx, void *dresidual, float *dweight, float *dbias, float *dscale, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

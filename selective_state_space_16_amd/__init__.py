@@ -43,6 +43,17 @@ Functions (same names as the C ABI):
       root-mean-square norm ahead of a block, and its gradient
   ssm_gate_norm_fwd(x, z, weight, groups=1, ...) -> y and ssm_gate_norm_bwd(dy, x,
       z, weight, ...) -> dict: the gate with the (grouped) norm behind a scan
+  ssm_conv_fwd_cache(x, conv_w, cu_seqlens, slots, conv_cache, ...) -> y and
+      ssm_conv_step_cache(x, conv_w, slots, conv_cache, ...) -> y: the short causal
+      convolution and SiLU over packed prompts and over one token per request, with
+      windows in a cache of slots
+  ssm_delta_fwd_cache(q, k, v, dt_raw, beta_raw, A, cu_seqlens, slots, state_cache,
+      ...) -> y and ssm_delta_step_cache(q, k, v, dt_raw, beta_raw, A, slots,
+      state_cache, ...) -> y: the gated delta rule over packed prompts and over one
+      token per request, with states in a cache of slots
+  ssm_add_layer_norm_fwd(x, weight, bias=None, residual=None, scale=None, ...) ->
+      (y, residual_out) and ssm_add_layer_norm_bwd(dy, r, weight, ...) -> dict: the
+      residual sum with the layer norm ahead of a block, and its gradient
   ssm_scan_workspace_bytes(batch, L, D, N, dtype) -> int
   ssm_scan_workspace_status(workspace, stream=None) -> int: SSM_OK, or
       SSM_ERR_TIMEOUT when a wait of the last scan on that workspace gave up
@@ -64,7 +75,9 @@ __all__ = [
     "workspace_error", "ssm_scan_workspace_status", "SSM_ERR_TIMEOUT", "ssm_scan_fwd_noalloc",
     "ssm_ssd_fwd_cache", "ssm_ssd_fwd_cache_workspace_bytes", "ssm_ssd_step_cache",
     "ssm_ssd_step_cache_workspace_bytes", "ssm_add_norm_fwd", "ssm_add_norm_bwd", "ssm_gate_norm_fwd",
-    "ssm_gate_norm_bwd", "ssm_norm_bwd_workspace_bytes",
+    "ssm_gate_norm_bwd", "ssm_norm_bwd_workspace_bytes", "ssm_conv_fwd_cache", "ssm_conv_step_cache",
+    "ssm_delta_fwd_cache", "ssm_delta_fwd_cache_workspace_bytes", "ssm_delta_step_cache", "ssm_add_layer_norm_fwd",
+    "ssm_add_layer_norm_bwd", "ssm_add_layer_norm_bwd_workspace_bytes",
 ]
 
 SSM_F32 = 0
@@ -87,7 +100,9 @@ EXPORTS = ("ssm_status_string", "ssm_version", "ssm_scan_workspace_bytes", "ssm_
            "ssm_scan_bwd_conv_workspace_bytes", "ssm_scan_bwd_conv",
            "ssm_ssd_fwd_cache_workspace_bytes", "ssm_ssd_fwd_cache", "ssm_ssd_step_cache_workspace_bytes",
            "ssm_ssd_step_cache", "ssm_norm_bwd_workspace_bytes", "ssm_add_norm_fwd", "ssm_add_norm_bwd",
-           "ssm_gate_norm_fwd", "ssm_gate_norm_bwd")
+           "ssm_gate_norm_fwd", "ssm_gate_norm_bwd", "ssm_delta_fwd_cache_workspace_bytes", "ssm_delta_fwd_cache",
+           "ssm_delta_step_cache", "ssm_conv_fwd_cache", "ssm_conv_step_cache", "ssm_add_layer_norm_fwd",
+           "ssm_add_layer_norm_bwd_workspace_bytes", "ssm_add_layer_norm_bwd")
 
 _lib: Optional[ctypes.CDLL] = None
 
@@ -171,6 +186,23 @@ def lib() -> ctypes.CDLL:
     L.ssm_gate_norm_fwd.restype = ci
     L.ssm_gate_norm_bwd.argtypes = [i64, i64, i64, ci, vp, vp, i64, vp, i64, vp, cf, vp, vp, i64, vp, vp, sz, vp]
     L.ssm_gate_norm_bwd.restype = ci
+    rows5 = [vp, i64] * 3 + [vp, i64, vp] + [vp, i64] + [vp, cf, cf, vp, vp]  # q, k, v, dt_raw and its bias, beta_raw, A ..
+    L.ssm_delta_fwd_cache_workspace_bytes.argtypes = [i64] * 6 + [ci]
+    L.ssm_delta_fwd_cache_workspace_bytes.restype = sz
+    L.ssm_delta_fwd_cache.argtypes = [i64] * 6 + [ci, vp, vp, vp, i64] + rows5 + [vp, sz, vp]
+    L.ssm_delta_fwd_cache.restype = ci
+    L.ssm_delta_step_cache.argtypes = [i64] * 5 + [ci, vp, i64] + rows5 + [vp]
+    L.ssm_delta_step_cache.restype = ci
+    L.ssm_conv_fwd_cache.argtypes = [i64, i64, i64, ci, vp, vp, vp, i64, vp, i64] + [vp] * 4 + [vp]
+    L.ssm_conv_fwd_cache.restype = ci
+    L.ssm_conv_step_cache.argtypes = [i64, i64, ci, vp, i64, vp, i64] + [vp] * 4 + [vp]
+    L.ssm_conv_step_cache.restype = ci
+    L.ssm_add_layer_norm_fwd.argtypes = [i64, i64, ci, ci] + [vp] * 5 + [cf] + [vp] * 2 + [vp]
+    L.ssm_add_layer_norm_fwd.restype = ci
+    L.ssm_add_layer_norm_bwd_workspace_bytes.argtypes = [i64, i64]
+    L.ssm_add_layer_norm_bwd_workspace_bytes.restype = sz
+    L.ssm_add_layer_norm_bwd.argtypes = [i64, i64, ci, ci] + [vp] * 6 + [cf] + [vp] * 5 + [vp, sz, vp]
+    L.ssm_add_layer_norm_bwd.restype = ci
     _lib = L
     return L
 
@@ -951,4 +983,196 @@ def ssm_gate_norm_bwd(dy, x, z, weight, groups=1, eps=1e-5, out=None, workspace=
           x_stride, z_ptr, z_stride, _arg(weight, "weight", dev, f32, (D,)), float(eps),
           _arg(o["dx"], "dx", dev, act, shape), dz_ptr, dz_stride, _arg(o["dweight"], "dweight", dev, f32, (D,)),
           *_bytes(workspace, dev))
+    return o
+
+
+def ssm_delta_fwd_cache_workspace_bytes(seqs: int, rows: int, H: int, P: int, G: int, N: int, dtype: int) -> int:
+    return int(lib().ssm_delta_fwd_cache_workspace_bytes(seqs, rows, H, P, G, N, dtype))
+
+
+def ssm_add_layer_norm_bwd_workspace_bytes(rows: int, D: int) -> int:
+    return int(lib().ssm_add_layer_norm_bwd_workspace_bytes(rows, D))
+
+
+def _conv_cache(name, x, conv_w, cu_seqlens, slots, conv_cache, conv_b, resume, y, stream):
+    import torch
+    if x.dim() != 2 or conv_cache.dim() != 3 or slots.dim() != 1:
+        raise ValueError("x must be (rows, C), conv_cache (slots, C, 3) and slots (sequences,)")
+    rows, C = x.shape
+    seqs, num_slots = slots.shape[0], conv_cache.shape[0]
+    act, f32, i32 = x.dtype, torch.float32, torch.int32
+    code = _dtype_code(x)
+    prompt = name == "ssm_conv_fwd_cache"
+    if not prompt and rows != seqs:
+        raise ValueError(f"one row per request: {rows} rows, {seqs} slots")
+    dev = _gpu(x, "x")
+    x_ptr, x_stride = _rows(x, "x", dev, act, (rows, C))
+    allocated = []
+    if y is None:
+        # rows outside every sequence are not written
+        y = (torch.zeros if prompt else torch.empty)((rows, C), dtype=act, device=x.device)
+        allocated.append(y)
+    args = [seqs, rows, C, code] if prompt else [seqs, C, code]
+    if prompt:
+        args.append(_arg(cu_seqlens, "cu_seqlens", dev, i32, (seqs + 1,)))
+    args.append(_arg(slots, "slots", dev, i32, (seqs,)))
+    if prompt:
+        args.append(_arg(resume, "resume", dev, i32, (seqs,)))
+    _call(name, dev, stream, allocated, *args, num_slots, x_ptr, x_stride, _arg(conv_w, "conv_w", dev, f32, (C, 4)),
+          _arg(conv_b, "conv_b", dev, f32, (C,)), _arg(conv_cache, "conv_cache", dev, act, (num_slots, C, 3)),
+          _arg(y, "y", dev, act, (rows, C)))
+    return y
+
+
+def ssm_conv_fwd_cache(x, conv_w, cu_seqlens, slots, conv_cache, conv_b=None, resume=None, y=None, stream=None):
+    """SiLU of the causal width-4 convolution over packed prompts, on a cache of
+    windows. Shapes: x (rows, C), float32 or bfloat16, rows dense but possibly apart
+    (a slice of the projection); conv_w (C, 4), conv_b (C,) float32; cu_seqlens
+    (seqs + 1,), slots, resume (seqs,) int32 on the device; conv_cache (slots, C, 3)
+    in x's dtype, updated in place; y (rows, C), not x. A y that the call allocates
+    is zero in rows outside every sequence; a given one keeps them."""
+    return _conv_cache("ssm_conv_fwd_cache", x, conv_w, cu_seqlens, slots, conv_cache, conv_b, resume, y, stream)
+
+
+def ssm_conv_step_cache(x, conv_w, slots, conv_cache, conv_b=None, y=None, stream=None):
+    """One token per request on the cache of ssm_conv_fwd_cache: x (batch, C); slots
+    (batch,) int32, a slot outside the cache (or named by an earlier row) marking a
+    padding row whose y is zeros."""
+    return _conv_cache("ssm_conv_step_cache", x, conv_w, None, slots, conv_cache, conv_b, None, y, stream)
+
+
+def _delta_cache(name, q, k, v, dt_raw, beta_raw, A, cu_seqlens, slots, state_cache, dt_bias, resume, scale, norm_eps,
+                 y, workspace, stream):
+    import torch
+    if q.dim() != 2 or state_cache.dim() != 4 or slots.dim() != 1:
+        raise ValueError("q must be (rows, G N), state_cache (slots, H, P, N) and slots (sequences,)")
+    rows, GN = q.shape
+    num_slots, H, P, N = state_cache.shape
+    if N == 0 or GN % N:
+        raise ValueError(f"a row of {GN} channels does not hold keys of {N}")
+    G, seqs = GN // N, slots.shape[0]
+    act, f32, i32 = q.dtype, torch.float32, torch.int32
+    code = _dtype_code(q)
+    prompt = name == "ssm_delta_fwd_cache"
+    if not prompt and rows != seqs:
+        raise ValueError(f"one row per request: {rows} rows, {seqs} slots")
+    dev = _gpu(q, "q")
+    allocated = []
+    if y is None:
+        # rows outside every sequence are not written
+        y = (torch.zeros if prompt else torch.empty)((rows, H, P), dtype=act, device=q.device)
+        allocated.append(y)
+    args = [seqs, rows, H, P, G, N, code] if prompt else [seqs, H, P, G, N, code]
+    if prompt:
+        if workspace is None:
+            need = ssm_delta_fwd_cache_workspace_bytes(seqs, rows, H, P, G, N, code)
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+            allocated.append(workspace)
+        args.append(_arg(cu_seqlens, "cu_seqlens", dev, i32, (seqs + 1,)))
+    args.append(_arg(slots, "slots", dev, i32, (seqs,)))
+    if prompt:
+        args.append(_arg(resume, "resume", dev, i32, (seqs,)))
+    _call(name, dev, stream, allocated, *args, num_slots, *_rows(q, "q", dev, act, (rows, GN)),
+          *_rows(k, "k", dev, act, (rows, GN)), *_rows(v, "v", dev, act, (rows, H * P)),
+          *_rows(dt_raw, "dt_raw", dev, act, (rows, H)), _arg(dt_bias, "dt_bias", dev, f32, (H,)),
+          *_rows(beta_raw, "beta_raw", dev, act, (rows, H)), _arg(A, "A", dev, f32, (H,)),
+          N ** -0.5 if scale is None else float(scale), float(norm_eps),
+          _arg(state_cache, "state_cache", dev, f32, (num_slots, H, P, N)), _arg(y, "y", dev, act, (rows, H, P)),
+          *(_bytes(workspace, dev) if prompt else ()))
+    return y
+
+
+def ssm_delta_fwd_cache(q, k, v, dt_raw, beta_raw, A, cu_seqlens, slots, state_cache, dt_bias=None, resume=None,
+                        scale=None, norm_eps=1e-6, y=None, workspace=None, stream=None):
+    """The gated delta rule over packed prompts, on a cache of states. Shapes: q, k
+    (rows, G N), v (rows, H P), dt_raw and beta_raw (rows, H) bfloat16, rows dense but
+    possibly apart (slices of a wider tensor); A, dt_bias (H,) float32; cu_seqlens
+    (seqs + 1,), slots, resume (seqs,) int32 on the device; state_cache (slots, H, P,
+    N) float32, updated in place; y (rows, H, P). Queries and keys are divided by
+    their length, sqrt(sum of squares + norm_eps), unless norm_eps < 0; queries are
+    multiplied by `scale` (N ** -0.5 if None). A y that the call allocates is zero in
+    rows outside every sequence; a given one keeps them. A workspace for the largest
+    batch serves smaller ones. Equal calls give equal bits."""
+    return _delta_cache("ssm_delta_fwd_cache", q, k, v, dt_raw, beta_raw, A, cu_seqlens, slots, state_cache, dt_bias,
+                        resume, scale, norm_eps, y, workspace, stream)
+
+
+def ssm_delta_step_cache(q, k, v, dt_raw, beta_raw, A, slots, state_cache, dt_bias=None, scale=None, norm_eps=1e-6,
+                         y=None, stream=None):
+    """One decode token per request on the cache of ssm_delta_fwd_cache: q, k, v,
+    dt_raw and beta_raw with one row per request, float32 or bfloat16; slots (batch,)
+    int32, a slot outside the cache (or named by an earlier row) marking a padding row
+    whose y is zeros."""
+    return _delta_cache("ssm_delta_step_cache", q, k, v, dt_raw, beta_raw, A, None, slots, state_cache, dt_bias, None,
+                        scale, norm_eps, y, None, stream)
+
+
+def ssm_add_layer_norm_fwd(x, weight, bias=None, residual=None, scale=None, eps=1e-5, y=None, residual_out=None,
+                           stream=None):
+    """r = residual + scale * x, y = layer_norm(r) * weight + bias; returns (y, r).
+    Shapes: x, y (rows, D); residual, r (rows, D) float32 or x's dtype; scale, weight,
+    bias (D,) float32. With neither a residual nor a scale r is x itself, and is
+    written only into a given residual_out; with a scale alone it is float32."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError("x must be (rows, D)")
+    rows, D = x.shape
+    act, f32 = x.dtype, torch.float32
+    code, dev = _dtype_code(x), _gpu(x, "x")
+    allocated = []
+    if y is None:
+        y = torch.empty((rows, D), dtype=act, device=x.device)
+        allocated.append(y)
+    if residual_out is None and (residual is not None or scale is not None):
+        residual_out = torch.empty((rows, D), dtype=f32 if residual is None else residual.dtype, device=x.device)
+        allocated.append(residual_out)
+    rt = act if residual_out is None else residual_out.dtype
+    rcode, shape = code if residual_out is None else _res_code(residual_out, act), (rows, D)
+    _call("ssm_add_layer_norm_fwd", dev, stream, allocated, rows, D, code, rcode, _arg(x, "x", dev, act, shape),
+          _arg(residual, "residual", dev, rt, shape), _arg(scale, "scale", dev, f32, (D,)),
+          _arg(weight, "weight", dev, f32, (D,)), _arg(bias, "bias", dev, f32, (D,)), float(eps),
+          _arg(y, "y", dev, act, shape), _arg(residual_out, "residual_out", dev, rt, shape))
+    return y, x if residual_out is None else residual_out
+
+
+def ssm_add_layer_norm_bwd(dy, r, weight, x=None, scale=None, dres=None, eps=1e-5, out=None, workspace=None,
+                           stream=None):
+    """Gradient of ssm_add_layer_norm_fwd for the loss sum(dy * y) + sum(dres * r). dy
+    (rows, D); r the forward's residual_out; x required with a scale. Returns a dict:
+    dx (like dy), dresidual (like r), dweight, dbias (D,) float32, dscale (D,) float32
+    or None. Without a scale and with r in dy's dtype, dresidual is dx: it is written
+    on its own only where `out` brings it. `out` may hold preallocated outputs by
+    those names."""
+    import torch
+    if dy.dim() != 2:
+        raise ValueError("dy must be (rows, D)")
+    rows, D = dy.shape
+    act, f32 = dy.dtype, torch.float32
+    code, rcode, rt, dev = _dtype_code(dy), _res_code(r, act), r.dtype, _gpu(dy, "dy")
+    o = dict(out or {})
+    allocated = []
+
+    def new(key, shape, dtype):
+        if o.get(key) is None:
+            o[key] = torch.empty(shape, dtype=dtype, device=dy.device)
+            allocated.append(o[key])
+        return o[key]
+
+    shape = (rows, D)
+    dx = new("dx", shape, act)
+    same = scale is None and rt == act and o.get("dresidual") is None
+    dr = None if same else new("dresidual", shape, rt)
+    dw, db = new("dweight", (D,), f32), new("dbias", (D,), f32)
+    ds = new("dscale", (D,), f32) if scale is not None else o.setdefault("dscale", None)
+    if workspace is None:
+        workspace = torch.empty(max(ssm_add_layer_norm_bwd_workspace_bytes(rows, D), 16), dtype=torch.uint8,
+                                device=dy.device)
+        allocated.append(workspace)
+    _call("ssm_add_layer_norm_bwd", dev, stream, allocated, rows, D, code, rcode, _arg(dy, "dy", dev, act, shape),
+          _arg(r, "r", dev, rt, shape), _arg(weight, "weight", dev, f32, (D,)), _arg(x, "x", dev, act, shape),
+          _arg(scale, "scale", dev, f32, (D,)), _arg(dres, "dres", dev, rt, shape), float(eps),
+          _arg(dx, "dx", dev, act, shape), _arg(dr, "dresidual", dev, rt, shape), _arg(dw, "dweight", dev, f32, (D,)),
+          _arg(db, "dbias", dev, f32, (D,)), _arg(ds, "dscale", dev, f32, (D,)), *_bytes(workspace, dev))
+    if same:
+        o["dresidual"] = dx
     return o

@@ -959,6 +959,224 @@ int ssm_gate_norm_bwd(int64_t rows, int64_t D, int64_t groups, int dtype, const 
     return ssm::launch_gate_norm(a, true, dtype, s) == hipSuccess ? SSM_OK : SSM_ERR_HIP;
 }
 
+// Sizes that the gated delta rule takes: threads of a launch per chunk of 64 tokens
+// (or request) and 64 rows of a head's state.
+static bool delta_sizes(int64_t seqs, int64_t rows, int64_t H, int64_t P, int64_t G, int64_t N) {
+    if (P < 64 || P > 256 || P % 64 != 0 || (N != 64 && N != 128)) return false;
+    if (seqs > 65535 || rows > INT32_MAX || H > 65535 || H >= kMaxRow / P || G >= kMaxRow / N) return false;
+    return (rows / 64 + seqs) * (H * P / 64 * 256 + G * 512) <= UINT32_MAX;
+}
+
+static int delta_check(int64_t seqs, int64_t rows, int64_t H, int64_t P, int64_t G, int64_t N, int dtype, bool prompt,
+                       const int32_t *cu_seqlens, const int32_t *slots, const int32_t *resume, int64_t num_slots,
+                       const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                       int64_t v_stride, const void *dt_raw, int64_t dt_stride, const float *dt_bias,
+                       const void *beta_raw, int64_t beta_stride, const float *A, float scale, float norm_eps,
+                       float *state_cache, void *y, ssm::DeltaArgs *a) {
+    if (seqs < 0 || rows < 0 || H < 0 || P < 0 || G < 0 || N < 0 || num_slots < 0) return SSM_ERR_SHAPE;
+    if (dtype != SSM_F32 && dtype != SSM_BF16) return SSM_ERR_DTYPE;
+    if ((prompt && dtype != SSM_BF16) || !delta_sizes(seqs, rows, H, P, G, N)) return SSM_ERR_UNSUPPORTED;
+    if (H > 0 && (G < 1 || H % G != 0)) return SSM_ERR_SHAPE;
+    if (num_slots > INT32_MAX || q_stride < G * N || k_stride < G * N || v_stride < H * P || dt_stride < H ||
+        beta_stride < H)
+        return SSM_ERR_SHAPE;
+    const int64_t strides[] = {q_stride, k_stride, v_stride, dt_stride, beta_stride};
+    for (const int64_t n : strides)
+        if (n >= kMaxRow) return SSM_ERR_UNSUPPORTED;
+    if (checked_mul3(checked_mul(num_slots, H), P, N) < 0) return SSM_ERR_SHAPE;
+    if (seqs == 0 || H == 0) return SSM_OK;
+    if (!slots || !A || !state_cache || (prompt && !cu_seqlens)) return SSM_ERR_NULL;
+    if (rows > 0 && (!q || !k || !v || !dt_raw || !beta_raw || !y)) return SSM_ERR_NULL;
+    const void *ptrs[] = {cu_seqlens, slots, resume, q, k, v, dt_bias, A, state_cache, y};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return SSM_ERR_ALIGN;
+    const int64_t size = dtype == SSM_F32 ? 4 : 2;
+    if ((uintptr_t)dt_raw % size != 0 || (uintptr_t)beta_raw % size != 0 || q_stride * size % 16 != 0 ||
+        k_stride * size % 16 != 0 || v_stride * size % 16 != 0)
+        return SSM_ERR_ALIGN;
+    a->seqs = seqs;
+    a->rows = rows;
+    a->H = H;
+    a->P = P;
+    a->G = G;
+    a->num_slots = num_slots;
+    a->q_stride = q_stride;
+    a->k_stride = k_stride;
+    a->v_stride = v_stride;
+    a->dt_stride = dt_stride;
+    a->beta_stride = beta_stride;
+    a->cu_seqlens = cu_seqlens;
+    a->slots = slots;
+    a->resume = resume;
+    a->q = q;
+    a->k = k;
+    a->v = v;
+    a->dt_raw = dt_raw;
+    a->beta_raw = beta_raw;
+    a->dt_bias = dt_bias;
+    a->A = A;
+    a->scale = scale;
+    a->norm_eps = norm_eps;
+    a->state_cache = state_cache;
+    a->y = y;
+    return SSM_OK;
+}
+
+size_t ssm_delta_fwd_cache_workspace_bytes(int64_t seqs, int64_t rows, int64_t H, int64_t P, int64_t G, int64_t N,
+                                           int dtype) {
+    if (dtype != SSM_BF16 || seqs <= 0 || rows < 0 || H <= 0 || G < 1 || H % G != 0 ||
+        !delta_sizes(seqs, rows, H, P, G, N))
+        return 0;
+    return ssm::delta_workspace(seqs, rows, H, P, G, N);
+}
+
+int ssm_delta_fwd_cache(int64_t seqs, int64_t rows, int64_t H, int64_t P, int64_t G, int64_t N, int dtype,
+                        const int32_t *cu_seqlens, const int32_t *slots, const int32_t *resume, int64_t num_slots,
+                        const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                        int64_t v_stride, const void *dt_raw, int64_t dt_stride, const float *dt_bias,
+                        const void *beta_raw, int64_t beta_stride, const float *A, float scale, float norm_eps,
+                        float *state_cache, void *y, void *workspace, size_t workspace_bytes, void *stream) {
+    ssm::DeltaArgs a{};
+    const int st = delta_check(seqs, rows, H, P, G, N, dtype, true, cu_seqlens, slots, resume, num_slots, q, q_stride,
+                               k, k_stride, v, v_stride, dt_raw, dt_stride, dt_bias, beta_raw, beta_stride, A, scale,
+                               norm_eps, state_cache, y, &a);
+    if (st != SSM_OK || seqs == 0 || H == 0) return st;
+    if (workspace && !aligned16(workspace)) return SSM_ERR_ALIGN;
+    if (!workspace || workspace_bytes < ssm::delta_workspace(seqs, rows, H, P, G, N)) return SSM_ERR_WORKSPACE;
+    return ssm::launch_delta(a, (int)N, workspace, (hipStream_t)stream) == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+}
+
+int ssm_delta_step_cache(int64_t batch, int64_t H, int64_t P, int64_t G, int64_t N, int dtype, const int32_t *slots,
+                         int64_t num_slots, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                         const void *v, int64_t v_stride, const void *dt_raw, int64_t dt_stride,
+                         const float *dt_bias, const void *beta_raw, int64_t beta_stride, const float *A, float scale,
+                         float norm_eps, float *state_cache, void *y, void *stream) {
+    ssm::DeltaArgs a{};
+    const int st = delta_check(batch, batch, H, P, G, N, dtype, false, nullptr, slots, nullptr, num_slots, q, q_stride,
+                               k, k_stride, v, v_stride, dt_raw, dt_stride, dt_bias, beta_raw, beta_stride, A, scale,
+                               norm_eps, state_cache, y, &a);
+    if (st != SSM_OK || batch == 0 || H == 0) return st;
+    return ssm::launch_delta_step(a, (int)N, dtype, (hipStream_t)stream) == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+}
+
+static int conv_cache(int64_t seqs, int64_t rows, int64_t C, int dtype, bool prompt, const int32_t *cu_seqlens,
+                      const int32_t *slots, const int32_t *resume, int64_t num_slots, const void *x, int64_t x_stride,
+                      const float *conv_w, const float *conv_b, void *conv_cache, void *y, void *stream) {
+    if (seqs < 0 || rows < 0 || C < 0 || num_slots < 0) return SSM_ERR_SHAPE;
+    if (dtype != SSM_F32 && dtype != SSM_BF16) return SSM_ERR_DTYPE;
+    // threads of a launch: 256 per 64 tokens (or request) and, at the least, 256 channels
+    if (seqs > 65535 || rows > INT32_MAX || C >= kMaxRow ||
+        ((prompt ? rows / 64 : 0) + seqs) * ((C + 255) / 256) * 256 > UINT32_MAX)
+        return SSM_ERR_UNSUPPORTED;
+    if (num_slots > INT32_MAX || x_stride < C || checked_mul3(num_slots, C, 3) < 0) return SSM_ERR_SHAPE;
+    if (x_stride >= kMaxRow) return SSM_ERR_UNSUPPORTED;
+    if (seqs == 0 || C == 0) return SSM_OK;
+    if (!slots || !conv_w || !conv_cache || (prompt && !cu_seqlens) || (rows > 0 && (!x || !y))) return SSM_ERR_NULL;
+    const void *ptrs[] = {cu_seqlens, slots, resume, x, conv_w, conv_b, conv_cache, y};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return SSM_ERR_ALIGN;
+    ssm::ConvCacheArgs a{};
+    a.seqs = seqs;
+    a.rows = rows;
+    a.C = C;
+    a.num_slots = num_slots;
+    a.x_stride = x_stride;
+    a.cu_seqlens = cu_seqlens;
+    a.slots = slots;
+    a.resume = resume;
+    a.x = x;
+    a.conv_w = conv_w;
+    a.conv_b = conv_b;
+    a.conv_cache = conv_cache;
+    a.y = y;
+    return ssm::launch_conv_cache(a, prompt, dtype, (hipStream_t)stream) == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+}
+
+int ssm_conv_fwd_cache(int64_t seqs, int64_t rows, int64_t C, int dtype, const int32_t *cu_seqlens,
+                       const int32_t *slots, const int32_t *resume, int64_t num_slots, const void *x,
+                       int64_t x_stride, const float *conv_w, const float *conv_b, void *cache, void *y,
+                       void *stream) {
+    return conv_cache(seqs, rows, C, dtype, true, cu_seqlens, slots, resume, num_slots, x, x_stride, conv_w, conv_b,
+                      cache, y, stream);
+}
+
+int ssm_conv_step_cache(int64_t batch, int64_t C, int dtype, const int32_t *slots, int64_t num_slots, const void *x,
+                        int64_t x_stride, const float *conv_w, const float *conv_b, void *cache, void *y,
+                        void *stream) {
+    return conv_cache(batch, batch, C, dtype, false, nullptr, slots, nullptr, num_slots, x, x_stride, conv_w, conv_b,
+                      cache, y, stream);
+}
+
+int ssm_add_layer_norm_fwd(int64_t rows, int64_t D, int dtype, int res_dtype, const void *x, const void *residual,
+                           const float *scale, const float *weight, const float *bias, float eps, void *y,
+                           void *residual_out, void *stream) {
+    const int st = norm_check(rows, D, 1, dtype);
+    if (st != SSM_OK) return st;
+    if (res_dtype != SSM_F32 && res_dtype != dtype) return SSM_ERR_DTYPE;
+    if (rows == 0 || D == 0) return SSM_OK;
+    if (!x || !weight || !y) return SSM_ERR_NULL;
+    const void *ptrs[] = {x, residual, scale, weight, bias, y, residual_out};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return SSM_ERR_ALIGN;
+    ssm::LayerNormArgs a{};
+    a.rows = rows;
+    a.D = D;
+    a.eps = eps;
+    a.x = x;
+    a.residual = residual;
+    a.scale = scale;
+    a.weight = weight;
+    a.bias = bias;
+    a.y = y;
+    a.residual_out = residual_out;
+    return ssm::launch_layer_norm(a, false, dtype, res_dtype, (hipStream_t)stream) == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+}
+
+size_t ssm_add_layer_norm_bwd_workspace_bytes(int64_t rows, int64_t D) {
+    if (rows <= 0 || D <= 0 || checked_mul(rows, D) < 0) return 0;
+    return (size_t)ssm::norm_bwd_blocks(rows) * 3 * (size_t)D * sizeof(float);
+}
+
+int ssm_add_layer_norm_bwd(int64_t rows, int64_t D, int dtype, int res_dtype, const void *dy, const void *r,
+                           const float *weight, const void *x, const float *scale, const void *dres, float eps,
+                           void *dx, void *dresidual, float *dweight, float *dbias, float *dscale, void *workspace,
+                           size_t workspace_bytes, void *stream) {
+    const int st = norm_check(rows, D, 1, dtype);
+    if (st != SSM_OK) return st;
+    if (res_dtype != SSM_F32 && res_dtype != dtype) return SSM_ERR_DTYPE;
+    if (D == 0) return SSM_OK;
+    if (!dweight || !dbias) return SSM_ERR_NULL;
+    if (rows > 0 && (!dy || !r || !weight || !dx || (scale && !x))) return SSM_ERR_NULL;
+    const void *ptrs[] = {dy, r, weight, x, scale, dres, dx, dresidual, dweight, dbias, dscale, workspace};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return SSM_ERR_ALIGN;
+    hipStream_t s = (hipStream_t)stream;
+    if (rows == 0) {
+        float *sums[] = {dweight, dbias, dscale};
+        for (float *p : sums)
+            if (p && ssm::launch_state_copy(nullptr, p, D, s) != hipSuccess) return SSM_ERR_HIP;
+        return SSM_OK;
+    }
+    if (!workspace || workspace_bytes < ssm_add_layer_norm_bwd_workspace_bytes(rows, D)) return SSM_ERR_WORKSPACE;
+    ssm::LayerNormArgs a{};
+    a.rows = rows;
+    a.D = D;
+    a.eps = eps;
+    a.x = x;
+    a.residual = r;
+    a.dy = dy;
+    a.dres = dres;
+    a.scale = scale;
+    a.weight = weight;
+    a.residual_out = dresidual;
+    a.dx = dx;
+    a.dweight = dweight;
+    a.dbias = dbias;
+    a.dscale = scale ? dscale : nullptr;
+    a.part = (float *)workspace;
+    return ssm::launch_layer_norm(a, true, dtype, res_dtype, s) == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+}
+
 }  // extern "C"
 
 namespace ssm {

@@ -241,6 +241,33 @@ size_t ssd_cache_workspace(int64_t seqs, int64_t rows, int64_t H, int64_t P, int
 hipError_t launch_ssd_cache(SsdCacheArgs a, int N, void *workspace, hipStream_t s);
 hipError_t launch_ssd_step_cache(const SsdCacheArgs &a, int N, int dtype, hipStream_t s);
 
+// The gated delta rule on a cache of states: packed prompts (ssm_delta.hip) and
+// one token per request (ssm_delta_step.hip).
+struct DeltaArgs {
+    int64_t seqs, rows, H, P, G, num_slots, q_stride, k_stride, v_stride, dt_stride, beta_stride;
+    const int32_t *cu_seqlens, *slots, *resume;
+    const void *q, *k, *v, *dt_raw, *beta_raw;
+    const float *dt_bias, *A;
+    float scale, norm_eps;  // norm_eps < 0: queries and keys as they are
+    float *state_cache;
+    void *y;
+    // workspace of the prompts
+    int32_t *ws_slot;  // (seqs) the slot a sequence owns, -1 for none
+};
+size_t delta_workspace(int64_t seqs, int64_t rows, int64_t H, int64_t P, int64_t G, int64_t N);
+hipError_t launch_delta(DeltaArgs a, int N, void *workspace, hipStream_t s);
+hipError_t launch_delta_step(const DeltaArgs &a, int N, int dtype, hipStream_t s);
+
+// The short causal convolution and SiLU on a cache of windows (ssm_conv_cache.hip).
+struct ConvCacheArgs {
+    int64_t seqs, rows, C, num_slots, x_stride;
+    const int32_t *cu_seqlens, *slots, *resume;
+    const void *x;
+    const float *conv_w, *conv_b;
+    void *conv_cache, *y;
+};
+hipError_t launch_conv_cache(const ConvCacheArgs &a, bool prompt, int dtype, hipStream_t s);
+
 // The norms of a block (ssm_norm.hip). `residual` and `residual_out` are the
 // sum and its gradient in the backward pass.
 constexpr int64_t kNormMaxWidth = 16384;  // channels of a row (or group) that a workgroup holds
@@ -261,7 +288,16 @@ struct GateNormArgs {
     void *y, *dx, *dz;
     float *dweight, *part;
 };
+struct LayerNormArgs {
+    int64_t rows, D;
+    float eps;
+    const void *x, *residual, *dy, *dres;
+    const float *scale, *weight, *bias;
+    void *y, *residual_out, *dx;
+    float *dweight, *dbias, *dscale, *part;
+};
 int64_t norm_bwd_blocks(int64_t rows);
+hipError_t launch_layer_norm(const LayerNormArgs &a, bool backward, int dtype, int res_dtype, hipStream_t s);
 hipError_t launch_add_norm(const AddNormArgs &a, bool backward, int dtype, int res_dtype, hipStream_t s);
 hipError_t launch_gate_norm(const GateNormArgs &a, bool backward, int dtype, hipStream_t s);
 
