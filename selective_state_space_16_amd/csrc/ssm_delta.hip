@@ -7,8 +7,42 @@
 //   u[p]    = beta (v[p] - a sum_n S[p][n] k'[n])
 //   S[p][n] = a S[p][n] + u[p] k'[n],   y[p] = sum_n S[p][n] q'[n]
 //
-// The rows p of a state never meet: a wave walks a sequence with 16 of them, a lane
-// with N / 4 elements of one row.
+// Every sequence is cut into chunks of 64 tokens. With G_i the summed log decay from
+// the chunk's start through token i, S the state that enters it and
+//
+//   A_ij = beta_i e^(G_i - G_j) k'_i.k'_j  (j < i),   T = (I + A)^-1
+//   M_ij = e^(G_i - G_j) q'_i.k'_j  (j <= i)
+//
+// a chunk's updates solve (I + A) U = diag(beta) (V - diag(e^G) K' S^T), and
+//
+//   U  = T diag(beta) (V - diag(e^G) K' S^T)
+//   y  = diag(e^G) Q' S^T + M U
+//   S^T <- e^(G_last) S^T + (diag(e^(G_last - G)) K')^T U
+//
+// T and M depend on keys, queries and gates alone: the first kernel forms them for
+// all chunks at once, the second walks the chunks of a sequence in order.
+//
+// The walk keeps everything that one chunk hands to the next in one wave's registers.
+// A column of S^T (a row p of the state) never meets another, so a wave takes 16 or
+// 32 of them and all of N and of the 64 tokens. The matrix cores leave a result with
+// its rows in a lane's registers and its columns across 16 lanes, and take their
+// right operand with the summed index in a lane's registers: the result of one
+// product is the next one's right operand as it stands, once its rows are numbered
+// so that the two tiles of 16 rows hold, lane for lane, the eight consecutive indexes
+// of the operand (tile_row). Keys, queries, T, M and the transposed keys are left
+// operands, shared by the waves of a workgroup through LDS, laid out there (and by
+// the first kernel in the workspace) as a wave loads them.
+//
+// Precision. Keys and queries are bfloat16 as they come; their lengths, the gates and
+// the decays are factors per token, applied in float32 to what they multiply. The
+// other operands are sums of bfloat16, 8 bits a part. The state must come out as a
+// float32 recurrence leaves it, so S, T, beta (V - ..) and U take three parts on
+// its way (24 bits); the products for y, which is rounded to 8 bits in the end, take
+// two parts of S, M and U (16 bits). Sums are float32, the summed log decays float64.
+//
+// Where an update is not finite, because an input is not, zeros of T and M no longer
+// keep a token from those before it: the wave takes such a chunk a token at a time
+// instead, from the state that entered it.
 #include "ssm_delta_device.h"
 #include "ssm_packed.h"
 
@@ -16,20 +50,27 @@ namespace ssm {
 
 namespace {
 
-constexpr int kCols = 16;  // state rows p of a wave
+constexpr int kQ = 64;  // tokens per chunk
+constexpr int kPrepThreads = 256;
+// T and M as left operands: (tile of 16 rows, 32 of the columns) where the columns
+// are not wholly above the diagonal, a register of 16 bytes of each lane per part.
+constexpr int kTri = 6, kPartsT = 3, kPartsM = 2;
+constexpr int kFragTM = kTri * (kPartsT + kPartsM);  // pieces of 1 KiB per (chunk, head)
+constexpr int kScalars = 4 * kQ;                      // floats per (chunk, head): e^G / |k|, beta, e^(G_last - G) / |k|, scale e^G / |q|
+constexpr int pieces_kt(int N) { return 2 * N / 16; }  // of the transposed keys per (chunk, group)
 
-// Which slot each sequence owns, -1 for none.
-__global__ __launch_bounds__(256) void delta_slots_kernel(DeltaArgs a) {
-    const int64_t s = blockIdx.x;
-    const int32_t slot = a.slots[s];
-    bool dead = slot < 0 || slot >= a.num_slots;
-    if (!dead) {
-        bool same = false;
-        for (int64_t i = threadIdx.x; i < s; i += 256) same |= a.slots[i] == slot;
-        dead = __syncthreads_or(same);
-    }
-    if (threadIdx.x == 0) a.ws_slot[s] = dead ? -1 : slot;
-}
+__device__ __forceinline__ int tri_index(int tile, int half) { return tile < 2 ? tile : 2 * tile - 2 + half; }
+
+// The index, within 64 tokens or N keys' elements, of row m of tile t: two tiles share
+// 32 indexes, of which lane group m / 4 holds eight consecutive ones.
+__device__ __forceinline__ int tile_row(int t, int m) { return 32 * (t >> 1) + 8 * (m >> 2) + 4 * (t & 1) + (m & 3); }
+
+// The product of two operands of three parts each, as six, the small ones first; the
+// last three are that of two parts each.
+constexpr int kTerm[6][2] = {{2, 0}, {0, 2}, {1, 1}, {1, 0}, {0, 1}, {0, 0}};
+constexpr int kTwo = 3;
+
+__device__ __forceinline__ f32x4 mfma_f32(float a, float b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
 
 // Eight bfloat16 as floats.
 __device__ __forceinline__ void ld8(const uint16_t *p, float *v) {
@@ -41,89 +82,564 @@ __device__ __forceinline__ void ld8(const uint16_t *p, float *v) {
     }
 }
 
-// v summed over the four lanes that share a state row.
+// v summed over the four lanes that hold the same place of a tile's 16.
 __device__ __forceinline__ float sum_groups(float v) {
     v += __shfl_xor(v, 16);
     return v + __shfl_xor(v, 32);
 }
 
+// -------------------------------------------------------------------- prepare
+
 template <int N>
-__global__ __launch_bounds__(64) void delta_walk_kernel(DeltaArgs a) {
+struct PrepShared {
+    static constexpr int R = kQ + 4, RK = N + 8;
+    alignas(16) float A[kQ][R], M[kQ][R];
+    union {
+        alignas(16) float T[kQ][R];
+        alignas(16) uint16_t K[kQ][RK];
+    };
+    double cum[kQ];
+    float beta[kQ], rk[kQ], rq[kQ];
+};
+
+// Which slot a sequence owns, -1 for none.
+__device__ __forceinline__ void own_slot(const DeltaArgs &a, int64_t s) {
+    const int32_t slot = a.slots[s];
+    bool dead = slot < 0 || slot >= a.num_slots;
+    if (!dead) {
+        bool same = false;
+        for (int64_t i = threadIdx.x; i < s; i += kPrepThreads) same |= a.slots[i] == slot;
+        dead = __syncthreads_or(same);
+    }
+    if (threadIdx.x == 0) a.ws_slot[s] = dead ? -1 : slot;
+}
+
+// One (chunk, head): T and M, the factors per token, and for the first head of a group
+// the transposed keys. Wave w takes tile w of 16 rows (tokens 16 w ..).
+template <int N>
+__global__ __launch_bounds__(kPrepThreads) void delta_prepare_kernel(DeltaArgs a) {
+    __shared__ PrepShared<N> sh;
     constexpr int KB = N / 32;
-    const int64_t h = blockIdx.y, s = blockIdx.z, g = h / (a.H / a.G);
-    const int lane = threadIdx.x, grp = lane >> 4;
-    const int64_t p = (int64_t)blockIdx.x * kCols + (lane & 15);
-    const uint32_t begin = seq_begin(a, s), len = seq_length(a, s, begin);
-    const int32_t slot = a.ws_slot[s];
-    uint16_t *y = (uint16_t *)a.y + ((int64_t)begin * a.H + h) * a.P + p;
-    if (slot < 0) {
-        if (grp == 0)
-            for (uint32_t t = 0; t < len; ++t) y[(int64_t)t * a.H * a.P] = 0;
+    uint32_t blk = blockIdx.x;
+    if (blk < a.seqs) {
+        own_slot(a, blk);
         return;
     }
-    float *cache = a.state_cache + (((int64_t)slot * a.H + h) * a.P + p) * N + 8 * grp;
-    const bool resume = a.resume && a.resume[s] != 0;
-    float S[KB][8];  // n = 32 b + 8 grp + e
-#pragma unroll
-    for (int b = 0; b < KB; ++b)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) S[b][e] = resume ? cache[32 * b + e] : 0.0f;
-    const uint16_t *qp = (const uint16_t *)a.q + begin * a.q_stride + g * N + 8 * grp;
-    const uint16_t *kp = (const uint16_t *)a.k + begin * a.k_stride + g * N + 8 * grp;
-    const uint16_t *vp = (const uint16_t *)a.v + begin * a.v_stride + h * a.P + p;
-    const float bias = a.dt_bias ? a.dt_bias[h] : 0.0f, A = a.A[h] * kLog2e;
-    for (uint32_t t = 0; t < len; ++t) {
-        float k[KB][8], q[KB][8], kk = 0.0f, qq = 0.0f, sk = 0.0f, sq = 0.0f;
-        const float v = ld_act(vp, t * a.v_stride);
-        const float dt = softplus(ld_act((const uint16_t *)a.dt_raw, (begin + t) * a.dt_stride + h) + bias);
-        const float beta = delta_gate(ld_act((const uint16_t *)a.beta_raw, (begin + t) * a.beta_stride + h));
-        const float decay = fast_exp2(dt * A);
+    blk -= (uint32_t)a.seqs;
+    const uint32_t H = (uint32_t)a.H, id = blk / H, h = blk % H, per = H / (uint32_t)a.G, g = h / per;
+    const int s = find_seq(a, id, kQ);
+    if (s < 0) return;
+    const uint32_t begin = seq_begin(a, s), len = seq_length(a, s, begin), piece = id - (begin / kQ + s);
+    if (piece >= (len + kQ - 1) / kQ) return;
+    const uint32_t row = begin + piece * kQ;
+    const int rem = len - piece * kQ < kQ ? (int)(len - piece * kQ) : kQ;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, m = lane & 15, grp = lane >> 4;
+    const bool keys = h % per == 0;
+
+    // operands: row `16 j + m` of the keys, elements 32 b + 8 grp ..
+    auto load = [&](const void *base, int64_t stride, int tile, bf16x8 (&f)[KB]) {
+        const int t = 16 * tile + m;
+        const uint16_t *p = (const uint16_t *)base + (int64_t)(row + (t < rem ? t : 0)) * stride + g * N + 8 * grp;
 #pragma unroll
         for (int b = 0; b < KB; ++b) {
-            ld8(kp + t * a.k_stride + 32 * b, k[b]);
-            ld8(qp + t * a.q_stride + 32 * b, q[b]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                kk = __builtin_fmaf(k[b][e], k[b][e], kk);
-                qq = __builtin_fmaf(q[b][e], q[b][e], qq);
-                S[b][e] *= decay;
-                sk = __builtin_fmaf(S[b][e], k[b][e], sk);
-            }
+            u32x4 u = *(const u32x4 *)(p + 32 * b);
+            if (t >= rem) u = u32x4{0, 0, 0, 0};
+            f[b] = __builtin_bit_cast(bf16x8, u);
         }
-        const float rk = unit_scale(sum_groups(kk), a.norm_eps), rq = unit_scale(sum_groups(qq), a.norm_eps) * a.scale;
-        const float u = beta * __builtin_fmaf(-rk, sum_groups(sk), v) * rk;
+    };
+    auto squares = [&](const bf16x8 (&f)[KB]) {
+        float v = 0.0f;
 #pragma unroll
         for (int b = 0; b < KB; ++b)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                S[b][e] = __builtin_fmaf(u, k[b][e], S[b][e]);
-                sq = __builtin_fmaf(S[b][e], q[b][e], sq);
+            for (int e = 0; e < 8; ++e) v = __builtin_fmaf((float)f[b][e], (float)f[b][e], v);
+        return sum_groups(v);
+    };
+    bf16x8 kw[KB], qw[KB];
+    load(a.k, a.k_stride, wave, kw);
+    load(a.q, a.q_stride, wave, qw);
+    if (wave == 0) {  // the gates, a lane per token
+        const int64_t t = row + (lane < rem ? lane : rem - 1);
+        const float dt = softplus(ld_act((const uint16_t *)a.dt_raw, t * a.dt_stride + h) + (a.dt_bias ? a.dt_bias[h] : 0.0f));
+        const float beta = delta_gate(ld_act((const uint16_t *)a.beta_raw, t * a.beta_stride + h));
+        // A decay of 2^-256 leaves nothing of a float32 state: no more than that.
+        double step = lane < rem ? (double)dt * ((double)a.A[h] * 1.4426950408889634) : 0.0;
+        step = step < -256.0 ? -256.0 : step;
+        sh.cum[lane] = wave_prefix_sum(step);
+        sh.beta[lane] = lane < rem ? beta : 0.0f;
+    }
+    {
+        const float kk = squares(kw), qq = squares(qw);
+        if (grp == 0) {
+            sh.rk[16 * wave + m] = unit_scale(kk, a.norm_eps);
+            sh.rq[16 * wave + m] = unit_scale(qq, a.norm_eps) * a.scale;
+        }
+        if (keys)
+#pragma unroll
+            for (int b = 0; b < KB; ++b) *(bf16x8 *)&sh.K[16 * wave + m][32 * b + 8 * grp] = kw[b];
+    }
+    f32x4 kk[4], qk[4];
+    for (int j = 0; j <= wave; ++j) {
+        bf16x8 kj[KB];
+        load(a.k, a.k_stride, j, kj);
+        f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f}, y = x;
+#pragma unroll
+        for (int b = 0; b < KB; ++b) {
+            x = mfma(kw[b], kj[b], x);
+            y = mfma(qw[b], kj[b], y);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i == j) kk[i] = x, qk[i] = y;
+    }
+    __syncthreads();
+    const int64_t at = (int64_t)id * H + h;
+    if (wave == 0) {
+        const double cum = sh.cum[lane], total = sh.cum[kQ - 1];
+        const float grow = fast_exp2((float)cum), rk = sh.rk[lane];
+        float *o = a.ws_scalars + at * kScalars;
+        o[lane] = grow * rk;
+        o[kQ + lane] = sh.beta[lane];
+        o[2 * kQ + lane] = fast_exp2((float)(total - cum)) * rk;
+        o[3 * kQ + lane] = grow * sh.rq[lane];
+        if (lane == kQ - 1) a.ws_decay[at] = grow;
+    }
+    // A and M from the products: rows 16 wave + 4 grp + r, column 16 j + m
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (j > (wave | 1)) break;  // above the diagonal of 32
+        const int col = 16 * j + m;
+        const double cc = sh.cum[col];
+        const float rk = sh.rk[col];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i = 16 * wave + 4 * grp + r;
+            float av = 0.0f, mv = 0.0f;
+            if (col <= i) {
+                const float d = fast_exp2((float)(sh.cum[i] - cc)) * rk;
+                mv = d * sh.rq[i] * qk[j][r];
+                if (col < i) av = d * sh.rk[i] * sh.beta[i] * kk[j][r];
             }
-        sq = sum_groups(sq);
-        if (grp == 0) st_act(y, t * a.H * a.P, sq * rq);
+            sh.A[i][col] = av;
+            sh.M[i][col] = mv;
+        }
+    }
+    if (keys) {  // the transposed keys as left operands: row tile_row(t, m), tokens 32 half + 8 grp ..
+        char *o = (char *)a.ws_kt + ((int64_t)id * a.G + g) * pieces_kt(N) * 1024;
+        for (int f = wave; f < pieces_kt(N); f += 4) {
+            const int n = tile_row(f >> 1, m), t0 = 32 * (f & 1) + 8 * grp;
+            u32x4 u;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) u[e] = (uint32_t)sh.K[t0 + 2 * e][n] | (uint32_t)sh.K[t0 + 2 * e + 1][n] << 16;
+            *(u32x4 *)(o + f * 1024 + lane * 16) = u;
+        }
+    }
+    __syncthreads();
+    // T's diagonal block of the wave: column m by substitution, x_i = (i == m) - sum_j<i A_ij x_j
+    const int d0 = 16 * wave;
+    {
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float v = i == m ? 1.0f : 0.0f;
+#pragma unroll
+            for (int j = 0; j < i; ++j) v = __builtin_fmaf(-sh.A[d0 + i][d0 + j], x[j], v);
+            x[i] = v;
+        }
+        if (grp == 0)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sh.T[d0 + i][d0 + m] = x[i];
+        if ((wave & 1) == 0 && grp == 1)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sh.T[d0 + i][d0 + 16 + m] = 0.0f;
+    }
+    __syncthreads();
+    // The blocks below in column `wave`, from the top: T_ij = -T_ii sum_l A_il T_lj (j <= l < i),
+    // on the float32 matrix cores, whose summed index is taken as 4 grp + r.
+    {
+        f32x4 t[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) t[0][r] = sh.T[d0 + 4 * grp + r][d0 + m];
+        for (int i = wave + 1; i < 4; ++i) {
+            f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f}, out = sum;
+#pragma unroll
+            for (int l = 0; l < 3; ++l) {
+                if (wave + l >= i) break;
+                const f32x4 al = *(const f32x4 *)&sh.A[16 * i + m][16 * (wave + l) + 4 * grp];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) sum = mfma_f32(al[r], t[l][r], sum);
+            }
+            const f32x4 ti = *(const f32x4 *)&sh.T[16 * i + m][16 * i + 4 * grp];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) out = mfma_f32(ti[r], -sum[r], out);
+#pragma unroll
+            for (int l = 1; l < 4; ++l)
+                if (wave + l == i) t[l] = out;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sh.T[16 * i + 4 * grp + r][d0 + m] = out[r];
+        }
+    }
+    __syncthreads();
+    // T and M as left operands: row tile_row(tile, m), columns 32 half + 8 grp ..
+    char *o = (char *)a.ws_tm + at * kFragTM * 1024;
+    for (int f = wave; f < 2 * kTri; f += 4) {
+        const int tri = f % kTri, tile = tri < 2 ? tri : tri < 4 ? 2 : 3, half = tri < 2 ? 0 : tri & 1;
+        const float *src = (f < kTri ? sh.T : sh.M)[tile_row(tile, m)] + 32 * half + 8 * grp;
+        float v[8];
+        *(f32x4 *)v = *(const f32x4 *)src;
+        *(f32x4 *)(v + 4) = *(const f32x4 *)(src + 4);
+        bf16x8 part[kPartsT];
+        split<kPartsT>(v, part);
+        const int base = f < kTri ? kPartsT * tri : kTri * kPartsT + kPartsM * tri;
+        *(bf16x8 *)(o + base * 1024 + lane * 16) = part[0];
+        *(bf16x8 *)(o + (base + 1) * 1024 + lane * 16) = part[1];
+        if (f < kTri) *(bf16x8 *)(o + (base + 2) * 1024 + lane * 16) = part[2];
+    }
+}
+
+// ----------------------------------------------------------------------- walk
+
+template <int N, int WAVES>
+struct WalkShared {
+    static constexpr int KB = N / 32;
+    // pieces of 1 KiB, a register of 16 bytes of each lane
+    alignas(16) char K[4 * KB][1024], Q[4 * KB][1024], Kt[pieces_kt(N)][1024], TM[kFragTM][1024];
+    alignas(16) float scalars[2][kScalars];
+};
+
+// One head of one sequence, WAVES x CT x 16 columns p of it.
+template <int N, int WAVES, int CT>
+__global__ __launch_bounds__(64 * WAVES) void delta_walk_kernel(DeltaArgs a) {
+    using Shared = WalkShared<N, WAVES>;
+    constexpr int KB = N / 32, NT = N / 16;
+    __shared__ Shared sh;
+    // the column blocks of a head are 8 workgroups apart: on one XCD, whose cache then
+    // holds what they share
+    const uint32_t nb = (uint32_t)a.P / (16 * WAVES * CT), lin = blockIdx.x;
+    const uint32_t pb = lin / 8 % nb, hs = lin / 8 / nb * 8 + lin % 8;
+    if (hs >= (uint32_t)(a.H * a.seqs)) return;
+    const uint32_t H = (uint32_t)a.H, s = hs / H, h = hs % H, g = h / (H / (uint32_t)a.G);
+    const int wave = uniform((int)(threadIdx.x >> 6)), lane = threadIdx.x & 63, m = lane & 15, grp = lane >> 4;
+    const uint32_t begin = seq_begin(a, s), len = seq_length(a, s, begin);
+    const int64_t p0 = (int64_t)(pb * WAVES + wave) * 16 * CT + CT * m;  // columns p0 .. p0 + CT - 1
+    const int64_t y_stride = a.H * a.P;
+    uint16_t *y = (uint16_t *)a.y + (int64_t)begin * y_stride + h * a.P + p0;
+    // CT columns of one token
+    auto store = [&](int64_t t, const float (&v)[CT]) {
+        if constexpr (CT == 2) {
+            float lo = v[0], hi = v[1];
+            *(uint32_t *)(y + t * y_stride) = bf16_pair(lo, hi);
+        } else {
+            st_act(y, t * y_stride, v[0]);
+        }
+    };
+    const int32_t slot = a.ws_slot[s];
+    if (slot < 0) {
+        const float zero[CT] = {};
+        for (uint32_t t = grp; t < len; t += 4) store(t, zero);
+        return;
+    }
+    const bool resume = a.resume && a.resume[s] != 0;
+    float *cache = a.state_cache + (((int64_t)slot * H + h) * a.P + p0) * N + 8 * grp;
+    f32x4 S[NT][CT];  // n = tile_row(t, 4 grp + r), column p0 + c
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+            S[t][c] = resume ? *(const f32x4 *)(cache + c * N + 32 * (t >> 1) + 4 * (t & 1)) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    const uint32_t chunks = (len + kQ - 1) / kQ, id0 = begin / kQ + s;
+    const uint16_t *qb = (const uint16_t *)a.q + (int64_t)begin * a.q_stride + g * N;
+    const uint16_t *kb = (const uint16_t *)a.k + (int64_t)begin * a.k_stride + g * N;
+    const uint16_t *vb = (const uint16_t *)a.v + (int64_t)begin * a.v_stride + h * a.P + p0;
+    const uint32_t last = len ? len - 1 : 0;
+    // keys and queries of chunk c into LDS as operands; tokens behind the last repeat it (their
+    // updates are zero), and the chunk's factors per token
+    auto fetch_kq = [&](uint32_t c) {
+#pragma unroll
+        for (int f = 0; f < 2 * 4 * KB; ++f) {
+            if (f % WAVES != wave) continue;
+            const int i = f % (4 * KB), tile = i / KB, b = i % KB;
+            uint32_t t = c * kQ + tile_row(tile, m);
+            t = t < last ? t : last;
+            if (f < 4 * KB) dma16(kb + (int64_t)t * a.k_stride + 32 * b + 8 * grp, lds_addr(sh.K[i]));
+            else dma16(qb + (int64_t)t * a.q_stride + 32 * b + 8 * grp, lds_addr(sh.Q[i]));
+        }
+        if (wave == WAVES - 1) dma16(a.ws_scalars + ((int64_t)(id0 + c) * H + h) * kScalars + 4 * lane, lds_addr(sh.scalars[c & 1]));
+    };
+    // T, M and the transposed keys
+    auto fetch_tm = [&](uint32_t c) {
+        const char *tm = (const char *)a.ws_tm + ((int64_t)(id0 + c) * H + h) * kFragTM * 1024 + lane * 16;
+        const char *kt = (const char *)a.ws_kt + ((int64_t)(id0 + c) * a.G + g) * pieces_kt(N) * 1024 + lane * 16;
+#pragma unroll
+        for (int f = 0; f < kFragTM; ++f)
+            if (f % WAVES == wave) dma16(tm + f * 1024, lds_addr(sh.TM[f]));
+#pragma unroll
+        for (int f = 0; f < pieces_kt(N); ++f)
+            if (f % WAVES == wave) dma16(kt + f * 1024, lds_addr(sh.Kt[f]));
+    };
+    // the values of chunk c: CT columns of tokens tile_row(tile, 4 grp + r)
+    uint32_t v[4][4];
+    auto fetch_v = [&](uint32_t c) {
+#pragma unroll
+        for (int tile = 0; tile < 4; ++tile)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                uint32_t t = c * kQ + tile_row(tile, 4 * grp + r);
+                t = t < last ? t : last;
+                const uint16_t *p = vb + (int64_t)t * a.v_stride;
+                if constexpr (CT == 2) v[tile][r] = *(const uint32_t *)p;
+                else v[tile][r] = *p;
+            }
+    };
+    auto frag = [&](const char *p) { return *(const bf16x8 *)(p + lane * 16); };
+
+    if (chunks > 0) {
+        fetch_kq(0);
+        fetch_v(0);
+    }
+    for (uint32_t c = 0; c < chunks; ++c) {
+        vm_wait();
+        lds_barrier();  // keys and queries are there; T, M and the keys of the chunk before are done with
+        fetch_tm(c);
+        const float decay = a.ws_decay[(int64_t)(id0 + c) * H + h];
+        const float *sc = sh.scalars[c & 1];
+        f32x4 ks[4][CT], ys[4][CT];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int j = 0; j < CT; ++j) ks[t][j] = ys[t][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int b = 0; b < KB; ++b) {
+            bf16x8 sp[CT][3];
+#pragma unroll
+            for (int j = 0; j < CT; ++j) {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = S[2 * b][j][e], x[4 + e] = S[2 * b + 1][j][e];
+                split<3>(x, sp[j]);
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const bf16x8 kf = frag(sh.K[t * KB + b]), qf = frag(sh.Q[t * KB + b]);
+#pragma unroll
+                for (int part = 2; part >= 0; --part)
+#pragma unroll
+                    for (int j = 0; j < CT; ++j) {
+                        ks[t][j] = mfma(kf, sp[j][part], ks[t][j]);
+                        if (part < 2) ys[t][j] = mfma(qf, sp[j][part], ys[t][j]);
+                    }
+            }
+        }
+        bf16x8 rp[2][CT][3];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            float x[CT][8];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int t = 2 * half + k, at = 32 * half + 8 * grp + 4 * k;
+                const f32x4 gk = *(const f32x4 *)(sc + at), be = *(const f32x4 *)(sc + kQ + at), gq = *(const f32x4 *)(sc + 3 * kQ + at);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int j = 0; j < CT; ++j) {
+                        const float val = __uint_as_float(j ? v[t][r] & 0xffff0000u : v[t][r] << 16);
+                        x[j][4 * k + r] = be[r] * __builtin_fmaf(-gk[r], ks[t][j][r], val);
+                        ys[t][j][r] *= gq[r];
+                    }
+            }
+#pragma unroll
+            for (int j = 0; j < CT; ++j) split<3>(x[j], rp[half][j]);
+        }
+        vm_wait();
+        lds_barrier();  // T, M and the transposed keys are there; keys and queries are done with
+        if (c + 1 < chunks) {
+            fetch_kq(c + 1);
+            fetch_v(c + 1);
+        }
+        f32x4 u[4][CT];
+        float odd = 0.0f;  // NaN where an update is not finite
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+#pragma unroll
+            for (int j = 0; j < CT; ++j) u[t][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int half = 0; half <= t >> 1; ++half) {
+                bf16x8 tf[3];
+#pragma unroll
+                for (int part = 0; part < 3; ++part) tf[part] = frag(sh.TM[kPartsT * tri_index(t, half) + part]);
+#pragma unroll
+                for (int k = 0; k < 6; ++k)
+#pragma unroll
+                    for (int j = 0; j < CT; ++j) u[t][j] = mfma(tf[kTerm[k][0]], rp[half][j][kTerm[k][1]], u[t][j]);
+            }
+#pragma unroll
+            for (int j = 0; j < CT; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) odd = __builtin_fmaf(u[t][j][r], 0.0f, odd);
+        }
+        const int64_t t0 = (int64_t)c * kQ;
+        const int rem = len - t0 < kQ ? (int)(len - t0) : kQ;
+        if (__any(odd != odd)) {
+            for (int t = 0; t < rem; ++t) {
+                const int64_t row = begin + t0 + t;
+                const float dt = softplus(ld_act((const uint16_t *)a.dt_raw, row * a.dt_stride + h) + (a.dt_bias ? a.dt_bias[h] : 0.0f));
+                const float beta = delta_gate(ld_act((const uint16_t *)a.beta_raw, row * a.beta_stride + h));
+                const float one = fast_exp2(dt * a.A[h] * kLog2e);
+                float kv[KB][8], qv[KB][8], kk = 0.0f, qq = 0.0f, out[CT];
+#pragma unroll
+                for (int b = 0; b < KB; ++b) {
+                    ld8(kb + (t0 + t) * a.k_stride + 32 * b + 8 * grp, kv[b]);
+                    ld8(qb + (t0 + t) * a.q_stride + 32 * b + 8 * grp, qv[b]);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        kk = __builtin_fmaf(kv[b][e], kv[b][e], kk);
+                        qq = __builtin_fmaf(qv[b][e], qv[b][e], qq);
+                    }
+                }
+                const float rk = unit_scale(sum_groups(kk), a.norm_eps), rq = unit_scale(sum_groups(qq), a.norm_eps) * a.scale;
+#pragma unroll
+                for (int j = 0; j < CT; ++j) {
+                    float sk = 0.0f, sq = 0.0f;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            S[n][j][r] *= one;
+                            sk = __builtin_fmaf(S[n][j][r], kv[n >> 1][4 * (n & 1) + r], sk);
+                        }
+                    const float up = beta * __builtin_fmaf(-rk, sum_groups(sk), ld_act(vb + j, (t0 + t) * a.v_stride)) * rk;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            S[n][j][r] = __builtin_fmaf(up, kv[n >> 1][4 * (n & 1) + r], S[n][j][r]);
+                            sq = __builtin_fmaf(S[n][j][r], qv[n >> 1][4 * (n & 1) + r], sq);
+                        }
+                    out[j] = sum_groups(sq) * rq;
+                }
+                if (grp == 0) store(t0 + t, out);
+            }
+            continue;
+        }
+        // y = diag(..) Q S^T + M U
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            bf16x8 up[CT][2];
+#pragma unroll
+            for (int j = 0; j < CT; ++j) {
+                float x[8];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) x[r] = u[2 * half][j][r], x[4 + r] = u[2 * half + 1][j][r];
+                split<2>(x, up[j]);
+            }
+#pragma unroll
+            for (int t = 2 * half; t < 4; ++t) {
+                bf16x8 mf[2];
+#pragma unroll
+                for (int part = 0; part < 2; ++part) mf[part] = frag(sh.TM[kTri * kPartsT + kPartsM * tri_index(t, half) + part]);
+#pragma unroll
+                for (int k = kTwo; k < 6; ++k)
+#pragma unroll
+                    for (int j = 0; j < CT; ++j) ys[t][j] = mfma(mf[kTerm[k][0]], up[j][kTerm[k][1]], ys[t][j]);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int tok = tile_row(t, 4 * grp + r);
+                float out[CT];
+#pragma unroll
+                for (int j = 0; j < CT; ++j) out[j] = ys[t][j][r];
+                if (tok < rem) store(t0 + tok, out);
+            }
+        // S^T <- decay S^T + K^T (diag(..) U)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < CT; ++j) S[n][j] *= decay;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            bf16x8 up[CT][3];
+#pragma unroll
+            for (int j = 0; j < CT; ++j) {
+                float x[8];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const f32x4 tk = *(const f32x4 *)(sc + 2 * kQ + 32 * half + 8 * grp + 4 * k);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) x[4 * k + r] = u[2 * half + k][j][r] * tk[r];
+                }
+                split<3>(x, up[j]);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const bf16x8 kf = frag(sh.Kt[2 * n + half]);
+#pragma unroll
+                for (int part = 2; part >= 0; --part)
+#pragma unroll
+                    for (int j = 0; j < CT; ++j) S[n][j] = mfma(kf, up[j][part], S[n][j]);
+            }
+        }
     }
     if (len > 0 || !resume)
 #pragma unroll
-        for (int b = 0; b < KB; ++b)
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) cache[32 * b + e] = S[b][e];
+            for (int j = 0; j < CT; ++j) *(f32x4 *)(cache + j * N + 32 * (t >> 1) + 4 * (t & 1)) = S[t][j];
+}
+
+int64_t chunk_ids(int64_t seqs, int64_t rows) { return rows / kQ + seqs; }
+
+template <int N, int WAVES, int CT>
+hipError_t walk(const DeltaArgs &a, hipStream_t s) {
+    const int64_t nb = a.P / (16 * WAVES * CT), heads = (a.H * a.seqs + 7) / 8 * 8;
+    hipLaunchKernelGGL((delta_walk_kernel<N, WAVES, CT>), dim3((unsigned)(heads * nb)), dim3(64 * WAVES), 0, s, a);
+    return hipGetLastError();
+}
+
+template <int N>
+hipError_t delta(const DeltaArgs &a, hipStream_t s) {
+    const int64_t blocks = a.seqs + chunk_ids(a.seqs, a.rows) * a.H;
+    hipLaunchKernelGGL((delta_prepare_kernel<N>), dim3((unsigned)blocks), dim3(kPrepThreads), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (a.H * a.seqs * a.P >= 256 * 64) return a.P % 128 == 0 ? walk<N, 4, 2>(a, s) : walk<N, 2, 2>(a, s);
+    return walk<N, 1, 1>(a, s);
 }
 
 }  // namespace
 
 size_t delta_workspace(int64_t seqs, int64_t rows, int64_t H, int64_t P, int64_t G, int64_t N) {
-    return ((size_t)seqs * 4 + 255) / 256 * 256;
+    DeltaArgs a{};
+    a.seqs = seqs;
+    a.rows = rows;
+    a.H = H;
+    a.G = G;
+    return delta_layout(a, N, nullptr);
+}
+
+// Places the workspace's arrays and returns its size.
+size_t delta_layout(DeltaArgs &a, int64_t N, void *workspace) {
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        void *p = (char *)workspace + at;
+        at += (bytes + 255) / 256 * 256;
+        return p;
+    };
+    const size_t ids = (size_t)chunk_ids(a.seqs, a.rows), heads = ids * (size_t)a.H;
+    a.ws_slot = (int32_t *)take((size_t)a.seqs * 4);
+    a.ws_decay = (float *)take(heads * 4);
+    a.ws_scalars = (float *)take(heads * kScalars * 4);
+    a.ws_tm = take(heads * kFragTM * 1024);
+    a.ws_kt = take(ids * (size_t)a.G * pieces_kt((int)N) * 1024);
+    return at;
 }
 
 hipError_t launch_delta(DeltaArgs a, int N, void *workspace, hipStream_t s) {
-    a.ws_slot = (int32_t *)workspace;
-    hipLaunchKernelGGL(delta_slots_kernel, dim3((unsigned)a.seqs), dim3(256), 0, s, a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    const dim3 grid((unsigned)(a.P / kCols), (unsigned)a.H, (unsigned)a.seqs);
-    if (N == 64) hipLaunchKernelGGL((delta_walk_kernel<64>), grid, dim3(64), 0, s, a);
-    else hipLaunchKernelGGL((delta_walk_kernel<128>), grid, dim3(64), 0, s, a);
-    return hipGetLastError();
+    delta_layout(a, N, workspace);
+    return N == 64 ? delta<64>(a, s) : delta<128>(a, s);
 }
 
 }  // namespace ssm
