@@ -45,6 +45,7 @@
 // instead, from the state that entered it.
 #include "ssm_delta_device.h"
 #include "ssm_packed.h"
+#include <stdlib.h>
 
 namespace ssm {
 
@@ -56,7 +57,8 @@ constexpr int kPrepThreads = 256;
 // are not wholly above the diagonal, a register of 16 bytes of each lane per part.
 constexpr int kTri = 6, kPartsT = 3, kPartsM = 2;
 constexpr int kFragTM = kTri * (kPartsT + kPartsM);  // pieces of 1 KiB per (chunk, head)
-constexpr int kScalars = 4 * kQ;                      // floats per (chunk, head): e^G / |k|, beta, e^(G_last - G) / |k|, scale e^G / |q|
+// and one more of factors per token: e^G / |k|, beta, e^(G_last - G) / |k|, scale e^G / |q|
+constexpr int kHeadPieces = kFragTM + 1;
 constexpr int pieces_kt(int N) { return 2 * N / 16; }  // of the transposed keys per (chunk, group)
 
 __device__ __forceinline__ int tri_index(int tile, int half) { return tile < 2 ? tile : 2 * tile - 2 + half; }
@@ -72,6 +74,25 @@ constexpr int kTwo = 3;
 
 __device__ __forceinline__ f32x4 mfma_f32(float a, float b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
 
+// The first of the two tiles that the three groups of products with T and M take; the
+// last group's columns are the second half.
+constexpr int kTile[3] = {0, 2, 2};
+
+// In what order the compiler places what stands ahead: READS reads of LDS; or COUNT
+// products with VALU other instructions behind each.
+template <int READS>
+__device__ __forceinline__ void interleave_reads() {
+    __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
+}
+template <int COUNT, int VALU>
+__device__ __forceinline__ void interleave() {
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x2, VALU, 0);
+    }
+}
+
 // Eight bfloat16 as floats.
 __device__ __forceinline__ void ld8(const uint16_t *p, float *v) {
     const u32x4 u = *(const u32x4 *)p;
@@ -80,6 +101,11 @@ __device__ __forceinline__ void ld8(const uint16_t *p, float *v) {
         v[2 * i] = __uint_as_float(u[i] << 16);
         v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
     }
+}
+
+// An index that every lane shares.
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+    return (int64_t)(uint32_t)uniform((int)v) | (int64_t)uniform((int)(v >> 32)) << 32;
 }
 
 // v summed over the four lanes that hold the same place of a tile's 16.
@@ -197,7 +223,7 @@ __global__ __launch_bounds__(kPrepThreads) void delta_prepare_kernel(DeltaArgs a
     if (wave == 0) {
         const double cum = sh.cum[lane], total = sh.cum[kQ - 1];
         const float grow = fast_exp2((float)cum), rk = sh.rk[lane];
-        float *o = a.ws_scalars + at * kScalars;
+        float *o = (float *)((char *)a.ws_tm + (at * kHeadPieces + kFragTM) * 1024);
         o[lane] = grow * rk;
         o[kQ + lane] = sh.beta[lane];
         o[2 * kQ + lane] = fast_exp2((float)(total - cum)) * rk;
@@ -281,7 +307,7 @@ __global__ __launch_bounds__(kPrepThreads) void delta_prepare_kernel(DeltaArgs a
     }
     __syncthreads();
     // T and M as left operands: row tile_row(tile, m), columns 32 half + 8 grp ..
-    char *o = (char *)a.ws_tm + at * kFragTM * 1024;
+    char *o = (char *)a.ws_tm + at * kHeadPieces * 1024;
     for (int f = wave; f < 2 * kTri; f += 4) {
         const int tri = f % kTri, tile = tri < 2 ? tri : tri < 4 ? 2 : 3, half = tri < 2 ? 0 : tri & 1;
         const float *src = (f < kTri ? sh.T : sh.M)[tile_row(tile, m)] + 32 * half + 8 * grp;
@@ -299,44 +325,35 @@ __global__ __launch_bounds__(kPrepThreads) void delta_prepare_kernel(DeltaArgs a
 
 // ----------------------------------------------------------------------- walk
 
-template <int N, int WAVES>
-struct WalkShared {
-    static constexpr int KB = N / 32;
-    // pieces of 1 KiB, a register of 16 bytes of each lane
-    alignas(16) char K[4 * KB][1024], Q[4 * KB][1024], Kt[pieces_kt(N)][1024], TM[kFragTM][1024];
-    alignas(16) float scalars[2][kScalars];
+// What the walk reads of one chunk: pieces of 1 KiB, a register of 16 bytes of each lane.
+template <int N>
+struct Chunk {
+    static constexpr int KB = N / 32, kPieces = 8 * KB + pieces_kt(N) + kHeadPieces;
+    static constexpr int kK = 0, kQ_ = 4 * KB, kKt = 8 * KB, kTM = kKt + pieces_kt(N), kFactors = kTM + kFragTM;
 };
 
 // One head of one sequence, WAVES x CT x 16 columns p of it.
 template <int N, int WAVES, int CT>
 __global__ __launch_bounds__(64 * WAVES) void delta_walk_kernel(DeltaArgs a) {
-    using Shared = WalkShared<N, WAVES>;
+    using C = Chunk<N>;
     constexpr int KB = N / 32, NT = N / 16;
-    __shared__ Shared sh;
-    // the column blocks of a head are 8 workgroups apart: on one XCD, whose cache then
-    // holds what they share
-    const uint32_t nb = (uint32_t)a.P / (16 * WAVES * CT), lin = blockIdx.x;
-    const uint32_t pb = lin / 8 % nb, hs = lin / 8 / nb * 8 + lin % 8;
-    if (hs >= (uint32_t)(a.H * a.seqs)) return;
-    const uint32_t H = (uint32_t)a.H, s = hs / H, h = hs % H, g = h / (H / (uint32_t)a.G);
+    __shared__ __align__(16) char sh[2][C::kPieces][1024];  // this chunk's and the next one's
+    // Workgroups go round the eight XCDs: those of a group of heads, which share its keys and
+    // queries, are 8 apart, so that they meet in one XCD's cache.
+    const uint32_t H = (uint32_t)a.H, G = (uint32_t)a.G, per = H / G, nb = (uint32_t)a.P / (16 * WAVES * CT);
+    const uint32_t lin = blockIdx.x, one = lin / 8 % (per * nb), unit = lin / 8 / (per * nb) * 8 + lin % 8;
+    if (unit >= G * (uint32_t)a.seqs) return;
+    const uint32_t s = unit / G, g = unit % G, h = g * per + one / nb, pb = one % nb;
     const int wave = uniform((int)(threadIdx.x >> 6)), lane = threadIdx.x & 63, m = lane & 15, grp = lane >> 4;
-    const uint32_t begin = seq_begin(a, s), len = seq_length(a, s, begin);
-    const int64_t p0 = (int64_t)(pb * WAVES + wave) * 16 * CT + CT * m;  // columns p0 .. p0 + CT - 1
+    const uint32_t begin = uniform(seq_begin(a, s)), len = uniform(seq_length(a, s, begin));
+    const int64_t pw = (int64_t)(pb * WAVES + wave) * 16 * CT, p0 = pw + CT * m;  // columns p0 .. p0 + CT - 1
     const int64_t y_stride = a.H * a.P;
-    uint16_t *y = (uint16_t *)a.y + (int64_t)begin * y_stride + h * a.P + p0;
-    // CT columns of one token
-    auto store = [&](int64_t t, const float (&v)[CT]) {
-        if constexpr (CT == 2) {
-            float lo = v[0], hi = v[1];
-            *(uint32_t *)(y + t * y_stride) = bf16_pair(lo, hi);
-        } else {
-            st_act(y, t * y_stride, v[0]);
-        }
-    };
-    const int32_t slot = a.ws_slot[s];
+    uint16_t *yb = (uint16_t *)a.y + (int64_t)begin * y_stride + h * a.P + pw;
+    const int32_t slot = uniform(a.ws_slot[s]);
     if (slot < 0) {
-        const float zero[CT] = {};
-        for (uint32_t t = grp; t < len; t += 4) store(t, zero);
+        for (uint32_t t = grp; t < len; t += 4)
+#pragma unroll
+            for (int j = 0; j < CT; ++j) yb[t * y_stride + CT * m + j] = 0;
         return;
     }
     const bool resume = a.resume && a.resume[s] != 0;
@@ -351,67 +368,97 @@ __global__ __launch_bounds__(64 * WAVES) void delta_walk_kernel(DeltaArgs a) {
     const uint32_t chunks = (len + kQ - 1) / kQ, id0 = begin / kQ + s;
     const uint16_t *qb = (const uint16_t *)a.q + (int64_t)begin * a.q_stride + g * N;
     const uint16_t *kb = (const uint16_t *)a.k + (int64_t)begin * a.k_stride + g * N;
-    const uint16_t *vb = (const uint16_t *)a.v + (int64_t)begin * a.v_stride + h * a.P + p0;
-    const uint32_t last = len ? len - 1 : 0;
-    // keys and queries of chunk c into LDS as operands; tokens behind the last repeat it (their
-    // updates are zero), and the chunk's factors per token
-    auto fetch_kq = [&](uint32_t c) {
+    const uint16_t *vb = (const uint16_t *)a.v + (int64_t)begin * a.v_stride + h * a.P + pw;
+    const uint32_t lds0 = lds_addr(sh);
+    // Chunk c into LDS. Keys and queries as operands: a wave takes tiles of 16 tokens; tokens
+    // behind the last repeat it (their updates are zero).
+    auto fetch = [&](uint32_t chunk) {
+        const uint32_t c = uniform((int)chunk), to = lds0 + (c & 1) * C::kPieces * 1024, left = len - c * kQ - 1;
 #pragma unroll
-        for (int f = 0; f < 2 * 4 * KB; ++f) {
-            if (f % WAVES != wave) continue;
-            const int i = f % (4 * KB), tile = i / KB, b = i % KB;
-            uint32_t t = c * kQ + tile_row(tile, m);
-            t = t < last ? t : last;
-            if (f < 4 * KB) dma16(kb + (int64_t)t * a.k_stride + 32 * b + 8 * grp, lds_addr(sh.K[i]));
-            else dma16(qb + (int64_t)t * a.q_stride + 32 * b + 8 * grp, lds_addr(sh.Q[i]));
+        for (int i = 0; i < 8 / WAVES; ++i) {
+            const int tile = (wave + i * WAVES) & 3;
+            const bool keys = wave + i * WAVES < 4;
+            const int64_t stride = keys ? a.k_stride : a.q_stride;
+            const uint16_t *base = (keys ? kb : qb) + (int64_t)c * kQ * stride;
+            uint32_t t = tile_row(tile, m);
+            t = t < left ? t : left;
+            const uint32_t off = t * (uint32_t)stride * 2 + 16 * grp;
+#pragma unroll
+            for (int b = 0; b < KB; ++b) dma16_s(base + 32 * b, off, to + ((keys ? C::kK : C::kQ_) + tile * KB + b) * 1024);
         }
-        if (wave == WAVES - 1) dma16(a.ws_scalars + ((int64_t)(id0 + c) * H + h) * kScalars + 4 * lane, lds_addr(sh.scalars[c & 1]));
-    };
-    // T, M and the transposed keys
-    auto fetch_tm = [&](uint32_t c) {
-        const char *tm = (const char *)a.ws_tm + ((int64_t)(id0 + c) * H + h) * kFragTM * 1024 + lane * 16;
-        const char *kt = (const char *)a.ws_kt + ((int64_t)(id0 + c) * a.G + g) * pieces_kt(N) * 1024 + lane * 16;
+        const char *tm = (const char *)a.ws_tm + ((int64_t)(id0 + c) * H + h) * kHeadPieces * 1024;
+        const char *kt = (const char *)a.ws_kt + ((int64_t)(id0 + c) * a.G + g) * pieces_kt(N) * 1024;
 #pragma unroll
-        for (int f = 0; f < kFragTM; ++f)
-            if (f % WAVES == wave) dma16(tm + f * 1024, lds_addr(sh.TM[f]));
+        for (int i = 0; i < (kHeadPieces + WAVES - 1) / WAVES; ++i) {
+            const int f = wave + i * WAVES;
+            if (f < kHeadPieces) dma16_s(tm + f * 1024, lane * 16, to + (C::kTM + f) * 1024);
+        }
 #pragma unroll
-        for (int f = 0; f < pieces_kt(N); ++f)
-            if (f % WAVES == wave) dma16(kt + f * 1024, lds_addr(sh.Kt[f]));
+        for (int i = 0; i < pieces_kt(N) / WAVES; ++i) {
+            const int f = wave + i * WAVES;
+            dma16_s(kt + f * 1024, lane * 16, to + (C::kKt + f) * 1024);
+        }
     };
-    // the values of chunk c: CT columns of tokens tile_row(tile, 4 grp + r)
+    // The values of chunk c: CT columns of tokens tile_row(tile, 4 grp + r); behind the last
+    // token zeros.
     uint32_t v[4][4];
+    const uint32_t v_row = (uint32_t)a.v_stride * 2, y_row = (uint32_t)y_stride * 2;
     auto fetch_v = [&](uint32_t c) {
+        const uint16_t *base = vb + (int64_t)c * kQ * a.v_stride;
+        const uint32_t left = len - c * kQ, lane_at = 8 * grp * v_row + 2 * CT * m;
+        const auto rows = buffer(base, (left < kQ ? left - 1 : kQ - 1) * v_row + 32 * CT);
 #pragma unroll
         for (int tile = 0; tile < 4; ++tile)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                uint32_t t = c * kQ + tile_row(tile, 4 * grp + r);
-                t = t < last ? t : last;
-                const uint16_t *p = vb + (int64_t)t * a.v_stride;
-                if constexpr (CT == 2) v[tile][r] = *(const uint32_t *)p;
-                else v[tile][r] = *p;
+                const uint32_t at = lane_at + tile_row(tile, r) * v_row;
+                if constexpr (CT == 2) v[tile][r] = __builtin_amdgcn_raw_buffer_load_b32(rows, at, 0, 0);
+                else v[tile][r] = __builtin_amdgcn_raw_buffer_load_b16(rows, at, 0, 0);
             }
     };
     auto frag = [&](const char *p) { return *(const bf16x8 *)(p + lane * 16); };
 
     if (chunks > 0) {
-        fetch_kq(0);
+        fetch(0);
         fetch_v(0);
     }
-    for (uint32_t c = 0; c < chunks; ++c) {
+    // y of chunk c, a chunk later: a wait for loads waits for the stores before them too. What
+    // lies behind the last token is dropped.
+    uint32_t out[4][4];
+    auto store_y = [&](uint32_t chunk) {
+        const uint32_t c = uniform((int)chunk), left = len - c * kQ, lane_at = 8 * grp * y_row + 2 * CT * m;
+        const auto rows = buffer(yb + (int64_t)c * kQ * y_stride, (left < kQ ? left - 1 : kQ - 1) * y_row + 32 * CT);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const uint32_t at = lane_at + tile_row(t, r) * y_row;
+                if constexpr (CT == 2) __builtin_amdgcn_raw_buffer_store_b32(out[t][r], rows, at, 0, 0);
+                else __builtin_amdgcn_raw_buffer_store_b16((uint16_t)out[t][r], rows, at, 0, 0);
+            }
+    };
+    uint32_t c = 0;
+    for (; c < chunks; ++c) {
         vm_wait();
-        lds_barrier();  // keys and queries are there; T, M and the keys of the chunk before are done with
-        fetch_tm(c);
-        const float decay = a.ws_decay[(int64_t)(id0 + c) * H + h];
-        const float *sc = sh.scalars[c & 1];
+        lds_barrier();  // this chunk is there, the one before is done with
+        if (c > 0) store_y(c - 1);
+        // The values are there as well, but the compiler would wait for them where they
+        // are used, and with them for the loads that it does not know of: here it waits for none.
+#pragma unroll
+        for (int t = 0; t < 4; ++t) asm volatile("" : "+v"(v[t][0]), "+v"(v[t][1]), "+v"(v[t][2]), "+v"(v[t][3]));
+        if (c + 1 < chunks) fetch(c + 1);
+        const float decay = *(cf32_ptr)(a.ws_decay + uniform64((int64_t)(id0 + c) * H + h));
+        const char(*in)[1024] = sh[c & 1];
+        const float *sc = (const float *)in[C::kFactors];
+
+        // K S^T and Q S^T. Operands are read from LDS a group of products ahead, and the
+        // next 32 of n are split between the products.
         f32x4 ks[4][CT], ys[4][CT];
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int j = 0; j < CT; ++j) ks[t][j] = ys[t][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int b = 0; b < KB; ++b) {
-            bf16x8 sp[CT][3];
+        auto split_state = [&](int b, bf16x8 (&sp)[CT][3]) {
 #pragma unroll
             for (int j = 0; j < CT; ++j) {
                 float x[8];
@@ -419,19 +466,43 @@ __global__ __launch_bounds__(64 * WAVES) void delta_walk_kernel(DeltaArgs a) {
                 for (int e = 0; e < 4; ++e) x[e] = S[2 * b][j][e], x[4 + e] = S[2 * b + 1][j][e];
                 split<3>(x, sp[j]);
             }
+        };
+        bf16x8 sp[2][CT][3], kf[2], qf[2];
+        kf[0] = frag(in[C::kK]), qf[0] = frag(in[C::kQ_]);
+        split_state(0, sp[0]);
+#pragma unroll
+        for (int b = 0; b < KB; ++b) {
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                const bf16x8 kf = frag(sh.K[t * KB + b]), qf = frag(sh.Q[t * KB + b]);
+                const int next = 4 * b + t + 1, tn = next & 3, bn = next >> 2;
+                if (next < 4 * KB) kf[next & 1] = frag(in[C::kK + tn * KB + bn]), qf[next & 1] = frag(in[C::kQ_ + tn * KB + bn]);
 #pragma unroll
                 for (int part = 2; part >= 0; --part)
 #pragma unroll
                     for (int j = 0; j < CT; ++j) {
-                        ks[t][j] = mfma(kf, sp[j][part], ks[t][j]);
-                        if (part < 2) ys[t][j] = mfma(qf, sp[j][part], ys[t][j]);
+                        ks[t][j] = mfma(kf[t & 1], sp[b & 1][j][part], ks[t][j]);
+                        if (part < 2) ys[t][j] = mfma(qf[t & 1], sp[b & 1][j][part], ys[t][j]);
                     }
             }
+            if (b + 1 < KB) split_state(b + 1, sp[(b + 1) & 1]);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                interleave_reads<2>();
+                interleave<5 * CT, 3>();
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
-        bf16x8 rp[2][CT][3];
+
+        // beta (V - diag(..) K S^T), in three parts
+        bf16x8 rp[2][CT][3], tf[2][2][3];
+        auto read_t = [&](int i) {  // two tiles
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int part = 0; part < 3; ++part)
+                    tf[i & 1][k][part] = frag(in[C::kTM + kPartsT * tri_index(kTile[i] + k, i >> 1) + part]);
+        };
+        read_t(0);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             float x[CT][8];
@@ -451,137 +522,166 @@ __global__ __launch_bounds__(64 * WAVES) void delta_walk_kernel(DeltaArgs a) {
 #pragma unroll
             for (int j = 0; j < CT; ++j) split<3>(x[j], rp[half][j]);
         }
-        vm_wait();
-        lds_barrier();  // T, M and the transposed keys are there; keys and queries are done with
-        if (c + 1 < chunks) {
-            fetch_kq(c + 1);
-            fetch_v(c + 1);
-        }
+        if (c + 1 < chunks) fetch_v(c + 1);
+        __builtin_amdgcn_sched_barrier(0);
+
+        // U = T times that; the first half's parts are formed between the second's products
         f32x4 u[4][CT];
-        float odd = 0.0f;  // NaN where an update is not finite
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
+        for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int j = 0; j < CT; ++j) u[t][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        bf16x8 um[2][CT][2], us[2][CT][3];  // of U for y, of diag(..) U for the state
+        auto split_update = [&](int half) {
 #pragma unroll
-            for (int half = 0; half <= t >> 1; ++half) {
-                bf16x8 tf[3];
+            for (int j = 0; j < CT; ++j) {
+                float x[8], w[8];
 #pragma unroll
-                for (int part = 0; part < 3; ++part) tf[part] = frag(sh.TM[kPartsT * tri_index(t, half) + part]);
+                for (int k = 0; k < 2; ++k) {
+                    const f32x4 tk = *(const f32x4 *)(sc + 2 * kQ + 32 * half + 8 * grp + 4 * k);
 #pragma unroll
-                for (int k = 0; k < 6; ++k)
-#pragma unroll
-                    for (int j = 0; j < CT; ++j) u[t][j] = mfma(tf[kTerm[k][0]], rp[half][j][kTerm[k][1]], u[t][j]);
+                    for (int r = 0; r < 4; ++r) {
+                        x[4 * k + r] = u[2 * half + k][j][r];
+                        w[4 * k + r] = x[4 * k + r] * tk[r];
+                    }
+                }
+                split<2>(x, um[half][j]);
+                split<3>(w, us[half][j]);
             }
+        };
+        float odd = 0.0f;  // NaN where an update is not finite
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            if (i < 2) read_t(i + 1);
+#pragma unroll
+            for (int k = 0; k < 6; ++k)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int j = 0; j < CT; ++j)
+                        u[kTile[i] + t][j] = mfma(tf[i & 1][t][kTerm[k][0]], rp[i >> 1][j][kTerm[k][1]], u[kTile[i] + t][j]);
+            if (i == 0) {
+                interleave_reads<6>();
+                __builtin_amdgcn_sched_barrier(0);
+                split_update(0);
+            }
+        }
+        interleave_reads<6>();
+        interleave<24 * CT, 4>();
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int j = 0; j < CT; ++j)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) odd = __builtin_fmaf(u[t][j][r], 0.0f, odd);
+        if (uniform(__any(odd != odd))) break;
+
+        // M U for y, two tiles at a time, and K^T (diag(..) U) for the state, two of the tiles of n
+        bf16x8 mf[2][2][2], tk[3][2];
+        auto read_m = [&](int i) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+                    mf[i & 1][k][part] = frag(in[C::kTM + kTri * kPartsT + kPartsM * tri_index(kTile[i] + k, i >> 1) + part]);
+        };
+        auto read_k = [&](int i) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) tk[i % 3][k] = frag(in[C::kKt + 2 * (2 * (i % (NT / 2)) + k) + i / (NT / 2)]);
+        };
+        read_m(0);
+        read_m(1);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+#pragma unroll
+            for (int k = kTwo; k < 6; ++k)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int j = 0; j < CT; ++j)
+                        ys[kTile[i] + t][j] = mfma(mf[i & 1][t][kTerm[k][0]], um[i >> 1][j][kTerm[k][1]], ys[kTile[i] + t][j]);
+            if (i == 0) {
+                read_m(2);
+                split_update(1);
+            }
+            if (i == 1) read_k(0);
+            if (i == 2) read_k(1);
         }
-        const int64_t t0 = (int64_t)c * kQ;
-        const int rem = len - t0 < kQ ? (int)(len - t0) : kQ;
-        if (__any(odd != odd)) {
-            for (int t = 0; t < rem; ++t) {
-                const int64_t row = begin + t0 + t;
-                const float dt = softplus(ld_act((const uint16_t *)a.dt_raw, row * a.dt_stride + h) + (a.dt_bias ? a.dt_bias[h] : 0.0f));
-                const float beta = delta_gate(ld_act((const uint16_t *)a.beta_raw, row * a.beta_stride + h));
-                const float one = fast_exp2(dt * a.A[h] * kLog2e);
-                float kv[KB][8], qv[KB][8], kk = 0.0f, qq = 0.0f, out[CT];
 #pragma unroll
-                for (int b = 0; b < KB; ++b) {
-                    ld8(kb + (t0 + t) * a.k_stride + 32 * b + 8 * grp, kv[b]);
-                    ld8(qb + (t0 + t) * a.q_stride + 32 * b + 8 * grp, qv[b]);
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        kk = __builtin_fmaf(kv[b][e], kv[b][e], kk);
-                        qq = __builtin_fmaf(qv[b][e], qv[b][e], qq);
-                    }
-                }
-                const float rk = unit_scale(sum_groups(kk), a.norm_eps), rq = unit_scale(sum_groups(qq), a.norm_eps) * a.scale;
+            for (int j = 0; j < CT; ++j) S[n][j] *= decay;
+        interleave<18 * CT, 6>();
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int j = 0; j < CT; ++j) {
-                    float sk = 0.0f, sq = 0.0f;
+        for (int i = 0; i < NT; ++i) {
+            const int half = i / (NT / 2), n = 2 * (i % (NT / 2));
+            if (i + 2 < NT) read_k(i + 2);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+            for (int part = 2; part >= 0; --part)
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            S[n][j][r] *= one;
-                            sk = __builtin_fmaf(S[n][j][r], kv[n >> 1][4 * (n & 1) + r], sk);
-                        }
-                    const float up = beta * __builtin_fmaf(-rk, sum_groups(sk), ld_act(vb + j, (t0 + t) * a.v_stride)) * rk;
+                for (int k = 0; k < 2; ++k)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            S[n][j][r] = __builtin_fmaf(up, kv[n >> 1][4 * (n & 1) + r], S[n][j][r]);
-                            sq = __builtin_fmaf(S[n][j][r], qv[n >> 1][4 * (n & 1) + r], sq);
-                        }
-                    out[j] = sum_groups(sq) * rq;
-                }
-                if (grp == 0) store(t0 + t, out);
-            }
-            continue;
-        }
-        // y = diag(..) Q S^T + M U
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            bf16x8 up[CT][2];
-#pragma unroll
-            for (int j = 0; j < CT; ++j) {
-                float x[8];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) x[r] = u[2 * half][j][r], x[4 + r] = u[2 * half + 1][j][r];
-                split<2>(x, up[j]);
-            }
-#pragma unroll
-            for (int t = 2 * half; t < 4; ++t) {
-                bf16x8 mf[2];
-#pragma unroll
-                for (int part = 0; part < 2; ++part) mf[part] = frag(sh.TM[kTri * kPartsT + kPartsM * tri_index(t, half) + part]);
-#pragma unroll
-                for (int k = kTwo; k < 6; ++k)
-#pragma unroll
-                    for (int j = 0; j < CT; ++j) ys[t][j] = mfma(mf[kTerm[k][0]], up[j][kTerm[k][1]], ys[t][j]);
-            }
+                    for (int j = 0; j < CT; ++j) S[n + k][j] = mfma(tk[i % 3][k], us[half][j][part], S[n + k][j]);
         }
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int tok = tile_row(t, 4 * grp + r);
-                float out[CT];
-#pragma unroll
-                for (int j = 0; j < CT; ++j) out[j] = ys[t][j][r];
-                if (tok < rem) store(t0 + tok, out);
+                float lo = ys[t][0][r], hi = ys[t][CT - 1][r];
+                out[t][r] = bf16_pair(lo, hi);
             }
-        // S^T <- decay S^T + K^T (diag(..) U)
+    }
+    if (c > 0) store_y(c - 1);
+    // What an update that is not finite leaves, a token at a time; the other waves go on, so
+    // this one still fetches its share of each chunk.
+    for (c = uniform((int)c); c < chunks; ++c) {
+        const uint32_t left = len - c * kQ;
+        const int rem = left < kQ ? (int)left : kQ;
+        for (int i = 0; i < rem; ++i) {
+            const int64_t t = (int64_t)c * kQ + i, row = begin + t;
+            const float dt = softplus(ld_act((const uint16_t *)a.dt_raw, row * a.dt_stride + h) + (a.dt_bias ? a.dt_bias[h] : 0.0f));
+            const float beta = delta_gate(ld_act((const uint16_t *)a.beta_raw, row * a.beta_stride + h));
+            const float one = fast_exp2(dt * a.A[h] * kLog2e);
+            float kv[KB][8], qv[KB][8], kk = 0.0f, qq = 0.0f, sk[CT], sq[CT];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+            for (int b = 0; b < KB; ++b) {
+                ld8(kb + t * a.k_stride + 32 * b + 8 * grp, kv[b]);
+                ld8(qb + t * a.q_stride + 32 * b + 8 * grp, qv[b]);
 #pragma unroll
-            for (int j = 0; j < CT; ++j) S[n][j] *= decay;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            bf16x8 up[CT][3];
+                for (int e = 0; e < 8; ++e) {
+                    kk = __builtin_fmaf(kv[b][e], kv[b][e], kk);
+                    qq = __builtin_fmaf(qv[b][e], qv[b][e], qq);
+                }
+            }
+            const float rk = unit_scale(sum_groups(kk), a.norm_eps), rq = unit_scale(sum_groups(qq), a.norm_eps) * a.scale;
 #pragma unroll
             for (int j = 0; j < CT; ++j) {
-                float x[8];
+                sk[j] = sq[j] = 0.0f;
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const f32x4 tk = *(const f32x4 *)(sc + 2 * kQ + 32 * half + 8 * grp + 4 * k);
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) x[4 * k + r] = u[2 * half + k][j][r] * tk[r];
-                }
-                split<3>(x, up[j]);
-            }
+                    for (int r = 0; r < 4; ++r) {
+                        S[n][j][r] *= one;
+                        sk[j] = __builtin_fmaf(S[n][j][r], kv[n >> 1][4 * (n & 1) + r], sk[j]);
+                    }
+                const float up = beta * __builtin_fmaf(-rk, sum_groups(sk[j]), ld_act(vb + CT * m + j, t * a.v_stride)) * rk;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const bf16x8 kf = frag(sh.Kt[2 * n + half]);
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int part = 2; part >= 0; --part)
-#pragma unroll
-                    for (int j = 0; j < CT; ++j) S[n][j] = mfma(kf, up[j][part], S[n][j]);
+                    for (int r = 0; r < 4; ++r) {
+                        S[n][j][r] = __builtin_fmaf(up, kv[n >> 1][4 * (n & 1) + r], S[n][j][r]);
+                        sq[j] = __builtin_fmaf(S[n][j][r], qv[n >> 1][4 * (n & 1) + r], sq[j]);
+                    }
+                const float out = sum_groups(sq[j]) * rq;
+                if (grp == 0) st_act(yb + CT * m + j, t * y_stride, out);
             }
         }
+        if (c + 1 >= chunks) break;
+        vm_wait();
+        lds_barrier();
+        if (c + 2 < chunks) fetch(c + 2);
     }
     if (len > 0 || !resume)
 #pragma unroll
@@ -594,8 +694,8 @@ int64_t chunk_ids(int64_t seqs, int64_t rows) { return rows / kQ + seqs; }
 
 template <int N, int WAVES, int CT>
 hipError_t walk(const DeltaArgs &a, hipStream_t s) {
-    const int64_t nb = a.P / (16 * WAVES * CT), heads = (a.H * a.seqs + 7) / 8 * 8;
-    hipLaunchKernelGGL((delta_walk_kernel<N, WAVES, CT>), dim3((unsigned)(heads * nb)), dim3(64 * WAVES), 0, s, a);
+    const int64_t blocks = (a.G * a.seqs + 7) / 8 * 8 * (a.H / a.G) * (a.P / (16 * WAVES * CT));
+    hipLaunchKernelGGL((delta_walk_kernel<N, WAVES, CT>), dim3((unsigned)blocks), dim3(64 * WAVES), 0, s, a);
     return hipGetLastError();
 }
 
@@ -605,8 +705,9 @@ hipError_t delta(const DeltaArgs &a, hipStream_t s) {
     hipLaunchKernelGGL((delta_prepare_kernel<N>), dim3((unsigned)blocks), dim3(kPrepThreads), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (a.H * a.seqs * a.P >= 256 * 64) return a.P % 128 == 0 ? walk<N, 4, 2>(a, s) : walk<N, 2, 2>(a, s);
-    return walk<N, 1, 1>(a, s);
+    const char *v = getenv("DW");
+    if (v && *v == '4') return walk<N, 4, 1>(a, s);
+    return a.P % 128 == 0 ? walk<N, 8, 1>(a, s) : walk<N, 4, 1>(a, s);
 }
 
 }  // namespace
@@ -631,8 +732,7 @@ size_t delta_layout(DeltaArgs &a, int64_t N, void *workspace) {
     const size_t ids = (size_t)chunk_ids(a.seqs, a.rows), heads = ids * (size_t)a.H;
     a.ws_slot = (int32_t *)take((size_t)a.seqs * 4);
     a.ws_decay = (float *)take(heads * 4);
-    a.ws_scalars = (float *)take(heads * kScalars * 4);
-    a.ws_tm = take(heads * kFragTM * 1024);
+    a.ws_tm = take(heads * kHeadPieces * 1024);
     a.ws_kt = take(ids * (size_t)a.G * pieces_kt((int)N) * 1024);
     return at;
 }

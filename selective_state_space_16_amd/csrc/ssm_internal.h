@@ -252,10 +252,10 @@ struct DeltaArgs {
     float *state_cache;
     void *y;
     // workspace of the prompts
-    int32_t *ws_slot;              // (seqs) the slot a sequence owns, -1 for none
-    float *ws_decay, *ws_scalars;  // per (chunk, head): decay of the whole chunk, factors per token
-    void *ws_tm;                   // per (chunk, head): T and M as operands
-    void *ws_kt;                   // per (chunk, group): the transposed keys as operands
+    int32_t *ws_slot;  // (seqs) the slot a sequence owns, -1 for none
+    float *ws_decay;   // per (chunk, head): decay of the whole chunk
+    void *ws_tm;       // per (chunk, head): T and M as operands, factors per token
+    void *ws_kt;       // per (chunk, group): the transposed keys as operands
 };
 size_t delta_layout(DeltaArgs &a, int64_t N, void *workspace);
 size_t delta_workspace(int64_t seqs, int64_t rows, int64_t H, int64_t P, int64_t G, int64_t N);
