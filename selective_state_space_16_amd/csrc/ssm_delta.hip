@@ -690,6 +690,378 @@ __global__ __launch_bounds__(64 * WAVES) void delta_walk_kernel(DeltaArgs a) {
             for (int j = 0; j < CT; ++j) *(f32x4 *)(cache + j * N + 32 * (t >> 1) + 4 * (t & 1)) = S[t][j];
 }
 
+// ---------------------------------------------------------- walk, shared by waves
+
+// LDS of a workgroup, in pieces of 1 KiB (16 bytes per lane): what the waves hand each other.
+template <int N, int CT>
+struct TeamShared {
+    static constexpr int NW = N / 32;  // waves: 32 of n each
+    union {
+        alignas(16) char part[2][4][NW - 1][CT][1024];  // of K S^T and Q S^T: (tile of tokens, from another wave)
+        float sums[2][NW][16 * CT];                     // where a chunk is taken a token at a time
+    };
+    alignas(16) char r[2][CT][3][1024];             // beta (V - ..), as right operands
+    alignas(16) char us[2][CT][3][1024], um[2][CT][2][1024];  // diag(..) U and U, as right operands
+};
+
+// One head of one sequence, CT x 16 columns p of it, by N / 32 waves: wave w holds the
+// columns' elements n = 32 w .. 32 w + 31, and takes TW of the chunk's four tiles of tokens.
+template <int N, int CT>
+__global__ __launch_bounds__(2 * N, N == 128 ? 2 : 1) void delta_team_kernel(DeltaArgs a) {
+    constexpr int NW = N / 32, TW = 4 / NW, KB = N / 32;
+    __shared__ TeamShared<N, CT> sh;
+    // Workgroups go round the eight XCDs: those of a group of heads, which share its keys and
+    // queries, are 8 apart, so that they meet in one XCD's cache.
+    const uint32_t H = (uint32_t)a.H, G = (uint32_t)a.G, per = H / G, nb = (uint32_t)a.P / (16 * CT);
+    const uint32_t lin = blockIdx.x, one = lin / 8 % (per * nb), unit = lin / 8 / (per * nb) * 8 + lin % 8;
+    if (unit >= G * (uint32_t)a.seqs) return;
+    const uint32_t s = unit / G, g = unit % G, h = g * per + one / nb, pb = one % nb;
+    const int wave = uniform((int)(threadIdx.x >> 6)), lane = threadIdx.x & 63, m = lane & 15, grp = lane >> 4;
+    const uint32_t begin = uniform(seq_begin(a, s)), len = uniform(seq_length(a, s, begin));
+    const int64_t pw = (int64_t)pb * 16 * CT, p0 = pw + CT * m;  // columns p0 .. p0 + CT - 1
+    const int64_t y_stride = a.H * a.P;
+    uint16_t *yb = (uint16_t *)a.y + (int64_t)begin * y_stride + h * a.P + pw;
+    const int32_t slot = uniform(a.ws_slot[s]);
+    if (slot < 0) {
+        for (uint32_t t = 4 * wave + grp; t < len; t += 4 * NW)
+#pragma unroll
+            for (int j = 0; j < CT; ++j) yb[t * y_stride + CT * m + j] = 0;
+        return;
+    }
+    const bool resume = a.resume && a.resume[s] != 0;
+    float *cache = a.state_cache + (((int64_t)slot * H + h) * a.P + p0) * N + 32 * wave + 8 * grp;
+    f32x4 S[2][CT];  // n = 32 wave + 8 grp + 4 k + r, column p0 + j
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int j = 0; j < CT; ++j)
+            S[k][j] = resume ? *(const f32x4 *)(cache + j * N + 4 * k) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    const uint32_t chunks = (len + kQ - 1) / kQ, id0 = begin / kQ + s;
+    const uint16_t *qb = (const uint16_t *)a.q + (int64_t)begin * a.q_stride + g * N;
+    const uint16_t *kb = (const uint16_t *)a.k + (int64_t)begin * a.k_stride + g * N;
+    const uint16_t *vb = (const uint16_t *)a.v + (int64_t)begin * a.v_stride + h * a.P + pw;
+    const uint32_t v_row = (uint32_t)a.v_stride * 2, y_row = (uint32_t)y_stride * 2;
+
+    // What a chunk reads, loaded a chunk ahead, each as soon as the one before is used. The
+    // last chunk loads itself once more. Keys and queries behind the last token repeat it
+    // (their updates are zero), values are zeros there.
+    bf16x8 kf[4], qf[4], tf[TW][2][3], mf[TW][2][2], tk[2][2];
+    f32x4 fk[TW], fb[TW], fd[TW], fq[TW];
+    uint32_t v[TW][4];
+    float decay;
+    auto load_kq = [&](uint32_t c) {
+        const uint32_t left = len - c * kQ - 1;
+        const char *k0 = (const char *)(kb + (int64_t)c * kQ * a.k_stride + 32 * wave);
+        const char *q0 = (const char *)(qb + (int64_t)c * kQ * a.q_stride + 32 * wave);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            uint32_t i = tile_row(t, m);
+            i = i < left ? i : left;
+            kf[t] = *(const bf16x8 *)(k0 + (i * (uint32_t)a.k_stride * 2 + 16 * grp));
+            qf[t] = *(const bf16x8 *)(q0 + (i * (uint32_t)a.q_stride * 2 + 16 * grp));
+        }
+    };
+    auto head = [&](uint32_t c) { return (const char *)a.ws_tm + ((int64_t)(id0 + c) * H + h) * kHeadPieces * 1024; };
+    auto load_v = [&](uint32_t c) {
+        const uint32_t left = len - c * kQ, lane_at = 8 * grp * v_row + 2 * CT * m;
+        const auto rows = buffer(vb + (int64_t)c * kQ * a.v_stride, (left < kQ ? left - 1 : kQ - 1) * v_row + 32 * CT);
+        const float *f = (const float *)(head(c) + kFragTM * 1024) + 8 * grp;
+#pragma unroll
+        for (int i = 0; i < TW; ++i) {
+            const int t = wave * TW + i, at = 32 * (t >> 1) + 4 * (t & 1);
+            fk[i] = *(const f32x4 *)(f + at), fb[i] = *(const f32x4 *)(f + kQ + at);
+            fd[i] = *(const f32x4 *)(f + 2 * kQ + at), fq[i] = *(const f32x4 *)(f + 3 * kQ + at);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const uint32_t o = lane_at + (at + r) * v_row;
+                if constexpr (CT == 2) v[i][r] = __builtin_amdgcn_raw_buffer_load_b32(rows, o, 0, 0);
+                else v[i][r] = __builtin_amdgcn_raw_buffer_load_b16(rows, o, 0, 0);
+            }
+        }
+        decay = *(cf32_ptr)(a.ws_decay + uniform64((int64_t)(id0 + c) * H + h));
+    };
+    auto load_t = [&](uint32_t c) {
+#pragma unroll
+        for (int i = 0; i < TW; ++i)
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+                if (half == 0 || wave * TW + i >= 2)
+#pragma unroll
+                    for (int part = 0; part < 3; ++part)
+                        tf[i][half][part] = *(const bf16x8 *)(head(c) + (kPartsT * tri_index(wave * TW + i, half) + part) * 1024 + lane * 16);
+    };
+    auto load_m = [&](uint32_t c) {
+        const char *kt = (const char *)a.ws_kt + ((int64_t)(id0 + c) * a.G + g) * pieces_kt(N) * 1024;
+#pragma unroll
+        for (int i = 0; i < TW; ++i)
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+                if (half == 0 || wave * TW + i >= 2)
+#pragma unroll
+                    for (int part = 0; part < 2; ++part)
+                        mf[i][half][part] = *(const bf16x8 *)(head(c) + (kTri * kPartsT + kPartsM * tri_index(wave * TW + i, half) + part) * 1024 + lane * 16);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) tk[k][half] = *(const bf16x8 *)(kt + (2 * (2 * wave + k) + half) * 1024 + lane * 16);
+    };
+    auto frag = [&](const char *p) { return *(const bf16x8 *)(p + lane * 16); };
+    // the partial sums of tile t from wave w, for the wave that takes the tile
+    auto slot_of = [&](int t, int w) { return w < t / TW ? w : w - 1; };
+
+    if (chunks > 0) {
+        load_kq(0);
+        load_v(0);
+        load_t(0);
+        load_m(0);
+    }
+    for (uint32_t c = 0; c < chunks; ++c) {
+        const uint32_t next = c + 1 < chunks ? c + 1 : c, left = len - c * kQ;
+        // K S^T and Q S^T over the wave's n, for all tokens
+        f32x4 ks[4][CT], ys[4][CT];
+        {
+            bf16x8 sp[CT][3];
+#pragma unroll
+            for (int j = 0; j < CT; ++j) {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = S[0][j][e], x[4 + e] = S[1][j][e];
+                split<3>(x, sp[j]);
+            }
+            const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int part = 2; part >= 0; --part)
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int j = 0; j < CT; ++j) ks[t][j] = mfma(kf[t], sp[j][part], part == 2 ? zero : ks[t][j]);
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                if (t / TW != wave)
+#pragma unroll
+                    for (int j = 0; j < CT; ++j) *(f32x4 *)(sh.part[0][t][slot_of(t, wave)][j] + lane * 16) = ks[t][j];
+#pragma unroll
+            for (int part = 1; part >= 0; --part)
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int j = 0; j < CT; ++j) ys[t][j] = mfma(qf[t], sp[j][part], part == 1 ? zero : ys[t][j]);
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                if (t / TW != wave)
+#pragma unroll
+                    for (int j = 0; j < CT; ++j) *(f32x4 *)(sh.part[1][t][slot_of(t, wave)][j] + lane * 16) = ys[t][j];
+        }
+        load_kq(next);
+        lds_barrier();
+        // the waves' sums of the wave's tokens, and beta (V - diag(..) K S^T) in three parts
+        f32x4 out[TW][CT];
+#pragma unroll
+        for (int i = 0; i < TW; ++i) {
+            const int t = wave * TW + i;
+#pragma unroll
+            for (int j = 0; j < CT; ++j) {
+                f32x4 sum = ks[0][j], rest = ys[0][j];
+#pragma unroll
+                for (int k = 1; k < 4; ++k) sum = t == k ? ks[k][j] : sum, rest = t == k ? ys[k][j] : rest;
+#pragma unroll
+                for (int w = 0; w < NW - 1; ++w) {
+                    sum += *(const f32x4 *)(sh.part[0][t][w][j] + lane * 16);
+                    rest += *(const f32x4 *)(sh.part[1][t][w][j] + lane * 16);
+                }
+                out[i][j] = rest * fq[i];
+                float x[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float val = __uint_as_float(j ? v[i][r] & 0xffff0000u : v[i][r] << 16);
+                    x[r] = fb[i][r] * __builtin_fmaf(-fk[i][r], sum[r], val);
+                }
+#pragma unroll
+                for (int part = 0; part < 3; ++part) {
+                    uint2 u;
+                    u.x = bf16_pair(x[0], x[1]);
+                    u.y = bf16_pair(x[2], x[3]);
+                    *(uint2 *)(sh.r[t >> 1][j][part] + lane * 16 + 8 * (t & 1)) = u;
+                }
+            }
+        }
+        lds_barrier();
+        // U = T times that
+#pragma unroll
+        for (int i = 0; i < TW; ++i) {
+            const int t = wave * TW + i;
+#pragma unroll
+            for (int j = 0; j < CT; ++j) {
+                f32x4 u[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+                    if (half == 0 || t >= 2) {
+                        bf16x8 rp[3];
+#pragma unroll
+                        for (int part = 0; part < 3; ++part) rp[part] = frag(sh.r[half][j][part]);
+#pragma unroll
+                        for (int k = 0; k < 6; ++k) u[half] = mfma(tf[i][half][kTerm[k][0]], rp[kTerm[k][1]], u[half]);
+                    }
+                float x[4], w[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    x[r] = u[0][r] + u[1][r];
+                    w[r] = x[r] * fd[i][r];
+                }
+#pragma unroll
+                for (int part = 0; part < 3; ++part) {
+                    uint2 o;
+                    o.x = bf16_pair(w[0], w[1]);
+                    o.y = bf16_pair(w[2], w[3]);
+                    *(uint2 *)(sh.us[t >> 1][j][part] + lane * 16 + 8 * (t & 1)) = o;
+                }
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    uint2 o;
+                    o.x = bf16_pair(x[0], x[1]);
+                    o.y = bf16_pair(x[2], x[3]);
+                    *(uint2 *)(sh.um[t >> 1][j][part] + lane * 16 + 8 * (t & 1)) = o;
+                }
+            }
+        }
+        load_t(next);
+        lds_barrier();
+        // All waves read all of diag(..) U, and so agree where an update is not finite.
+        bf16x8 up[CT][2][3];
+        float odd = 0.0f;
+#pragma unroll
+        for (int j = 0; j < CT; ++j)
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                for (int part = 0; part < 3; ++part) up[j][half][part] = frag(sh.us[half][j][part]);
+#pragma unroll
+        for (int j = 0; j < CT; ++j)
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    const bf16x2 two = {up[j][half][0][e], up[j][half][0][e + 1]};
+                    odd = __builtin_amdgcn_fdot2_f32_bf16(two, bf16x2{(__bf16)0.0f, (__bf16)0.0f}, odd, false);
+                }
+        if (uniform(__any(odd != odd))) {
+            // a token at a time; the barriers pass each token's sums over n from wave to wave
+            const int rem = left < kQ ? (int)left : kQ;
+            for (int i = 0; i < rem; ++i) {
+                const int64_t t = (int64_t)c * kQ + i, row = begin + t;
+                const float dt = softplus(ld_act((const uint16_t *)a.dt_raw, row * a.dt_stride + h) + (a.dt_bias ? a.dt_bias[h] : 0.0f));
+                const float beta = delta_gate(ld_act((const uint16_t *)a.beta_raw, row * a.beta_stride + h));
+                const float keep = fast_exp2(dt * a.A[h] * kLog2e);
+                float kv[8], qv[8], kk = 0.0f, qq = 0.0f;
+                for (int b = 0; b < KB; ++b) {
+                    const int n = 32 * ((b + wave + 1) % KB) + 8 * grp;  // the wave's own block last
+                    ld8(kb + t * a.k_stride + n, kv);
+                    ld8(qb + t * a.q_stride + n, qv);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        kk = __builtin_fmaf(kv[e], kv[e], kk);
+                        qq = __builtin_fmaf(qv[e], qv[e], qq);
+                    }
+                }
+                const float rk = unit_scale(sum_groups(kk), a.norm_eps), rq = unit_scale(sum_groups(qq), a.norm_eps) * a.scale;
+#pragma unroll
+                for (int j = 0; j < CT; ++j) {
+                    float sk = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        S[e >> 2][j][e & 3] *= keep;
+                        sk = __builtin_fmaf(S[e >> 2][j][e & 3], kv[e], sk);
+                    }
+                    sh.sums[0][wave][CT * m + j] = sum_groups(sk);
+                }
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < CT; ++j) {
+                    float sk = 0.0f, sq = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < NW; ++w) sk += sh.sums[0][w][CT * m + j];
+                    const float up = beta * __builtin_fmaf(-rk, sk, ld_act(vb + CT * m + j, t * a.v_stride)) * rk;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        S[e >> 2][j][e & 3] = __builtin_fmaf(up, kv[e], S[e >> 2][j][e & 3]);
+                        sq = __builtin_fmaf(S[e >> 2][j][e & 3], qv[e], sq);
+                    }
+                    sh.sums[1][wave][CT * m + j] = sum_groups(sq);
+                }
+                __syncthreads();
+                if (wave == 0 && grp == 0)
+#pragma unroll
+                    for (int j = 0; j < CT; ++j) {
+                        float sq = 0.0f;
+#pragma unroll
+                        for (int w = 0; w < NW; ++w) sq += sh.sums[1][w][CT * m + j];
+                        st_act(yb + CT * m + j, t * y_stride, sq * rq);
+                    }
+            }
+            load_m(next);
+            load_v(next);
+            continue;
+        }
+        // S^T <- decay S^T + K^T (diag(..) U) over the wave's n
+#pragma unroll
+        for (int j = 0; j < CT; ++j) {
+            f32x4 more[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+#pragma unroll
+            for (int part = 2; part >= 0; --part)
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) more[k] = mfma(tk[k][half], up[j][half][part], more[k]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) S[k][j][r] = __builtin_fmaf(S[k][j][r], decay, more[k][r]);
+        }
+        // y = diag(..) Q S^T + M U of the wave's tokens; what lies behind the last is dropped
+        const uint32_t y_lane = 8 * grp * y_row + 2 * CT * m;
+        const auto rows = buffer(yb + (int64_t)c * kQ * y_stride, (left < kQ ? left - 1 : kQ - 1) * y_row + 32 * CT);
+#pragma unroll
+        for (int i = 0; i < TW; ++i) {
+            const int t = wave * TW + i;
+#pragma unroll
+            for (int j = 0; j < CT; ++j) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+                    if (half == 0 || t >= 2) {
+                        bf16x8 uf[2];
+#pragma unroll
+                        for (int part = 0; part < 2; ++part) uf[part] = frag(sh.um[half][j][part]);
+#pragma unroll
+                        for (int k = kTwo; k < 6; ++k) out[i][j] = mfma(mf[i][half][kTerm[k][0]], uf[kTerm[k][1]], out[i][j]);
+                    }
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const uint32_t at = y_lane + (32 * (t >> 1) + 4 * (t & 1) + r) * y_row;
+                float lo = out[i][0][r], hi = out[i][CT - 1][r];
+                const uint32_t two = bf16_pair(lo, hi);
+                if constexpr (CT == 2) __builtin_amdgcn_raw_buffer_store_b32(two, rows, at, 0, 0);
+                else __builtin_amdgcn_raw_buffer_store_b16((uint16_t)two, rows, at, 0, 0);
+            }
+        }
+        load_m(next);
+        load_v(next);
+    }
+    if (len > 0 || !resume)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int j = 0; j < CT; ++j) *(f32x4 *)(cache + j * N + 4 * k) = S[k][j];
+}
+
+template <int N, int CT>
+hipError_t team(const DeltaArgs &a, hipStream_t s) {
+    const int64_t blocks = (a.G * a.seqs + 7) / 8 * 8 * (a.H / a.G) * (a.P / (16 * CT));
+    hipLaunchKernelGGL((delta_team_kernel<N, CT>), dim3((unsigned)blocks), dim3(2 * N), 0, s, a);
+    return hipGetLastError();
+}
+
 int64_t chunk_ids(int64_t seqs, int64_t rows) { return rows / kQ + seqs; }
 
 template <int N, int WAVES, int CT>
@@ -706,7 +1078,8 @@ hipError_t delta(const DeltaArgs &a, hipStream_t s) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const char *v = getenv("DW");
-    if (v && *v == '4') return walk<N, 4, 1>(a, s);
+    if (v && *v == '1') return team<N, 1>(a, s);
+    if (v && *v == '2') return team<N, 2>(a, s);
     return a.P % 128 == 0 ? walk<N, 8, 1>(a, s) : walk<N, 4, 1>(a, s);
 }
 
