@@ -45,7 +45,6 @@
 // instead, from the state that entered it.
 #include "ssm_delta_device.h"
 #include "ssm_packed.h"
-#include <stdlib.h>
 
 namespace ssm {
 
@@ -61,7 +60,7 @@ constexpr int kFragTM = kTri * (kPartsT + kPartsM);  // pieces of 1 KiB per (chu
 constexpr int kHeadPieces = kFragTM + 1;
 constexpr int pieces_kt(int N) { return 2 * N / 16; }  // of the transposed keys per (chunk, group)
 
-__device__ __forceinline__ int tri_index(int tile, int half) { return tile < 2 ? tile : 2 * tile - 2 + half; }
+__device__ __forceinline__ int tri_index(int tile, int half) { return tile < 2 ? tile : 2 * tile - 2 + half; }  // (tiles 0, 1: half 0 alone)
 
 // The index, within 64 tokens or N keys' elements, of row m of tile t: two tiles share
 // 32 indexes, of which lane group m / 4 holds eight consecutive ones.
@@ -119,7 +118,7 @@ __device__ __forceinline__ float sum_groups(float v) {
 template <int N>
 struct PrepShared {
     static constexpr int R = kQ + 4, RK = N + 8;
-    alignas(16) float A[kQ][R], M[kQ][R];
+    alignas(16) float A[kQ][R];  // then M
     union {
         alignas(16) float T[kQ][R];
         alignas(16) uint16_t K[kQ][RK];
@@ -204,7 +203,7 @@ __global__ __launch_bounds__(kPrepThreads) void delta_prepare_kernel(DeltaArgs a
 #pragma unroll
             for (int b = 0; b < KB; ++b) *(bf16x8 *)&sh.K[16 * wave + m][32 * b + 8 * grp] = kw[b];
     }
-    f32x4 kk[4], qk[4];
+    f32x4 kk[4] = {}, qk[4] = {};
     for (int j = 0; j <= wave; ++j) {
         bf16x8 kj[KB];
         load(a.k, a.k_stride, j, kj);
@@ -247,7 +246,7 @@ __global__ __launch_bounds__(kPrepThreads) void delta_prepare_kernel(DeltaArgs a
                 if (col < i) av = d * sh.rk[i] * sh.beta[i] * kk[j][r];
             }
             sh.A[i][col] = av;
-            sh.M[i][col] = mv;
+            qk[j][r] = mv;  // M, once A is done with
         }
     }
     if (keys) {  // the transposed keys as left operands: row tile_row(t, m), tokens 32 half + 8 grp ..
@@ -308,19 +307,27 @@ __global__ __launch_bounds__(kPrepThreads) void delta_prepare_kernel(DeltaArgs a
     __syncthreads();
     // T and M as left operands: row tile_row(tile, m), columns 32 half + 8 grp ..
     char *o = (char *)a.ws_tm + at * kHeadPieces * 1024;
-    for (int f = wave; f < 2 * kTri; f += 4) {
-        const int tri = f % kTri, tile = tri < 2 ? tri : tri < 4 ? 2 : 3, half = tri < 2 ? 0 : tri & 1;
-        const float *src = (f < kTri ? sh.T : sh.M)[tile_row(tile, m)] + 32 * half + 8 * grp;
+    auto write = [&](const float (&src)[kQ][PrepShared<N>::R], int tri, auto count, int base) {
+        constexpr int kParts = decltype(count)::value;
+        const int tile = tri < 2 ? tri : tri < 4 ? 2 : 3, half = tri < 2 ? 0 : tri & 1;
+        const float *p = src[tile_row(tile, m)] + 32 * half + 8 * grp;
         float v[8];
-        *(f32x4 *)v = *(const f32x4 *)src;
-        *(f32x4 *)(v + 4) = *(const f32x4 *)(src + 4);
-        bf16x8 part[kPartsT];
-        split<kPartsT>(v, part);
-        const int base = f < kTri ? kPartsT * tri : kTri * kPartsT + kPartsM * tri;
-        *(bf16x8 *)(o + base * 1024 + lane * 16) = part[0];
-        *(bf16x8 *)(o + (base + 1) * 1024 + lane * 16) = part[1];
-        if (f < kTri) *(bf16x8 *)(o + (base + 2) * 1024 + lane * 16) = part[2];
+        *(f32x4 *)v = *(const f32x4 *)p;
+        *(f32x4 *)(v + 4) = *(const f32x4 *)(p + 4);
+        bf16x8 part[kParts];
+        split<kParts>(v, part);
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) *(bf16x8 *)(o + (base + kParts * tri + k) * 1024 + lane * 16) = part[k];
+    };
+    for (int tri = wave; tri < kTri; tri += 4) write(sh.T, tri, std::integral_constant<int, kPartsT>{}, 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (j > (wave | 1)) break;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sh.A[16 * wave + 4 * grp + r][16 * j + m] = qk[j][r];
     }
+    __syncthreads();
+    for (int tri = 3 - wave; tri < kTri; tri += 4) write(sh.A, tri, std::integral_constant<int, kPartsM>{}, kTri * kPartsT);
 }
 
 // ----------------------------------------------------------------------- walk
@@ -786,10 +793,9 @@ __global__ __launch_bounds__(2 * N, N == 128 ? 2 : 1) void delta_team_kernel(Del
         for (int i = 0; i < TW; ++i)
 #pragma unroll
             for (int half = 0; half < 2; ++half)
-                if (half == 0 || wave * TW + i >= 2)
 #pragma unroll
-                    for (int part = 0; part < 3; ++part)
-                        tf[i][half][part] = *(const bf16x8 *)(head(c) + (kPartsT * tri_index(wave * TW + i, half) + part) * 1024 + lane * 16);
+                for (int part = 0; part < 3; ++part)
+                    tf[i][half][part] = *(const bf16x8 *)(head(c) + (kPartsT * tri_index(wave * TW + i, half) + part) * 1024 + lane * 16);
     };
     auto load_m = [&](uint32_t c) {
         const char *kt = (const char *)a.ws_kt + ((int64_t)(id0 + c) * a.G + g) * pieces_kt(N) * 1024;
@@ -797,10 +803,9 @@ __global__ __launch_bounds__(2 * N, N == 128 ? 2 : 1) void delta_team_kernel(Del
         for (int i = 0; i < TW; ++i)
 #pragma unroll
             for (int half = 0; half < 2; ++half)
-                if (half == 0 || wave * TW + i >= 2)
 #pragma unroll
-                    for (int part = 0; part < 2; ++part)
-                        mf[i][half][part] = *(const bf16x8 *)(head(c) + (kTri * kPartsT + kPartsM * tri_index(wave * TW + i, half) + part) * 1024 + lane * 16);
+                for (int part = 0; part < 2; ++part)
+                    mf[i][half][part] = *(const bf16x8 *)(head(c) + (kTri * kPartsT + kPartsM * tri_index(wave * TW + i, half) + part) * 1024 + lane * 16);
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -999,10 +1004,7 @@ __global__ __launch_bounds__(2 * N, N == 128 ? 2 : 1) void delta_team_kernel(Del
                         st_act(yb + CT * m + j, t * y_stride, sq * rq);
                     }
             }
-            load_m(next);
-            load_v(next);
-            continue;
-        }
+        } else {
         // S^T <- decay S^T + K^T (diag(..) U) over the wave's n
 #pragma unroll
         for (int j = 0; j < CT; ++j) {
@@ -1045,6 +1047,7 @@ __global__ __launch_bounds__(2 * N, N == 128 ? 2 : 1) void delta_team_kernel(Del
                 else __builtin_amdgcn_raw_buffer_store_b16((uint16_t)two, rows, at, 0, 0);
             }
         }
+        }
         load_m(next);
         load_v(next);
     }
@@ -1077,10 +1080,15 @@ hipError_t delta(const DeltaArgs &a, hipStream_t s) {
     hipLaunchKernelGGL((delta_prepare_kernel<N>), dim3((unsigned)blocks), dim3(kPrepThreads), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const char *v = getenv("DW");
-    if (v && *v == '1') return team<N, 1>(a, s);
-    if (v && *v == '2') return team<N, 2>(a, s);
-    return a.P % 128 == 0 ? walk<N, 8, 1>(a, s) : walk<N, 4, 1>(a, s);
+    // A wave of the walk keeps all of N and takes 4.6 us a chunk (N = 128, 5.5 with two on a
+    // SIMD, 7.1 with the chip full), a team of waves 2.7 us for 16 columns and 4.4 for 32. So
+    // the walk is for a chip that it fills, in workgroups of 128 columns (or 64). Whole calls
+    // (us) at 32 heads of 128 x 128, walk / team of 32 / of 16 columns: 8 x 4096 tokens 810 /
+    // 1020 / 1290, 6 x 4096 595 / 773 / 984, 4 x 8192 997 / 927 / 1311, 2 x 8192 873 / 653 /
+    // 684, 1 x 16384 1576 / 1134 / 809.
+    const int64_t filled = a.H * a.seqs * a.P / (a.P % 128 == 0 ? 128 : 64);
+    if (filled >= 160) return a.P % 128 == 0 ? walk<N, 8, 1>(a, s) : walk<N, 4, 1>(a, s);
+    return filled >= 64 ? team<N, 2>(a, s) : team<N, 1>(a, s);
 }
 
 }  // namespace
