@@ -9,12 +9,10 @@
 //   dw = sum over rows of dy hat,   db = sum over rows of dy,   dscale = sum of dr x.
 //
 // A row is held in registers by the lanes that read it, as in the root-mean-square
-// norms, and summed twice: first for its mean (and that of g), then the squares of
-// what is left (and g times it). The variance as a difference of two sums would
-// take one pass over registers instead of two, and lose a row whose mean is large
-// against its spread; for the same reason the second pass also sums what the
-// first mean's rounding left, and takes it off (where mean / spread is 2^12, the
-// mean's last bit alone is 2^-12 of y). HBM bounds both passes: each input is read once, each output
+// norms. The variance as a difference of two sums over the whole row would lose a row
+// whose mean is large against its spread, and two sums one after the other cost a
+// barrier more where several waves share a row; so each wave takes its own elements'
+// mean off first, and what the waves found is joined at one barrier (row_stats). HBM bounds both passes: each input is read once, each output
 // written once.
 //
 // dw, db and dscale sum over all rows: a workgroup keeps its rows' sums in
@@ -22,23 +20,126 @@
 // order. Equal inputs give equal bits.
 #include "ssm_internal.h"
 #include "ssm_norm_rows.h"
+#include "ssm_packed.h"
 
 namespace ssm {
 
 namespace {
 
+// The lanes that share a row each take its elements' part (cnt of them in a wave, or in
+// the row's lanes where they are fewer) less a centre of their own wave, near its mean:
+// part = sums of d = r - centre, of d^2, and of g and g d in the backward pass. From
+// these the row's statistics, exactly as from one centre:
+//   mean   = (sum over waves of (sum d + cnt centre)) / D
+//   spread = sum over waves of (sum d^2 - 2 e sum d + cnt e^2),  e = mean - centre
+//   sum g (r - mean) = sum over waves of (sum g d - e sum g)
+// In double precision from the lanes' sums on, for one barrier per row.
+struct RowStats {
+    float rest, rstd, mg, mh;  // mean - centre, 1 / sd, mean(g), mean(g hat)
+};
+template <int TPR>
+__device__ __forceinline__ double lanes_sum(double v) {
+    if constexpr (TPR >= 64) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, wave_prefix_sum(v));
+        const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)u, 63), hi = __builtin_amdgcn_readlane((uint32_t)(u >> 32), 63);
+        return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+    } else {
+#pragma unroll
+        for (int m = 1; m < TPR; m *= 2) v += __shfl_xor(v, m);
+        return v;
+    }
+}
+template <int TPR, int NV>
+__device__ __forceinline__ RowStats row_stats(const float (&part)[NV], float centre, float cnt, double (*sh)[16][NV + 2],
+                                              int &turn, double inv, float eps) {
+    double v[NV], sum = 0.0, spread = 0.0, g = 0.0, gd = 0.0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] = lanes_sum<TPR>((double)part[i]);
+    double mean;
+    auto add = [&](const double (&p)[NV], double c, double n) {
+        const double e = mean - c;
+        spread += p[1] - e * (2.0 * p[0] - n * e);
+        if constexpr (NV == 4) g += p[2], gd += p[3] - e * p[2];
+    };
+    if constexpr (TPR <= 64) {
+        mean = (v[0] + (double)cnt * centre) * inv;
+        add(v, centre, cnt);
+    } else {
+        constexpr int WAVES = TPR / 64;
+        const int w = threadIdx.x >> 6;
+        if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) sh[turn][w][i] = v[i];
+            sh[turn][w][NV] = centre;
+            sh[turn][w][NV + 1] = cnt;
+        }
+        __syncthreads();
+        if constexpr (WAVES <= 8) {
+#pragma unroll
+            for (int k = 0; k < WAVES; ++k) sum += sh[turn][k][0] + sh[turn][k][NV + 1] * sh[turn][k][NV];
+            mean = sum * inv;
+#pragma unroll
+            for (int k = 0; k < WAVES; ++k) {
+                double p[NV];
+#pragma unroll
+                for (int i = 0; i < NV; ++i) p[i] = sh[turn][k][i];
+                add(p, sh[turn][k][NV], sh[turn][k][NV + 1]);
+            }
+        } else {  // a lane per wave, four times over, as row_sum does
+            const int k = threadIdx.x & 15;
+            double p[NV], c = 0.0, n = 0.0;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) p[i] = k < WAVES ? sh[turn][k][i] : 0.0;
+            if (k < WAVES) c = sh[turn][k][NV], n = sh[turn][k][NV + 1];
+            sum = p[0] + n * c;
+#pragma unroll
+            for (int m = 1; m < 16; m *= 2) sum += __shfl_xor(sum, m);
+            mean = sum * inv;
+            add(p, c, n);
+#pragma unroll
+            for (int m = 1; m < 16; m *= 2) {
+                spread += __shfl_xor(spread, m);
+                if constexpr (NV == 4) g += __shfl_xor(g, m), gd += __shfl_xor(gd, m);
+            }
+        }
+        turn ^= 1;
+    }
+    RowStats s;
+    s.rest = (float)(mean - (double)centre);
+    s.rstd = inv_rms(spread > 0.0 || spread != spread ? spread : 0.0, inv, eps);
+    s.mg = (float)(g * inv);
+    s.mh = (float)(gd * inv) * s.rstd;
+    return s;
+}
+
+// A wave's (or a row's fewer lanes') centre and number of elements.
+template <int TPR, int ITER>
+__device__ __forceinline__ void row_centre(float sum, int64_t D, float &centre, float &cnt) {
+    constexpr int LANES = TPR < 64 ? TPR : 64;
+#pragma unroll
+    for (int m = 1; m < LANES; m *= 2) sum += __shfl_xor(sum, m);
+    const int base = TPR > 64 ? (int)(threadIdx.x % TPR) / 64 * 64 : 0;
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < ITER; ++k) {
+        const int left = (int)D - (k * TPR + base) * kVec;
+        n += left < 0 ? 0 : left < LANES * kVec ? left : LANES * kVec;
+    }
+    cnt = (float)n;
+    centre = n > 0 ? sum / cnt : 0.0f;
+}
+
 template <int TPR, bool ODD, int ITER, typename T, typename R>
 __global__ __launch_bounds__(block_threads(TPR)) void layer_norm_fwd_kernel(LayerNormArgs a) {
     constexpr int RPB = block_threads(TPR) / TPR;
-    __shared__ double sh[2][16][1], sh2[2][16][2];
+    __shared__ double sh[2][16][4];
     int turn = 0;
     const int lane = threadIdx.x % TPR;
     const int64_t D = a.D;
     const double inv = 1.0 / (double)D;
     for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; row < a.rows; row += (int64_t)gridDim.x * RPB) {
         const int64_t base = row * D;
-        float r[ITER][kVec], part[1] = {0.0f}, part2[2] = {0.0f, 0.0f};
-        double sum[1], sum2[2];
+        float r[ITER][kVec], sum = 0.0f, part[2] = {0.0f, 0.0f}, centre, cnt;
 #pragma unroll
         for (int k = 0; k < ITER; ++k) {
             const int c = (k * TPR + lane) * kVec, left = (int)D - c;
@@ -51,12 +152,11 @@ __global__ __launch_bounds__(block_threads(TPR)) void layer_norm_fwd_kernel(Laye
                 for (int i = 0; i < kVec; ++i) {
                     const float add = a.scale ? s[i] * x[i] : x[i];
                     r[k][i] = a.residual ? r[k][i] + add : add;
-                    part[0] += r[k][i];
+                    sum += r[k][i];
                 }
             }
         }
-        row_sum<TPR, 1>(part, sum, sh, turn);
-        const float mean = (float)(sum[0] * inv);
+        row_centre<TPR, ITER>(sum, D, centre, cnt);
 #pragma unroll
         for (int k = 0; k < ITER; ++k) {
             const int c = (k * TPR + lane) * kVec, left = (int)D - c;
@@ -64,15 +164,13 @@ __global__ __launch_bounds__(block_threads(TPR)) void layer_norm_fwd_kernel(Laye
                 if (a.residual_out) st_vec<ODD>((R *)a.residual_out + base + c, left, r[k]);
 #pragma unroll
                 for (int i = 0; i < kVec; ++i) {
-                    r[k][i] = ODD && i >= left ? 0.0f : r[k][i] - mean;
-                    part2[0] = __builtin_fmaf(r[k][i], r[k][i], part2[0]);
-                    part2[1] += r[k][i];
+                    r[k][i] = ODD && i >= left ? 0.0f : r[k][i] - centre;
+                    part[0] += r[k][i];
+                    part[1] = __builtin_fmaf(r[k][i], r[k][i], part[1]);
                 }
             }
         }
-        row_sum<TPR, 2>(part2, sum2, sh2, turn);
-        const double low = sum2[1] * inv;  // what the rounding of the mean left
-        const float rstd = inv_rms(sum2[0] - low * sum2[1], inv, a.eps), rest = (float)low;
+        const RowStats st = row_stats<TPR, 2>(part, centre, cnt, sh, turn, inv, a.eps);
 #pragma unroll
         for (int k = 0; k < ITER; ++k) {
             const int c = (k * TPR + lane) * kVec, left = (int)D - c;
@@ -82,7 +180,7 @@ __global__ __launch_bounds__(block_threads(TPR)) void layer_norm_fwd_kernel(Laye
                 if (a.bias) ld_vec<ODD>(a.bias + c, left, b);
 #pragma unroll
                 for (int i = 0; i < kVec; ++i) {
-                    const float hat = (r[k][i] - rest) * rstd;
+                    const float hat = (r[k][i] - st.rest) * st.rstd;
                     y[i] = a.bias ? __builtin_fmaf(hat, w[i], b[i]) : hat * w[i];
                 }
                 st_vec<ODD>((T *)a.y + base + c, left, y);
@@ -94,7 +192,7 @@ __global__ __launch_bounds__(block_threads(TPR)) void layer_norm_fwd_kernel(Laye
 template <int TPR, bool ODD, int ITER, typename T, typename R>
 __global__ __launch_bounds__(block_threads(TPR)) void layer_norm_bwd_kernel(LayerNormArgs a) {
     constexpr int RPB = block_threads(TPR) / TPR;
-    __shared__ double sh[2][16][2], sh3[2][16][3];
+    __shared__ double sh[2][16][6];
     __shared__ float cols[RPB > 1 ? TPR * kVec * ITER : 1];
     int turn = 0;
     const int lane = threadIdx.x % TPR;
@@ -107,25 +205,18 @@ __global__ __launch_bounds__(block_threads(TPR)) void layer_norm_bwd_kernel(Laye
         for (int i = 0; i < kVec; ++i) dw[k][i] = db[k][i] = ds[k][i] = 0.0f;
     for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; row < a.rows; row += (int64_t)gridDim.x * RPB) {
         const int64_t base = row * D;
-        float r[ITER][kVec], dy[ITER][kVec], part[2] = {0.0f, 0.0f}, part3[3] = {0.0f, 0.0f, 0.0f};
-        double sum[2], sum3[3];
+        float r[ITER][kVec], dy[ITER][kVec], sum = 0.0f, part[4] = {0.0f, 0.0f, 0.0f, 0.0f}, centre, cnt;
 #pragma unroll
         for (int k = 0; k < ITER; ++k) {
             const int c = (k * TPR + lane) * kVec, left = (int)D - c;
             if (left > 0) {
-                float w[kVec];
                 ld_vec<ODD>((const R *)a.residual + base + c, left, r[k]);
                 ld_vec<ODD>((const T *)a.dy + base + c, left, dy[k]);
-                ld_vec<ODD>(a.weight + c, left, w);
 #pragma unroll
-                for (int i = 0; i < kVec; ++i) {
-                    part[0] += r[k][i];
-                    part[1] = __builtin_fmaf(dy[k][i], w[i], part[1]);
-                }
+                for (int i = 0; i < kVec; ++i) sum += r[k][i];
             }
         }
-        row_sum<TPR, 2>(part, sum, sh, turn);
-        const float mean = (float)(sum[0] * inv), mg = (float)(sum[1] * inv);
+        row_centre<TPR, ITER>(sum, D, centre, cnt);
 #pragma unroll
         for (int k = 0; k < ITER; ++k) {
             const int c = (k * TPR + lane) * kVec, left = (int)D - c;
@@ -134,17 +225,16 @@ __global__ __launch_bounds__(block_threads(TPR)) void layer_norm_bwd_kernel(Laye
                 ld_vec<ODD>(a.weight + c, left, w);
 #pragma unroll
                 for (int i = 0; i < kVec; ++i) {
-                    r[k][i] = ODD && i >= left ? 0.0f : r[k][i] - mean;
-                    part3[0] = __builtin_fmaf(r[k][i], r[k][i], part3[0]);
-                    part3[1] = __builtin_fmaf(dy[k][i] * w[i], r[k][i], part3[1]);
-                    part3[2] += r[k][i];
+                    const float g = dy[k][i] * w[i];
+                    r[k][i] = ODD && i >= left ? 0.0f : r[k][i] - centre;
+                    part[0] += r[k][i];
+                    part[1] = __builtin_fmaf(r[k][i], r[k][i], part[1]);
+                    part[2] += g;
+                    part[3] = __builtin_fmaf(g, r[k][i], part[3]);
                 }
             }
         }
-        row_sum<TPR, 3>(part3, sum3, sh3, turn);
-        const double low = sum3[2] * inv;  // what the rounding of the mean left
-        const float rstd = inv_rms(sum3[0] - low * sum3[2], inv, a.eps), rest = (float)low;
-        const float mh = (float)((sum3[1] - low * sum[1]) * inv) * rstd;  // mean(g hat)
+        const RowStats st = row_stats<TPR, 4>(part, centre, cnt, sh, turn, inv, a.eps);
 #pragma unroll
         for (int k = 0; k < ITER; ++k) {
             const int c = (k * TPR + lane) * kVec, left = (int)D - c;
@@ -158,10 +248,10 @@ __global__ __launch_bounds__(block_threads(TPR)) void layer_norm_bwd_kernel(Laye
                 }
 #pragma unroll
                 for (int i = 0; i < kVec; ++i) {
-                    const float hat = (r[k][i] - rest) * rstd;
+                    const float hat = (r[k][i] - st.rest) * st.rstd;
                     dw[k][i] = __builtin_fmaf(dy[k][i], hat, dw[k][i]);
                     db[k][i] += dy[k][i];
-                    float v = rstd * __builtin_fmaf(-mh, hat, __builtin_fmaf(dy[k][i], w[i], -mg));
+                    float v = st.rstd * __builtin_fmaf(-st.mh, hat, __builtin_fmaf(dy[k][i], w[i], -st.mg));
                     if (a.dres) v += up[i];
                     dr[i] = v;
                     if (a.scale) {

@@ -5,6 +5,7 @@
 #include <type_traits>
 
 #include "ssm_common.h"
+#include "ssm_packed.h"
 
 namespace ssm {
 
@@ -127,8 +128,6 @@ __device__ __forceinline__ void row_sum(const float (&part)[NV], double (&v)[NV]
         turn ^= 1;
     }
 }
-
-__device__ __forceinline__ bool finite(float v) { return (__float_as_uint(v) & 0x7f800000u) != 0x7f800000u; }
 
 // (sum / n + eps)^-1/2 rounded once: its error is a whole row's. The hardware's
 // reciprocal root and one step of Newton's in double precision, four
