@@ -23,8 +23,9 @@
 // all chunks at once, the second walks the chunks of a sequence in order.
 //
 // The walk keeps everything that one chunk hands to the next in one wave's registers.
-// A column of S^T (a row p of the state) never meets another, so a wave takes 16 or
-// 32 of them and all of N and of the 64 tokens. The matrix cores leave a result with
+// A column of S^T (a row p of the state) never meets another, so a wave takes 16 of
+// them and all of N and of the 64 tokens (a call that leaves most of the chip idle so
+// has each 16 or 32 columns shared by N / 32 waves instead: delta_team_kernel). The matrix cores leave a result with
 // its rows in a lane's registers and its columns across 16 lanes, and take their
 // right operand with the summed index in a lane's registers: the result of one
 // product is the next one's right operand as it stands, once its rows are numbered
@@ -41,8 +42,15 @@
 // two parts of S, M and U (16 bits). Sums are float32, the summed log decays float64.
 //
 // Where an update is not finite, because an input is not, zeros of T and M no longer
-// keep a token from those before it: the wave takes such a chunk a token at a time
-// instead, from the state that entered it.
+// keep a token from those before it: such a chunk is taken a token at a time instead,
+// from the state that entered it.
+//
+// Measured (us): 16384 tokens of 32 heads of 128 x 128, 135 ahead of the chunks and 680
+// for them (2.65 a chunk); eight prompts of 4096 tokens, 260 and 525; one chunk of 24
+// heads 9.5 and 7. The first kernel is bound by the latency of T's chain (four workgroups
+// of 36 KB a CU; three of 53 KB took 165 and 300), the chunks by the instructions of a
+// wave: without their products they take 75 % of the time, and the matrix cores are busy
+// for 35 %.
 #include "ssm_delta_device.h"
 #include "ssm_packed.h"
 
@@ -339,11 +347,11 @@ struct Chunk {
     static constexpr int kK = 0, kQ_ = 4 * KB, kKt = 8 * KB, kTM = kKt + pieces_kt(N), kFactors = kTM + kFragTM;
 };
 
-// One head of one sequence, WAVES x CT x 16 columns p of it.
-template <int N, int WAVES, int CT>
+// One head of one sequence, WAVES x 16 columns p of it.
+template <int N, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void delta_walk_kernel(DeltaArgs a) {
     using C = Chunk<N>;
-    constexpr int KB = N / 32, NT = N / 16;
+    constexpr int KB = N / 32, NT = N / 16, CT = 1;  // CT: tiles of 16 columns per wave
     __shared__ __align__(16) char sh[2][C::kPieces][1024];  // this chunk's and the next one's
     // Workgroups go round the eight XCDs: those of a group of heads, which share its keys and
     // queries, are 8 apart, so that they meet in one XCD's cache.
@@ -419,8 +427,7 @@ __global__ __launch_bounds__(64 * WAVES) void delta_walk_kernel(DeltaArgs a) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const uint32_t at = lane_at + tile_row(tile, r) * v_row;
-                if constexpr (CT == 2) v[tile][r] = __builtin_amdgcn_raw_buffer_load_b32(rows, at, 0, 0);
-                else v[tile][r] = __builtin_amdgcn_raw_buffer_load_b16(rows, at, 0, 0);
+                v[tile][r] = __builtin_amdgcn_raw_buffer_load_b16(rows, at, 0, 0);
             }
     };
     auto frag = [&](const char *p) { return *(const bf16x8 *)(p + lane * 16); };
@@ -440,8 +447,7 @@ __global__ __launch_bounds__(64 * WAVES) void delta_walk_kernel(DeltaArgs a) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const uint32_t at = lane_at + tile_row(t, r) * y_row;
-                if constexpr (CT == 2) __builtin_amdgcn_raw_buffer_store_b32(out[t][r], rows, at, 0, 0);
-                else __builtin_amdgcn_raw_buffer_store_b16((uint16_t)out[t][r], rows, at, 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b16((uint16_t)out[t][r], rows, at, 0, 0);
             }
     };
     uint32_t c = 0;
@@ -521,7 +527,7 @@ __global__ __launch_bounds__(64 * WAVES) void delta_walk_kernel(DeltaArgs a) {
                 for (int r = 0; r < 4; ++r)
 #pragma unroll
                     for (int j = 0; j < CT; ++j) {
-                        const float val = __uint_as_float(j ? v[t][r] & 0xffff0000u : v[t][r] << 16);
+                        const float val = __uint_as_float(v[t][r] << 16);
                         x[j][4 * k + r] = be[r] * __builtin_fmaf(-gk[r], ks[t][j][r], val);
                         ys[t][j][r] *= gq[r];
                     }
@@ -1067,10 +1073,10 @@ hipError_t team(const DeltaArgs &a, hipStream_t s) {
 
 int64_t chunk_ids(int64_t seqs, int64_t rows) { return rows / kQ + seqs; }
 
-template <int N, int WAVES, int CT>
+template <int N, int WAVES>
 hipError_t walk(const DeltaArgs &a, hipStream_t s) {
-    const int64_t blocks = (a.G * a.seqs + 7) / 8 * 8 * (a.H / a.G) * (a.P / (16 * WAVES * CT));
-    hipLaunchKernelGGL((delta_walk_kernel<N, WAVES, CT>), dim3((unsigned)blocks), dim3(64 * WAVES), 0, s, a);
+    const int64_t blocks = (a.G * a.seqs + 7) / 8 * 8 * (a.H / a.G) * (a.P / (16 * WAVES));
+    hipLaunchKernelGGL((delta_walk_kernel<N, WAVES>), dim3((unsigned)blocks), dim3(64 * WAVES), 0, s, a);
     return hipGetLastError();
 }
 
@@ -1087,7 +1093,7 @@ hipError_t delta(const DeltaArgs &a, hipStream_t s) {
     // 1020 / 1290, 6 x 4096 595 / 773 / 984, 4 x 8192 997 / 927 / 1311, 2 x 8192 873 / 653 /
     // 684, 1 x 16384 1576 / 1134 / 809.
     const int64_t filled = a.H * a.seqs * a.P / (a.P % 128 == 0 ? 128 : 64);
-    if (filled >= 160) return a.P % 128 == 0 ? walk<N, 8, 1>(a, s) : walk<N, 4, 1>(a, s);
+    if (filled >= 160) return a.P % 128 == 0 ? walk<N, 8>(a, s) : walk<N, 4>(a, s);
     return filled >= 64 ? team<N, 2>(a, s) : team<N, 1>(a, s);
 }
 
