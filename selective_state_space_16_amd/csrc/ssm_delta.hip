@@ -1010,6 +1010,7 @@ __global__ __launch_bounds__(2 * N, N == 128 ? 2 : 1) void delta_team_kernel(Del
                         st_act(yb + CT * m + j, t * y_stride, sq * rq);
                     }
             }
+            __syncthreads();  // the next chunk's partial sums lie where the last token's were read
         } else {
         // S^T <- decay S^T + K^T (diag(..) U) over the wave's n
 #pragma unroll

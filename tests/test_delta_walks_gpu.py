@@ -1,0 +1,66 @@
+"""The gated delta rule over packed prompts by every kernel that a call may be given:
+teams of waves on 16 or 32 columns of a state, and workgroups of four or eight waves of
+16 columns each, for states of 64 and of 128 elements per column (needs MI355X). Which
+one a call takes goes by its heads, columns and sequences: WAYS reaches each with few
+heads and many sequences, nearly all of them empty. Error bounds as in
+test_delta_cache_gpu.py.
+"""
+import pytest
+import torch
+
+from block_util import owned, to_gpu
+from delta_util import delta_inputs, delta_reference, parts
+from gpu_util import say
+from test_delta_cache_gpu import C, before, prompt
+
+pytestmark = pytest.mark.gpu
+H, G = 2, 1
+# (columns P, sequences): team of 16 columns, team of 32, walk of four waves, walk of eight
+WAYS = [(64, 8), (64, 40), (64, 90), (128, 90)]
+ALL = [(P, seqs, N) for P, seqs in WAYS for N in (64, 128)]
+
+
+def inputs(lens, P, seqs, N, *, seed, slots=(), spare=0, **kw):
+    """`lens` among `seqs` sequences, spread over them, the others empty."""
+    n = seqs // len(lens)
+    full = [0] * seqs
+    for i, v in enumerate(lens):
+        full[i * n] = v
+    d = delta_inputs(full, H, P, G, N, seed=seed, spare=spare, **kw)
+    for i, v in enumerate(slots):
+        if v is not None:
+            d["slots"][i * n] = v
+    d["at"] = [sum(full[:i * n]) for i in range(len(lens))]  # the first rows of the sequences that are not empty
+    return d
+
+
+def compare(d, g, y, y0, what="", **kw):
+    """`y` and the cache against the definition, which says where they are not finite."""
+    yr, st, yt, stol = delta_reference(d, y0, c=C, cy=2.0 ** -15, **kw)
+    got, gs = y.cpu().double(), g["state_cache"].cpu().double()
+    ok, oks = torch.isfinite(yr), torch.isfinite(st)
+    ty = 2.0 ** -8 * yr.abs() + yt
+    worst = lambda a, b, tol, m: float((((a - b).abs() / tol.clamp_min(1e-300))[m]).max()) if bool(m.any()) else 0.0  # noqa: E731
+    say(f"  {what} y of bound {worst(got, yr, ty, ok):.2f}, state of bound {worst(gs, st, stol.expand(st.shape), oks):.2f}")
+    assert torch.equal(torch.isfinite(got), ok) and torch.equal(torch.isfinite(gs), oks)
+    assert ((got - yr).abs() <= ty)[ok].all(), "y"
+    assert ((gs - st).abs() <= stol)[oks].all(), "state"
+    mine = set(owned(d["slots"], st.shape[0]))
+    for k in range(st.shape[0]):
+        if k not in mine:
+            assert torch.equal(g["state_cache"][k].cpu(), d["state_cache"][k]), "a slot of no sequence"
+
+
+@pytest.mark.parametrize("P,seqs,N", ALL)
+@pytest.mark.parametrize("at", [3, 63, 70])
+def test_an_infinite_value_stays_in_its_column(P, seqs, N, at):
+    """A value of one column that is not finite, in a chunk that others follow: every other
+    column, of every token, is what the definition says."""
+    say(f"case delta walks, infinite value at {at} P={P} N={N} sequences={seqs}")
+    d = inputs([200, 70, 130], P, seqs, N, seed=at + N)
+    for k, col in enumerate((17, P + 5)):  # of either head, of the first sequence and the last
+        parts(d)[2][d["at"][2 * k] + at, col] = (float("inf"), float("nan"))[k]
+    g, y0 = to_gpu(d), before(d)
+    y = prompt(g, y0.cuda())
+    torch.cuda.synchronize()
+    compare(d, g, y, y0)
