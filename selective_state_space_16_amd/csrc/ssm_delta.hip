@@ -36,10 +36,11 @@
 //
 // Precision. Keys and queries are bfloat16 as they come; their lengths, the gates and
 // the decays are factors per token, applied in float32 to what they multiply. The
-// other operands are sums of bfloat16, 8 bits a part. The state must come out as a
-// float32 recurrence leaves it, so S, T, beta (V - ..) and U take three parts on
-// its way (24 bits); the products for y, which is rounded to 8 bits in the end, take
-// two parts of S, M and U (16 bits). Sums are float32, the summed log decays float64.
+// other operands (S, T, M, beta (V - ..), U) are sums of three bfloat16, 8 bits a part,
+// which hold a float32 whole: the state and y, before its one rounding, come out as a
+// float32 recurrence leaves them, also where large terms of y cancel. (With two parts in
+// the products for y the walk of eight prompts of 4096 tokens took 525 us instead of 610.)
+// Sums are float32, the summed log decays float64.
 //
 // Where an update is not finite, because an input is not, zeros of T and M no longer
 // keep a token from those before it: such a chunk is taken a token at a time instead,
@@ -62,10 +63,12 @@ constexpr int kQ = 64;  // tokens per chunk
 constexpr int kPrepThreads = 256;
 // T and M as left operands: (tile of 16 rows, 32 of the columns) where the columns
 // are not wholly above the diagonal, a register of 16 bytes of each lane per part.
-constexpr int kTri = 6, kPartsT = 3, kPartsM = 2;
-constexpr int kFragTM = kTri * (kPartsT + kPartsM);  // pieces of 1 KiB per (chunk, head)
-// and one more of factors per token: e^G / |k|, beta, e^(G_last - G) / |k|, scale e^G / |q|
-constexpr int kHeadPieces = kFragTM + 1;
+constexpr int kTri = 6, kParts = 3;
+constexpr int kFragTM = kTri * (kParts + kParts - 1);  // pieces of 1 KiB per (chunk, head): T, and M but for its last part
+// behind them one of factors per token, e^G / |k|, beta, e^(G_last - G) / |k|, scale e^G / |q|, then M's last part
+constexpr int kFactors = kFragTM, kLastM = kFactors + 1, kHeadPieces = kLastM + kTri;
+constexpr int piece_t(int tri, int part) { return kParts * tri + part; }
+constexpr int piece_m(int tri, int part) { return part < 2 ? kTri * kParts + 2 * tri + part : kLastM + tri; }
 constexpr int pieces_kt(int N) { return 2 * N / 16; }  // of the transposed keys per (chunk, group)
 
 __device__ __forceinline__ int tri_index(int tile, int half) { return tile < 2 ? tile : 2 * tile - 2 + half; }  // (tiles 0, 1: half 0 alone)
@@ -74,10 +77,8 @@ __device__ __forceinline__ int tri_index(int tile, int half) { return tile < 2 ?
 // 32 indexes, of which lane group m / 4 holds eight consecutive ones.
 __device__ __forceinline__ int tile_row(int t, int m) { return 32 * (t >> 1) + 8 * (m >> 2) + 4 * (t & 1) + (m & 3); }
 
-// The product of two operands of three parts each, as six, the small ones first; the
-// last three are that of two parts each.
+// The product of two operands of three parts each, as six, the small ones first.
 constexpr int kTerm[6][2] = {{2, 0}, {0, 2}, {1, 1}, {1, 0}, {0, 1}, {0, 0}};
-constexpr int kTwo = 3;
 
 __device__ __forceinline__ f32x4 mfma_f32(float a, float b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
 
@@ -230,7 +231,7 @@ __global__ __launch_bounds__(kPrepThreads) void delta_prepare_kernel(DeltaArgs a
     if (wave == 0) {
         const double cum = sh.cum[lane], total = sh.cum[kQ - 1];
         const float grow = fast_exp2((float)cum), rk = sh.rk[lane];
-        float *o = (float *)((char *)a.ws_tm + (at * kHeadPieces + kFragTM) * 1024);
+        float *o = (float *)((char *)a.ws_tm + (at * kHeadPieces + kFactors) * 1024);
         o[lane] = grow * rk;
         o[kQ + lane] = sh.beta[lane];
         o[2 * kQ + lane] = fast_exp2((float)(total - cum)) * rk;
@@ -315,8 +316,7 @@ __global__ __launch_bounds__(kPrepThreads) void delta_prepare_kernel(DeltaArgs a
     __syncthreads();
     // T and M as left operands: row tile_row(tile, m), columns 32 half + 8 grp ..
     char *o = (char *)a.ws_tm + at * kHeadPieces * 1024;
-    auto write = [&](const float (&src)[kQ][PrepShared<N>::R], int tri, auto count, int base) {
-        constexpr int kParts = decltype(count)::value;
+    auto write = [&](const float (&src)[kQ][PrepShared<N>::R], int tri, auto piece) {
         const int tile = tri < 2 ? tri : tri < 4 ? 2 : 3, half = tri < 2 ? 0 : tri & 1;
         const float *p = src[tile_row(tile, m)] + 32 * half + 8 * grp;
         float v[8];
@@ -325,9 +325,9 @@ __global__ __launch_bounds__(kPrepThreads) void delta_prepare_kernel(DeltaArgs a
         bf16x8 part[kParts];
         split<kParts>(v, part);
 #pragma unroll
-        for (int k = 0; k < kParts; ++k) *(bf16x8 *)(o + (base + kParts * tri + k) * 1024 + lane * 16) = part[k];
+        for (int k = 0; k < kParts; ++k) *(bf16x8 *)(o + piece(tri, k) * 1024 + lane * 16) = part[k];
     };
-    for (int tri = wave; tri < kTri; tri += 4) write(sh.T, tri, std::integral_constant<int, kPartsT>{}, 0);
+    for (int tri = wave; tri < kTri; tri += 4) write(sh.T, tri, piece_t);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         if (j > (wave | 1)) break;
@@ -335,7 +335,7 @@ __global__ __launch_bounds__(kPrepThreads) void delta_prepare_kernel(DeltaArgs a
         for (int r = 0; r < 4; ++r) sh.A[16 * wave + 4 * grp + r][16 * j + m] = qk[j][r];
     }
     __syncthreads();
-    for (int tri = 3 - wave; tri < kTri; tri += 4) write(sh.A, tri, std::integral_constant<int, kPartsM>{}, kTri * kPartsT);
+    for (int tri = 3 - wave; tri < kTri; tri += 4) write(sh.A, tri, piece_m);
 }
 
 // ----------------------------------------------------------------------- walk
@@ -343,8 +343,8 @@ __global__ __launch_bounds__(kPrepThreads) void delta_prepare_kernel(DeltaArgs a
 // What the walk reads of one chunk: pieces of 1 KiB, a register of 16 bytes of each lane.
 template <int N>
 struct Chunk {
-    static constexpr int KB = N / 32, kPieces = 8 * KB + pieces_kt(N) + kHeadPieces;
-    static constexpr int kK = 0, kQ_ = 4 * KB, kKt = 8 * KB, kTM = kKt + pieces_kt(N), kFactors = kTM + kFragTM;
+    static constexpr int KB = N / 32, kHead = kFactors + 1, kPieces = 8 * KB + pieces_kt(N) + kHead;
+    static constexpr int kK = 0, kQ_ = 4 * KB, kKt = 8 * KB, kTM = kKt + pieces_kt(N);
 };
 
 // One head of one sequence, WAVES x 16 columns p of it.
@@ -404,9 +404,9 @@ __global__ __launch_bounds__(64 * WAVES) void delta_walk_kernel(DeltaArgs a) {
         const char *tm = (const char *)a.ws_tm + ((int64_t)(id0 + c) * H + h) * kHeadPieces * 1024;
         const char *kt = (const char *)a.ws_kt + ((int64_t)(id0 + c) * a.G + g) * pieces_kt(N) * 1024;
 #pragma unroll
-        for (int i = 0; i < (kHeadPieces + WAVES - 1) / WAVES; ++i) {
+        for (int i = 0; i < (C::kHead + WAVES - 1) / WAVES; ++i) {
             const int f = wave + i * WAVES;
-            if (f < kHeadPieces) dma16_s(tm + f * 1024, lane * 16, to + (C::kTM + f) * 1024);
+            if (f < C::kHead) dma16_s(tm + f * 1024, lane * 16, to + (C::kTM + f) * 1024);
         }
 #pragma unroll
         for (int i = 0; i < pieces_kt(N) / WAVES; ++i) {
@@ -454,6 +454,14 @@ __global__ __launch_bounds__(64 * WAVES) void delta_walk_kernel(DeltaArgs a) {
     for (; c < chunks; ++c) {
         vm_wait();
         lds_barrier();  // this chunk is there, the one before is done with
+        // M's last part comes by registers: two chunks of it would not fit into LDS beside the
+        // rest. (Loaded ahead of the products with T, the walk above took 640 us.)
+        bf16x8 last[kTri];
+        {
+            const char *p = (const char *)a.ws_tm + (((int64_t)(id0 + c) * H + h) * kHeadPieces + kLastM) * 1024;
+#pragma unroll
+            for (int i = 0; i < kTri; ++i) last[i] = *(const bf16x8 *)(p + i * 1024 + lane * 16);
+        }
         if (c > 0) store_y(c - 1);
         // The values are there as well, but the compiler would wait for them where they
         // are used, and with them for the loads that it does not know of: here it waits for none.
@@ -462,7 +470,7 @@ __global__ __launch_bounds__(64 * WAVES) void delta_walk_kernel(DeltaArgs a) {
         if (c + 1 < chunks) fetch(c + 1);
         const float decay = *(cf32_ptr)(a.ws_decay + uniform64((int64_t)(id0 + c) * H + h));
         const char(*in)[1024] = sh[c & 1];
-        const float *sc = (const float *)in[C::kFactors];
+        const float *sc = (const float *)in[C::kTM + kFactors];
 
         // K S^T and Q S^T. Operands are read from LDS a group of products ahead, and the
         // next 32 of n are split between the products.
@@ -494,14 +502,14 @@ __global__ __launch_bounds__(64 * WAVES) void delta_walk_kernel(DeltaArgs a) {
 #pragma unroll
                     for (int j = 0; j < CT; ++j) {
                         ks[t][j] = mfma(kf[t & 1], sp[b & 1][j][part], ks[t][j]);
-                        if (part < 2) ys[t][j] = mfma(qf[t & 1], sp[b & 1][j][part], ys[t][j]);
+                        ys[t][j] = mfma(qf[t & 1], sp[b & 1][j][part], ys[t][j]);
                     }
             }
             if (b + 1 < KB) split_state(b + 1, sp[(b + 1) & 1]);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 interleave_reads<2>();
-                interleave<5 * CT, 3>();
+                interleave<6 * CT, 3>();
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -513,7 +521,7 @@ __global__ __launch_bounds__(64 * WAVES) void delta_walk_kernel(DeltaArgs a) {
             for (int k = 0; k < 2; ++k)
 #pragma unroll
                 for (int part = 0; part < 3; ++part)
-                    tf[i & 1][k][part] = frag(in[C::kTM + kPartsT * tri_index(kTile[i] + k, i >> 1) + part]);
+                    tf[i & 1][k][part] = frag(in[C::kTM + piece_t(tri_index(kTile[i] + k, i >> 1), part)]);
         };
         read_t(0);
 #pragma unroll
@@ -544,7 +552,7 @@ __global__ __launch_bounds__(64 * WAVES) void delta_walk_kernel(DeltaArgs a) {
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int j = 0; j < CT; ++j) u[t][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        bf16x8 um[2][CT][2], us[2][CT][3];  // of U for y, of diag(..) U for the state
+        bf16x8 um[2][CT][3], us[2][CT][3];  // of U for y, of diag(..) U for the state
         auto split_update = [&](int half) {
 #pragma unroll
             for (int j = 0; j < CT; ++j) {
@@ -558,7 +566,7 @@ __global__ __launch_bounds__(64 * WAVES) void delta_walk_kernel(DeltaArgs a) {
                         w[4 * k + r] = x[4 * k + r] * tk[r];
                     }
                 }
-                split<2>(x, um[half][j]);
+                split<3>(x, um[half][j]);
                 split<3>(w, us[half][j]);
             }
         };
@@ -580,7 +588,7 @@ __global__ __launch_bounds__(64 * WAVES) void delta_walk_kernel(DeltaArgs a) {
             }
         }
         interleave_reads<6>();
-        interleave<24 * CT, 4>();
+        interleave<24 * CT, 5>();
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int t = 0; t < 4; ++t)
@@ -591,13 +599,15 @@ __global__ __launch_bounds__(64 * WAVES) void delta_walk_kernel(DeltaArgs a) {
         if (uniform(__any(odd != odd))) break;
 
         // M U for y, two tiles at a time, and K^T (diag(..) U) for the state, two of the tiles of n
-        bf16x8 mf[2][2][2], tk[3][2];
+        bf16x8 mf[2][2][3], tk[3][2];
         auto read_m = [&](int i) {
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
+            for (int k = 0; k < 2; ++k) {
+                const int tri = tri_index(kTile[i] + k, i >> 1);
 #pragma unroll
-                for (int part = 0; part < 2; ++part)
-                    mf[i & 1][k][part] = frag(in[C::kTM + kTri * kPartsT + kPartsM * tri_index(kTile[i] + k, i >> 1) + part]);
+                for (int part = 0; part < 2; ++part) mf[i & 1][k][part] = frag(in[C::kTM + piece_m(tri, part)]);
+                mf[i & 1][k][2] = last[tri];
+            }
         };
         auto read_k = [&](int i) {
 #pragma unroll
@@ -608,7 +618,7 @@ __global__ __launch_bounds__(64 * WAVES) void delta_walk_kernel(DeltaArgs a) {
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
 #pragma unroll
-            for (int k = kTwo; k < 6; ++k)
+            for (int k = 0; k < 6; ++k)
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -625,7 +635,7 @@ __global__ __launch_bounds__(64 * WAVES) void delta_walk_kernel(DeltaArgs a) {
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int j = 0; j < CT; ++j) S[n][j] *= decay;
-        interleave<18 * CT, 6>();
+        interleave<36 * CT, 4>();
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
@@ -714,13 +724,13 @@ struct TeamShared {
         float sums[2][NW][16 * CT];                     // where a chunk is taken a token at a time
     };
     alignas(16) char r[2][CT][3][1024];             // beta (V - ..), as right operands
-    alignas(16) char us[2][CT][3][1024], um[2][CT][2][1024];  // diag(..) U and U, as right operands
+    alignas(16) char us[2][CT][3][1024], um[2][CT][3][1024];  // diag(..) U and U, as right operands
 };
 
 // One head of one sequence, CT x 16 columns p of it, by N / 32 waves: wave w holds the
 // columns' elements n = 32 w .. 32 w + 31, and takes TW of the chunk's four tiles of tokens.
 template <int N, int CT>
-__global__ __launch_bounds__(2 * N, N == 128 ? 2 : 1) void delta_team_kernel(DeltaArgs a) {
+__global__ __launch_bounds__(2 * N, N == 128 && CT == 1 ? 2 : 1) void delta_team_kernel(DeltaArgs a) {
     constexpr int NW = N / 32, TW = 4 / NW, KB = N / 32;
     __shared__ TeamShared<N, CT> sh;
     // Workgroups go round the eight XCDs: those of a group of heads, which share its keys and
@@ -759,7 +769,7 @@ __global__ __launch_bounds__(2 * N, N == 128 ? 2 : 1) void delta_team_kernel(Del
     // What a chunk reads, loaded a chunk ahead, each as soon as the one before is used. The
     // last chunk loads itself once more. Keys and queries behind the last token repeat it
     // (their updates are zero), values are zeros there.
-    bf16x8 kf[4], qf[4], tf[TW][2][3], mf[TW][2][2], tk[2][2];
+    bf16x8 kf[4], qf[4], tf[TW][2][3], mf[TW][2][3], tk[2][2];
     f32x4 fk[TW], fb[TW], fd[TW], fq[TW];
     uint32_t v[TW][4];
     float decay;
@@ -779,7 +789,7 @@ __global__ __launch_bounds__(2 * N, N == 128 ? 2 : 1) void delta_team_kernel(Del
     auto load_v = [&](uint32_t c) {
         const uint32_t left = len - c * kQ, lane_at = 8 * grp * v_row + 2 * CT * m;
         const auto rows = buffer(vb + (int64_t)c * kQ * a.v_stride, (left < kQ ? left - 1 : kQ - 1) * v_row + 32 * CT);
-        const float *f = (const float *)(head(c) + kFragTM * 1024) + 8 * grp;
+        const float *f = (const float *)(head(c) + kFactors * 1024) + 8 * grp;
 #pragma unroll
         for (int i = 0; i < TW; ++i) {
             const int t = wave * TW + i, at = 32 * (t >> 1) + 4 * (t & 1);
@@ -801,7 +811,7 @@ __global__ __launch_bounds__(2 * N, N == 128 ? 2 : 1) void delta_team_kernel(Del
             for (int half = 0; half < 2; ++half)
 #pragma unroll
                 for (int part = 0; part < 3; ++part)
-                    tf[i][half][part] = *(const bf16x8 *)(head(c) + (kPartsT * tri_index(wave * TW + i, half) + part) * 1024 + lane * 16);
+                    tf[i][half][part] = *(const bf16x8 *)(head(c) + piece_t(tri_index(wave * TW + i, half), part) * 1024 + lane * 16);
     };
     auto load_m = [&](uint32_t c) {
         const char *kt = (const char *)a.ws_kt + ((int64_t)(id0 + c) * a.G + g) * pieces_kt(N) * 1024;
@@ -810,8 +820,8 @@ __global__ __launch_bounds__(2 * N, N == 128 ? 2 : 1) void delta_team_kernel(Del
 #pragma unroll
             for (int half = 0; half < 2; ++half)
 #pragma unroll
-                for (int part = 0; part < 2; ++part)
-                    mf[i][half][part] = *(const bf16x8 *)(head(c) + (kTri * kPartsT + kPartsM * tri_index(wave * TW + i, half) + part) * 1024 + lane * 16);
+                for (int part = 0; part < 3; ++part)
+                    mf[i][half][part] = *(const bf16x8 *)(head(c) + piece_m(tri_index(wave * TW + i, half), part) * 1024 + lane * 16);
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -853,11 +863,11 @@ __global__ __launch_bounds__(2 * N, N == 128 ? 2 : 1) void delta_team_kernel(Del
 #pragma unroll
                     for (int j = 0; j < CT; ++j) *(f32x4 *)(sh.part[0][t][slot_of(t, wave)][j] + lane * 16) = ks[t][j];
 #pragma unroll
-            for (int part = 1; part >= 0; --part)
+            for (int part = 2; part >= 0; --part)
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
 #pragma unroll
-                    for (int j = 0; j < CT; ++j) ys[t][j] = mfma(qf[t], sp[j][part], part == 1 ? zero : ys[t][j]);
+                    for (int j = 0; j < CT; ++j) ys[t][j] = mfma(qf[t], sp[j][part], part == 2 ? zero : ys[t][j]);
 #pragma unroll
             for (int t = 0; t < 4; ++t)
                 if (t / TW != wave)
@@ -928,7 +938,7 @@ __global__ __launch_bounds__(2 * N, N == 128 ? 2 : 1) void delta_team_kernel(Del
                     *(uint2 *)(sh.us[t >> 1][j][part] + lane * 16 + 8 * (t & 1)) = o;
                 }
 #pragma unroll
-                for (int part = 0; part < 2; ++part) {
+                for (int part = 0; part < 3; ++part) {
                     uint2 o;
                     o.x = bf16_pair(x[0], x[1]);
                     o.y = bf16_pair(x[2], x[3]);
@@ -1038,11 +1048,11 @@ __global__ __launch_bounds__(2 * N, N == 128 ? 2 : 1) void delta_team_kernel(Del
 #pragma unroll
                 for (int half = 0; half < 2; ++half)
                     if (half == 0 || t >= 2) {
-                        bf16x8 uf[2];
+                        bf16x8 uf[3];
 #pragma unroll
-                        for (int part = 0; part < 2; ++part) uf[part] = frag(sh.um[half][j][part]);
+                        for (int part = 0; part < 3; ++part) uf[part] = frag(sh.um[half][j][part]);
 #pragma unroll
-                        for (int k = kTwo; k < 6; ++k) out[i][j] = mfma(mf[i][half][kTerm[k][0]], uf[kTerm[k][1]], out[i][j]);
+                        for (int k = 0; k < 6; ++k) out[i][j] = mfma(mf[i][half][kTerm[k][0]], uf[kTerm[k][1]], out[i][j]);
                     }
             }
 #pragma unroll

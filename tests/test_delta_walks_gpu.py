@@ -64,3 +64,52 @@ def test_an_infinite_value_stays_in_its_column(P, seqs, N, at):
     y = prompt(g, y0.cuda())
     torch.cuda.synchronize()
     compare(d, g, y, y0)
+
+
+def cancelling(P, seqs, N):
+    """Outputs that are small differences of large terms. The first sequence starts from
+    nothing and takes tokens in threes: two whose keys are alone in their directions and
+    whose updates are nearly alike, then a query of their difference with a key of zeros;
+    the second resumes a state whose columns are nearly alike in pairs, under such queries
+    alone. Everything that is summed up is positive."""
+    d = inputs([96, 70], P, seqs, N, seed=P + N)
+    g = torch.Generator().manual_seed(N)
+    q, k, v, dt, be = parts(d)
+    q.zero_(), k.zero_(), v.zero_()
+    a = torch.exp(torch.logaddexp(dt.double() + d["dt_bias"].double(), torch.zeros(())) * d["A"].double())
+    beta = torch.sigmoid(be.double())
+    for i in range(32):
+        t = d["at"][0] + 3 * i
+        k[t, 2 * i], k[t + 1, 2 * i + 1] = (torch.rand(2, generator=g) + 0.5).bfloat16()
+        v[t] = (torch.rand(H * P, generator=g) + 0.5).bfloat16()
+        v[t + 1] = (v[t].double() * (beta[t] * a[t + 1] / beta[t + 1]).repeat_interleave(P)).bfloat16()
+        q[t + 2, 2 * i], q[t + 2, 2 * i + 1] = 1, -1
+    n = seqs // 2
+    for t in range(70):
+        i = 2 * int(torch.randint(N // 2, (1,), generator=g))
+        q[d["at"][1] + t, i], q[d["at"][1] + t, i + 1] = 1, -1
+    d["resume"][0], d["resume"][n] = 0, 1
+    st = d["state_cache"][d["slots"][n]]
+    st.abs_()
+    st[..., 1::2] = st[..., ::2] * (1 + 2.0 ** -12 * torch.rand(H, P, N // 2, generator=g))
+    return d
+
+
+@pytest.mark.parametrize("P,seqs,N", ALL)
+def test_outputs_are_products_of_float32_operands(P, seqs, N):
+    """Where two terms nearly cancel, what each was rounded to before shows. In float32 a
+    term takes at most 24 roundings: of beta 5, of u and its factors in T and M (two
+    lengths, a decay with its exponent, their products) 11, the sum of two terms with what
+    an operand of three parts leaves out 8; y is then rounded once to bfloat16."""
+    say(f"case delta walks, cancelling terms P={P} N={N} sequences={seqs}")
+    d = cancelling(P, seqs, N)
+    g, y0 = to_gpu(d), before(d)
+    y = prompt(g, y0.cuda())
+    torch.cuda.synchronize()
+    yr = delta_reference(d, y0)[0]
+    big = dict(d, qkv=d["qkv"].clone())
+    parts(big)[0].abs_()
+    terms = delta_reference(big, y0)[0]
+    err, tol = (y.cpu().double() - yr).abs(), 2.0 ** -8 * yr.abs() + 24 * 2.0 ** -24 * terms
+    say(f"  of bound {float((err / tol.clamp_min(1e-300)).max()):.2f}, size of the terms {float((terms.sum() / yr.abs().sum())):.0f} times")
+    assert (err <= tol).all()
