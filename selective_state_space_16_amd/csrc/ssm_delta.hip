@@ -204,9 +204,10 @@ __global__ __launch_bounds__(kPrepThreads) void delta_prepare_kernel(DeltaArgs a
     }
     {
         const float kk = squares(kw), qq = squares(qw);
-        if (grp == 0) {
-            sh.rk[16 * wave + m] = unit_scale(kk, a.norm_eps);
-            sh.rq[16 * wave + m] = unit_scale(qq, a.norm_eps) * a.scale;
+        if (grp == 0) {  // zeros behind the last token: with norm_eps = 0 its zeros would have infinite factors
+            const bool in = 16 * wave + m < rem;
+            sh.rk[16 * wave + m] = in ? unit_scale(kk, a.norm_eps) : 0.0f;
+            sh.rq[16 * wave + m] = in ? unit_scale(qq, a.norm_eps) * a.scale : 0.0f;
         }
         if (keys)
 #pragma unroll

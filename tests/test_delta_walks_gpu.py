@@ -113,3 +113,16 @@ def test_outputs_are_products_of_float32_operands(P, seqs, N):
     err, tol = (y.cpu().double() - yr).abs(), 2.0 ** -8 * yr.abs() + 24 * 2.0 ** -24 * terms
     say(f"  of bound {float((err / tol.clamp_min(1e-300)).max()):.2f}, size of the terms {float((terms.sum() / yr.abs().sum())):.0f} times")
     assert (err <= tol).all()
+
+
+@pytest.mark.parametrize("P,seqs,N", ALL)
+def test_lengths_without_a_floor_under_them(P, seqs, N):
+    """norm_eps = 0 is a floor too small to change any length here: the same bits, also of
+    sequences that end inside a chunk, whose rows behind the last token have no length."""
+    say(f"case delta walks, norm_eps = 0 P={P} N={N} sequences={seqs}")
+    d = inputs([150, 1, 64, 37], P, seqs, N, seed=P + N + 1)
+    g, h, y0 = to_gpu(d), to_gpu(d), before(d)
+    y, z = prompt(g, y0.cuda(), norm_eps=0.0), prompt(h, y0.cuda(), norm_eps=1e-30)
+    torch.cuda.synchronize()
+    compare(d, g, y, y0, norm_eps=0.0)
+    assert torch.equal(y, z) and torch.equal(g["state_cache"], h["state_cache"])
