@@ -960,10 +960,12 @@ int ssm_gate_norm_bwd(int64_t rows, int64_t D, int64_t groups, int dtype, const 
 }
 
 // Sizes that the gated delta rule takes: threads of a launch per chunk of 64 tokens
-// (or request) and 64 rows of a head's state.
-static bool delta_sizes(int64_t seqs, int64_t rows, int64_t H, int64_t P, int64_t G, int64_t N) {
+// (or request) and 64 rows of a head's state; of the prompts' walk, four per row, the
+// groups of all sequences rounded up to whole eights.
+static bool delta_sizes(int64_t seqs, int64_t rows, int64_t H, int64_t P, int64_t G, int64_t N, bool prompt) {
     if (P < 64 || P > 256 || P % 64 != 0 || (N != 64 && N != 128)) return false;
     if (seqs > 65535 || rows > INT32_MAX || H > 65535 || H >= kMaxRow / P || G >= kMaxRow / N) return false;
+    if (prompt && G > 0 && (G * seqs + 7) / 8 * 8 * (H / G) * P * 4 > UINT32_MAX) return false;
     return (rows / 64 + seqs) * (H * P / 64 * 256 + G * 512) <= UINT32_MAX;
 }
 
@@ -975,7 +977,7 @@ static int delta_check(int64_t seqs, int64_t rows, int64_t H, int64_t P, int64_t
                        float *state_cache, void *y, ssm::DeltaArgs *a) {
     if (seqs < 0 || rows < 0 || H < 0 || P < 0 || G < 0 || N < 0 || num_slots < 0) return SSM_ERR_SHAPE;
     if (dtype != SSM_F32 && dtype != SSM_BF16) return SSM_ERR_DTYPE;
-    if ((prompt && dtype != SSM_BF16) || !delta_sizes(seqs, rows, H, P, G, N)) return SSM_ERR_UNSUPPORTED;
+    if ((prompt && dtype != SSM_BF16) || !delta_sizes(seqs, rows, H, P, G, N, prompt)) return SSM_ERR_UNSUPPORTED;
     if (H > 0 && (G < 1 || H % G != 0)) return SSM_ERR_SHAPE;
     if (num_slots > INT32_MAX || q_stride < G * N || k_stride < G * N || v_stride < H * P || dt_stride < H ||
         beta_stride < H)
@@ -1025,7 +1027,7 @@ static int delta_check(int64_t seqs, int64_t rows, int64_t H, int64_t P, int64_t
 size_t ssm_delta_fwd_cache_workspace_bytes(int64_t seqs, int64_t rows, int64_t H, int64_t P, int64_t G, int64_t N,
                                            int dtype) {
     if (dtype != SSM_BF16 || seqs <= 0 || rows < 0 || H <= 0 || G < 1 || H % G != 0 ||
-        !delta_sizes(seqs, rows, H, P, G, N))
+        !delta_sizes(seqs, rows, H, P, G, N, true))
         return 0;
     return ssm::delta_workspace(seqs, rows, H, P, G, N);
 }
