@@ -25,12 +25,12 @@
 // The walk keeps everything that one chunk hands to the next in one wave's registers.
 // A column of S^T (a row p of the state) never meets another, so a wave takes 16 of
 // them and all of N and of the 64 tokens (a call that leaves most of the chip idle so
-// has each 16 or 32 columns shared by N / 32 waves instead: delta_team_kernel). The matrix cores leave a result with
-// its rows in a lane's registers and its columns across 16 lanes, and take their
-// right operand with the summed index in a lane's registers: the result of one
-// product is the next one's right operand as it stands, once its rows are numbered
-// so that the two tiles of 16 rows hold, lane for lane, the eight consecutive indexes
-// of the operand (tile_row). Keys, queries, T, M and the transposed keys are left
+// has each 16 columns shared by N / 32 waves instead: delta_team_kernel). The matrix
+// cores leave a result with its rows in a lane's registers and its columns across 16
+// lanes, and take their right operand with the summed index in a lane's registers: the
+// result of one product is the next one's right operand as it stands, once its rows are
+// numbered so that the two tiles of 16 rows hold, lane for lane, the eight consecutive
+// indexes of the operand (tile_row). Keys, queries, T, M and the transposed keys are left
 // operands, shared by the waves of a workgroup through LDS, laid out there (and by
 // the first kernel in the workspace) as a wave loads them.
 //
@@ -100,6 +100,8 @@ __device__ __forceinline__ void interleave() {
         __builtin_amdgcn_sched_group_barrier(0x2, VALU, 0);
     }
 }
+
+__device__ __forceinline__ uint16_t bf16_bits(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
 
 // Eight bfloat16 as floats.
 __device__ __forceinline__ void ld8(const uint16_t *p, float *v) {
@@ -352,34 +354,30 @@ struct Chunk {
 template <int N, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void delta_walk_kernel(DeltaArgs a) {
     using C = Chunk<N>;
-    constexpr int KB = N / 32, NT = N / 16, CT = 1;  // CT: tiles of 16 columns per wave
+    constexpr int KB = N / 32, NT = N / 16;
     __shared__ __align__(16) char sh[2][C::kPieces][1024];  // this chunk's and the next one's
     // Workgroups go round the eight XCDs: those of a group of heads, which share its keys and
     // queries, are 8 apart, so that they meet in one XCD's cache.
-    const uint32_t H = (uint32_t)a.H, G = (uint32_t)a.G, per = H / G, nb = (uint32_t)a.P / (16 * WAVES * CT);
+    const uint32_t H = (uint32_t)a.H, G = (uint32_t)a.G, per = H / G, nb = (uint32_t)a.P / (16 * WAVES);
     const uint32_t lin = blockIdx.x, one = lin / 8 % (per * nb), unit = lin / 8 / (per * nb) * 8 + lin % 8;
     if (unit >= G * (uint32_t)a.seqs) return;
     const uint32_t s = unit / G, g = unit % G, h = g * per + one / nb, pb = one % nb;
     const int wave = uniform((int)(threadIdx.x >> 6)), lane = threadIdx.x & 63, m = lane & 15, grp = lane >> 4;
     const uint32_t begin = uniform(seq_begin(a, s)), len = uniform(seq_length(a, s, begin));
-    const int64_t pw = (int64_t)(pb * WAVES + wave) * 16 * CT, p0 = pw + CT * m;  // columns p0 .. p0 + CT - 1
+    const int64_t pw = (int64_t)(pb * WAVES + wave) * 16, p0 = pw + m;
     const int64_t y_stride = a.H * a.P;
     uint16_t *yb = (uint16_t *)a.y + (int64_t)begin * y_stride + h * a.P + pw;
     const int32_t slot = uniform(a.ws_slot[s]);
     if (slot < 0) {
-        for (uint32_t t = grp; t < len; t += 4)
-#pragma unroll
-            for (int j = 0; j < CT; ++j) yb[t * y_stride + CT * m + j] = 0;
+        for (uint32_t t = grp; t < len; t += 4) yb[t * y_stride + m] = 0;
         return;
     }
     const bool resume = a.resume && a.resume[s] != 0;
     float *cache = a.state_cache + (((int64_t)slot * H + h) * a.P + p0) * N + 8 * grp;
-    f32x4 S[NT][CT];  // n = tile_row(t, 4 grp + r), column p0 + c
+    f32x4 S[NT];  // n = tile_row(t, 4 grp + r), column p0
 #pragma unroll
     for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int c = 0; c < CT; ++c)
-            S[t][c] = resume ? *(const f32x4 *)(cache + c * N + 32 * (t >> 1) + 4 * (t & 1)) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        S[t] = resume ? *(const f32x4 *)(cache + 32 * (t >> 1) + 4 * (t & 1)) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
     const uint32_t chunks = (len + kQ - 1) / kQ, id0 = begin / kQ + s;
     const uint16_t *qb = (const uint16_t *)a.q + (int64_t)begin * a.q_stride + g * N;
@@ -415,14 +413,14 @@ __global__ __launch_bounds__(64 * WAVES) void delta_walk_kernel(DeltaArgs a) {
             dma16_s(kt + f * 1024, lane * 16, to + (C::kKt + f) * 1024);
         }
     };
-    // The values of chunk c: CT columns of tokens tile_row(tile, 4 grp + r); behind the last
+    // The values of chunk c: column p0, tokens tile_row(tile, 4 grp + r); behind the last
     // token zeros.
     uint32_t v[4][4];
     const uint32_t v_row = (uint32_t)a.v_stride * 2, y_row = (uint32_t)y_stride * 2;
     auto fetch_v = [&](uint32_t c) {
         const uint16_t *base = vb + (int64_t)c * kQ * a.v_stride;
-        const uint32_t left = len - c * kQ, lane_at = 8 * grp * v_row + 2 * CT * m;
-        const auto rows = buffer(base, (left < kQ ? left - 1 : kQ - 1) * v_row + 32 * CT);
+        const uint32_t left = len - c * kQ, lane_at = 8 * grp * v_row + 2 * m;
+        const auto rows = buffer(base, (left < kQ ? left - 1 : kQ - 1) * v_row + 32);
 #pragma unroll
         for (int tile = 0; tile < 4; ++tile)
 #pragma unroll
@@ -439,16 +437,16 @@ __global__ __launch_bounds__(64 * WAVES) void delta_walk_kernel(DeltaArgs a) {
     }
     // y of chunk c, a chunk later: a wait for loads waits for the stores before them too. What
     // lies behind the last token is dropped.
-    uint32_t out[4][4];
+    uint16_t out[4][4];
     auto store_y = [&](uint32_t chunk) {
-        const uint32_t c = uniform((int)chunk), left = len - c * kQ, lane_at = 8 * grp * y_row + 2 * CT * m;
-        const auto rows = buffer(yb + (int64_t)c * kQ * y_stride, (left < kQ ? left - 1 : kQ - 1) * y_row + 32 * CT);
+        const uint32_t c = uniform((int)chunk), left = len - c * kQ, lane_at = 8 * grp * y_row + 2 * m;
+        const auto rows = buffer(yb + (int64_t)c * kQ * y_stride, (left < kQ ? left - 1 : kQ - 1) * y_row + 32);
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const uint32_t at = lane_at + tile_row(t, r) * y_row;
-                __builtin_amdgcn_raw_buffer_store_b16((uint16_t)out[t][r], rows, at, 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b16(out[t][r], rows, at, 0, 0);
             }
     };
     uint32_t c = 0;
@@ -475,21 +473,16 @@ __global__ __launch_bounds__(64 * WAVES) void delta_walk_kernel(DeltaArgs a) {
 
         // K S^T and Q S^T. Operands are read from LDS a group of products ahead, and the
         // next 32 of n are split between the products.
-        f32x4 ks[4][CT], ys[4][CT];
+        f32x4 ks[4], ys[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < 4; ++t) ks[t] = ys[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        auto split_state = [&](int b, bf16x8 (&sp)[3]) {
+            float x[8];
 #pragma unroll
-            for (int j = 0; j < CT; ++j) ks[t][j] = ys[t][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        auto split_state = [&](int b, bf16x8 (&sp)[CT][3]) {
-#pragma unroll
-            for (int j = 0; j < CT; ++j) {
-                float x[8];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = S[2 * b][j][e], x[4 + e] = S[2 * b + 1][j][e];
-                split<3>(x, sp[j]);
-            }
+            for (int e = 0; e < 4; ++e) x[e] = S[2 * b][e], x[4 + e] = S[2 * b + 1][e];
+            split<3>(x, sp);
         };
-        bf16x8 sp[2][CT][3], kf[2], qf[2];
+        bf16x8 sp[2][3], kf[2], qf[2];
         kf[0] = frag(in[C::kK]), qf[0] = frag(in[C::kQ_]);
         split_state(0, sp[0]);
 #pragma unroll
@@ -499,24 +492,22 @@ __global__ __launch_bounds__(64 * WAVES) void delta_walk_kernel(DeltaArgs a) {
                 const int next = 4 * b + t + 1, tn = next & 3, bn = next >> 2;
                 if (next < 4 * KB) kf[next & 1] = frag(in[C::kK + tn * KB + bn]), qf[next & 1] = frag(in[C::kQ_ + tn * KB + bn]);
 #pragma unroll
-                for (int part = 2; part >= 0; --part)
-#pragma unroll
-                    for (int j = 0; j < CT; ++j) {
-                        ks[t][j] = mfma(kf[t & 1], sp[b & 1][j][part], ks[t][j]);
-                        ys[t][j] = mfma(qf[t & 1], sp[b & 1][j][part], ys[t][j]);
-                    }
+                for (int part = 2; part >= 0; --part) {
+                    ks[t] = mfma(kf[t & 1], sp[b & 1][part], ks[t]);
+                    ys[t] = mfma(qf[t & 1], sp[b & 1][part], ys[t]);
+                }
             }
             if (b + 1 < KB) split_state(b + 1, sp[(b + 1) & 1]);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 interleave_reads<2>();
-                interleave<6 * CT, 3>();
+                interleave<6, 3>();
             }
             __builtin_amdgcn_sched_barrier(0);
         }
 
         // beta (V - diag(..) K S^T), in three parts
-        bf16x8 rp[2][CT][3], tf[2][2][3];
+        bf16x8 rp[2][3], tf[2][2][3];
         auto read_t = [&](int i) {  // two tiles
 #pragma unroll
             for (int k = 0; k < 2; ++k)
@@ -527,49 +518,41 @@ __global__ __launch_bounds__(64 * WAVES) void delta_walk_kernel(DeltaArgs a) {
         read_t(0);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            float x[CT][8];
+            float x[8];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int t = 2 * half + k, at = 32 * half + 8 * grp + 4 * k;
                 const f32x4 gk = *(const f32x4 *)(sc + at), be = *(const f32x4 *)(sc + kQ + at), gq = *(const f32x4 *)(sc + 3 * kQ + at);
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-#pragma unroll
-                    for (int j = 0; j < CT; ++j) {
-                        const float val = __uint_as_float(v[t][r] << 16);
-                        x[j][4 * k + r] = be[r] * __builtin_fmaf(-gk[r], ks[t][j][r], val);
-                        ys[t][j][r] *= gq[r];
-                    }
+                for (int r = 0; r < 4; ++r) {
+                    const float val = __uint_as_float(v[t][r] << 16);
+                    x[4 * k + r] = be[r] * __builtin_fmaf(-gk[r], ks[t][r], val);
+                    ys[t][r] *= gq[r];
+                }
             }
-#pragma unroll
-            for (int j = 0; j < CT; ++j) split<3>(x[j], rp[half][j]);
+            split<3>(x, rp[half]);
         }
         if (c + 1 < chunks) fetch_v(c + 1);
         __builtin_amdgcn_sched_barrier(0);
 
         // U = T times that; the first half's parts are formed between the second's products
-        f32x4 u[4][CT];
+        f32x4 u[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int j = 0; j < CT; ++j) u[t][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        bf16x8 um[2][CT][3], us[2][CT][3];  // of U for y, of diag(..) U for the state
+        for (int t = 0; t < 4; ++t) u[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        bf16x8 um[2][3], us[2][3];  // of U for y, of diag(..) U for the state
         auto split_update = [&](int half) {
+            float x[8], w[8];
 #pragma unroll
-            for (int j = 0; j < CT; ++j) {
-                float x[8], w[8];
+            for (int k = 0; k < 2; ++k) {
+                const f32x4 tk = *(const f32x4 *)(sc + 2 * kQ + 32 * half + 8 * grp + 4 * k);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const f32x4 tk = *(const f32x4 *)(sc + 2 * kQ + 32 * half + 8 * grp + 4 * k);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        x[4 * k + r] = u[2 * half + k][j][r];
-                        w[4 * k + r] = x[4 * k + r] * tk[r];
-                    }
+                for (int r = 0; r < 4; ++r) {
+                    x[4 * k + r] = u[2 * half + k][r];
+                    w[4 * k + r] = x[4 * k + r] * tk[r];
                 }
-                split<3>(x, um[half][j]);
-                split<3>(w, us[half][j]);
             }
+            split<3>(x, um[half]);
+            split<3>(w, us[half]);
         };
         float odd = 0.0f;  // NaN where an update is not finite
 #pragma unroll
@@ -579,9 +562,7 @@ __global__ __launch_bounds__(64 * WAVES) void delta_walk_kernel(DeltaArgs a) {
             for (int k = 0; k < 6; ++k)
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int j = 0; j < CT; ++j)
-                        u[kTile[i] + t][j] = mfma(tf[i & 1][t][kTerm[k][0]], rp[i >> 1][j][kTerm[k][1]], u[kTile[i] + t][j]);
+                    u[kTile[i] + t] = mfma(tf[i & 1][t][kTerm[k][0]], rp[i >> 1][kTerm[k][1]], u[kTile[i] + t]);
             if (i == 0) {
                 interleave_reads<6>();
                 __builtin_amdgcn_sched_barrier(0);
@@ -589,14 +570,12 @@ __global__ __launch_bounds__(64 * WAVES) void delta_walk_kernel(DeltaArgs a) {
             }
         }
         interleave_reads<6>();
-        interleave<24 * CT, 5>();
+        interleave<24, 5>();
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int j = 0; j < CT; ++j)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) odd = __builtin_fmaf(u[t][j][r], 0.0f, odd);
+            for (int r = 0; r < 4; ++r) odd = __builtin_fmaf(u[t][r], 0.0f, odd);
         if (uniform(__any(odd != odd))) break;
 
         // M U for y, two tiles at a time, and K^T (diag(..) U) for the state, two of the tiles of n
@@ -622,9 +601,7 @@ __global__ __launch_bounds__(64 * WAVES) void delta_walk_kernel(DeltaArgs a) {
             for (int k = 0; k < 6; ++k)
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int j = 0; j < CT; ++j)
-                        ys[kTile[i] + t][j] = mfma(mf[i & 1][t][kTerm[k][0]], um[i >> 1][j][kTerm[k][1]], ys[kTile[i] + t][j]);
+                    ys[kTile[i] + t] = mfma(mf[i & 1][t][kTerm[k][0]], um[i >> 1][kTerm[k][1]], ys[kTile[i] + t]);
             if (i == 0) {
                 read_m(2);
                 split_update(1);
@@ -633,10 +610,8 @@ __global__ __launch_bounds__(64 * WAVES) void delta_walk_kernel(DeltaArgs a) {
             if (i == 2) read_k(1);
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int j = 0; j < CT; ++j) S[n][j] *= decay;
-        interleave<36 * CT, 4>();
+        for (int n = 0; n < NT; ++n) S[n] *= decay;
+        interleave<36, 4>();
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
@@ -645,17 +620,12 @@ __global__ __launch_bounds__(64 * WAVES) void delta_walk_kernel(DeltaArgs a) {
 #pragma unroll
             for (int part = 2; part >= 0; --part)
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
-#pragma unroll
-                    for (int j = 0; j < CT; ++j) S[n + k][j] = mfma(tk[i % 3][k], us[half][j][part], S[n + k][j]);
+                for (int k = 0; k < 2; ++k) S[n + k] = mfma(tk[i % 3][k], us[half][part], S[n + k]);
         }
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                float lo = ys[t][0][r], hi = ys[t][CT - 1][r];
-                out[t][r] = bf16_pair(lo, hi);
-            }
+            for (int r = 0; r < 4; ++r) out[t][r] = bf16_bits(ys[t][r]);
     }
     if (c > 0) store_y(c - 1);
     // What an update that is not finite leaves, a token at a time; the other waves go on, so
@@ -668,7 +638,7 @@ __global__ __launch_bounds__(64 * WAVES) void delta_walk_kernel(DeltaArgs a) {
             const float dt = softplus(ld_act((const uint16_t *)a.dt_raw, row * a.dt_stride + h) + (a.dt_bias ? a.dt_bias[h] : 0.0f));
             const float beta = delta_gate(ld_act((const uint16_t *)a.beta_raw, row * a.beta_stride + h));
             const float one = fast_exp2(dt * a.A[h] * kLog2e);
-            float kv[KB][8], qv[KB][8], kk = 0.0f, qq = 0.0f, sk[CT], sq[CT];
+            float kv[KB][8], qv[KB][8], kk = 0.0f, qq = 0.0f, sk = 0.0f, sq = 0.0f;
 #pragma unroll
             for (int b = 0; b < KB; ++b) {
                 ld8(kb + t * a.k_stride + 32 * b + 8 * grp, kv[b]);
@@ -681,26 +651,22 @@ __global__ __launch_bounds__(64 * WAVES) void delta_walk_kernel(DeltaArgs a) {
             }
             const float rk = unit_scale(sum_groups(kk), a.norm_eps), rq = unit_scale(sum_groups(qq), a.norm_eps) * a.scale;
 #pragma unroll
-            for (int j = 0; j < CT; ++j) {
-                sk[j] = sq[j] = 0.0f;
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int r = 0; r < 4; ++r) {
+                    S[n][r] *= one;
+                    sk = __builtin_fmaf(S[n][r], kv[n >> 1][4 * (n & 1) + r], sk);
+                }
+            const float up = beta * __builtin_fmaf(-rk, sum_groups(sk), ld_act(vb + m, t * a.v_stride)) * rk;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        S[n][j][r] *= one;
-                        sk[j] = __builtin_fmaf(S[n][j][r], kv[n >> 1][4 * (n & 1) + r], sk[j]);
-                    }
-                const float up = beta * __builtin_fmaf(-rk, sum_groups(sk[j]), ld_act(vb + CT * m + j, t * a.v_stride)) * rk;
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        S[n][j][r] = __builtin_fmaf(up, kv[n >> 1][4 * (n & 1) + r], S[n][j][r]);
-                        sq[j] = __builtin_fmaf(S[n][j][r], qv[n >> 1][4 * (n & 1) + r], sq[j]);
-                    }
-                const float out = sum_groups(sq[j]) * rq;
-                if (grp == 0) st_act(yb + CT * m + j, t * y_stride, out);
-            }
+                for (int r = 0; r < 4; ++r) {
+                    S[n][r] = __builtin_fmaf(up, kv[n >> 1][4 * (n & 1) + r], S[n][r]);
+                    sq = __builtin_fmaf(S[n][r], qv[n >> 1][4 * (n & 1) + r], sq);
+                }
+            const float out = sum_groups(sq) * rq;
+            if (grp == 0) st_act(yb + m, t * y_stride, out);
         }
         if (c + 1 >= chunks) break;
         vm_wait();
@@ -710,56 +676,51 @@ __global__ __launch_bounds__(64 * WAVES) void delta_walk_kernel(DeltaArgs a) {
     if (len > 0 || !resume)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int j = 0; j < CT; ++j) *(f32x4 *)(cache + j * N + 32 * (t >> 1) + 4 * (t & 1)) = S[t][j];
+            *(f32x4 *)(cache + 32 * (t >> 1) + 4 * (t & 1)) = S[t];
 }
 
 // ---------------------------------------------------------- walk, shared by waves
 
 // LDS of a workgroup, in pieces of 1 KiB (16 bytes per lane): what the waves hand each other.
-template <int N, int CT>
+template <int N>
 struct TeamShared {
     static constexpr int NW = N / 32;  // waves: 32 of n each
     union {
-        alignas(16) char part[2][4][NW - 1][CT][1024];  // of K S^T and Q S^T: (tile of tokens, from another wave)
-        float sums[2][NW][16 * CT];                     // where a chunk is taken a token at a time
+        alignas(16) char part[2][4][NW - 1][1024];  // of K S^T and Q S^T: (tile of tokens, from another wave)
+        float sums[2][NW][16];                      // where a chunk is taken a token at a time
     };
-    alignas(16) char r[2][CT][3][1024];             // beta (V - ..), as right operands
-    alignas(16) char us[2][CT][3][1024], um[2][CT][3][1024];  // diag(..) U and U, as right operands
+    alignas(16) char r[2][3][1024];                   // beta (V - ..), as right operands
+    alignas(16) char us[2][3][1024], um[2][3][1024];  // diag(..) U and U, as right operands
 };
 
-// One head of one sequence, CT x 16 columns p of it, by N / 32 waves: wave w holds the
+// One head of one sequence, 16 columns p of it, by N / 32 waves: wave w holds the
 // columns' elements n = 32 w .. 32 w + 31, and takes TW of the chunk's four tiles of tokens.
-template <int N, int CT>
-__global__ __launch_bounds__(2 * N, N == 128 && CT == 1 ? 2 : 1) void delta_team_kernel(DeltaArgs a) {
+template <int N>
+__global__ __launch_bounds__(2 * N, N == 128 ? 2 : 1) void delta_team_kernel(DeltaArgs a) {
     constexpr int NW = N / 32, TW = 4 / NW, KB = N / 32;
-    __shared__ TeamShared<N, CT> sh;
+    __shared__ TeamShared<N> sh;
     // Workgroups go round the eight XCDs: those of a group of heads, which share its keys and
     // queries, are 8 apart, so that they meet in one XCD's cache.
-    const uint32_t H = (uint32_t)a.H, G = (uint32_t)a.G, per = H / G, nb = (uint32_t)a.P / (16 * CT);
+    const uint32_t H = (uint32_t)a.H, G = (uint32_t)a.G, per = H / G, nb = (uint32_t)a.P / 16;
     const uint32_t lin = blockIdx.x, one = lin / 8 % (per * nb), unit = lin / 8 / (per * nb) * 8 + lin % 8;
     if (unit >= G * (uint32_t)a.seqs) return;
     const uint32_t s = unit / G, g = unit % G, h = g * per + one / nb, pb = one % nb;
     const int wave = uniform((int)(threadIdx.x >> 6)), lane = threadIdx.x & 63, m = lane & 15, grp = lane >> 4;
     const uint32_t begin = uniform(seq_begin(a, s)), len = uniform(seq_length(a, s, begin));
-    const int64_t pw = (int64_t)pb * 16 * CT, p0 = pw + CT * m;  // columns p0 .. p0 + CT - 1
+    const int64_t pw = (int64_t)pb * 16, p0 = pw + m;
     const int64_t y_stride = a.H * a.P;
     uint16_t *yb = (uint16_t *)a.y + (int64_t)begin * y_stride + h * a.P + pw;
     const int32_t slot = uniform(a.ws_slot[s]);
     if (slot < 0) {
-        for (uint32_t t = 4 * wave + grp; t < len; t += 4 * NW)
-#pragma unroll
-            for (int j = 0; j < CT; ++j) yb[t * y_stride + CT * m + j] = 0;
+        for (uint32_t t = 4 * wave + grp; t < len; t += 4 * NW) yb[t * y_stride + m] = 0;
         return;
     }
     const bool resume = a.resume && a.resume[s] != 0;
     float *cache = a.state_cache + (((int64_t)slot * H + h) * a.P + p0) * N + 32 * wave + 8 * grp;
-    f32x4 S[2][CT];  // n = 32 wave + 8 grp + 4 k + r, column p0 + j
+    f32x4 S[2];  // n = 32 wave + 8 grp + 4 k + r, column p0
 #pragma unroll
     for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int j = 0; j < CT; ++j)
-            S[k][j] = resume ? *(const f32x4 *)(cache + j * N + 4 * k) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        S[k] = resume ? *(const f32x4 *)(cache + 4 * k) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
     const uint32_t chunks = (len + kQ - 1) / kQ, id0 = begin / kQ + s;
     const uint16_t *qb = (const uint16_t *)a.q + (int64_t)begin * a.q_stride + g * N;
@@ -788,8 +749,8 @@ __global__ __launch_bounds__(2 * N, N == 128 && CT == 1 ? 2 : 1) void delta_team
     };
     auto head = [&](uint32_t c) { return (const char *)a.ws_tm + ((int64_t)(id0 + c) * H + h) * kHeadPieces * 1024; };
     auto load_v = [&](uint32_t c) {
-        const uint32_t left = len - c * kQ, lane_at = 8 * grp * v_row + 2 * CT * m;
-        const auto rows = buffer(vb + (int64_t)c * kQ * a.v_stride, (left < kQ ? left - 1 : kQ - 1) * v_row + 32 * CT);
+        const uint32_t left = len - c * kQ, lane_at = 8 * grp * v_row + 2 * m;
+        const auto rows = buffer(vb + (int64_t)c * kQ * a.v_stride, (left < kQ ? left - 1 : kQ - 1) * v_row + 32);
         const float *f = (const float *)(head(c) + kFactors * 1024) + 8 * grp;
 #pragma unroll
         for (int i = 0; i < TW; ++i) {
@@ -799,8 +760,7 @@ __global__ __launch_bounds__(2 * N, N == 128 && CT == 1 ? 2 : 1) void delta_team
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const uint32_t o = lane_at + (at + r) * v_row;
-                if constexpr (CT == 2) v[i][r] = __builtin_amdgcn_raw_buffer_load_b32(rows, o, 0, 0);
-                else v[i][r] = __builtin_amdgcn_raw_buffer_load_b16(rows, o, 0, 0);
+                v[i][r] = __builtin_amdgcn_raw_buffer_load_b16(rows, o, 0, 0);
             }
         }
         decay = *(cf32_ptr)(a.ws_decay + uniform64((int64_t)(id0 + c) * H + h));
@@ -838,74 +798,65 @@ __global__ __launch_bounds__(2 * N, N == 128 && CT == 1 ? 2 : 1) void delta_team
         load_t(0);
         load_m(0);
     }
+    // The state's loads are waited for here: the compiler may else wait for them at the head
+    // of the loop, and for the next chunk's in every round of it (16384 tokens: 727 us, and 843 without this).
+    asm volatile("" : "+v"(S[0]), "+v"(S[1]));
     for (uint32_t c = 0; c < chunks; ++c) {
         const uint32_t next = c + 1 < chunks ? c + 1 : c, left = len - c * kQ;
         // K S^T and Q S^T over the wave's n, for all tokens
-        f32x4 ks[4][CT], ys[4][CT];
+        f32x4 ks[4], ys[4];
         {
-            bf16x8 sp[CT][3];
+            bf16x8 sp[3];
+            float x[8];
 #pragma unroll
-            for (int j = 0; j < CT; ++j) {
-                float x[8];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = S[0][j][e], x[4 + e] = S[1][j][e];
-                split<3>(x, sp[j]);
-            }
+            for (int e = 0; e < 4; ++e) x[e] = S[0][e], x[4 + e] = S[1][e];
+            split<3>(x, sp);
             const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int part = 2; part >= 0; --part)
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
-#pragma unroll
-                    for (int j = 0; j < CT; ++j) ks[t][j] = mfma(kf[t], sp[j][part], part == 2 ? zero : ks[t][j]);
+                for (int t = 0; t < 4; ++t) ks[t] = mfma(kf[t], sp[part], part == 2 ? zero : ks[t]);
 #pragma unroll
             for (int t = 0; t < 4; ++t)
                 if (t / TW != wave)
-#pragma unroll
-                    for (int j = 0; j < CT; ++j) *(f32x4 *)(sh.part[0][t][slot_of(t, wave)][j] + lane * 16) = ks[t][j];
+                    *(f32x4 *)(sh.part[0][t][slot_of(t, wave)] + lane * 16) = ks[t];
 #pragma unroll
             for (int part = 2; part >= 0; --part)
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
-#pragma unroll
-                    for (int j = 0; j < CT; ++j) ys[t][j] = mfma(qf[t], sp[j][part], part == 2 ? zero : ys[t][j]);
+                for (int t = 0; t < 4; ++t) ys[t] = mfma(qf[t], sp[part], part == 2 ? zero : ys[t]);
 #pragma unroll
             for (int t = 0; t < 4; ++t)
                 if (t / TW != wave)
-#pragma unroll
-                    for (int j = 0; j < CT; ++j) *(f32x4 *)(sh.part[1][t][slot_of(t, wave)][j] + lane * 16) = ys[t][j];
+                    *(f32x4 *)(sh.part[1][t][slot_of(t, wave)] + lane * 16) = ys[t];
         }
         load_kq(next);
         lds_barrier();
         // the waves' sums of the wave's tokens, and beta (V - diag(..) K S^T) in three parts
-        f32x4 out[TW][CT];
+        f32x4 out[TW];
 #pragma unroll
         for (int i = 0; i < TW; ++i) {
             const int t = wave * TW + i;
+            f32x4 sum = ks[0], rest = ys[0];
 #pragma unroll
-            for (int j = 0; j < CT; ++j) {
-                f32x4 sum = ks[0][j], rest = ys[0][j];
+            for (int k = 1; k < 4; ++k) sum = t == k ? ks[k] : sum, rest = t == k ? ys[k] : rest;
 #pragma unroll
-                for (int k = 1; k < 4; ++k) sum = t == k ? ks[k][j] : sum, rest = t == k ? ys[k][j] : rest;
+            for (int w = 0; w < NW - 1; ++w) {
+                sum += *(const f32x4 *)(sh.part[0][t][w] + lane * 16);
+                rest += *(const f32x4 *)(sh.part[1][t][w] + lane * 16);
+            }
+            out[i] = rest * fq[i];
+            float x[4];
 #pragma unroll
-                for (int w = 0; w < NW - 1; ++w) {
-                    sum += *(const f32x4 *)(sh.part[0][t][w][j] + lane * 16);
-                    rest += *(const f32x4 *)(sh.part[1][t][w][j] + lane * 16);
-                }
-                out[i][j] = rest * fq[i];
-                float x[4];
+            for (int r = 0; r < 4; ++r) {
+                const float val = __uint_as_float(v[i][r] << 16);
+                x[r] = fb[i][r] * __builtin_fmaf(-fk[i][r], sum[r], val);
+            }
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float val = __uint_as_float(j ? v[i][r] & 0xffff0000u : v[i][r] << 16);
-                    x[r] = fb[i][r] * __builtin_fmaf(-fk[i][r], sum[r], val);
-                }
-#pragma unroll
-                for (int part = 0; part < 3; ++part) {
-                    uint2 u;
-                    u.x = bf16_pair(x[0], x[1]);
-                    u.y = bf16_pair(x[2], x[3]);
-                    *(uint2 *)(sh.r[t >> 1][j][part] + lane * 16 + 8 * (t & 1)) = u;
-                }
+            for (int part = 0; part < 3; ++part) {
+                uint2 u;
+                u.x = bf16_pair(x[0], x[1]);
+                u.y = bf16_pair(x[2], x[3]);
+                *(uint2 *)(sh.r[t >> 1][part] + lane * 16 + 8 * (t & 1)) = u;
             }
         }
         lds_barrier();
@@ -913,60 +864,53 @@ __global__ __launch_bounds__(2 * N, N == 128 && CT == 1 ? 2 : 1) void delta_team
 #pragma unroll
         for (int i = 0; i < TW; ++i) {
             const int t = wave * TW + i;
+            f32x4 u[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
 #pragma unroll
-            for (int j = 0; j < CT; ++j) {
-                f32x4 u[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+            for (int half = 0; half < 2; ++half)
+                if (half == 0 || t >= 2) {
+                    bf16x8 rp[3];
 #pragma unroll
-                for (int half = 0; half < 2; ++half)
-                    if (half == 0 || t >= 2) {
-                        bf16x8 rp[3];
+                    for (int part = 0; part < 3; ++part) rp[part] = frag(sh.r[half][part]);
 #pragma unroll
-                        for (int part = 0; part < 3; ++part) rp[part] = frag(sh.r[half][j][part]);
-#pragma unroll
-                        for (int k = 0; k < 6; ++k) u[half] = mfma(tf[i][half][kTerm[k][0]], rp[kTerm[k][1]], u[half]);
-                    }
-                float x[4], w[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    x[r] = u[0][r] + u[1][r];
-                    w[r] = x[r] * fd[i][r];
+                    for (int k = 0; k < 6; ++k) u[half] = mfma(tf[i][half][kTerm[k][0]], rp[kTerm[k][1]], u[half]);
                 }
+            float x[4], w[4];
 #pragma unroll
-                for (int part = 0; part < 3; ++part) {
-                    uint2 o;
-                    o.x = bf16_pair(w[0], w[1]);
-                    o.y = bf16_pair(w[2], w[3]);
-                    *(uint2 *)(sh.us[t >> 1][j][part] + lane * 16 + 8 * (t & 1)) = o;
-                }
+            for (int r = 0; r < 4; ++r) {
+                x[r] = u[0][r] + u[1][r];
+                w[r] = x[r] * fd[i][r];
+            }
 #pragma unroll
-                for (int part = 0; part < 3; ++part) {
-                    uint2 o;
-                    o.x = bf16_pair(x[0], x[1]);
-                    o.y = bf16_pair(x[2], x[3]);
-                    *(uint2 *)(sh.um[t >> 1][j][part] + lane * 16 + 8 * (t & 1)) = o;
-                }
+            for (int part = 0; part < 3; ++part) {
+                uint2 o;
+                o.x = bf16_pair(w[0], w[1]);
+                o.y = bf16_pair(w[2], w[3]);
+                *(uint2 *)(sh.us[t >> 1][part] + lane * 16 + 8 * (t & 1)) = o;
+            }
+#pragma unroll
+            for (int part = 0; part < 3; ++part) {
+                uint2 o;
+                o.x = bf16_pair(x[0], x[1]);
+                o.y = bf16_pair(x[2], x[3]);
+                *(uint2 *)(sh.um[t >> 1][part] + lane * 16 + 8 * (t & 1)) = o;
             }
         }
         load_t(next);
         lds_barrier();
         // All waves read all of diag(..) U, and so agree where an update is not finite.
-        bf16x8 up[CT][2][3];
+        bf16x8 up[2][3];
         float odd = 0.0f;
 #pragma unroll
-        for (int j = 0; j < CT; ++j)
+        for (int half = 0; half < 2; ++half)
 #pragma unroll
-            for (int half = 0; half < 2; ++half)
+            for (int part = 0; part < 3; ++part) up[half][part] = frag(sh.us[half][part]);
 #pragma unroll
-                for (int part = 0; part < 3; ++part) up[j][half][part] = frag(sh.us[half][j][part]);
+        for (int half = 0; half < 2; ++half)
 #pragma unroll
-        for (int j = 0; j < CT; ++j)
-#pragma unroll
-            for (int half = 0; half < 2; ++half)
-#pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    const bf16x2 two = {up[j][half][0][e], up[j][half][0][e + 1]};
-                    odd = __builtin_amdgcn_fdot2_f32_bf16(two, bf16x2{(__bf16)0.0f, (__bf16)0.0f}, odd, false);
-                }
+            for (int e = 0; e < 8; e += 2) {
+                const bf16x2 two = {up[half][0][e], up[half][0][e + 1]};
+                odd = __builtin_amdgcn_fdot2_f32_bf16(two, bf16x2{(__bf16)0.0f, (__bf16)0.0f}, odd, false);
+            }
         if (uniform(__any(odd != odd))) {
             // a token at a time; the barriers pass each token's sums over n from wave to wave
             const int rem = left < kQ ? (int)left : kQ;
@@ -987,82 +931,65 @@ __global__ __launch_bounds__(2 * N, N == 128 && CT == 1 ? 2 : 1) void delta_team
                     }
                 }
                 const float rk = unit_scale(sum_groups(kk), a.norm_eps), rq = unit_scale(sum_groups(qq), a.norm_eps) * a.scale;
+                float sk = 0.0f;
 #pragma unroll
-                for (int j = 0; j < CT; ++j) {
-                    float sk = 0.0f;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        S[e >> 2][j][e & 3] *= keep;
-                        sk = __builtin_fmaf(S[e >> 2][j][e & 3], kv[e], sk);
-                    }
-                    sh.sums[0][wave][CT * m + j] = sum_groups(sk);
+                for (int e = 0; e < 8; ++e) {
+                    S[e >> 2][e & 3] *= keep;
+                    sk = __builtin_fmaf(S[e >> 2][e & 3], kv[e], sk);
                 }
+                sh.sums[0][wave][m] = sum_groups(sk);
                 __syncthreads();
+                float all = 0.0f, sq = 0.0f;
 #pragma unroll
-                for (int j = 0; j < CT; ++j) {
-                    float sk = 0.0f, sq = 0.0f;
+                for (int w = 0; w < NW; ++w) all += sh.sums[0][w][m];
+                const float up = beta * __builtin_fmaf(-rk, all, ld_act(vb + m, t * a.v_stride)) * rk;
 #pragma unroll
-                    for (int w = 0; w < NW; ++w) sk += sh.sums[0][w][CT * m + j];
-                    const float up = beta * __builtin_fmaf(-rk, sk, ld_act(vb + CT * m + j, t * a.v_stride)) * rk;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        S[e >> 2][j][e & 3] = __builtin_fmaf(up, kv[e], S[e >> 2][j][e & 3]);
-                        sq = __builtin_fmaf(S[e >> 2][j][e & 3], qv[e], sq);
-                    }
-                    sh.sums[1][wave][CT * m + j] = sum_groups(sq);
+                for (int e = 0; e < 8; ++e) {
+                    S[e >> 2][e & 3] = __builtin_fmaf(up, kv[e], S[e >> 2][e & 3]);
+                    sq = __builtin_fmaf(S[e >> 2][e & 3], qv[e], sq);
                 }
+                sh.sums[1][wave][m] = sum_groups(sq);
                 __syncthreads();
-                if (wave == 0 && grp == 0)
+                if (wave == 0 && grp == 0) {
+                    float out = 0.0f;
 #pragma unroll
-                    for (int j = 0; j < CT; ++j) {
-                        float sq = 0.0f;
-#pragma unroll
-                        for (int w = 0; w < NW; ++w) sq += sh.sums[1][w][CT * m + j];
-                        st_act(yb + CT * m + j, t * y_stride, sq * rq);
-                    }
+                    for (int w = 0; w < NW; ++w) out += sh.sums[1][w][m];
+                    st_act(yb + m, t * y_stride, out * rq);
+                }
             }
             __syncthreads();  // the next chunk's partial sums lie where the last token's were read
         } else {
         // S^T <- decay S^T + K^T (diag(..) U) over the wave's n
+        f32x4 more[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
 #pragma unroll
-        for (int j = 0; j < CT; ++j) {
-            f32x4 more[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+        for (int part = 2; part >= 0; --part)
 #pragma unroll
-            for (int part = 2; part >= 0; --part)
+            for (int half = 0; half < 2; ++half)
 #pragma unroll
-                for (int half = 0; half < 2; ++half)
+                for (int k = 0; k < 2; ++k) more[k] = mfma(tk[k][half], up[half][part], more[k]);
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) more[k] = mfma(tk[k][half], up[j][half][part], more[k]);
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) S[k][j][r] = __builtin_fmaf(S[k][j][r], decay, more[k][r]);
-        }
+            for (int r = 0; r < 4; ++r) S[k][r] = __builtin_fmaf(S[k][r], decay, more[k][r]);
         // y = diag(..) Q S^T + M U of the wave's tokens; what lies behind the last is dropped
-        const uint32_t y_lane = 8 * grp * y_row + 2 * CT * m;
-        const auto rows = buffer(yb + (int64_t)c * kQ * y_stride, (left < kQ ? left - 1 : kQ - 1) * y_row + 32 * CT);
+        const uint32_t y_lane = 8 * grp * y_row + 2 * m;
+        const auto rows = buffer(yb + (int64_t)c * kQ * y_stride, (left < kQ ? left - 1 : kQ - 1) * y_row + 32);
 #pragma unroll
         for (int i = 0; i < TW; ++i) {
             const int t = wave * TW + i;
 #pragma unroll
-            for (int j = 0; j < CT; ++j) {
+            for (int half = 0; half < 2; ++half)
+                if (half == 0 || t >= 2) {
+                    bf16x8 uf[3];
 #pragma unroll
-                for (int half = 0; half < 2; ++half)
-                    if (half == 0 || t >= 2) {
-                        bf16x8 uf[3];
+                    for (int part = 0; part < 3; ++part) uf[part] = frag(sh.um[half][part]);
 #pragma unroll
-                        for (int part = 0; part < 3; ++part) uf[part] = frag(sh.um[half][j][part]);
-#pragma unroll
-                        for (int k = 0; k < 6; ++k) out[i][j] = mfma(mf[i][half][kTerm[k][0]], uf[kTerm[k][1]], out[i][j]);
-                    }
-            }
+                    for (int k = 0; k < 6; ++k) out[i] = mfma(mf[i][half][kTerm[k][0]], uf[kTerm[k][1]], out[i]);
+                }
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const uint32_t at = y_lane + (32 * (t >> 1) + 4 * (t & 1) + r) * y_row;
-                float lo = out[i][0][r], hi = out[i][CT - 1][r];
-                const uint32_t two = bf16_pair(lo, hi);
-                if constexpr (CT == 2) __builtin_amdgcn_raw_buffer_store_b32(two, rows, at, 0, 0);
-                else __builtin_amdgcn_raw_buffer_store_b16((uint16_t)two, rows, at, 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b16(bf16_bits(out[i][r]), rows, at, 0, 0);
             }
         }
         }
@@ -1072,14 +999,13 @@ __global__ __launch_bounds__(2 * N, N == 128 && CT == 1 ? 2 : 1) void delta_team
     if (len > 0 || !resume)
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int j = 0; j < CT; ++j) *(f32x4 *)(cache + j * N + 4 * k) = S[k][j];
+            *(f32x4 *)(cache + 4 * k) = S[k];
 }
 
-template <int N, int CT>
+template <int N>
 hipError_t team(const DeltaArgs &a, hipStream_t s) {
-    const int64_t blocks = (a.G * a.seqs + 7) / 8 * 8 * (a.H / a.G) * (a.P / (16 * CT));
-    hipLaunchKernelGGL((delta_team_kernel<N, CT>), dim3((unsigned)blocks), dim3(2 * N), 0, s, a);
+    const int64_t blocks = (a.G * a.seqs + 7) / 8 * 8 * (a.H / a.G) * (a.P / 16);
+    hipLaunchKernelGGL((delta_team_kernel<N>), dim3((unsigned)blocks), dim3(2 * N), 0, s, a);
     return hipGetLastError();
 }
 
@@ -1098,15 +1024,19 @@ hipError_t delta(const DeltaArgs &a, hipStream_t s) {
     hipLaunchKernelGGL((delta_prepare_kernel<N>), dim3((unsigned)blocks), dim3(kPrepThreads), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    // A wave of the walk keeps all of N and takes 4.6 us a chunk (N = 128, 5.5 with two on a
-    // SIMD, 7.1 with the chip full), a team of waves 2.7 us for 16 columns and 4.4 for 32. So
-    // the walk is for a chip that it fills, in workgroups of 128 columns (or 64). Whole calls
-    // (us) at 32 heads of 128 x 128, walk / team of 32 / of 16 columns: 8 x 4096 tokens 810 /
-    // 1020 / 1290, 6 x 4096 595 / 773 / 984, 4 x 8192 997 / 927 / 1311, 2 x 8192 873 / 653 /
-    // 684, 1 x 16384 1576 / 1134 / 809.
-    const int64_t filled = a.H * a.seqs * a.P / (a.P % 128 == 0 ? 128 : 64);
-    if (filled >= 160) return a.P % 128 == 0 ? walk<N, 8>(a, s) : walk<N, 4>(a, s);
-    return filled >= 64 ? team<N, 2>(a, s) : team<N, 1>(a, s);
+    // A wave of the walk keeps all of N and fills the chip with less work in all; a team of
+    // waves takes a chunk of 16 columns in less time. Teams are for calls whose workgroups all
+    // run at once: two on each of 256 CUs. Whole calls (us), walk / team, by teams:
+    //   N = 128   256: 397 / 243    384: 372 / 307, 447 / 407    512: 1054 / 720, 460 / 320, 498 / 456
+    //             576: 422 / 496    640: 525 / 626    768: 1127 / 1098, 527 / 515    1024: 1196 / 1388, 557 / 649
+    //   N = 64    256: 297 / 255    384: 285 / 247, 343 / 322    512: 823 / 616, 360 / 250, 387 / 372
+    //             576: 305 / 449    768: 881 / 1011, 389 / 459    1024: 940 / 1095, 429 / 510
+    //   2048 (8 prompts of 4096 tokens)  829 / 1369, N = 64: 640 / 1103    48 prompts of 64 tokens  119 / 219
+    // That is for equal lengths. The host does not know them: a call with one long sequence among
+    // short ones pays the walk's longer chain (13 ragged prompts 168 / 140 us, 16384 tokens beside
+    // forty prompts of one token 1962 / 927).
+    if (a.H * a.seqs * a.P / 16 <= 512) return team<N>(a, s);
+    return a.P % 128 == 0 ? walk<N, 8>(a, s) : walk<N, 4>(a, s);
 }
 
 }  // namespace

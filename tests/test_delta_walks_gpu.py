@@ -1,9 +1,8 @@
 """The gated delta rule over packed prompts by every kernel that a call may be given:
-teams of waves on 16 or 32 columns of a state, and workgroups of four or eight waves of
-16 columns each, for states of 64 and of 128 elements per column (needs MI355X). Which
-one a call takes goes by its heads, columns and sequences: WAYS reaches each with few
-heads and many sequences, nearly all of them empty. Error bounds as in
-test_delta_cache_gpu.py.
+teams of waves on 16 columns of a state, and workgroups of four or eight waves of 16
+columns each, for states of 64 and of 128 elements per column (needs MI355X). Which one
+a call takes goes by its heads, columns and sequences: WAYS reaches each with few heads
+and many sequences, nearly all of them empty. Error bounds as in test_delta_cache_gpu.py.
 """
 import pytest
 import torch
@@ -15,8 +14,8 @@ from test_delta_cache_gpu import C, before, prompt
 
 pytestmark = pytest.mark.gpu
 H, G = 2, 1
-# (columns P, sequences): team of 16 columns, team of 32, walk of four waves, walk of eight
-WAYS = [(64, 8), (64, 40), (64, 90), (128, 90)]
+# (columns P, sequences): teams, walk of four waves, the same with three workgroups a head, walk of eight
+WAYS = [(64, 8), (64, 90), (192, 40), (128, 90)]
 ALL = [(P, seqs, N) for P, seqs in WAYS for N in (64, 128)]
 
 
