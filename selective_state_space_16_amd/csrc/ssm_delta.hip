@@ -77,9 +77,6 @@ __device__ __forceinline__ int tri_index(int tile, int half) { return tile < 2 ?
 // 32 indexes, of which lane group m / 4 holds eight consecutive ones.
 __device__ __forceinline__ int tile_row(int t, int m) { return 32 * (t >> 1) + 8 * (m >> 2) + 4 * (t & 1) + (m & 3); }
 
-// The product of two operands of three parts each, as six, the small ones first.
-constexpr int kTerm[6][2] = {{2, 0}, {0, 2}, {1, 1}, {1, 0}, {0, 1}, {0, 0}};
-
 __device__ __forceinline__ f32x4 mfma_f32(float a, float b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
 
 // The first of the two tiles that the three groups of products with T and M take; the

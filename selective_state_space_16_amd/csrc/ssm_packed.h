@@ -35,6 +35,10 @@ __device__ __forceinline__ void split(float (&v)[8], bf16x8 (&out)[PARTS]) {
         out[p] = __builtin_bit_cast(bf16x8, u);
     }
 }
+// The product of two operands of three parts each, as six, the small ones first;
+// the last three are that of two parts each.
+constexpr int kTerm[6][2] = {{2, 0}, {0, 2}, {1, 1}, {1, 0}, {0, 1}, {0, 0}};
+constexpr int kTwo = 3;
 // Buffer accesses: bytes from a wave-uniform base, a range that the hardware
 // checks (loads outside it give 0, stores outside it are dropped).
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *base, uint32_t bytes) {

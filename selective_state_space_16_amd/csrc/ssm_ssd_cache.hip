@@ -71,10 +71,6 @@ constexpr int kHead = 4 * kQ;
 constexpr int kDtHeads = 5;
 constexpr int dt_heads(int N) { return prep_threads(N) / 64 * kDtHeads; }
 
-// The product of two operands of three parts each, as six, the small ones first;
-// the last three are that of two parts each.
-constexpr int kTerm[6][2] = {{2, 0}, {0, 2}, {1, 1}, {1, 0}, {0, 1}, {0, 0}};
-constexpr int kTwo = 3;
 // Tokens per segment.
 __device__ __forceinline__ uint32_t segment(const SsdCacheArgs &a) {
     return a.ws_plan ? (uint32_t)uniform(a.ws_plan[0]) : (uint32_t)a.seg;
