@@ -1091,7 +1091,8 @@ def ssm_delta_fwd_cache(q, k, v, dt_raw, beta_raw, A, cu_seqlens, slots, state_c
     N) float32, updated in place; y (rows, H, P). Queries and keys are divided by
     their length, sqrt(sum of squares + norm_eps), unless norm_eps < 0; queries are
     multiplied by `scale` (N ** -0.5 if None). A y that the call allocates is zero in
-    rows outside every sequence; a given one keeps them. A workspace for the largest
+    rows outside every sequence; a given one keeps them. A workspace (37 KiB per head
+    and N / 8 KiB per group for every 64 tokens, and for every sequence) for the largest
     batch serves smaller ones. Equal calls give equal bits."""
     return _delta_cache("ssm_delta_fwd_cache", q, k, v, dt_raw, beta_raw, A, cu_seqlens, slots, state_cache, dt_bias,
                         resume, scale, norm_eps, y, workspace, stream)

@@ -216,7 +216,9 @@ hipError_t launch_conv_cache(const ConvCacheArgs &a, bool prompt, int dtype, hip
         else hipLaunchKernelGGL((conv_step_kernel<1>), grid, dim3(kThreads), 0, s, a);
         return hipGetLastError();
     }
-    // 16 bytes per access where every row is whole pieces of them
+    // 16 bytes per access where every row is whole pieces of them, else one element. 32768
+    // tokens, us: bfloat16, 8192 channels 225 (rows 8256 apart 246), by one element 261 (rows
+    // 8193 apart) and 302 (8191 channels); float32, 4096 channels 221, 4097 by one element 293.
     if (dtype == 0) return a.C % 4 == 0 && a.x_stride % 4 == 0 ? conv_prompt<0, 4>(a, s) : conv_prompt<0, 1>(a, s);
     return a.C % 8 == 0 && a.x_stride % 8 == 0 ? conv_prompt<1, 8>(a, s) : conv_prompt<1, 1>(a, s);
 }

@@ -44,14 +44,18 @@
 //
 // Where an update is not finite, because an input is not, zeros of T and M no longer
 // keep a token from those before it: such a chunk is taken a token at a time instead,
-// from the state that entered it.
+// from the state that entered it. A state that is not finite stays so, and with it the
+// sequence's later chunks are taken so too: 0.9 us a token in the walk, where the whole
+// workgroup waits for one wave's column, 1.8 us in a team (eight prompts of 4096 tokens
+// with a NaN in the middle of the first 0.85 -> 2.7 ms, one of 16384 tokens 0.86 -> 15.5).
 //
-// Measured (us): 16384 tokens of 32 heads of 128 x 128, 135 ahead of the chunks and 680
-// for them (2.65 a chunk); eight prompts of 4096 tokens, 260 and 525; one chunk of 24
-// heads 9.5 and 7. The first kernel is bound by the latency of T's chain (four workgroups
-// of 36 KB a CU; three of 53 KB took 165 and 300), the chunks by the instructions of a
-// wave: without their products they take 75 % of the time, and the matrix cores are busy
-// for 35 %.
+// Measured (us): 16384 tokens of 32 heads of 128 x 128, 140 ahead of the chunks and 725
+// for them (2.8 a chunk); eight prompts of 4096 tokens, 275 and 620; one chunk of 24
+// heads 9.5 and 7. The first kernel takes four workgroups of 36 KB a CU (three of 53 KB
+// took 165 and 300); a wave waits there for the keys' tiles that it loads one after the
+// other, for T's chain of substitutions and products and at five barriers. The chunks are
+// bound by the instructions of a wave: 863 vector instructions a chunk, 216 of them
+// products, the matrix cores busy for 34 % of the time.
 #include "ssm_delta_device.h"
 #include "ssm_packed.h"
 
